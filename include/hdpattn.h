@@ -255,10 +255,146 @@ hdp_status_t hdp_lse_merge_rows(int32_t m, int64_t rows, int32_t d, const float*
  */
 hdp_status_t hdp_flops_per_shard(hdp_plan_t plan, int32_t d, int32_t hq, int64_t* d_out, void* stream);
 
+/* ====================================================================== */
+/* 8-bit key/value cache: writing it, reading it back, attention over it for
+ * the newest tokens of each sequence, a cheap score that chooses blocks of it
+ * for each query, and attention over the chosen blocks.  With it a packed
+ * prompt that went through hdp_attention_fwd is continued token by token.
+ *
+ * A cache is a pool of pages of HDP_CACHE_BLOCK tokens, shared by any number
+ * of sequences; a page table says which page holds block b (tokens 64 b ..
+ * 64 b + 63) of sequence i.  The caller owns every buffer, hands out pages and
+ * advances the lengths; nothing is kept inside the library between calls, all
+ * calls are asynchronous, none blocks the host, allocates or needs a
+ * workspace in a given state, and all of them may be captured into a CUDA
+ * graph and replayed while the caller changes the lengths, tables and inputs
+ * in place.
+ *
+ * Codes.  Each (page, kv head) has two scales, one for K and one for V; a
+ * value is code * scale.  A scale is a power of two: the smallest 2^e,
+ * e >= -126, with |x| <= M 2^e for every row ever written to the block since
+ * its first one (M = 448 for e4m3, 127 for int8).  Division by it, code *
+ * scale (in bf16 too) and a change of scale are exact but for one rounding of
+ * the code to the nearest (ties to even).  When a row needs a larger scale,
+ * the block's codes are rounded to the new one; over any number of such
+ * changes an int8 value is off by less than one step and an e4m3 value by at
+ * most half a step plus one subnormal step (2^-9 scale).  A row with an
+ * infinity or NaN makes the scale NaN: the block then reads as NaN until its
+ * first row is written again.
+ *
+ * Bounds.  For each (page, kv head) the channel-wise minimum and maximum of
+ * the K rows ever written, rounded outwards to whole multiples of the K scale
+ * (int8) or of four K scales (e4m3): a function of the rows alone.
+ */
+#define HDP_CACHE_BLOCK 64
+#define HDP_CACHE_E4M3 0
+#define HDP_CACHE_INT8 1
+
+typedef struct {
+  void* k;               /* [num_pages][hkv][64][d] codes, 16-byte aligned    */
+  void* v;               /* [num_pages][hkv][d][64] codes, 16-byte aligned:
+                            token t = 16 j + 8 h + 2 c + e of a block stands
+                            at byte 16 c + 4 j + 2 h + e                       */
+  float* scales;         /* [num_pages][hkv][2] {K, V}, 8-byte aligned         */
+  int8_t* bounds;        /* [num_pages][hkv][2][d] {min, max}, 16-byte aligned */
+  int32_t num_pages;     /* >= 1                                               */
+  int32_t hkv;           /* >= 1                                               */
+  int32_t d;             /* 64 or 128                                          */
+  int32_t format;        /* HDP_CACHE_E4M3 or HDP_CACHE_INT8                   */
+  const int32_t* page_table; /* [num_seqs][max_pages] page of each block       */
+  const int32_t* lens;   /* [num_seqs] tokens of each sequence, the rows of the
+                            call included                                      */
+  int32_t num_seqs;      /* >= 1                                               */
+  int32_t max_pages;     /* columns of page_table, >= 1                        */
+} hdp_cache_t;
+
+/*
+ * Common to the calls below.  The rows of a call are the newest tokens of each
+ * sequence, packed: cu [num_seqs + 1] (device int32, cu[0] = 0, ascending)
+ * gives sequence i the rows cu[i] .. cu[i+1] - 1, and row r of it is the token
+ * at position lens[i] - (cu[i+1] - cu[i]) + r.  cu NULL means one row for each
+ * sequence; `rows` must then equal num_seqs.  `rows` is the row count of the
+ * row tensors (0 .. 2^31-1); rows from cu[num_seqs] on belong to no sequence:
+ * they are not read, and their outputs are left as they were.  A row at a
+ * negative position (more rows than tokens) is not written, reads as zeros,
+ * attends to nothing and selects nothing.
+ * A length outside [0, 64 max_pages] is taken as the nearest bound, and a page
+ * outside [0, num_pages) is never touched (its tokens are not written, read
+ * as zeros, and are masked in the attention); both are reported by the next
+ * hdp_device_status as INVALID_ARGUMENT.  Table entries beyond a sequence's
+ * last block are not read.
+ * Host-side errors: INVALID_ARGUMENT for NULL pointers, sizes, alignment and
+ * workspaces; UNSUPPORTED for a d other than 64 and 128.
+ */
+
+/*
+ * Writes K and V rows (bf16 [rows][hkv][d], 16-byte aligned) into the cache.
+ * A block's first row starts the block anew: its codes, scales and bounds do
+ * not depend on what the page held before (other rows get zero codes).  Rows
+ * appended behind the first keep the codes that are there, at a larger scale
+ * if the new rows need one.  Positions may be written again (a rejected draft
+ * is overwritten by appending with a smaller length).  A page that the call
+ * writes must belong to one sequence only; complete pages may be shared.
+ */
+hdp_status_t hdp_cache_append(const hdp_cache_t* cache, const int32_t* cu, int64_t rows, const void* k, const void* v,
+                              void* stream);
+
+/* Reads the rows back: k, v [rows][hkv][d] bf16 (exactly code * scale). */
+hdp_status_t hdp_cache_read(const hdp_cache_t* cache, const int32_t* cu, int64_t rows, void* k, void* v, void* stream);
+
+/*
+ * Attention of the rows over the cache: for row r of sequence i at position p
+ * and query head h (kv head h / (hq / hkv)),
+ *   S_j = scale * q . k_j over cached tokens j <= p,
+ *   lse = ln sum_j exp(S_j),  o = sum_j exp(S_j - lse) v_j,
+ * and o = 0, lse = -inf where no token is left.  Inputs are the dequantised
+ * codes; sums and the softmax's statistics are fp32.
+ *   q, o [rows][hq][d] bf16, 16-byte aligned; lse [hq][rows] fp32; hq % hkv == 0.
+ *   blocks NULL (count 0): every block.  Else device int32 [rows][hkv][count],
+ *   count >= 1: for each row and kv head the blocks to attend to, strictly
+ *   ascending.  An entry that is negative, beyond the row's position or not
+ *   above the entry before it is skipped (hdp_cache_select pads with -1).
+ *   workspace: device, 256-byte aligned, at least
+ *   hdp_cache_attention_workspace_bytes (which depends on the device's SM
+ *   count, hq, hkv and d only); calls that may overlap need one each.
+ * Deterministic: the order of all sums depends only on the shapes and lengths.
+ * Made for a few rows per sequence (16 rows times heads of a group share one
+ * pass over the cache); more rows are correct and read the cache again.
+ */
+hdp_status_t hdp_cache_attention_workspace_bytes(const hdp_cache_t* cache, int32_t hq, size_t* bytes);
+hdp_status_t hdp_cache_attention(const hdp_cache_t* cache, const int32_t* cu, int64_t rows, const void* q, int32_t hq,
+                                 float scale, const int32_t* blocks, int32_t count, void* workspace,
+                                 size_t workspace_bytes, void* o, float* lse, void* stream);
+
+/*
+ * Chooses `count` blocks for each row and kv head by an upper bound of its
+ * scores.  The query rows of the head's group are rounded to whole numbers c
+ * with one power of two for the group (largest magnitude at most 127); with
+ * lo, hi the bounds of a block and s its K scale,
+ *   U = sum over heads and channels of max(c, 0) hi + min(c, 0) lo   (integer),
+ *   score = fp32(U) * s.
+ * Of the blocks 0 .. p / 64 of a row at position p, the first keep_first and
+ * the last keep_last are always chosen, then those with the highest scores,
+ * ties to the lower block; a block whose scale is NaN counts as highest, one
+ * whose page is invalid as lowest.
+ * Whole-number sums make the choice independent of any order of summation.
+ * (An infinity or NaN in q counts as 0 here; the attention returns NaN.)
+ *   q [rows][hq][d] bf16, 16-byte aligned, hq / hkv <= 128;
+ *   blocks [rows][hkv][count] int32 out: ascending, -1 behind the last;
+ *   count >= 1, keep_first >= 0, keep_last >= 0, keep_first + keep_last <= count;
+ *   workspace: device, 256-byte aligned, hdp_cache_select_workspace_bytes
+ *   (rows * hkv * max_pages scores).
+ */
+hdp_status_t hdp_cache_select_workspace_bytes(const hdp_cache_t* cache, int64_t rows, size_t* bytes);
+hdp_status_t hdp_cache_select(const hdp_cache_t* cache, const int32_t* cu, int64_t rows, const void* q, int32_t hq,
+                              int32_t count, int32_t keep_first, int32_t keep_last, void* workspace,
+                              size_t workspace_bytes, int32_t* blocks, void* stream);
+
 /*
  * Synchronizes `stream` and reports (then clears) a device-side failure
  * recorded by an earlier kernel of this library on the current device:
- * HDP_ERR_DEVICE_TIMEOUT when a bounded wait expired, HDP_ERR_CUDA when the
+ * HDP_ERR_DEVICE_TIMEOUT when a bounded wait expired, INVALID_ARGUMENT when a
+ * cache call met a length or page outside its tables, HDP_ERR_CUDA when the
  * stream reports a CUDA error, else HDP_OK.
  */
 hdp_status_t hdp_device_status(void* stream);

@@ -15,6 +15,9 @@ from .binding import (  # noqa: F401
     EXPORTED,
     HDP_BALANCE_DP,
     HDP_BALANCE_PP,
+    HDP_CACHE_BLOCK,
+    HDP_CACHE_E4M3,
+    HDP_CACHE_INT8,
     HDP_ERR_CUDA,
     HDP_ERR_DEVICE_TIMEOUT,
     HDP_ERR_INVALID_ARGUMENT,
@@ -27,6 +30,7 @@ from .binding import (  # noqa: F401
     HDP_PLAN_NO_SHARDS,
     HDP_PLAN_NO_SPLIT,
     HdpError,
+    KVCache,
     OffloadModel,
     Plan,
     hdp_attention_bwd,
@@ -35,6 +39,12 @@ from .binding import (  # noqa: F401
     hdp_attention_fwd_split_noalloc,
     hdp_balance_schedule,
     hdp_attention_workspace_bytes,
+    hdp_cache_append,
+    hdp_cache_attention,
+    hdp_cache_attention_workspace_bytes,
+    hdp_cache_read,
+    hdp_cache_select,
+    hdp_cache_select_workspace_bytes,
     hdp_device_status,
     hdp_fit_cost_model,
     hdp_flops_per_shard,
@@ -93,3 +103,69 @@ def attention_backward(plan: Plan, q, k, v, o, lse, dout, scale: float | None = 
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     hdp_attention_bwd(plan, q, k, v, o, lse, dout, hq, hkv, d, scale, ws, dq, dk, dv, stream=stream)
     return dq, dk, dv
+
+
+_cache_ws_bytes: dict = {}
+
+
+def _new(stream, *wanted):
+    """torch.empty of each (shape, dtype, device), from the pool of the stream that the call runs on: what is freed
+    after the call is only given out again in that stream's order."""
+    import torch
+
+    if stream is None:
+        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype, device in wanted]
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=wanted[0][2])
+    with torch.cuda.stream(stream):
+        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype, device in wanted]
+
+
+def cache_append(cache: KVCache, page_table, lens, k, v, cu=None, stream=None):
+    """Writes k, v [rows][hkv][d] bf16 into the cache: the newest tokens of each sequence, packed, with prefix sums cu
+    (None: one row for each sequence).  lens counts them already."""
+    hdp_cache_append(cache, page_table, lens, k, v, cu=cu, stream=stream)
+
+
+def cache_read(cache: KVCache, page_table, lens, rows: int, cu=None, stream=None):
+    """The newest tokens of each sequence as (k, v) [rows][hkv][d] bf16, exactly code * scale."""
+    import torch
+
+    what = ((rows, cache.hkv, cache.d), torch.bfloat16, cache.device)
+    k, v = _new(stream, what, what)
+    hdp_cache_read(cache, page_table, lens, k, v, cu=cu, stream=stream)
+    return k, v
+
+
+def cache_select(cache: KVCache, page_table, lens, q, count: int, cu=None, keep_first: int = 1, keep_last: int = 1,
+                 stream=None):
+    """The `count` blocks of the cache with the highest upper bound of their scores, for each row of q [rows][hq][d]
+    bf16 and kv head: int32 [rows][hkv][count], ascending, -1 behind the last."""
+    import torch
+
+    rows = q.shape[0]
+    nbytes = (rows * cache.hkv * page_table.shape[1] * 4 + 255) // 256 * 256  # hdp_cache_select_workspace_bytes
+    blocks, ws = _new(stream, ((rows, cache.hkv, count), torch.int32, cache.device),
+                      ((nbytes,), torch.uint8, cache.device))
+    hdp_cache_select(cache, page_table, lens, q, keep_first, keep_last, ws, blocks, cu=cu, stream=stream)
+    return blocks
+
+
+def cache_attention(cache: KVCache, page_table, lens, q, cu=None, blocks=None, scale: float | None = None,
+                    stream=None):
+    """Attention of q [rows][hq][d] bf16, the newest tokens of each sequence, over the cache, or over the chosen
+    blocks only; returns (o bf16 [rows][hq][d], lse fp32 [hq][rows]).  Outputs that a call on another stream than the
+    current one returns belong to that stream."""
+    import torch
+
+    rows, hq, d = q.shape
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    key = (cache.device, cache.d)
+    if key not in _cache_ws_bytes:
+        _cache_ws_bytes[key] = hdp_cache_attention_workspace_bytes(cache, hq)
+    o, lse, ws = _new(stream, ((rows, hq, d), torch.bfloat16, cache.device),
+                      ((hq, rows), torch.float32, cache.device),
+                      ((_cache_ws_bytes[key],), torch.uint8, cache.device))
+    hdp_cache_attention(cache, page_table, lens, q, scale, ws, o, lse, cu=cu, blocks=blocks, stream=stream)
+    return o, lse

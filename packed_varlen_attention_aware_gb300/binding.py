@@ -26,6 +26,9 @@ HDP_PLAN_NO_SHARDS = 1
 HDP_PLAN_NO_SPLIT = 2
 HDP_BALANCE_DP = 0
 HDP_BALANCE_PP = 1
+HDP_CACHE_BLOCK = 64
+HDP_CACHE_E4M3 = 0
+HDP_CACHE_INT8 = 1
 
 # Every symbol include/hdpattn.h declares.
 EXPORTED = (
@@ -35,6 +38,8 @@ EXPORTED = (
     "hdp_kernel_launch_count", "hdp_host_sync_count", "hdp_set_wait_budget", "hdp_attention_fwd_split_noalloc",
     "hdp_ring_step_compute", "hdp_ring_attention_time", "hdp_offload_ranks", "hdp_fit_cost_model",
     "hdp_balance_schedule", "hdp_attention_bwd_workspace_bytes", "hdp_attention_bwd",
+    "hdp_cache_append", "hdp_cache_read", "hdp_cache_attention_workspace_bytes", "hdp_cache_attention",
+    "hdp_cache_select_workspace_bytes", "hdp_cache_select",
 )
 
 
@@ -43,6 +48,14 @@ class OffloadModel(ctypes.Structure):
     _fields_ = [("alpha1", ctypes.c_double), ("beta1", ctypes.c_double), ("gamma", ctypes.c_double),
                 ("alpha2", ctypes.c_double), ("beta2", ctypes.c_double), ("bw_d2h", ctypes.c_double),
                 ("bw_h2d", ctypes.c_double), ("layers", ctypes.c_int32)]
+
+
+class CacheStruct(ctypes.Structure):
+    """hdp_cache_t."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("bounds", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("hkv", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("format", ctypes.c_int32), ("page_table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("num_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
 
 class HdpError(RuntimeError):
@@ -102,6 +115,12 @@ def load(path: str | None = None):
             "hdp_balance_schedule": [V, I32, I32, I32, I64, I32, V, V, V],
             "hdp_attention_bwd_workspace_bytes": [V, I32, I32, ctypes.POINTER(SZ)],
             "hdp_attention_bwd": [V, V, V, V, V, V, V, I32, I32, I32, F32, V, SZ, V, V, V, V],
+            "hdp_cache_append": [ctypes.POINTER(CacheStruct), V, I64, V, V, V],
+            "hdp_cache_read": [ctypes.POINTER(CacheStruct), V, I64, V, V, V],
+            "hdp_cache_attention_workspace_bytes": [ctypes.POINTER(CacheStruct), I32, ctypes.POINTER(SZ)],
+            "hdp_cache_attention": [ctypes.POINTER(CacheStruct), V, I64, V, I32, F32, V, I32, V, SZ, V, V, V],
+            "hdp_cache_select_workspace_bytes": [ctypes.POINTER(CacheStruct), I64, ctypes.POINTER(SZ)],
+            "hdp_cache_select": [ctypes.POINTER(CacheStruct), V, I64, V, I32, I32, I32, I32, V, SZ, V, V],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -304,6 +323,163 @@ def hdp_set_wait_budget(clocks: int) -> None:
 
 def hdp_last_error_message() -> str:
     return load().hdp_last_error_message().decode(errors="replace")
+
+
+# ---------------------------------------------------------------- 8-bit key/value cache
+
+class KVCache:
+    """A pool of pages of 64 tokens with 8-bit K and V codes (hdp_cache_t without the sequences).
+
+    k [pages][hkv][64][d] and v [pages][hkv][d][64] uint8 codes, scales [pages][hkv][2] float32, bounds
+    [pages][hkv][2][d] int8: contiguous CUDA tensors of one device.  The caller hands out the pages: a page table
+    int32 [sequences][columns] and lengths int32 [sequences] go with every call."""
+
+    def __init__(self, k, v, scales, bounds, format: int):
+        import torch
+
+        if k.dim() != 4:
+            raise ValueError("k must be [pages][hkv][64][d]")
+        pages, hkv, block, d = k.shape
+        _tensor(k, "k", torch.uint8, (pages, hkv, HDP_CACHE_BLOCK, d), k.device)
+        _tensor(v, "v", torch.uint8, (pages, hkv, d, HDP_CACHE_BLOCK), k.device)
+        _tensor(scales, "scales", torch.float32, (pages, hkv, 2), k.device)
+        _tensor(bounds, "bounds", torch.int8, (pages, hkv, 2, d), k.device)
+        if format not in (HDP_CACHE_E4M3, HDP_CACHE_INT8):
+            raise ValueError("format must be HDP_CACHE_E4M3 or HDP_CACHE_INT8")
+        self.k, self.v, self.scales, self.bounds, self.format = k, v, scales, bounds, int(format)
+        self.num_pages, self.hkv, self.d, self.device = pages, hkv, d, k.device
+        self._struct = CacheStruct(k.data_ptr(), v.data_ptr(), scales.data_ptr(), bounds.data_ptr(), pages, hkv, d,
+                                   self.format, None, None, 0, 0)
+
+    @classmethod
+    def empty(cls, num_pages: int, hkv: int, d: int, format: int, device="cuda"):
+        """A pool of unwritten pages (a block's first row initialises it)."""
+        import torch
+
+        dev = torch.device(device)
+        return cls(torch.empty((num_pages, hkv, HDP_CACHE_BLOCK, d), dtype=torch.uint8, device=dev),
+                   torch.empty((num_pages, hkv, d, HDP_CACHE_BLOCK), dtype=torch.uint8, device=dev),
+                   torch.empty((num_pages, hkv, 2), dtype=torch.float32, device=dev),
+                   torch.empty((num_pages, hkv, 2, d), dtype=torch.int8, device=dev), format)
+
+    def _with(self, page_table, lens, cu, rows):
+        """hdp_cache_t of a call over these sequences."""
+        import torch
+
+        n = lens.shape[0] if lens.dim() == 1 else -1
+        _tensor(lens, "lens", torch.int32, (n,), self.device)
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [sequences][columns]")
+        _tensor(page_table, "page_table", torch.int32, (n, page_table.shape[1]), self.device)
+        if cu is not None:
+            _tensor(cu, "cu", torch.int32, (n + 1,), self.device)
+        elif rows != n:
+            raise ValueError(f"without cu there is one row for each of the {n} sequences, not {rows}")
+        s = CacheStruct.from_buffer_copy(self._struct)
+        s.page_table, s.lens, s.num_seqs, s.max_pages = page_table.data_ptr(), lens.data_ptr(), n, page_table.shape[1]
+        return s
+
+
+def _tensor(t, name, dtype, shape, device):
+    """Raises unless t is a contiguous tensor of this type, shape and CUDA device."""
+    if t.dtype != dtype or t.device != device or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor on {device} (a CUDA device)")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+class _OnDevice:
+    """Makes `device` current for a call, if it is not."""
+
+    def __init__(self, device):
+        import torch
+
+        self._guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def hdp_cache_append(cache: KVCache, page_table, lens, k, v, cu=None, stream=None):
+    """Writes the rows k, v [rows][hkv][d] bf16, the newest tokens of each sequence, into the cache."""
+    import torch
+
+    rows = k.shape[0]
+    _tensor(k, "k", torch.bfloat16, (rows, cache.hkv, cache.d), cache.device)
+    _tensor(v, "v", torch.bfloat16, (rows, cache.hkv, cache.d), cache.device)
+    s = cache._with(page_table, lens, cu, rows)
+    with _OnDevice(cache.device):
+        _check(load().hdp_cache_append(s, _ptr(cu), rows, _ptr(k), _ptr(v), _stream(stream)), "hdp_cache_append")
+
+
+def hdp_cache_read(cache: KVCache, page_table, lens, k, v, cu=None, stream=None):
+    """Reads the newest tokens of each sequence into k, v [rows][hkv][d] bf16."""
+    import torch
+
+    rows = k.shape[0]
+    _tensor(k, "k", torch.bfloat16, (rows, cache.hkv, cache.d), cache.device)
+    _tensor(v, "v", torch.bfloat16, (rows, cache.hkv, cache.d), cache.device)
+    s = cache._with(page_table, lens, cu, rows)
+    with _OnDevice(cache.device):
+        _check(load().hdp_cache_read(s, _ptr(cu), rows, _ptr(k), _ptr(v), _stream(stream)), "hdp_cache_read")
+
+
+def hdp_cache_attention_workspace_bytes(cache: KVCache, hq: int) -> int:
+    n = ctypes.c_size_t()
+    with _OnDevice(cache.device):
+        _check(load().hdp_cache_attention_workspace_bytes(cache._struct, hq, ctypes.byref(n)),
+               "hdp_cache_attention_workspace_bytes")
+    return n.value
+
+
+def hdp_cache_attention(cache: KVCache, page_table, lens, q, scale: float, workspace, o, lse, cu=None, blocks=None,
+                        stream=None):
+    """Attention of the rows q [rows][hq][d] bf16 over the cache (over `blocks` int32 [rows][hkv][count] only, if
+    given) into o (like q) and lse [hq][rows] float32."""
+    import torch
+
+    rows, hq = q.shape[0], q.shape[1] if q.dim() == 3 else -1
+    _tensor(q, "q", torch.bfloat16, (rows, hq, cache.d), cache.device)
+    _tensor(o, "o", torch.bfloat16, (rows, hq, cache.d), cache.device)
+    _tensor(lse, "lse", torch.float32, (hq, rows), cache.device)
+    count = 0
+    if blocks is not None:
+        count = blocks.shape[-1]
+        _tensor(blocks, "blocks", torch.int32, (rows, cache.hkv, count), cache.device)
+    s = cache._with(page_table, lens, cu, rows)
+    with _OnDevice(cache.device):
+        _check(load().hdp_cache_attention(s, _ptr(cu), rows, _ptr(q), hq, float(scale), _ptr(blocks), count,
+                                          _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(o),
+                                          _ptr(lse), _stream(stream)), "hdp_cache_attention")
+
+
+def hdp_cache_select_workspace_bytes(cache: KVCache, page_table, rows: int) -> int:
+    n = ctypes.c_size_t()
+    s = CacheStruct.from_buffer_copy(cache._struct)
+    s.max_pages = page_table.shape[1]
+    _check(load().hdp_cache_select_workspace_bytes(s, rows, ctypes.byref(n)), "hdp_cache_select_workspace_bytes")
+    return n.value
+
+
+def hdp_cache_select(cache: KVCache, page_table, lens, q, keep_first: int, keep_last: int, workspace, blocks, cu=None,
+                     stream=None):
+    """Chooses blocks for each row of q [rows][hq][d] bf16 and kv head into blocks int32 [rows][hkv][count]."""
+    import torch
+
+    rows, hq = q.shape[0], q.shape[1] if q.dim() == 3 else -1
+    _tensor(q, "q", torch.bfloat16, (rows, hq, cache.d), cache.device)
+    count = blocks.shape[-1]
+    _tensor(blocks, "blocks", torch.int32, (rows, cache.hkv, count), cache.device)
+    s = cache._with(page_table, lens, cu, rows)
+    with _OnDevice(cache.device):
+        _check(load().hdp_cache_select(s, _ptr(cu), rows, _ptr(q), hq, count, keep_first, keep_last, _ptr(workspace),
+                                       workspace.numel() * workspace.element_size(), _ptr(blocks), _stream(stream)),
+               "hdp_cache_select")
 
 
 # ---------------------------------------------------------------- cost models (host arithmetic)

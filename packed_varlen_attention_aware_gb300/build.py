@@ -16,8 +16,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhdpattn.so")
-SOURCES = ["api.cu", "plan.cu", "attn_fwd.cu", "attn_bwd.cu", "lse_merge.cu", "cost_model.cpp", "balance.cpp"]
-HEADERS = ["internal.h", "sm103_ptx.cuh"]
+SOURCES = ["api.cu", "plan.cu", "attn_fwd.cu", "attn_bwd.cu", "lse_merge.cu", "kv_cache.cu",
+           "kv_attention.cu", "kv_select.cu", "cost_model.cpp", "balance.cpp"]
+HEADERS = ["internal.h", "kv_cache.cuh", "sm103_ptx.cuh"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

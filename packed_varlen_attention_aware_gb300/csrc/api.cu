@@ -87,6 +87,9 @@ hdp_status_t hdp_device_status(void* stream) {
   HDP_CUDA_TRY(cudaMemcpyFromSymbol(&code, g_device_error, sizeof code));
   if (code != 0) {
     HDP_CUDA_TRY(cudaMemcpyToSymbol(g_device_error, &zero, sizeof zero));
+    if (code == hdp::kErrCacheTable)
+      return hdp::fail(HDP_ERR_INVALID_ARGUMENT,
+                       "a cache call met a length outside its page table or a page outside the pool");
     char buf[128];
     std::snprintf(buf, sizeof buf, "a kernel's bounded wait expired (code %u)", code);
     return hdp::fail(HDP_ERR_DEVICE_TIMEOUT, buf);

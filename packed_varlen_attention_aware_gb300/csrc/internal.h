@@ -32,6 +32,9 @@ inline int heads_per_round(long long max_doc_len, int hkv) { return max_doc_len 
 // Device error word shared by all kernels (bounded-wait timeouts, internal
 // consistency checks).  Defined in api.cu; read by hdp_device_status.
 unsigned int* device_error_word();
+// Code of a cache length or page outside its bounds (the codes of expired
+// waits are 0x1xx and 0x2xx).
+constexpr unsigned int kErrCacheTable = 0x301;
 
 // Count one kernel enqueued by this library (reported by hdp_kernel_launch_count).
 void note_launch();

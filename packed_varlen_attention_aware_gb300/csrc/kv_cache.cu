@@ -1,0 +1,549 @@
+// Writing rows into the 8-bit cache and reading them back.
+//
+// One CTA has one (block of 64 tokens, kv head): 128 threads hold its new K and
+// V rows in registers (16 bytes = 8 channels of a row each, d / 16 rows), so
+// the largest magnitude, the scale, the bounds and the codes come from one read.
+//
+// The scale is 2^e with the smallest e that fits the largest magnitude ever
+// written, so x / s is a shift of the exponent and the code is the only
+// rounding; a block whose scale grows has its codes shifted and rounded again.
+//
+// V codes lie [channel][token] with the tokens in the order in which a 16-row
+// matrix fragment takes its k index (the attention then feeds 16-byte loads
+// straight to the tensor cores).  Each warp here has the tokens of one 16-byte
+// chunk, so the transposition is a byte shuffle between two (d = 128) or four
+// (d = 64) lanes and the chunk is stored whole; nothing goes through shared
+// memory.
+#include <cuda_fp8.h>
+
+#include <string>
+
+#include "kv_cache.cuh"
+
+namespace hdp {
+
+hdp_status_t cache_view(const char* call, const hdp_cache_t* c, const int32_t* cu, int64_t rows, CacheView* out) {
+  const std::string name(call);
+  if (!c) return fail(HDP_ERR_INVALID_ARGUMENT, name + ": cache is NULL");
+  if (!c->k || !c->v || !c->scales || !c->bounds || !c->page_table || !c->lens)
+    return fail(HDP_ERR_INVALID_ARGUMENT, name + ": the cache has a NULL pointer");
+  if (c->num_pages < 1 || c->hkv < 1 || c->num_seqs < 1 || c->max_pages < 1)
+    return fail(HDP_ERR_INVALID_ARGUMENT, name + ": num_pages, hkv, num_seqs and max_pages must be >= 1");
+  if (c->num_seqs > (1 << 24)) return fail(HDP_ERR_UNSUPPORTED, name + ": num_seqs must be at most 2^24");
+  if (c->hkv > 65535) return fail(HDP_ERR_UNSUPPORTED, name + ": hkv must be at most 65535");
+  if (c->d != 64 && c->d != 128) return fail(HDP_ERR_UNSUPPORTED, name + ": d must be 64 or 128");
+  if (c->format != HDP_CACHE_E4M3 && c->format != HDP_CACHE_INT8)
+    return fail(HDP_ERR_INVALID_ARGUMENT, name + ": unknown cache format");
+  if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v) |
+       reinterpret_cast<uintptr_t>(c->bounds)) & 15 ||
+      reinterpret_cast<uintptr_t>(c->scales) & 7)
+    return fail(HDP_ERR_INVALID_ARGUMENT,
+                name + ": k, v and bounds must be 16-byte and scales 8-byte aligned");
+  if (rows < 0 || rows > 2147483647LL)
+    return fail(HDP_ERR_INVALID_ARGUMENT, name + ": rows must be 0 .. 2^31-1");
+  if (!cu && rows != c->num_seqs)
+    return fail(HDP_ERR_INVALID_ARGUMENT, name + ": without cu, rows must equal num_seqs");
+  out->k = static_cast<uint8_t*>(c->k);
+  out->v = static_cast<uint8_t*>(c->v);
+  out->scales = c->scales;
+  out->bounds = c->bounds;
+  out->table = c->page_table;
+  out->lens = c->lens;
+  out->cu = cu;
+  out->num_pages = c->num_pages;
+  out->hkv = c->hkv;
+  out->num_seqs = c->num_seqs;
+  out->max_pages = c->max_pages;
+  out->rows = static_cast<int>(rows);
+  return HDP_OK;
+}
+
+namespace {
+
+constexpr int kThreads = 128;
+
+// Code of x (already divided by the scale): nearest, ties to even.
+template <int FMT>
+__device__ __forceinline__ uint32_t code_pair(float a, float b) {
+  if constexpr (FMT == HDP_CACHE_INT8) {
+    return (static_cast<uint32_t>(__float2int_rn(a)) & 0xffu) | ((static_cast<uint32_t>(__float2int_rn(b)) & 0xffu) << 8);
+  } else {
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ float2 value_pair(uint32_t two) {
+  if constexpr (FMT == HDP_CACHE_INT8) {
+    return make_float2(static_cast<float>(static_cast<int8_t>(two & 0xff)),
+                       static_cast<float>(static_cast<int8_t>((two >> 8) & 0xff)));
+  } else {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xffff), __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+  }
+}
+
+// Four codes at a new scale (`ratio` = old scale / new scale).
+template <int FMT>
+__device__ __forceinline__ uint32_t rescale4(uint32_t x, float ratio) {
+  const float2 a = value_pair<FMT>(x), b = value_pair<FMT>(x >> 16);
+  return code_pair<FMT>(a.x * ratio, a.y * ratio) | (code_pair<FMT>(b.x * ratio, b.y * ratio) << 16);
+}
+
+// Exponent of the smallest power of two 2^e, e >= -126, with |x| <= M 2^e, for
+// the bf16 bits of |x|: M is 1.984375 * 2^6 (int8) or 1.75 * 2^8 (e4m3).
+template <int FMT>
+__device__ __forceinline__ int scale_exponent(uint32_t abs_bits) {
+  const int x = static_cast<int>(abs_bits >> 7) - 127, m = abs_bits & 0x7f;
+  const int e = FMT == HDP_CACHE_INT8 ? x - 6 + (m > 0x7e) : x - 8 + (m > 0x60);
+  return max(e, -126);
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+// Words of byte x of each of four words: (a.x, b.x, c.x, d.x) for x = 0..3.
+__device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&t)[4]) {
+  const uint32_t ab0 = __byte_perm(a, b, 0x5140), ab1 = __byte_perm(a, b, 0x7362);
+  const uint32_t cd0 = __byte_perm(c, d, 0x5140), cd1 = __byte_perm(c, d, 0x7362);
+  t[0] = __byte_perm(ab0, cd0, 0x5410);
+  t[1] = __byte_perm(ab0, cd0, 0x7632);
+  t[2] = __byte_perm(ab1, cd1, 0x5410);
+  t[3] = __byte_perm(ab1, cd1, 0x7632);
+}
+
+// Where a thread's rows and channels lie.  Pass p of a thread is token
+//   d = 128: 8 p + 2 warp + e            (e = lane / 16)
+//   d =  64: 16 p + 8 h + 2 warp + e     (e = lane / 8 % 2, h = lane / 16)
+// of the block, so warp c has exactly the tokens of V chunk c.
+template <int D>
+struct Place {
+  static constexpr int kPasses = D / 16;
+  static constexpr int kLanes = D / 8;  // lanes of a row
+  int c, e, h, ch;
+  __device__ __forceinline__ Place() {
+    const int lane = threadIdx.x & 31;
+    c = threadIdx.x >> 5;
+    ch = (lane % kLanes) * 8;
+    e = (lane / kLanes) & 1;
+    h = D == 64 ? lane >> 4 : 0;
+  }
+  __device__ __forceinline__ int token(int p) const { return D == 128 ? 8 * p + 2 * c + e : 16 * p + 8 * h + 2 * c + e; }
+  // Byte of token(p) inside a channel's 64 bytes of V.
+  __device__ __forceinline__ int v_byte(int p) const {
+    const int j = D == 128 ? p >> 1 : p, hh = D == 128 ? p & 1 : h;
+    return 16 * c + 4 * j + 2 * hh + e;
+  }
+};
+
+// Row-wise codes w[p][2] (8 channels of token(p)) to whole 16-byte chunks of
+// channels (out[x] belongs to channel v_channel(x)) and back.
+template <int D>
+__device__ __forceinline__ void to_chunks(const Place<D>& pl, const uint32_t (&w)[Place<D>::kPasses][2],
+                                          uint32_t (&out)[D / 32][4]) {
+  constexpr int P = Place<D>::kPasses;
+  uint32_t lo[P], hi[P];  // of this lane's four channels: tokens with e = 0 and e = 1
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const uint32_t mine = pl.e ? w[p][1] : w[p][0];
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, pl.e ? w[p][0] : w[p][1], Place<D>::kLanes);
+    lo[p] = pl.e ? got : mine;
+    hi[p] = pl.e ? mine : got;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t t[4];
+    if constexpr (D == 128) {
+      transpose4(lo[2 * j], hi[2 * j], lo[2 * j + 1], hi[2 * j + 1], t);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) out[x][j] = t[x];
+    } else {
+      const uint32_t lo2 = __shfl_xor_sync(0xffffffffu, lo[j], 16), hi2 = __shfl_xor_sync(0xffffffffu, hi[j], 16);
+      if (pl.h) transpose4(lo2, hi2, lo[j], hi[j], t);
+      else transpose4(lo[j], hi[j], lo2, hi2, t);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) out[x][j] = pl.h ? t[2 + x] : t[x];
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ int v_channel(const Place<D>& pl, int x) {
+  return pl.ch + 4 * pl.e + (D == 64 ? 2 * pl.h : 0) + x;
+}
+
+template <int D>
+__device__ __forceinline__ void from_chunks(const Place<D>& pl, const uint32_t (&in)[D / 32][4],
+                                            uint32_t (&w)[Place<D>::kPasses][2]) {
+  constexpr int P = Place<D>::kPasses;
+  uint32_t lo[P], hi[P];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t t[4];
+    if constexpr (D == 128) {
+      transpose4(in[0][j], in[1][j], in[2][j], in[3][j], t);  // its own inverse
+      lo[2 * j] = t[0];
+      hi[2 * j] = t[1];
+      lo[2 * j + 1] = t[2];
+      hi[2 * j + 1] = t[3];
+    } else {
+      const uint32_t a = __shfl_xor_sync(0xffffffffu, in[0][j], 16), b = __shfl_xor_sync(0xffffffffu, in[1][j], 16);
+      if (pl.h) transpose4(a, b, in[0][j], in[1][j], t);
+      else transpose4(in[0][j], in[1][j], a, b, t);
+      lo[j] = pl.h ? t[2] : t[0];
+      hi[j] = pl.h ? t[3] : t[1];
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const uint32_t mine = pl.e ? hi[p] : lo[p];
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, pl.e ? lo[p] : hi[p], Place<D>::kLanes);
+    w[p][0] = pl.e ? got : mine;
+    w[p][1] = pl.e ? mine : got;
+  }
+}
+
+// The block of a CTA: which sequence, block and rows `slot` stands for.
+// Sequence i has the slots from cu[i] / 64 + 2 i on; n rows touch at most
+// ceil((n + 62) / 64) + 1 <= cu[i+1] / 64 - cu[i] / 64 + 2 blocks.
+struct Touched {
+  int seq, block;
+  int first, count;  // first token of the block that the call has, and how many
+  long long row;     // row of that token
+  bool fresh;        // the block's first token is among them
+  long long row0, before;  // the slot also stands for `before` rows from row0 on, at negative positions
+};
+
+__device__ __forceinline__ bool touched_block(const CacheView& c, int slot, Touched& t) {
+  const int i = c.cu ? find_last(c.num_seqs, slot,
+                                 [&](int s) { return static_cast<long long>(__ldg(c.cu + s)) / kBlock + 2LL * s; })
+                     : slot;
+  int row0, n;
+  seq_rows(c, i, row0, n);
+  t.before = 0;
+  if (n == 0) return false;
+  const long long len = seq_len(c, i), p0 = first_position(c, i, len);
+  const long long nth = c.cu ? slot - (row0 / kBlock + 2LL * i) : 0;
+  if (nth == 0 && p0 < 0) {
+    t.row0 = row0;
+    t.before = min(static_cast<long long>(n), -p0);
+  }
+  const long long a0 = p0 > 0 ? p0 : 0;
+  const long long b = a0 / kBlock + nth;
+  const long long end = min(len, p0 + n);
+  if (nth < 0 || b * kBlock >= end) return false;
+  const long long a = max(a0, b * kBlock), z = min(end, (b + 1) * kBlock);
+  if (z <= a) return false;
+  t.seq = i;
+  t.block = static_cast<int>(b);
+  t.first = static_cast<int>(a - b * kBlock);
+  t.count = static_cast<int>(z - a);
+  t.row = row0 + (a - p0);
+  t.fresh = t.first == 0;
+  return true;
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads) k_cache_append(CacheView c, const uint4* __restrict__ k,
+                                                           const uint4* __restrict__ v) {
+  constexpr int P = Place<D>::kPasses;
+  __shared__ uint32_t s_amax[2][4];
+  __shared__ float s_bound[4][2][D];
+  Touched t;
+  if (!touched_block(c, blockIdx.x, t)) return;
+  const int head = blockIdx.y;
+  const int page = page_of(c, t.seq, t.block);
+  if (page < 0) return;
+  const Place<D> pl;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const size_t ph = static_cast<size_t>(page) * c.hkv + head;
+
+  uint4 x[2][P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int r = pl.token(p) - t.first;
+    const size_t at = ((static_cast<size_t>(t.row) + r) * c.hkv + head) * (D / 8) + pl.ch / 8;
+    const bool in = r >= 0 && r < t.count;
+    x[0][p] = in ? __ldg(k + at) : make_uint4(0, 0, 0, 0);
+    x[1][p] = in ? __ldg(v + at) : make_uint4(0, 0, 0, 0);
+  }
+  const float2 old = t.fresh ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(c.scales + 2 * ph);
+
+  // Largest magnitudes, as bf16 bits: their order is the values' order, with
+  // infinity and NaN (>= 0x7f80) on top.
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[w][p].x & 0x7fff7fffu, x[w][p].y & 0x7fff7fffu),
+                               __vmaxu2(x[w][p].z & 0x7fff7fffu, x[w][p].w & 0x7fff7fffu)));
+    }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+    if (lane == 0) s_amax[w][warp] = top;
+  }
+  // Channel-wise minimum and maximum of the new K rows.
+  float lo[8], hi[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    lo[i] = __int_as_float(0x7f800000);
+    hi[i] = -lo[i];
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int r = pl.token(p) - t.first;
+    if (r >= 0 && r < t.count) {
+      const uint32_t q[4] = {x[0][p].x, x[0][p].y, x[0][p].z, x[0][p].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo[2 * i] = fminf(lo[2 * i], bf_lo(q[i]));
+        hi[2 * i] = fmaxf(hi[2 * i], bf_lo(q[i]));
+        lo[2 * i + 1] = fminf(lo[2 * i + 1], bf_hi(q[i]));
+        hi[2 * i + 1] = fmaxf(hi[2 * i + 1], bf_hi(q[i]));
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int o = Place<D>::kLanes; o < 32; o *= 2) {
+      lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+      hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+    }
+  }
+  if (lane < Place<D>::kLanes) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s_bound[warp][0][pl.ch + i] = lo[i];
+      s_bound[warp][1][pl.ch + i] = hi[i];
+    }
+  }
+  __syncthreads();
+
+  float scale[2], inv[2], ratio[2];
+  bool grown[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const uint32_t top = max(max(s_amax[w][0], s_amax[w][1]), max(s_amax[w][2], s_amax[w][3]));
+    const float before = w ? old.y : old.x;
+    const int e = scale_exponent<FMT>(top);
+    const bool lost = top >= 0x7f80u || (!t.fresh && before != before);
+    const float need = lost ? 0.f : pow2i(e);
+    scale[w] = lost ? __int_as_float(0x7fc00000) : fmaxf(need, before);
+    // 1 / scale: the scale is a power of two, so its exponent changes sign
+    inv[w] = lost ? 1.f : __int_as_float((254 << 23) - __float_as_int(scale[w]));
+    grown[w] = !t.fresh && !lost && scale[w] != before;
+    ratio[w] = grown[w] ? before * inv[w] : 1.f;
+  }
+
+  uint8_t* kb = c.k + ph * (kBlock * D);
+  uint8_t* vb = c.v + ph * (kBlock * D);
+  // A larger scale: the codes that are there are rounded to it (every byte of
+  // the block is one, written or zero).
+  if (grown[0] || grown[1]) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      if (!grown[w]) continue;
+      uint4* b = reinterpret_cast<uint4*>(w ? vb : kb);
+      for (int i = threadIdx.x; i < kBlock * D / 16; i += kThreads) {
+        uint4 y = b[i];
+        y.x = rescale4<FMT>(y.x, ratio[w]);
+        y.y = rescale4<FMT>(y.y, ratio[w]);
+        y.z = rescale4<FMT>(y.z, ratio[w]);
+        y.w = rescale4<FMT>(y.w, ratio[w]);
+        b[i] = y;
+      }
+    }
+    __syncthreads();  // the new rows go over them
+  }
+
+  uint32_t code[P][2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const float s = inv[w];
+      const uint4 y = x[w][p];
+      code[p][0] = code_pair<FMT>(bf_lo(y.x) * s, bf_hi(y.x) * s) | (code_pair<FMT>(bf_lo(y.y) * s, bf_hi(y.y) * s) << 16);
+      code[p][1] = code_pair<FMT>(bf_lo(y.z) * s, bf_hi(y.z) * s) | (code_pair<FMT>(bf_lo(y.w) * s, bf_hi(y.w) * s) << 16);
+    }
+    if (w == 0) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int r = pl.token(p) - t.first;
+        if (t.fresh || (r >= 0 && r < t.count))
+          *reinterpret_cast<uint2*>(kb + pl.token(p) * D + pl.ch) = make_uint2(code[p][0], code[p][1]);
+      }
+    } else if (t.fresh) {
+      uint32_t chunk[D / 32][4];
+      to_chunks<D>(pl, code, chunk);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+        *reinterpret_cast<uint4*>(vb + v_channel<D>(pl, i) * kBlock + pl.c * 16) =
+            make_uint4(chunk[i][0], chunk[i][1], chunk[i][2], chunk[i][3]);
+    } else {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int r = pl.token(p) - t.first;
+        if (r >= 0 && r < t.count) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            vb[(pl.ch + i) * kBlock + pl.v_byte(p)] = static_cast<uint8_t>(code[p][i >> 2] >> (8 * (i & 3)));
+        }
+      }
+    }
+  }
+
+  // Bounds, in whole units (one K scale, four for e4m3): rounding outwards
+  // nests, so a change of unit loses nothing but the finer grid.
+  if (threadIdx.x < D) {
+    const int i = threadIdx.x;
+    const float unit = FMT == HDP_CACHE_INT8 ? inv[0] : inv[0] * 0.25f;
+    float a = fminf(fminf(s_bound[0][0][i], s_bound[1][0][i]), fminf(s_bound[2][0][i], s_bound[3][0][i]));
+    float b = fmaxf(fmaxf(s_bound[0][1][i], s_bound[1][1][i]), fmaxf(s_bound[2][1][i], s_bound[3][1][i]));
+    a = floorf(a * unit);
+    b = ceilf(b * unit);
+    int8_t* out = c.bounds + ph * (2 * D) + i;
+    if (!t.fresh) {
+      a = fminf(a, floorf(static_cast<float>(out[0]) * ratio[0]));
+      b = fmaxf(b, ceilf(static_cast<float>(out[D]) * ratio[0]));
+    }
+    out[0] = static_cast<int8_t>(fminf(fmaxf(a, -127.f), 127.f));
+    out[D] = static_cast<int8_t>(fminf(fmaxf(b, -127.f), 127.f));
+  }
+  if (threadIdx.x == 0) *reinterpret_cast<float2*>(c.scales + 2 * ph) = make_float2(scale[0], scale[1]);
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t bf16_pair(uint32_t two, float s) {
+  const float2 a = value_pair<FMT>(two);
+  const __nv_bfloat162 r = __floats2bfloat162_rn(a.x * s, a.y * s);  // exact: 7 significant bits
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads) k_cache_read(CacheView c, uint4* __restrict__ k, uint4* __restrict__ v) {
+  constexpr int P = Place<D>::kPasses;
+  Touched t;
+  const bool any = touched_block(c, blockIdx.x, t);
+  const int head = blockIdx.y;
+  for (long long i = threadIdx.x; i < t.before * (D / 8); i += kThreads) {  // negative positions: zeros
+    const size_t at = (static_cast<size_t>(t.row0 + i / (D / 8)) * c.hkv + head) * (D / 8) + i % (D / 8);
+    k[at] = v[at] = make_uint4(0, 0, 0, 0);
+  }
+  if (!any) return;
+  const int page = page_of(c, t.seq, t.block);
+  const Place<D> pl;
+  uint32_t code[2][P][2] = {};
+  float2 scale = make_float2(0.f, 0.f);
+  if (page >= 0) {
+    const size_t ph = static_cast<size_t>(page) * c.hkv + head;
+    const uint8_t* kb = c.k + ph * (kBlock * D);
+    const uint8_t* vb = c.v + ph * (kBlock * D);
+    uint32_t chunk[D / 32][4];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 y = __ldg(reinterpret_cast<const uint4*>(vb + v_channel<D>(pl, i) * kBlock + pl.c * 16));
+      chunk[i][0] = y.x;
+      chunk[i][1] = y.y;
+      chunk[i][2] = y.z;
+      chunk[i][3] = y.w;
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int r = pl.token(p) - t.first;
+      if (r >= 0 && r < t.count) {
+        const uint2 y = __ldg(reinterpret_cast<const uint2*>(kb + pl.token(p) * D + pl.ch));
+        code[0][p][0] = y.x;
+        code[0][p][1] = y.y;
+      }
+    }
+    scale = __ldg(reinterpret_cast<const float2*>(c.scales + 2 * ph));
+    from_chunks<D>(pl, chunk, code[1]);
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const float s = w ? scale.y : scale.x;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int r = pl.token(p) - t.first;
+      if (r < 0 || r >= t.count) continue;
+      const size_t at = ((static_cast<size_t>(t.row) + r) * c.hkv + head) * (D / 8) + pl.ch / 8;
+      const uint32_t* y = code[w][p];
+      (w ? v : k)[at] = make_uint4(bf16_pair<FMT>(y[0], s), bf16_pair<FMT>(y[0] >> 16, s), bf16_pair<FMT>(y[1], s),
+                                   bf16_pair<FMT>(y[1] >> 16, s));
+    }
+  }
+}
+
+hdp_status_t check_rows(const char* call, const void* k, const void* v, int64_t rows) {
+  if (rows > 0 && (!k || !v)) return fail(HDP_ERR_INVALID_ARGUMENT, std::string(call) + ": k or v is NULL");
+  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15)
+    return fail(HDP_ERR_INVALID_ARGUMENT, std::string(call) + ": k and v must be 16-byte aligned");
+  return HDP_OK;
+}
+
+// CTAs in x: a slot for every block that the call may touch (below 2^25 + 2^25).
+dim3 slot_grid(const CacheView& c) {
+  const long long slots = c.cu ? c.rows / kBlock + 2LL * c.num_seqs : c.num_seqs;
+  return dim3(static_cast<unsigned>(slots), c.hkv);
+}
+
+}  // namespace
+}  // namespace hdp
+
+using namespace hdp;
+
+#define HDP_TRY(expr)                    \
+  do {                                   \
+    const hdp_status_t s_ = (expr);      \
+    if (s_ != HDP_OK) return s_;         \
+  } while (0)
+
+extern "C" hdp_status_t hdp_cache_append(const hdp_cache_t* cache, const int32_t* cu, int64_t rows, const void* k,
+                                         const void* v, void* stream) {
+  CacheView c;
+  HDP_TRY(cache_view("hdp_cache_append", cache, cu, rows, &c));
+  HDP_TRY(check_rows("hdp_cache_append", k, v, rows));
+  if (rows == 0) return HDP_OK;
+  c.err = device_error_word();
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const dim3 g = slot_grid(c);
+  const uint4* kp = static_cast<const uint4*>(k);
+  const uint4* vp = static_cast<const uint4*>(v);
+  const bool i8 = cache->format == HDP_CACHE_INT8;
+  if (cache->d == 128) {
+    if (i8) k_cache_append<128, HDP_CACHE_INT8><<<g, kThreads, 0, st>>>(c, kp, vp);
+    else k_cache_append<128, HDP_CACHE_E4M3><<<g, kThreads, 0, st>>>(c, kp, vp);
+  } else {
+    if (i8) k_cache_append<64, HDP_CACHE_INT8><<<g, kThreads, 0, st>>>(c, kp, vp);
+    else k_cache_append<64, HDP_CACHE_E4M3><<<g, kThreads, 0, st>>>(c, kp, vp);
+  }
+  note_launch();
+  HDP_CUDA_TRY(cudaGetLastError());
+  return HDP_OK;
+}
+
+extern "C" hdp_status_t hdp_cache_read(const hdp_cache_t* cache, const int32_t* cu, int64_t rows, void* k, void* v,
+                                       void* stream) {
+  CacheView c;
+  HDP_TRY(cache_view("hdp_cache_read", cache, cu, rows, &c));
+  HDP_TRY(check_rows("hdp_cache_read", k, v, rows));
+  if (rows == 0) return HDP_OK;
+  c.err = device_error_word();
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const dim3 g = slot_grid(c);
+  uint4* kp = static_cast<uint4*>(k);
+  uint4* vp = static_cast<uint4*>(v);
+  const bool i8 = cache->format == HDP_CACHE_INT8;
+  if (cache->d == 128) {
+    if (i8) k_cache_read<128, HDP_CACHE_INT8><<<g, kThreads, 0, st>>>(c, kp, vp);
+    else k_cache_read<128, HDP_CACHE_E4M3><<<g, kThreads, 0, st>>>(c, kp, vp);
+  } else {
+    if (i8) k_cache_read<64, HDP_CACHE_INT8><<<g, kThreads, 0, st>>>(c, kp, vp);
+    else k_cache_read<64, HDP_CACHE_E4M3><<<g, kThreads, 0, st>>>(c, kp, vp);
+  }
+  note_launch();
+  HDP_CUDA_TRY(cudaGetLastError());
+  return HDP_OK;
+}

@@ -1,0 +1,348 @@
+// Choosing blocks of the 8-bit cache for each query by an upper bound of the
+// scores of their keys.
+//
+// The bound of a block is sum_ch max(q_ch, 0) hi_ch + min(q_ch, 0) lo_ch with
+// the channel-wise extremes lo, hi of its keys.  Everything in it is a whole
+// number (8-bit extremes, query rows rounded to 8 bits, added up over the heads
+// of the group to 16), so a block costs 2 d bytes and d two-way integer dot
+// products whatever the group's size is, and the choice does not depend on the
+// order of summation.  HBM bounds the scores (1/64 of the cache's bytes).
+//
+//   k_cache_scores: 256 blocks of one (row, kv head) a CTA; a lane has 16
+//   channels of one extreme, so 16 (d = 128) or 8 lanes have a block.
+//   k_cache_top: one CTA for each (row, kv head).  The keys stay in registers;
+//   a binary search over the key's value counts the keys above it (no atomics,
+//   so many equal keys cost nothing), and ballots give each chosen block its
+//   place in ascending order.
+#include <string>
+
+#include "kv_cache.cuh"
+
+namespace hdp {
+namespace {
+
+constexpr int kScoreThreads = 256;
+constexpr int kScoreBlocks = 256;  // blocks of a CTA: 32 a warp
+constexpr int kTopThreads = 1024;
+constexpr uint32_t kForced = 0xffffffffu, kNanKey = 0xfffffffeu;
+
+struct SelectParams {
+  CacheView c;
+  const __nv_bfloat16* q;
+  uint32_t* keys;  // [rows][hkv][max_pages]
+  int32_t* out;
+  int hq, g, count, first, last;
+};
+
+// Sequence, position and visible blocks of a row; false for a row of no sequence.
+__device__ __forceinline__ bool row_place(const CacheView& c, int t, int& seq, int& have) {
+  seq = seq_of_row(c, t);
+  if (seq < 0) return false;
+  const long long p = first_position(c, seq, seq_len(c, seq)) + (c.cu ? t - __ldg(c.cu + seq) : 0);
+  have = p < 0 ? 0 : static_cast<int>(p / kBlock) + 1;
+  return true;
+}
+
+// Keys in the order of the scores.
+__device__ __forceinline__ uint32_t key_of(float score) {
+  const uint32_t b = __float_as_uint(score);
+  return b ^ (b & 0x80000000u ? 0xffffffffu : 0x80000000u);
+}
+
+__device__ __forceinline__ int dp2a_lo(int a, int b, int c) {
+  int r;
+  asm("dp2a.lo.s32.s32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ int dp2a_hi(int a, int b, int c) {
+  int r;
+  asm("dp2a.hi.s32.s32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kScoreThreads) k_cache_scores(const SelectParams p, int chunks) {
+  constexpr int kLanes = D / 8;  // of a block: D / 16 for each extreme
+  __shared__ __align__(16) int16_t s_q[2][D];  // sums of min(c, 0) and of max(c, 0)
+  __shared__ uint32_t s_top[kScoreThreads / 32];
+  const int unit = blockIdx.x / chunks, chunk = blockIdx.x - unit * chunks;
+  const int row = unit / p.c.hkv, head = unit - row * p.c.hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int seq, have;
+  if (!row_place(p.c, row, seq, have)) return;
+  if (have <= p.count || chunk * kScoreBlocks >= have) return;  // all are chosen, or none here
+
+  // pages first: their latency hides behind the query's
+  const int b = chunk * kScoreBlocks + warp * 32 + lane;
+  const int page = b < have ? page_of(p.c, seq, b) : -1;
+  const size_t ph = static_cast<size_t>(max(page, 0)) * p.c.hkv + head;
+  const float scale = page >= 0 ? __ldg(p.c.scales + 2 * ph) : 0.f;
+
+  const __nv_bfloat16* q = p.q + (static_cast<size_t>(row) * p.hq + head * p.g) * D;
+  uint32_t top = 0;
+  for (int i = threadIdx.x; i < p.g * D / 8; i += kScoreThreads) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(q) + i);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
+      top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+    }
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+  if (threadIdx.x < D) {
+#pragma unroll
+    for (int w = 0; w < kScoreThreads / 32; ++w) top = max(top, s_top[w]);
+    // the smallest 2^e, e >= -126, with the largest magnitude at most 127 * 2^e (127 = 1.984375 * 2^6)
+    const int e = max(static_cast<int>(top >> 7) - 127 - 6 + ((top & 0x7f) > 0x7e), -126);
+    const float down = pow2i(-e);
+    int neg = 0, pos = 0;
+    for (int h = 0; h < p.g; ++h) {
+      const float x = __bfloat162float(q[h * D + threadIdx.x]);
+      const int c = (__float_as_uint(x) & 0x7fffffffu) < 0x7f800000u ? __float2int_rn(x * down) : 0;
+      neg += min(c, 0);
+      pos += max(c, 0);
+    }
+    s_q[0][threadIdx.x] = static_cast<int16_t>(neg);
+    s_q[1][threadIdx.x] = static_cast<int16_t>(pos);
+  }
+  __syncthreads();
+
+  // this lane's 16 channels of one extreme
+  const int part = lane % kLanes;
+  int qr[8];
+  {
+    const int4* src = reinterpret_cast<const int4*>(&s_q[0][0] + part * 16);
+    const int4 a = src[0], c = src[1];
+    qr[0] = a.x;
+    qr[1] = a.y;
+    qr[2] = a.z;
+    qr[3] = a.w;
+    qr[4] = c.x;
+    qr[5] = c.y;
+    qr[6] = c.z;
+    qr[7] = c.w;
+  }
+  int mine = 0;
+  uint4 x[kLanes];
+#pragma unroll
+  for (int i = 0; i < kLanes; ++i) {  // block i of this group of lanes: lane (group, i) keeps its sum
+    const int pg = __shfl_sync(0xffffffffu, page, (lane & ~(kLanes - 1)) + i);
+    x[i] = pg >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.c.bounds + (static_cast<size_t>(pg) * p.c.hkv + head) * (2 * D)) + part)
+                   : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < kLanes; ++i) {
+    int u = dp2a_lo(qr[0], x[i].x, 0);
+    u = dp2a_hi(qr[1], x[i].x, u);
+    u = dp2a_lo(qr[2], x[i].y, u);
+    u = dp2a_hi(qr[3], x[i].y, u);
+    u = dp2a_lo(qr[4], x[i].z, u);
+    u = dp2a_hi(qr[5], x[i].z, u);
+    u = dp2a_lo(qr[6], x[i].w, u);
+    u = dp2a_hi(qr[7], x[i].w, u);
+#pragma unroll
+    for (int s = 1; s < kLanes; s *= 2) u += __shfl_xor_sync(0xffffffffu, u, s);
+    if (part == i) mine = u;
+  }
+  if (b < have) {
+    uint32_t key = scale == scale ? key_of(static_cast<float>(mine) * scale) : kNanKey;
+    if (page < 0) key = 0;
+    if (b < p.first || b >= have - p.last) key = kForced;
+    p.keys[(static_cast<size_t>(row) * p.c.hkv + head) * p.c.max_pages + b] = key;
+  }
+}
+
+// ITEMS keys of a thread in registers (ITEMS * 1024 blocks at most); 0: the
+// keys are read again for each step.
+template <int ITEMS>
+__global__ void __launch_bounds__(kTopThreads) k_cache_top(const SelectParams p) {
+  __shared__ int s_count[2][32];
+  __shared__ uint32_t s_low[32], s_high[32];
+  const int row = blockIdx.x / p.c.hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int seq, have;
+  if (!row_place(p.c, row, seq, have)) return;
+  int32_t* out = p.out + static_cast<size_t>(blockIdx.x) * p.count;
+  if (have <= p.count) {
+    for (int i = threadIdx.x; i < p.count; i += kTopThreads) out[i] = i < have ? i : -1;
+    return;
+  }
+  const uint32_t* keys = p.keys + static_cast<size_t>(blockIdx.x) * p.c.max_pages;
+  // a warp has a run of `items` * 32 keys
+  const int items = (have + kTopThreads - 1) / kTopThreads;
+  const int base = warp * items * 32 + lane;
+  uint32_t key[ITEMS ? ITEMS : 1];
+  if constexpr (ITEMS > 0) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) key[i] = i < items && base + i * 32 < have ? __ldcg(keys + base + i * 32) : 0u;
+  }
+  // key i of this thread; `in` tells whether there is one
+  auto at = [&](int i) { return __ldcg(keys + base + i * 32); };
+
+  uint32_t low = 0xffffffffu, high = 0;
+  if constexpr (ITEMS > 0) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      if (i < items && base + i * 32 < have) {
+        low = min(low, key[i]);
+        high = max(high, key[i]);
+      }
+    }
+  } else {
+    for (int i = 0; i < items && base + i * 32 < have; ++i) {
+      low = min(low, at(i));
+      high = max(high, at(i));
+    }
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  if (lane == 0) {
+    s_low[warp] = low;
+    s_high[warp] = high;
+  }
+  __syncthreads();
+  low = __reduce_min_sync(0xffffffffu, s_low[lane]);
+  high = __reduce_max_sync(0xffffffffu, s_high[lane]);
+
+  // the largest x with at least `count` keys >= x: between low (all of them) and high
+  int turn = 0;
+  while (low < high) {
+    const uint32_t mid = low + ((high - low) >> 1) + ((high - low) & 1);
+    int n = 0;
+    if constexpr (ITEMS > 0) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) n += key[i] >= mid;  // mid > low >= 0: padding (0) never counts
+    } else {
+      for (int i = 0; i < items && base + i * 32 < have; ++i) n += at(i) >= mid;
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) s_count[turn][warp] = n;
+    __syncthreads();
+    n = __reduce_add_sync(0xffffffffu, s_count[turn][lane]);
+    turn ^= 1;
+    if (n >= p.count) low = mid;
+    else high = mid - 1;
+  }
+
+  // keys above it are chosen, and of those equal to it the first ones
+  int above = 0, equal = 0;
+  auto count_at = [&](int i, uint32_t k) {
+    const bool in = i < items && base + i * 32 < have;
+    above += __popc(__ballot_sync(0xffffffffu, in && k > low));
+    equal += __popc(__ballot_sync(0xffffffffu, in && k == low));
+  };
+  if constexpr (ITEMS > 0) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) count_at(i, key[i]);
+  } else {
+    for (int i = 0; i < items; ++i) count_at(i, base + i * 32 < have ? at(i) : 0u);
+  }
+  __syncthreads();  // the search's last counts have been read
+  if (lane == 0) {
+    s_count[0][warp] = above;
+    s_count[1][warp] = equal;
+  }
+  __syncthreads();
+  const int a = s_count[0][lane], e = s_count[1][lane];
+  const int total_above = __reduce_add_sync(0xffffffffu, a);
+  int before_above = __reduce_add_sync(0xffffffffu, lane < warp ? a : 0);
+  int before_equal = __reduce_add_sync(0xffffffffu, lane < warp ? e : 0);
+  const int take = p.count - total_above;  // of the equal ones
+  const unsigned under = (1u << lane) - 1;
+  auto place = [&](int i, uint32_t k) {
+    const bool in = i < items && base + i * 32 < have;
+    const unsigned ma = __ballot_sync(0xffffffffu, in && k > low), me = __ballot_sync(0xffffffffu, in && k == low);
+    const int ra = before_above + __popc(ma & under), re = before_equal + __popc(me & under);
+    if (in && (k > low || (k == low && re < take))) out[ra + min(re, take)] = base + i * 32;
+    before_above += __popc(ma);
+    before_equal += __popc(me);
+  };
+  if constexpr (ITEMS > 0) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) place(i, key[i]);
+  } else {
+    for (int i = 0; i < items; ++i) place(i, base + i * 32 < have ? at(i) : 0u);
+  }
+}
+
+hdp_status_t select_bytes(const CacheView& c, size_t* bytes) {
+  *bytes = (static_cast<size_t>(c.rows) * c.hkv * c.max_pages * sizeof(uint32_t) + 255) & ~size_t(255);
+  return HDP_OK;
+}
+
+}  // namespace
+}  // namespace hdp
+
+using namespace hdp;
+
+extern "C" hdp_status_t hdp_cache_select_workspace_bytes(const hdp_cache_t* cache, int64_t rows, size_t* bytes) {
+  if (!cache || !bytes) return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_select_workspace_bytes: NULL argument");
+  if (cache->hkv < 1 || cache->max_pages < 1 || rows < 0 || rows > 2147483647LL)
+    return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_select_workspace_bytes: need hkv >= 1, max_pages >= 1, 0 <= rows < 2^31");
+  CacheView c = {};
+  c.rows = static_cast<int>(rows);
+  c.hkv = cache->hkv;
+  c.max_pages = cache->max_pages;
+  return select_bytes(c, bytes);
+}
+
+extern "C" hdp_status_t hdp_cache_select(const hdp_cache_t* cache, const int32_t* cu, int64_t rows, const void* q,
+                                         int32_t hq, int32_t count, int32_t keep_first, int32_t keep_last,
+                                         void* workspace, size_t workspace_bytes, int32_t* blocks, void* stream) {
+  SelectParams p = {};
+  const hdp_status_t r = cache_view("hdp_cache_select", cache, cu, rows, &p.c);
+  if (r != HDP_OK) return r;
+  if (hq < 1 || hq % cache->hkv != 0)
+    return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_select: need hq >= 1 and hq % hkv == 0");
+  if (hq / cache->hkv > 128) return fail(HDP_ERR_UNSUPPORTED, "hdp_cache_select: hq / hkv must be at most 128");
+  if (count < 1 || keep_first < 0 || keep_last < 0 || static_cast<int64_t>(keep_first) + keep_last > count)
+    return fail(HDP_ERR_INVALID_ARGUMENT,
+                "hdp_cache_select: need count >= 1, keep_first >= 0, keep_last >= 0, keep_first + keep_last <= count");
+  if (rows == 0) return HDP_OK;
+  if (!q || !blocks) return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_select: NULL argument");
+  if (reinterpret_cast<uintptr_t>(q) & 15)
+    return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_select: q must be 16-byte aligned");
+  const int chunks = (cache->max_pages + kScoreBlocks - 1) / kScoreBlocks;
+  if (rows * cache->hkv > 2147483647LL / chunks)
+    return fail(HDP_ERR_UNSUPPORTED, "hdp_cache_select: rows * hkv * max_pages / 256 must be below 2^31");
+  size_t need = 0;
+  select_bytes(p.c, &need);
+  if (!workspace || workspace_bytes < need)
+    return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_select: workspace too small (need " + std::to_string(need) + " bytes)");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255)
+    return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_select: workspace must be 256-byte aligned");
+  p.c.err = device_error_word();
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.keys = static_cast<uint32_t*>(workspace);
+  p.out = blocks;
+  p.hq = hq;
+  p.g = hq / cache->hkv;
+  p.count = count;
+  p.first = keep_first;
+  p.last = keep_last;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const unsigned units = static_cast<unsigned>(rows * cache->hkv);
+  if (cache->d == 128) k_cache_scores<128><<<units * chunks, kScoreThreads, 0, st>>>(p, chunks);
+  else k_cache_scores<64><<<units * chunks, kScoreThreads, 0, st>>>(p, chunks);
+  note_launch();
+  HDP_CUDA_TRY(cudaGetLastError());
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(units);
+  cfg.blockDim = dim3(kTopThreads);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cache->max_pages <= 4 * kTopThreads) HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_cache_top<4>, p));
+  else if (cache->max_pages <= 32 * kTopThreads) HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_cache_top<32>, p));
+  else HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_cache_top<0>, p));
+  note_launch();
+  return HDP_OK;
+}
