@@ -108,17 +108,18 @@ def attention_backward(plan: Plan, q, k, v, o, lse, dout, scale: float | None = 
 _cache_ws_bytes: dict = {}
 
 
-def _new(stream, *wanted):
-    """torch.empty of each (shape, dtype, device), from the pool of the stream that the call runs on: what is freed
-    after the call is only given out again in that stream's order."""
+def _pool(stream, cache):
+    """The stream whose memory pool a call's tensors come from: what is freed after the call is only given out again in
+    that stream's order."""
+    import contextlib
+
     import torch
 
     if stream is None:
-        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype, device in wanted]
+        return contextlib.nullcontext()
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=wanted[0][2])
-    with torch.cuda.stream(stream):
-        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype, device in wanted]
+        stream = torch.cuda.ExternalStream(stream, device=cache.device)
+    return torch.cuda.stream(stream)
 
 
 def cache_append(cache: KVCache, page_table, lens, k, v, cu=None, stream=None):
@@ -128,11 +129,16 @@ def cache_append(cache: KVCache, page_table, lens, k, v, cu=None, stream=None):
 
 
 def cache_read(cache: KVCache, page_table, lens, rows: int, cu=None, stream=None):
-    """The newest tokens of each sequence as (k, v) [rows][hkv][d] bf16, exactly code * scale."""
+    """The newest tokens of each sequence as (k, v) [rows][hkv][d] bf16, exactly code * scale.  Outputs that a cache
+    call on another stream than the current one returns belong to that stream."""
     import torch
 
-    what = ((rows, cache.hkv, cache.d), torch.bfloat16, cache.device)
-    k, v = _new(stream, what, what)
+    if stream is not None:
+        with _pool(stream, cache):
+            k, v = (torch.empty((rows, cache.hkv, cache.d), dtype=torch.bfloat16, device=cache.device) for _ in "kv")
+    else:
+        k = torch.empty((rows, cache.hkv, cache.d), dtype=torch.bfloat16, device=cache.device)
+        v = torch.empty_like(k)
     hdp_cache_read(cache, page_table, lens, k, v, cu=cu, stream=stream)
     return k, v
 
@@ -143,10 +149,15 @@ def cache_select(cache: KVCache, page_table, lens, q, count: int, cu=None, keep_
     bf16 and kv head: int32 [rows][hkv][count], ascending, -1 behind the last."""
     import torch
 
-    rows = q.shape[0]
-    nbytes = (rows * cache.hkv * page_table.shape[1] * 4 + 255) // 256 * 256  # hdp_cache_select_workspace_bytes
-    blocks, ws = _new(stream, ((rows, cache.hkv, count), torch.int32, cache.device),
-                      ((nbytes,), torch.uint8, cache.device))
+    rows, hkv = q.shape[0], cache.hkv
+    nbytes = (rows * hkv * page_table.shape[1] * 4 + 255) // 256 * 256  # hdp_cache_select_workspace_bytes
+    if stream is not None:
+        with _pool(stream, cache):
+            blocks = torch.empty((rows, hkv, count), dtype=torch.int32, device=cache.device)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+    else:
+        blocks = torch.empty((rows, hkv, count), dtype=torch.int32, device=cache.device)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
     hdp_cache_select(cache, page_table, lens, q, keep_first, keep_last, ws, blocks, cu=cu, stream=stream)
     return blocks
 
@@ -154,18 +165,24 @@ def cache_select(cache: KVCache, page_table, lens, q, count: int, cu=None, keep_
 def cache_attention(cache: KVCache, page_table, lens, q, cu=None, blocks=None, scale: float | None = None,
                     stream=None):
     """Attention of q [rows][hq][d] bf16, the newest tokens of each sequence, over the cache, or over the chosen
-    blocks only; returns (o bf16 [rows][hq][d], lse fp32 [hq][rows]).  Outputs that a call on another stream than the
-    current one returns belong to that stream."""
+    blocks only; returns (o bf16 [rows][hq][d], lse fp32 [hq][rows])."""
     import torch
 
     rows, hq, d = q.shape
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    key = (cache.device, cache.d)
-    if key not in _cache_ws_bytes:
-        _cache_ws_bytes[key] = hdp_cache_attention_workspace_bytes(cache, hq)
-    o, lse, ws = _new(stream, ((rows, hq, d), torch.bfloat16, cache.device),
-                      ((hq, rows), torch.float32, cache.device),
-                      ((_cache_ws_bytes[key],), torch.uint8, cache.device))
+    device = cache.device
+    nbytes = _cache_ws_bytes.get((device, d))
+    if nbytes is None:
+        nbytes = _cache_ws_bytes[device, d] = hdp_cache_attention_workspace_bytes(cache, hq)
+    if stream is not None:
+        with _pool(stream, cache):
+            o = torch.empty_like(q)
+            lse = torch.empty((hq, rows), dtype=torch.float32, device=device)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        o = torch.empty_like(q)
+        lse = torch.empty((hq, rows), dtype=torch.float32, device=device)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     hdp_cache_attention(cache, page_table, lens, q, scale, ws, o, lse, cu=cu, blocks=blocks, stream=stream)
     return o, lse

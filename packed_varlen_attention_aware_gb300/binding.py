@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -327,6 +328,28 @@ def hdp_last_error_message() -> str:
 
 # ---------------------------------------------------------------- 8-bit key/value cache
 
+# A decoding step makes these calls once for each layer, and with a small batch the host's time is the step's time, so
+# their wrappers are kept short: one attribute of a tensor at a time, addresses as plain integers, the struct packed
+# into bytes.
+_CACHE_FORMAT = struct.Struct("PPPPiiiiPPii")
+assert _CACHE_FORMAT.size == ctypes.sizeof(CacheStruct)
+_cache_calls = None
+
+
+def _cache_lib():
+    """The cache entry points with hdp_cache_t passed as packed bytes."""
+    global _cache_calls
+    if _cache_calls is None:
+        lib, calls = load(), {}
+        for name in ("hdp_cache_append", "hdp_cache_read", "hdp_cache_attention", "hdp_cache_select"):
+            f = lib[name]  # a handle of its own: the attribute keeps its typed struct argument
+            f.argtypes = [ctypes.c_void_p] + getattr(lib, name).argtypes[1:]
+            f.restype = ctypes.c_int
+            calls[name] = f
+        _cache_calls = calls
+    return _cache_calls
+
+
 class KVCache:
     """A pool of pages of 64 tokens with 8-bit K and V codes (hdp_cache_t without the sequences).
 
@@ -339,17 +362,20 @@ class KVCache:
 
         if k.dim() != 4:
             raise ValueError("k must be [pages][hkv][64][d]")
-        pages, hkv, block, d = k.shape
-        _tensor(k, "k", torch.uint8, (pages, hkv, HDP_CACHE_BLOCK, d), k.device)
-        _tensor(v, "v", torch.uint8, (pages, hkv, d, HDP_CACHE_BLOCK), k.device)
-        _tensor(scales, "scales", torch.float32, (pages, hkv, 2), k.device)
-        _tensor(bounds, "bounds", torch.int8, (pages, hkv, 2, d), k.device)
+        pages, hkv, _, d = k.shape
+        dev = k.get_device()
+        _tensor(k, "k", torch.uint8, (pages, hkv, HDP_CACHE_BLOCK, d), dev)
+        _tensor(v, "v", torch.uint8, (pages, hkv, d, HDP_CACHE_BLOCK), dev)
+        _tensor(scales, "scales", torch.float32, (pages, hkv, 2), dev)
+        _tensor(bounds, "bounds", torch.int8, (pages, hkv, 2, d), dev)
         if format not in (HDP_CACHE_E4M3, HDP_CACHE_INT8):
             raise ValueError("format must be HDP_CACHE_E4M3 or HDP_CACHE_INT8")
         self.k, self.v, self.scales, self.bounds, self.format = k, v, scales, bounds, int(format)
-        self.num_pages, self.hkv, self.d, self.device = pages, hkv, d, k.device
-        self._struct = CacheStruct(k.data_ptr(), v.data_ptr(), scales.data_ptr(), bounds.data_ptr(), pages, hkv, d,
-                                   self.format, None, None, 0, 0)
+        self.num_pages, self.hkv, self.d, self._dev = pages, hkv, d, dev
+
+    @property
+    def device(self):
+        return self.k.device
 
     @classmethod
     def empty(cls, num_pages: int, hkv: int, d: int, format: int, device="cuda"):
@@ -363,46 +389,48 @@ class KVCache:
                    torch.empty((num_pages, hkv, 2, d), dtype=torch.int8, device=dev), format)
 
     def _with(self, page_table, lens, cu, rows):
-        """hdp_cache_t of a call over these sequences."""
+        """hdp_cache_t of a call over these sequences, as bytes."""
         import torch
 
         n = lens.shape[0] if lens.dim() == 1 else -1
-        _tensor(lens, "lens", torch.int32, (n,), self.device)
-        if page_table.dim() != 2:
-            raise ValueError("page_table must be [sequences][columns]")
-        _tensor(page_table, "page_table", torch.int32, (n, page_table.shape[1]), self.device)
+        columns = page_table.shape[1] if page_table.dim() == 2 else -1
+        _tensor(lens, "lens", torch.int32, (n,), self._dev)
+        _tensor(page_table, "page_table", torch.int32, (n, columns), self._dev)
         if cu is not None:
-            _tensor(cu, "cu", torch.int32, (n + 1,), self.device)
+            _tensor(cu, "cu", torch.int32, (n + 1,), self._dev)
         elif rows != n:
             raise ValueError(f"without cu there is one row for each of the {n} sequences, not {rows}")
-        s = CacheStruct.from_buffer_copy(self._struct)
-        s.page_table, s.lens, s.num_seqs, s.max_pages = page_table.data_ptr(), lens.data_ptr(), n, page_table.shape[1]
-        return s
+        return _CACHE_FORMAT.pack(self.k.data_ptr(), self.v.data_ptr(), self.scales.data_ptr(), self.bounds.data_ptr(),
+                                  self.num_pages, self.hkv, self.d, self.format, page_table.data_ptr(),
+                                  lens.data_ptr(), n, columns)
+
+    def _call(self, name, stream, *args):
+        """Runs an entry point with the cache's device current, on `stream` or that device's current one."""
+        import torch
+
+        f = (_cache_calls or _cache_lib())[name]
+        if torch._C._cuda_getDevice() != self._dev:
+            with torch.cuda.device(self._dev):
+                status = f(*args, self._raw(stream))
+        else:
+            status = f(*args, self._raw(stream))
+        if status:
+            _check(status, name)
+
+    def _raw(self, stream):
+        if stream is None:
+            import torch
+
+            return torch._C._cuda_getCurrentRawStream(self._dev)
+        return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _tensor(t, name, dtype, shape, device):
-    """Raises unless t is a contiguous tensor of this type, shape and CUDA device."""
-    if t.dtype != dtype or t.device != device or not t.is_cuda or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous {dtype} tensor on {device} (a CUDA device)")
+    """Raises unless t is a contiguous tensor of this type and shape on the CUDA device of this index."""
+    if t.dtype is not dtype or device < 0 or t.get_device() != device or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor on CUDA device {max(device, 0)}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-
-
-class _OnDevice:
-    """Makes `device` current for a call, if it is not."""
-
-    def __init__(self, device):
-        import torch
-
-        self._guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
 
 
 def hdp_cache_append(cache: KVCache, page_table, lens, k, v, cu=None, stream=None):
@@ -410,11 +438,10 @@ def hdp_cache_append(cache: KVCache, page_table, lens, k, v, cu=None, stream=Non
     import torch
 
     rows = k.shape[0]
-    _tensor(k, "k", torch.bfloat16, (rows, cache.hkv, cache.d), cache.device)
-    _tensor(v, "v", torch.bfloat16, (rows, cache.hkv, cache.d), cache.device)
-    s = cache._with(page_table, lens, cu, rows)
-    with _OnDevice(cache.device):
-        _check(load().hdp_cache_append(s, _ptr(cu), rows, _ptr(k), _ptr(v), _stream(stream)), "hdp_cache_append")
+    _tensor(k, "k", torch.bfloat16, (rows, cache.hkv, cache.d), cache._dev)
+    _tensor(v, "v", torch.bfloat16, (rows, cache.hkv, cache.d), cache._dev)
+    cache._call("hdp_cache_append", stream, cache._with(page_table, lens, cu, rows),
+                None if cu is None else cu.data_ptr(), rows, k.data_ptr(), v.data_ptr())
 
 
 def hdp_cache_read(cache: KVCache, page_table, lens, k, v, cu=None, stream=None):
@@ -422,17 +449,19 @@ def hdp_cache_read(cache: KVCache, page_table, lens, k, v, cu=None, stream=None)
     import torch
 
     rows = k.shape[0]
-    _tensor(k, "k", torch.bfloat16, (rows, cache.hkv, cache.d), cache.device)
-    _tensor(v, "v", torch.bfloat16, (rows, cache.hkv, cache.d), cache.device)
-    s = cache._with(page_table, lens, cu, rows)
-    with _OnDevice(cache.device):
-        _check(load().hdp_cache_read(s, _ptr(cu), rows, _ptr(k), _ptr(v), _stream(stream)), "hdp_cache_read")
+    _tensor(k, "k", torch.bfloat16, (rows, cache.hkv, cache.d), cache._dev)
+    _tensor(v, "v", torch.bfloat16, (rows, cache.hkv, cache.d), cache._dev)
+    cache._call("hdp_cache_read", stream, cache._with(page_table, lens, cu, rows),
+                None if cu is None else cu.data_ptr(), rows, k.data_ptr(), v.data_ptr())
 
 
 def hdp_cache_attention_workspace_bytes(cache: KVCache, hq: int) -> int:
+    import torch
+
     n = ctypes.c_size_t()
-    with _OnDevice(cache.device):
-        _check(load().hdp_cache_attention_workspace_bytes(cache._struct, hq, ctypes.byref(n)),
+    s = CacheStruct(hkv=cache.hkv, d=cache.d)
+    with torch.cuda.device(cache._dev):
+        _check(load().hdp_cache_attention_workspace_bytes(s, hq, ctypes.byref(n)),
                "hdp_cache_attention_workspace_bytes")
     return n.value
 
@@ -444,24 +473,24 @@ def hdp_cache_attention(cache: KVCache, page_table, lens, q, scale: float, works
     import torch
 
     rows, hq = q.shape[0], q.shape[1] if q.dim() == 3 else -1
-    _tensor(q, "q", torch.bfloat16, (rows, hq, cache.d), cache.device)
-    _tensor(o, "o", torch.bfloat16, (rows, hq, cache.d), cache.device)
-    _tensor(lse, "lse", torch.float32, (hq, rows), cache.device)
-    count = 0
+    shape = (rows, hq, cache.d)
+    _tensor(q, "q", torch.bfloat16, shape, cache._dev)
+    _tensor(o, "o", torch.bfloat16, shape, cache._dev)
+    _tensor(lse, "lse", torch.float32, (hq, rows), cache._dev)
+    _tensor(workspace, "workspace", torch.uint8, (workspace.numel(),), cache._dev)
+    count, list_ptr = 0, None
     if blocks is not None:
         count = blocks.shape[-1]
-        _tensor(blocks, "blocks", torch.int32, (rows, cache.hkv, count), cache.device)
-    s = cache._with(page_table, lens, cu, rows)
-    with _OnDevice(cache.device):
-        _check(load().hdp_cache_attention(s, _ptr(cu), rows, _ptr(q), hq, float(scale), _ptr(blocks), count,
-                                          _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(o),
-                                          _ptr(lse), _stream(stream)), "hdp_cache_attention")
+        _tensor(blocks, "blocks", torch.int32, (rows, cache.hkv, count), cache._dev)
+        list_ptr = blocks.data_ptr()
+    cache._call("hdp_cache_attention", stream, cache._with(page_table, lens, cu, rows),
+                None if cu is None else cu.data_ptr(), rows, q.data_ptr(), hq, scale, list_ptr, count,
+                workspace.data_ptr(), workspace.numel(), o.data_ptr(), lse.data_ptr())
 
 
 def hdp_cache_select_workspace_bytes(cache: KVCache, page_table, rows: int) -> int:
     n = ctypes.c_size_t()
-    s = CacheStruct.from_buffer_copy(cache._struct)
-    s.max_pages = page_table.shape[1]
+    s = CacheStruct(hkv=cache.hkv, d=cache.d, max_pages=page_table.shape[1])
     _check(load().hdp_cache_select_workspace_bytes(s, rows, ctypes.byref(n)), "hdp_cache_select_workspace_bytes")
     return n.value
 
@@ -472,14 +501,13 @@ def hdp_cache_select(cache: KVCache, page_table, lens, q, keep_first: int, keep_
     import torch
 
     rows, hq = q.shape[0], q.shape[1] if q.dim() == 3 else -1
-    _tensor(q, "q", torch.bfloat16, (rows, hq, cache.d), cache.device)
+    _tensor(q, "q", torch.bfloat16, (rows, hq, cache.d), cache._dev)
     count = blocks.shape[-1]
-    _tensor(blocks, "blocks", torch.int32, (rows, cache.hkv, count), cache.device)
-    s = cache._with(page_table, lens, cu, rows)
-    with _OnDevice(cache.device):
-        _check(load().hdp_cache_select(s, _ptr(cu), rows, _ptr(q), hq, count, keep_first, keep_last, _ptr(workspace),
-                                       workspace.numel() * workspace.element_size(), _ptr(blocks), _stream(stream)),
-               "hdp_cache_select")
+    _tensor(blocks, "blocks", torch.int32, (rows, cache.hkv, count), cache._dev)
+    _tensor(workspace, "workspace", torch.uint8, (workspace.numel(),), cache._dev)
+    cache._call("hdp_cache_select", stream, cache._with(page_table, lens, cu, rows),
+                None if cu is None else cu.data_ptr(), rows, q.data_ptr(), hq, count, keep_first, keep_last,
+                workspace.data_ptr(), workspace.numel(), blocks.data_ptr())
 
 
 # ---------------------------------------------------------------- cost models (host arithmetic)

@@ -10,6 +10,10 @@
 //   break: 16-byte asynchronous copies run two to three half blocks ahead, over
 //   the ends of sequences.  Each lane copies exactly the bytes that it later
 //   reads, so no barrier stands between the copies and the arithmetic.
+//   SMs do not get equal shares of the memory's rate (with equal runs the
+//   fastest CTAs were done at 0.78 of the slowest's time), so the last fifth of
+//   every run is cut into pieces of falling size that warps take as they come
+//   free.  The pieces are fixed; who computes one changes no result.
 //   Products.  S^T = K Q^T with the 64 keys as rows of m16n8k16 fragments and
 //   the query rows of the group as the 8 columns, so one decoded token of 8
 //   query heads fills the instruction and the keys fill the rest; O^T = V^T P^T
@@ -23,11 +27,11 @@
 //   Softmax.  The reference exponents are whole numbers: m of the row sum, M of
 //   the output, which also takes in the V scales' exponents; every rescaling is
 //   then by a power of two, and blocks with very different V scales lose nothing.
-//   Joining.  Warps leave a normalised (O, LSE) for a unit that they share with
-//   a neighbour; each CTA joins those of its own warps, and a second small
-//   kernel joins those of neighbouring CTAs, always in the order of the keys.
+//   Joining.  A piece leaves a normalised (O, LSE) for a unit that it shares with
+//   its neighbours; a second small kernel joins them in the order of the keys.
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <string>
 
 #include "kv_cache.cuh"
@@ -44,15 +48,14 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 struct Meta {
   float sk, sv;
-  int key0;  // first key of the block; -1: nothing of it is seen
-  int pad;
+  int key0;   // first key of the block; -1: nothing of it is seen
+  int piece;  // the piece that the block belongs to
 };
 
-// What a CTA leaves for its right neighbours: the unit that begins here and
-// ends in CTA `last`.
-struct Open {
-  int active, last, row0, head, nrows, pad;
-  long long rr0;
+// A unit that several pieces share, for the kernel that joins them.
+struct __align__(16) Open {
+  int parts, first, row0, head;  // parts: pieces first, first + 1, ...; 0: no unit
+  int nrows, rr0, pad[2];
 };
 
 struct AttnParams {
@@ -63,10 +66,11 @@ struct AttnParams {
   const int32_t* blocks;
   int count, hq, g;
   float scale_log2;
-  float* part;      // [ctas][2][rows of a tile][d]
-  float* part_lse;  // [ctas][2][rows of a tile]
-  float* warp_part; // [ctas][warps][rows of a tile][d], tiles of 16 rows only
-  Open* open;       // [ctas]
+  bool dynamic;     // the ends of the runs are handed out through the counter
+  float* part;      // [pieces][2][rows of a tile][d]: of a unit begun before the piece, and of one begun in it
+  float* part_lse;  // [pieces][2][rows of a tile]
+  Open* open;       // [pieces]: one for each piece, or, with a counter, as they come
+  int* head;        // [0] entries of open (dynamic), [1] next ticket, [2] entries of open (static)
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -130,59 +134,78 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t x) {
   return x & ~((full >> 7) * 0xffu);
 }
 
+constexpr int kSeqs = 512;  // sequences whose places are kept in shared memory
+
+// A sequence's rows in the call, its tokens, and the position of its first row.
+struct SeqPlace {
+  int row0, n, len, p0;
+};
+
+__device__ __forceinline__ SeqPlace seq_place(const CacheView& c, int i) {
+  SeqPlace s;
+  seq_rows(c, i, s.row0, s.n);
+  const long long len = seq_len(c, i);
+  s.len = static_cast<int>(len);
+  s.p0 = static_cast<int>(max(first_position(c, i, len), -2147483647LL));
+  return s;
+}
+
+struct Shared {
+  unsigned char ring[kWarps][kRingBytes];
+  SeqPlace seq[kSeqs];
+  Meta meta[kWarps][kMeta];
+  long long pre[kThreads];  // steps before each thread's sequences
+  long long warp_sum[kWarps];
+};
+
 // A place in the flat order.  A unit is (sequence or row, kv head, tile of
 // query rows); a step is one block of it.
 template <bool SPARSE, int NT>
 struct Cursor {
-  int seq, row0, n, head, tile, tiles, nb, blk;
-  long long len, p0;
+  int seq, head, tile, tiles, nb, blk;
+  SeqPlace s;
 
-  __device__ __forceinline__ static int tiles_of(long long n, int g) {
-    return static_cast<int>((n * g + 8 * NT - 1) / (8 * NT));
+  __device__ __forceinline__ static int tiles_of(int n, int g) { return static_cast<int>((n * g + 8u * NT - 1) / (8u * NT)); }
+  __device__ __forceinline__ static int blocks_of(const SeqPlace& s) { return max(1, static_cast<int>((s.len + (kBlock - 1u)) / kBlock)); }
+  __device__ __forceinline__ static SeqPlace place(const AttnParams& p, const Shared& sm, int i) {
+    return i < kSeqs ? sm.seq[i] : seq_place(p.c, i);
   }
-  // Blocks of all units of sequence i.
-  __device__ __forceinline__ static long long cost(const AttnParams& p, int i) {
-    int row0, n;
-    seq_rows(p.c, i, row0, n);
-    if (n == 0) return 0;
-    const long long nb = max(1LL, (seq_len(p.c, i) + kBlock - 1) / kBlock);
-    return nb * tiles_of(n, p.g) * p.c.hkv;
+  // Steps of all units of a sequence.
+  __device__ __forceinline__ static long long cost(const AttnParams& p, const SeqPlace& s) {
+    return s.n ? static_cast<long long>(blocks_of(s)) * tiles_of(s.n, p.g) * p.c.hkv : 0;
   }
-  __device__ __forceinline__ void enter(const AttnParams& p, int i) {
+  __device__ __forceinline__ void enter(const AttnParams& p, const Shared& sm, int i) {
     head = tile = blk = 0;
     if constexpr (SPARSE) {
-      row0 = i;
-      n = 1;
       nb = p.count;
       seq = seq_of_row(p.c, i);
+      s.len = s.p0 = 0;
       if (seq >= 0) {
-        len = seq_len(p.c, seq);
-        const int first = p.c.cu ? __ldg(p.c.cu + seq) : i;
-        p0 = first_position(p.c, seq, len) + (i - first);
-      } else {
-        len = p0 = 0;
+        s = seq_place(p.c, seq);
+        s.p0 += i - s.row0;
       }
+      s.row0 = i;
+      s.n = 1;
     } else {
       seq = i;
-      seq_rows(p.c, i, row0, n);
-      len = seq_len(p.c, i);
-      p0 = first_position(p.c, i, len);
-      nb = static_cast<int>(max(1LL, (len + kBlock - 1) / kBlock));
+      s = place(p, sm, i);
+      nb = blocks_of(s);
     }
-    tiles = tiles_of(n, p.g);
+    tiles = tiles_of(s.n, p.g);
   }
-  __device__ __forceinline__ void next_unit(const AttnParams& p) {
+  // The sequence after this one that has rows.
+  __device__ __forceinline__ int next_seq(const AttnParams& p, const Shared& sm) const {
+    int i = seq + 1;
+    while (i < p.c.num_seqs && place(p, sm, i).n == 0) ++i;
+    return i;
+  }
+  __device__ __forceinline__ void next_unit(const AttnParams& p, const Shared& sm) {
     blk = 0;
     if (++tile < tiles) return;
     tile = 0;
     if (++head < p.c.hkv) return;
-    int i = (SPARSE ? row0 : seq) + 1;
-    if constexpr (SPARSE) {
-      if (i < p.c.rows) enter(p, i);
-    } else {
-      while (i < p.c.num_seqs && cost(p, i) == 0) ++i;
-      if (i < p.c.num_seqs) enter(p, i);
-    }
+    const int i = SPARSE ? s.row0 + 1 : next_seq(p, sm);
+    if (i < (SPARSE ? p.c.rows : p.c.num_seqs)) enter(p, sm, i);
   }
   // Skips `off` steps from the sequence's first.
   __device__ __forceinline__ void skip(long long off) {
@@ -191,39 +214,22 @@ struct Cursor {
     head = static_cast<int>(unit / tiles);
     tile = static_cast<int>(unit - static_cast<long long>(head) * tiles);
   }
-  __device__ __forceinline__ long long rr0() const { return static_cast<long long>(tile) * (8 * NT); }
-  __device__ __forceinline__ int nrows(int g) const {
-    return static_cast<int>(min(static_cast<long long>(8 * NT), static_cast<long long>(n) * g - rr0()));
-  }
+  __device__ __forceinline__ bool last_unit(const AttnParams& p) const { return tile + 1 == tiles && head + 1 == p.c.hkv; }
+  __device__ __forceinline__ int rr0() const { return tile * (8 * NT); }
+  __device__ __forceinline__ int nrows(int g) const { return min(8 * NT, s.n * g - rr0()); }
   // Positions of the tile's first and last row.
-  __device__ __forceinline__ long long first_pos(int g) const { return p0 + rr0() / g; }
-  __device__ __forceinline__ long long last_pos(int g) const { return p0 + (rr0() + nrows(g) - 1) / g; }
-};
-
-struct Seg {
-  int valid, begins, ends, row0, head, nrows;
-  long long rr0, unit_end;  // unit_end: flat end of the unit
-};
-
-template <int D, int NT>
-struct Shared {
-  static constexpr int kRows = 8 * NT;
-  unsigned char ring[kWarps][kRingBytes];
-  union {
-    long long pre[kThreads + 1];  // steps before each thread's sequences; read before the first part is written
-    float part[NT == 1 ? kWarps : 1][NT == 1 ? kRows : 1][D];
-  };
-  float lse[kWarps][2][kRows];
-  Meta meta[kWarps][kMeta];
-  Seg seg[kWarps][2];
-  long long warp_sum[kWarps];
+  __device__ __forceinline__ int first_pos(int g) const { return s.p0 + static_cast<int>(static_cast<unsigned>(rr0()) / g); }
+  __device__ __forceinline__ int last_pos(int g) const {
+    return s.p0 + static_cast<int>((rr0() + nrows(g) - 1u) / g);
+  }
 };
 
 template <int D>
-__device__ __forceinline__ void write_o(const AttnParams& p, int row0, int head, long long rr, const float* x, float lse,
+__device__ __forceinline__ void write_o(const AttnParams& p, int row0, int head, unsigned rr, const float* x, float lse,
                                         int lane) {
-  const long long t = row0 + rr / p.g;
-  const int h = head * p.g + static_cast<int>(rr % p.g);
+  const unsigned token = rr / p.g;
+  const long long t = row0 + token;
+  const int h = head * p.g + static_cast<int>(rr - token * p.g);
   __nv_bfloat16* out = p.o + (t * p.hq + h) * D;
   if constexpr (D == 128) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
@@ -240,55 +246,107 @@ __device__ __forceinline__ void write_o(const AttnParams& p, int row0, int head,
 // x = sum 2^(lse_k - L) o_k, L = log2 sum 2^lse_k.  o_at(k) points at the row.
 template <int D, class L, class O>
 __device__ __forceinline__ float join_row(int m, int lane, float (&x)[D / 32], L lse_at, O o_at) {
-  float top = -__int_as_float(0x7f800000);
-  bool nan = false;
-  for (int k = lane; k < m; k += 32) {
-    const float l = lse_at(k);
-    nan |= l != l;
-    top = fmaxf(top, l);
-  }
+  constexpr int V = D / 32;
+  constexpr int kAhead = 16;  // partial rows in flight
+  const float low = -__int_as_float(0x7f800000);
+  float top = low, sum = 0.f;
 #pragma unroll
-  for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-  nan = __any_sync(0xffffffffu, nan);
+  for (int i = 0; i < V; ++i) x[i] = 0.f;
+  for (int base = 0; base < m; base += 32) {
+    const int here = min(32, m - base);
+    const float l = lane < here ? lse_at(base + lane) : low;
+    float t = l;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) x[i] = 0.f;
-  if (top == -__int_as_float(0x7f800000) && !nan) return top;  // no key in any of them: o = 0
-  float sum = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < m; ++k) {
-    const float l = lse_at(k);
-    const float w = exp2_approx(l - top);
-    sum += w;
-    const float* o = o_at(k) + lane * (D / 32);
-    if constexpr (D == 128) {
-      const float4 y = *reinterpret_cast<const float4*>(o);
-      x[0] = fmaf(w, y.x, x[0]);
-      x[1] = fmaf(w, y.y, x[1]);
-      x[2] = fmaf(w, y.z, x[2]);
-      x[3] = fmaf(w, y.w, x[3]);
-    } else {
-      const float2 y = *reinterpret_cast<const float2*>(o);
-      x[0] = fmaf(w, y.x, x[0]);
-      x[1] = fmaf(w, y.y, x[1]);
+    for (int s = 16; s; s >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
+    t = fmaxf(t, top);
+    const float ref = t == low ? 0.f : t;  // no key so far: every weight is 2^-inf = 0 (a NaN stays one)
+    const float w = exp2_approx(l - ref), old = exp2_approx(top - ref);
+    top = t;
+    sum *= old;
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] *= old;
+    for (int k = 0; k < here; k += kAhead) {
+      float y[kAhead][V];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {  // past the end: the last row again, with weight 0
+        const float* o = o_at(base + min(k + u, here - 1)) + lane * V;
+        if constexpr (V == 4) {
+          const float4 z = *reinterpret_cast<const float4*>(o);
+          y[u][0] = z.x;
+          y[u][1] = z.y;
+          y[u][2] = z.z;
+          y[u][3] = z.w;
+        } else {
+          const float2 z = *reinterpret_cast<const float2*>(o);
+          y[u][0] = z.x;
+          y[u][1] = z.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const float f = __shfl_sync(0xffffffffu, w, (k + u) & 31);
+        const float g = k + u < here ? f : 0.f;
+        sum += g;
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = k + u < here ? fmaf(g, y[u][i], x[i]) : x[i];
+      }
     }
   }
+  if (sum == 0.f) return low;  // no key in any of them: o = 0
   const float inv = 1.f / sum;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) x[i] *= inv;
+  for (int i = 0; i < V; ++i) x[i] *= inv;
   return top + log2f(sum);
 }
 
-// How the flat order of `total` steps is cut: `used` warps of each CTA take
-// `per` steps each.  While there are fewer steps than warps, the steps are
-// spread over the CTAs first.
+// How the flat order of `total` steps is cut.  `used` warps of each CTA have a
+// run of `per` steps each; while there are fewer steps than warps, the steps
+// are spread over the CTAs first.  A run is one piece, or, where pieces are
+// handed out, a first piece of four fifths and up to kMorePieces more of half
+// of the rest each, but not below kLeast steps (a piece costs its warp about a
+// step: its query rows, its partial).  Pieces are numbered in the flat order.
+constexpr int kMorePieces = 5;
+constexpr int kLeast = 4;
 struct Cut {
-  int used;
-  long long per;
-  __device__ __forceinline__ Cut(long long total, int ctas) {
+  long long total, per, tail;
+  int workers, pieces;  // warps with a run, pieces of a run
+  __device__ __forceinline__ Cut(long long steps, int ctas, bool dynamic) : total(steps) {
     const long long each = (total + ctas - 1) / ctas;
-    used = static_cast<int>(min(static_cast<long long>(kWarps), max(1LL, each)));
-    const long long workers = static_cast<long long>(ctas) * used;
+    const int used = static_cast<int>(min(static_cast<long long>(kWarps), max(1LL, each)));
+    workers = ctas * used;
     per = max(1LL, (total + workers - 1) / workers);
+    tail = dynamic && per >= 5 * kLeast ? per / 5 : 0;
+    pieces = 1;
+    for (long long left = tail; left > 0 && pieces <= kMorePieces; ++pieces) left -= size_of(left, pieces);
+  }
+  __device__ __forceinline__ int used(int ctas) const { return workers / ctas; }
+  // Size of piece k >= 1 of a run when `left` steps of the tail are left.
+  __device__ __forceinline__ static long long size_of(long long left, int k) {
+    return k == kMorePieces || left < 2 * kLeast ? left : (left + 1) / 2;
+  }
+  // Steps [start, stop) of piece k of run w.
+  __device__ __forceinline__ void range(int w, int k, long long& start, long long& stop) const {
+    long long a = 0, size = per - tail, left = tail;
+    for (int i = 1; i <= k; ++i) {
+      a += size;
+      size = size_of(left, i);
+      left -= size;
+    }
+    start = w * per + a;
+    stop = min(total, start + size);
+  }
+  // The piece that step x lies in.
+  __device__ __forceinline__ int piece_of(long long x) const {
+    const long long w = x / per;
+    long long off = x - w * per - (per - tail), left = tail;
+    int k = 0;
+    while (off >= 0 && k + 1 < pieces) {
+      ++k;
+      const long long size = size_of(left, k);
+      off -= size;
+      left -= size;
+    }
+    return static_cast<int>(w) * pieces + k;
   }
 };
 
@@ -301,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
   constexpr int kRows = 8 * NT;
   using Cur = Cursor<SPARSE, NT>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  Shared<D, NT>& sm = *reinterpret_cast<Shared<D, NT>*>(smem_raw);
+  Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gr = lane >> 2, tc = lane & 3;  // fragment row group and column pair
 
@@ -315,7 +373,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
     long long mine = 0;
     for (int i = 0; i < per_thread; ++i) {
       const int s = threadIdx.x * per_thread + i;
-      if (s < p.c.num_seqs) mine += Cur::cost(p, s);
+      if (s < p.c.num_seqs) {
+        const SeqPlace at = seq_place(p.c, s);
+        if (s < kSeqs) sm.seq[s] = at;
+        mine += Cur::cost(p, at);
+      }
     }
     long long run = mine;
 #pragma unroll
@@ -334,72 +396,115 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
     }
     sm.pre[threadIdx.x] = before + run - mine;
   }
-  if (lane < 2) sm.seg[warp][lane].valid = 0;
-  if (threadIdx.x == 0) p.open[blockIdx.x].active = 0;
   __syncthreads();
-  const Cut cut(total, gridDim.x);
-  const long long start = (static_cast<long long>(blockIdx.x) * cut.used + warp) * cut.per;
-  const long long stop = warp < cut.used ? min(total, start + cut.per) : 0;
+  const Cut cut(total, gridDim.x, p.dynamic);
+  const int used = cut.used(gridDim.x);
+  if (!p.dynamic && blockIdx.x == 0 && threadIdx.x == 0) p.head[2] = cut.workers;
+  if (warp >= used) return;
+  const int run = blockIdx.x * used + warp;
+  if (!p.dynamic && lane == 0) p.open[run].parts = 0;
 
-  Cur cc;  // of the arithmetic
-  if (start < stop) {
+  // Puts a cursor on a step of the flat order.
+  auto locate = [&](Cur& cur, long long x) {
     if constexpr (SPARSE) {
       const long long row_cost = static_cast<long long>(per_row) * p.count;
-      const int row = static_cast<int>(start / row_cost);
-      cc.enter(p, row);
-      cc.skip(start - row * row_cost);
+      const int row = static_cast<int>(x / row_cost);
+      const long long off = x - row * row_cost;
+      const int head = static_cast<int>(off / (static_cast<long long>(p.count) * (per_row / p.c.hkv)));
+      const int at = min(static_cast<int>(off % p.count) + lane, p.count - 1);  // of the list that comes next
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(p.blocks + (static_cast<long long>(row) * p.c.hkv + head) * p.count + at));
+      cur.enter(p, sm, row);
+      cur.skip(off);
     } else {
-      const int slice = find_last(kThreads, start, [&](int s) { return sm.pre[s]; });
+      const int slice = find_last(kThreads, x, [&](int s) { return sm.pre[s]; });
       long long at = sm.pre[slice];
       int i = slice * per_thread;
-      for (long long c = Cur::cost(p, i); start - at >= c && i + 1 < p.c.num_seqs; c = Cur::cost(p, i)) {
-        at += c;
-        ++i;
-      }
-      cc.enter(p, i);
-      cc.skip(start - at);
+      for (long long c; x - at >= (c = Cur::cost(p, Cur::place(p, sm, i))) && i + 1 < p.c.num_seqs; ++i) at += c;
+      cur.enter(p, sm, i);
+      cur.skip(x - at);
     }
-  }
-  __syncthreads();
+  };
 
-  if (start < stop) {
-    Cur lc = cc;  // of the copies, which run ahead
+  long long start, stop;
+  cut.range(run, 0, start, stop);
+  if (start < total) {
+    Cur cc, lc;  // of the arithmetic; of the copies, which run ahead
+    locate(lc, start);
+    cc = lc;
+    int piece = run * cut.pieces;  // of the copies
     long long to_load = stop - start;
+    int loaded = 0, done = 0;      // blocks
+    int ticket = 0;                // lane 0: the next piece to take
+    bool asked = false, more_pieces = p.dynamic;
+    auto ask = [&]() {
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
+      if (lane == 0) ticket = atomicAdd(p.head + 1, 1);
+      asked = true;
+    };
     int half = 0;                 // 0: K of lc's block next, 1: V
     int load_slot = 0, load_meta = 0;
     int ids = -1, ids_at = -1;    // 32 blocks' pages (dense) or blocks and pages (sparse) of lc's unit, one a lane
     int ids_page = -1;
+    int next_page = 0, next_of = -1;  // dense: a page of sequence next_of's first blocks, asked for early
     const unsigned char* cur_v = nullptr;  // V of the block whose K went last
     const uint32_t ring = smem_addr(sm.ring[warp]) + lane * 16;
 
     auto issue = [&]() {
+      while (to_load == 0 && more_pieces) {
+        if (!asked) ask();
+        asked = false;
+        const int j = __shfl_sync(0xffffffffu, ticket, 0);
+        const int k = 1 + j / cut.workers, w = j - (k - 1) * cut.workers;
+        more_pieces = k < cut.pieces;
+        if (!more_pieces) break;
+        long long a, z;
+        cut.range(w, k, a, z);
+        if (a >= z) continue;
+        locate(lc, a);
+        to_load = z - a;
+        piece = w * cut.pieces + k;
+        ids_at = -1;
+      }
       if (to_load > 0) {
         if (half == 0) {
-          const long long last = lc.last_pos(p.g);
-          if (ids_at != (lc.blk & ~31)) {  // a new unit, or the next 32 blocks
+          ++loaded;
+          if (ids_at != (lc.blk & ~31)) {  // a new list, or the next 32 blocks
+            const int last = lc.last_pos(p.g);
             ids_at = lc.blk & ~31;
             const int b = ids_at + lane;
             ids = ids_page = -1;
-            if (b < lc.nb) {
-              if constexpr (SPARSE) {
-                if (lc.seq >= 0) {
-                  const int32_t* list = p.blocks + (static_cast<long long>(lc.row0) * p.c.hkv + lc.head) * p.count;
-                  const int x = __ldg(list + b), before = b ? __ldg(list + b - 1) : -1;
-                  if (x > before && x >= 0 && static_cast<long long>(x) * kBlock <= last) {
-                    ids = x;
-                    ids_page = page_of(p.c, lc.seq, x);
-                  }
+            if constexpr (SPARSE) {
+              if (b < lc.nb && lc.seq >= 0) {
+                const int32_t* list = p.blocks + (static_cast<long long>(lc.s.row0) * p.c.hkv + lc.head) * p.count;
+                const int x = __ldg(list + b), before = b ? __ldg(list + b - 1) : -1;
+                if (x > before && x >= 0 && x <= last / kBlock && last >= 0) {
+                  ids = x;
+                  ids_page = page_of(p.c, lc.seq, x);
                 }
-              } else if (static_cast<long long>(b) * kBlock <= last) {
-                ids = b;
-                ids_page = page_of(p.c, lc.seq, b);
               }
+            } else {
+              const bool early = next_of == lc.seq && ids_at == 0;
+              if (b < lc.nb && b <= last / kBlock && last >= 0) {
+                ids = b;
+                ids_page = early ? next_page : __ldg(p.c.table + static_cast<long long>(lc.seq) * p.c.max_pages + b);
+                if (ids_page < 0 || ids_page >= p.c.num_pages) {
+                  report_table(p.c);
+                  ids_page = -1;
+                }
+              }
+              next_of = -1;
             }
+          }
+          if (!SPARSE && next_of < 0 && lc.last_unit(p)) {
+            next_of = lc.next_seq(p, sm);
+            if (next_of < p.c.num_seqs && lane < p.c.max_pages)
+              next_page = __ldg(p.c.table + static_cast<long long>(next_of) * p.c.max_pages + lane);
           }
           const int b = __shfl_sync(0xffffffffu, ids, lc.blk & 31);
           const int page = __shfl_sync(0xffffffffu, ids_page, lc.blk & 31);
           const bool seen = b >= 0 && page >= 0;
           Meta* meta = &sm.meta[warp][load_meta];
+          if (lane == 0) meta->piece = piece;
           if (seen) {
             const size_t ph = static_cast<size_t>(page) * p.c.hkv + lc.head;
             if (lane == 0) {
@@ -425,9 +530,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
           }
           load_meta = (load_meta + 1) % kMeta;
           --to_load;
-          if (++lc.blk == lc.nb) {
-            lc.next_unit(p);
-            ids_at = -1;
+          if (to_load == 1 && more_pieces) ask();  // not earlier: a slow warp must not sit on a piece
+          if (++lc.blk == lc.nb && to_load > 0) {
+            // heads of a sequence share its pages: a list of up to 32 serves them all (its
+            // visible blocks are those of the sequence's last rows)
+            const bool same = !SPARSE && lc.nb <= 32 && lc.tiles == 1 && !lc.last_unit(p);
+            lc.next_unit(p, sm);
+            if (!same) ids_at = -1;
           }
         }
         half ^= 1;
@@ -439,15 +548,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) issue();
 
-    int slot = 0, meta_at = 0, segs = 0;
+    int slot = 0, meta_at = 0, at_piece = piece;
     long long at = start;
-    while (at < stop) {
-      // ---- one unit, or the part of it that this warp has
+    uint4 qx[NT][kMt / 2];  // raw query rows of cc's unit, this lane's channels
+    auto fetch_q = [&]() {
+      const unsigned rr0 = cc.rr0();
+      const int nrows = cc.nrows(p.g);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int r = t * 8 + gr;
+#pragma unroll
+        for (int i = 0; i < kMt / 2; ++i) qx[t][i] = make_uint4(0, 0, 0, 0);
+        if (r < nrows) {
+          const unsigned token = (rr0 + r) / p.g;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              p.q + (static_cast<long long>(cc.s.row0 + token) * p.hq + cc.head * p.g + (rr0 + r - token * p.g)) * D + tc * 16);
+#pragma unroll
+          for (int i = 0; i < kMt / 2; ++i) qx[t][i] = __ldg(src + (i >> 1) * 8 + (i & 1));
+        }
+      }
+    };
+    fetch_q();
+    while (true) {
+      // ---- one unit, or the part of it that the piece has
       const bool begins = cc.blk == 0;
       const int steps = static_cast<int>(min(static_cast<long long>(cc.nb - cc.blk), stop - at));
       const bool ends = cc.blk + steps == cc.nb;
-      const int nrows = cc.nrows(p.g);
-      const long long rr0 = cc.rr0();
+      const int nrows = cc.nrows(p.g), rr0 = cc.rr0(), row0 = cc.s.row0, head = cc.head;
       const bool live = !SPARSE || cc.seq >= 0;
 
       uint32_t qf[NT][kMt][2];
@@ -455,22 +582,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
       int pos[NT][2];    // their positions
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const int r = t * 8 + gr;
-        uint4 x[kMt / 2];
-#pragma unroll
-        for (int i = 0; i < kMt / 2; ++i) x[i] = make_uint4(0, 0, 0, 0);
-        if (r < nrows) {
-          const long long rr = rr0 + r;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              p.q + ((cc.row0 + rr / p.g) * p.hq + cc.head * p.g + rr % p.g) * D + tc * 16);
-#pragma unroll
-          for (int i = 0; i < kMt / 2; ++i) x[i] = __ldg(src + (i >> 1) * 8 + (i & 1));
-        }
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < kMt / 2; ++i)
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                       __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(qx[t][i].x & 0x7fff7fffu, qx[t][i].y & 0x7fff7fffu),
+                                       __vmaxu2(qx[t][i].z & 0x7fff7fffu, qx[t][i].w & 0x7fff7fffu)));
         top = max(top & 0xffffu, top >> 16);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -479,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
         const float down = pow2i(-e);
 #pragma unroll
         for (int i = 0; i < kMt / 2; ++i) {
-          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          const uint32_t w[4] = {qx[t][i].x, qx[t][i].y, qx[t][i].z, qx[t][i].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const __half2 y = __floats2half2_rn(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
@@ -491,11 +607,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
         qs[t][1] = __shfl_sync(0xffffffffu, s, tc * 8 + 4);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int rc = min(t * 8 + 2 * tc + k, nrows - 1);
-          pos[t][k] = static_cast<int>(max(-1LL, cc.p0 + (rr0 + rc) / p.g));
+          const unsigned rc = rr0 + min(t * 8 + 2 * tc + k, nrows - 1);
+          pos[t][k] = max(-1, cc.s.p0 + static_cast<int>(rc / p.g));
         }
       }
-      const long long low_pos = cc.first_pos(p.g);
+      const int low_pos = cc.first_pos(p.g);
 
       float acc[NT][kMt][4], m[NT][2], M[NT][2], l[NT][2];
 #pragma unroll
@@ -627,16 +743,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
         issue();
       }
       at += steps;
+      done += steps;
+      const int rest = cc.nb - cc.blk - steps;  // steps of the unit behind the piece
+      const int this_piece = at_piece;
+      const long long this_at = at;
+
+      // ---- the next unit's query rows are asked for before this one is written
+      bool more = true;
+      if (at < stop) {
+        cc.next_unit(p, sm);
+      } else {
+        __syncwarp();
+        more = done != loaded;
+        if (more) {  // the piece that the copies went on to
+          at_piece = sm.meta[warp][meta_at].piece;
+          const int w = at_piece / cut.pieces;
+          cut.range(w, at_piece - w * cut.pieces, at, stop);
+          locate(cc, at);
+        }
+      }
+      if (more) fetch_q();
 
       // ---- the unit's part is done: normalise, then out, or into a partial
       const bool whole = begins && ends;
-      float* part = segs == 0 ? (NT == 1 ? &sm.part[warp][0][0]
-                                         : p.warp_part + (static_cast<size_t>(blockIdx.x) * kWarps + warp) * kRows * D)
-                              : reinterpret_cast<float*>(sm.ring[warp]);
-      if (!whole && segs > 0) {
-        copies_wait<0>();  // the ring becomes the partial's place: this is the warp's last unit
-        __syncwarp();
-      }
+      const size_t part_at = (static_cast<size_t>(this_piece) * 2 + (begins ? 1 : 0)) * kRows;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float inv[2], lse2[2];
@@ -649,6 +779,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
           lse2[k] = none ? -__int_as_float(0x7f800000) : m[t][k] + log2f(l[t][k]);
         }
         if (whole) {
+          const int r = t * 8 + gr;
+          const unsigned rr = rr0 + r, token = rr / p.g;
+          __nv_bfloat16* out =
+              p.o + (static_cast<long long>(row0 + token) * p.hq + head * p.g + (rr - token * p.g)) * D + tc * 2;
 #pragma unroll
           for (int i = 0; i < kMt; ++i) {
 #pragma unroll
@@ -656,170 +790,197 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
               // [8 channels][8 rows] to [8 rows][8 channels]: lane then has row gr, channels 2 tc and 2 tc + 1
               const __nv_bfloat162 y = __floats2bfloat162_rn(acc[t][i][2 * h] * inv[0], acc[t][i][2 * h + 1] * inv[1]);
               const uint32_t z = transpose8x8(*reinterpret_cast<const uint32_t*>(&y));
-              const int r = t * 8 + gr;
-              if (r < nrows && live) {
-                const long long rr = rr0 + r;
-                __nv_bfloat16* out = p.o + ((cc.row0 + rr / p.g) * p.hq + cc.head * p.g + rr % p.g) * D;
-                *reinterpret_cast<uint32_t*>(out + i * 16 + h * 8 + tc * 2) = z;
-              }
+              if (r < nrows && live) *reinterpret_cast<uint32_t*>(out + i * 16 + h * 8) = z;
             }
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int r = t * 8 + 2 * tc + k;
-            if (gr == 0 && r < nrows && live) {
-              const long long rr = rr0 + r;
-              p.lse[(static_cast<long long>(cc.head) * p.g + rr % p.g) * p.c.rows + cc.row0 + rr / p.g] = lse2[k] * kLn2;
+            const int rc = t * 8 + 2 * tc + k;
+            if (gr == 0 && rc < nrows && live) {
+              const unsigned tk = static_cast<unsigned>(rr0 + rc) / p.g;
+              p.lse[(static_cast<long long>(head) * p.g + (rr0 + rc - tk * p.g)) * p.c.rows + row0 + tk] = lse2[k] * kLn2;
             }
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < kMt; ++i)
+          for (int k = 0; k < 4; ++k) {
+            const int r = t * 8 + 2 * tc + (k & 1);
+            if (r < nrows) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              part[(t * 8 + 2 * tc + (k & 1)) * D + i * 16 + (k >> 1) * 8 + gr] = acc[t][i][k] * inv[k & 1];
-          if (gr == 0) {
-            sm.lse[warp][min(segs, 1)][t * 8 + 2 * tc] = lse2[0];
-            sm.lse[warp][min(segs, 1)][t * 8 + 2 * tc + 1] = lse2[1];
+              for (int i = 0; i < kMt; ++i)
+                p.part[(part_at + r) * D + i * 16 + (k >> 1) * 8 + gr] = acc[t][i][k] * inv[k & 1];
+              if (gr == 0 && k < 2) p.part_lse[part_at + r] = lse2[k & 1];
+            }
           }
         }
       }
-      if (!whole && lane == 0) {
-        Seg& sg = sm.seg[warp][min(segs, 1)];
-        sg.valid = 1;
-        sg.begins = begins;
-        sg.ends = ends;
-        sg.row0 = live ? cc.row0 : -1;
-        sg.head = cc.head;
-        sg.nrows = nrows;
-        sg.rr0 = rr0;
-        sg.unit_end = at + (cc.nb - cc.blk - steps);
+      if (begins && !ends && live && lane == 0) {
+        Open o = {};
+        o.first = this_piece;
+        o.parts = cut.piece_of(this_at + rest - 1) - this_piece + 1;
+        o.row0 = row0;
+        o.head = head;
+        o.nrows = nrows;
+        o.rr0 = rr0;
+        p.open[p.dynamic ? atomicAdd(p.head, 1) : this_piece] = o;
       }
-      segs = 1;
-      cc.blk += steps;
-      if (cc.blk == cc.nb && at < stop) cc.next_unit(p);
+      if (!more) break;
     }
     copies_wait<0>();
   }
-  __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-  // ---- units that warps of this CTA share: a group is a run of parts (w, s),
-  // (w + 1, 0), ...; all warps take rows of the groups in turn
-  int item = 0;
-  for (int w0 = 0; w0 < cut.used; ++w0) {
-#pragma unroll
-    for (int s0 = 0; s0 < 2; ++s0) {
-      const Seg& a = sm.seg[w0][s0];
-      if (!a.valid || (!a.begins && !(w0 == 0 && s0 == 0))) continue;
-      int w1 = w0;
-      bool ends = a.ends;
-      while (!ends && w1 + 1 < cut.used && sm.seg[w1 + 1][0].valid) ends = sm.seg[++w1][0].ends;
-      const bool whole = a.begins && ends;
-      for (int r = 0; r < a.nrows; ++r, ++item) {
-        if (item % kWarps != warp) continue;
-        float x[D / 32];
-        const float lse2 = join_row<D>(
-            w1 - w0 + 1, lane, x, [&](int k) { return sm.lse[w0 + k][k ? 0 : s0][r]; },
-            [&](int k) {
-              const float* base = (k == 0 && s0 == 1) ? reinterpret_cast<const float*>(sm.ring[w0])
-                                  : NT == 1 ? &sm.part[w0 + k][0][0]
-                                            : p.warp_part + (static_cast<size_t>(blockIdx.x) * kWarps + w0 + k) * kRows * D;
-              return base + r * D;
-            });
-        if (whole) {
-          if (a.row0 >= 0) write_o<D>(p, a.row0, a.head, a.rr0 + r, x, lse2 * kLn2, lane);
-        } else {
-          const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + (a.begins ? 1 : 0)) * kRows + r;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) p.part[at * D + lane * (D / 32) + i] = x[i];
-          if (lane == 0) p.part_lse[at] = lse2;
-        }
-      }
-      if (a.begins && !ends && threadIdx.x == 0) {
-        Open o;
-        o.active = a.row0 >= 0;
-        o.last = static_cast<int>((a.unit_end - 1) / cut.per / cut.used);
-        o.row0 = a.row0;
-        o.head = a.head;
-        o.nrows = a.nrows;
-        o.pad = 0;
-        o.rr0 = a.rr0;
-        p.open[blockIdx.x] = o;
-      }
-    }
-  }
 }
 
-// Joins the parts of units that several CTAs share: CTA e takes the unit that
-// begins in the attention's CTA e and goes on in CTAs e + 1 .. last.
+// Zeroes the counters while the attention's CTAs are starting.
+__global__ void k_cache_attention_start(const AttnParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x < 2) p.head[threadIdx.x] = 0;
+}
+
+// Joins the parts of units that several pieces share.  A CTA has every n-th
+// open unit (n CTAs): its warps take rows of up to kAlone parts in turn, and
+// share those of larger units (a 2M-token sequence leaves several hundred parts
+// for each head), all rows at once.
+constexpr int kJoinWarps = 16;
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) k_cache_attention_join(const AttnParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 1) k_cache_attention_join(const AttnParams p, int pieces) {
   constexpr int kRows = 8 * NT;
+  constexpr int kAlone = 48;
+  constexpr int V = D / 32;
+  static_assert(kRows <= kJoinWarps, "a warp for each row");
+  __shared__ __align__(16) float s_x[kJoinWarps][D];
+  __shared__ float s_lse[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Open o = p.open[blockIdx.x];
-  if (!o.active) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < o.nrows; r += kWarps) {
-    float x[D / 32];
-    auto at = [&](int k) { return (static_cast<size_t>(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * kRows + r; };
-    const float lse2 = join_row<D>(
-        o.last - static_cast<int>(blockIdx.x) + 1, lane, x, [&](int k) { return p.part_lse[at(k)]; },
-        [&](int k) { return p.part + at(k) * D; });
-    write_o<D>(p, o.row0, o.head, o.rr0 + r, x, lse2 * kLn2, lane);
+  const int made = __ldcg(p.head + (p.dynamic ? 0 : 2));
+  int nth = 0;
+  for (int base = blockIdx.x; base < pieces; base += gridDim.x * 32) {
+    const int mine = min(base + lane * static_cast<int>(gridDim.x), pieces - 1);
+    const int4 a = __ldcg(reinterpret_cast<const int4*>(p.open + mine));  // before `made` is here
+    const int4 b = __ldcg(reinterpret_cast<const int4*>(p.open + mine) + 1);
+    if (base >= made) break;
+    unsigned todo = __ballot_sync(0xffffffffu, base + lane * gridDim.x < min(pieces, made) && a.x != 0);
+    while (todo) {
+      const int bit = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int m = __shfl_sync(0xffffffffu, a.x, bit), e = __shfl_sync(0xffffffffu, a.y, bit);
+      const int row0 = __shfl_sync(0xffffffffu, a.z, bit), head = __shfl_sync(0xffffffffu, a.w, bit);
+      const int nrows = __shfl_sync(0xffffffffu, b.x, bit), rr0 = __shfl_sync(0xffffffffu, b.y, bit);
+      auto at = [&](int k, int r) { return (static_cast<size_t>(e + k) * 2 + (k == 0 ? 1 : 0)) * kRows + r; };
+      float x[V];
+      if (m <= kAlone) {
+        for (int r = 0; r < nrows; ++r) {
+          if (nth++ % kJoinWarps != warp) continue;
+          const float lse2 = join_row<D>(
+              m, lane, x, [&](int k) { return __ldcg(p.part_lse + at(k, r)); },
+              [&](int k) { return p.part + at(k, r) * D; });
+          write_o<D>(p, row0, head, rr0 + r, x, lse2 * kLn2, lane);
+        }
+        continue;
+      }
+      // `each` warps have one row, a run of its parts each
+      const int each = kJoinWarps >> (32 - __clz(nrows - 1));
+      const int r = warp / each, run = warp - r * each;
+      if (r < nrows) {
+        const int k0 = static_cast<int>(static_cast<long long>(m) * run / each);
+        const int k1 = static_cast<int>(static_cast<long long>(m) * (run + 1) / each);
+        const float part = join_row<D>(
+            k1 - k0, lane, x, [&](int k) { return __ldcg(p.part_lse + at(k0 + k, r)); },
+            [&](int k) { return p.part + at(k0 + k, r) * D; });
+#pragma unroll
+        for (int i = 0; i < V; ++i) s_x[warp][lane * V + i] = x[i];
+        if (lane == 0) s_lse[warp] = part;
+      }
+      __syncthreads();
+      if (r < nrows && run == 0) {
+        const float lse2 = join_row<D>(each, lane, x, [&](int k) { return s_lse[warp + k]; },
+                                       [&](int k) { return &s_x[warp + k][0]; });
+        write_o<D>(p, row0, head, rr0 + r, x, lse2 * kLn2, lane);
+      }
+      __syncthreads();  // the sums have been read
+    }
   }
 }
 
 constexpr int kMaxNt = 2;
 constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-hdp_status_t sm_count(int* sms) {
-  int dev = 0;
-  HDP_CUDA_TRY(cudaGetDevice(&dev));
-  HDP_CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+constexpr int kDevices = 64;
+
+// The current device and its SMs (asked for once).
+hdp_status_t sm_count(int* device, int* sms) {
+  static std::atomic<int> known[kDevices];
+  HDP_CUDA_TRY(cudaGetDevice(device));
+  const bool kept = *device < kDevices;
+  *sms = kept ? known[*device].load(std::memory_order_relaxed) : 0;
+  if (*sms > 0) return HDP_OK;
+  HDP_CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *device));
+  if (kept) known[*device].store(*sms, std::memory_order_relaxed);
   return HDP_OK;
 }
 
 struct Layout {
-  size_t part, part_lse, warp_part, open, bytes;
-  Layout(int ctas, int d) {
+  int pieces;
+  size_t part, part_lse, open, head, bytes;
+  Layout(int sms, int d) {
     const size_t rows = 8 * kMaxNt;
+    pieces = sms * kWarps * (1 + kMorePieces);
     part = 0;
-    part_lse = part + align256(ctas * 2 * rows * d * sizeof(float));
-    warp_part = part_lse + align256(ctas * 2 * rows * sizeof(float));
-    open = warp_part + align256(ctas * kWarps * rows * d * sizeof(float));
-    bytes = open + align256(ctas * sizeof(Open));
+    part_lse = part + align256(pieces * 2 * rows * d * sizeof(float));
+    open = part_lse + align256(pieces * 2 * rows * sizeof(float));
+    head = open + align256(pieces * sizeof(Open));
+    bytes = head + 256;
   }
 };
 
-template <int D, int FMT, int NT, bool SPARSE>
-hdp_status_t launch(const AttnParams& p, int ctas, cudaStream_t st) {
-  auto* kernel = k_cache_attention<D, FMT, NT, SPARSE>;
-  constexpr int smem = sizeof(Shared<D, NT>);
-  static_assert(smem <= 232448, "shared memory of a CTA");
-  HDP_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  kernel<<<ctas, kThreads, smem, st>>>(p);
-  note_launch();
-  HDP_CUDA_TRY(cudaGetLastError());
-  // The join's launch overlaps the attention's tail; it waits for its results.
+// A launch that may begin before the kernel in front of it has ended; it waits
+// for that kernel's results itself.
+template <class... T>
+hdp_status_t launch_early(void (*kernel)(T...), dim3 grid, int threads, int smem, cudaStream_t st, T... args) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_cache_attention_join<D, NT>, p));
+  HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
   note_launch();
   return HDP_OK;
 }
 
+template <int D, int FMT, int NT, bool SPARSE>
+hdp_status_t launch(const AttnParams& p, int device, int ctas, cudaStream_t st) {
+  auto* kernel = k_cache_attention<D, FMT, NT, SPARSE>;
+  constexpr int smem = sizeof(Shared);
+  static_assert(smem <= 232448, "shared memory of a CTA");
+  static std::atomic<bool> ready[kDevices];
+  if (device >= kDevices || !ready[device].load(std::memory_order_relaxed)) {
+    HDP_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    if (device < kDevices) ready[device].store(true, std::memory_order_relaxed);
+  }
+  const int pieces = ctas * kWarps * (p.dynamic ? 1 + kMorePieces : 1);
+  if (p.dynamic) {
+    k_cache_attention_start<<<1, 32, 0, st>>>(p);
+    note_launch();
+    HDP_CUDA_TRY(cudaGetLastError());
+    const hdp_status_t r = launch_early(kernel, dim3(ctas), kThreads, smem, st, p);
+    if (r != HDP_OK) return r;
+  } else {
+    kernel<<<ctas, kThreads, smem, st>>>(p);
+    note_launch();
+    HDP_CUDA_TRY(cudaGetLastError());
+  }
+  return launch_early(k_cache_attention_join<D, NT>, dim3(ctas), kJoinWarps * 32, 0, st, p, pieces);
+}
+
 template <int D, int FMT>
-hdp_status_t launch_for(const AttnParams& p, int nt, int ctas, cudaStream_t st) {
-  if (p.blocks) return nt == 1 ? launch<D, FMT, 1, true>(p, ctas, st) : launch<D, FMT, 2, true>(p, ctas, st);
-  return nt == 1 ? launch<D, FMT, 1, false>(p, ctas, st) : launch<D, FMT, 2, false>(p, ctas, st);
+hdp_status_t launch_for(const AttnParams& p, int nt, int device, int ctas, cudaStream_t st) {
+  if (p.blocks) return nt == 1 ? launch<D, FMT, 1, true>(p, device, ctas, st) : launch<D, FMT, 2, true>(p, device, ctas, st);
+  return nt == 1 ? launch<D, FMT, 1, false>(p, device, ctas, st) : launch<D, FMT, 2, false>(p, device, ctas, st);
 }
 
 }  // namespace
@@ -833,8 +994,8 @@ extern "C" hdp_status_t hdp_cache_attention_workspace_bytes(const hdp_cache_t* c
     return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_attention_workspace_bytes: need hq >= 1 and hq % hkv == 0");
   if (cache->d != 64 && cache->d != 128)
     return fail(HDP_ERR_UNSUPPORTED, "hdp_cache_attention_workspace_bytes: d must be 64 or 128");
-  int sms = 0;
-  const hdp_status_t r = sm_count(&sms);
+  int device = 0, sms = 0;
+  const hdp_status_t r = sm_count(&device, &sms);
   if (r != HDP_OK) return r;
   *bytes = Layout(sms, cache->d).bytes;
   return HDP_OK;
@@ -853,11 +1014,13 @@ extern "C" hdp_status_t hdp_cache_attention(const hdp_cache_t* cache, const int3
   if (blocks ? count < 1 : count != 0)
     return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_attention: count must be >= 1 with blocks and 0 without");
   if (rows == 0) return HDP_OK;
+  if (rows * (hq / cache->hkv) > 2147483647LL)
+    return fail(HDP_ERR_UNSUPPORTED, "hdp_cache_attention: rows * hq / hkv must be below 2^31");
   if (!q || !o || !lse) return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_attention: NULL argument");
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(o)) & 15)
     return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_attention: q and o must be 16-byte aligned");
-  int sms = 0;
-  r = sm_count(&sms);
+  int device = 0, sms = 0;
+  r = sm_count(&device, &sms);
   if (r != HDP_OK) return r;
   const Layout lay(sms, cache->d);
   if (!workspace || workspace_bytes < lay.bytes)
@@ -877,8 +1040,8 @@ extern "C" hdp_status_t hdp_cache_attention(const hdp_cache_t* cache, const int3
   char* ws = static_cast<char*>(workspace);
   p.part = reinterpret_cast<float*>(ws + lay.part);
   p.part_lse = reinterpret_cast<float*>(ws + lay.part_lse);
-  p.warp_part = reinterpret_cast<float*>(ws + lay.warp_part);
   p.open = reinterpret_cast<Open*>(ws + lay.open);
+  p.head = reinterpret_cast<int*>(ws + lay.head);
 
   // Tiles of 8 query rows while they hold a sequence's rows on average, of 16
   // beyond: a second tile reads the cache again.
@@ -889,9 +1052,12 @@ extern "C" hdp_status_t hdp_cache_attention(const hdp_cache_t* cache, const int3
                               : static_cast<double>(rows) * p.g / (8 * nt) + cache->num_seqs;
   const double steps = tiles * cache->hkv * (blocks ? count : cache->max_pages);
   const int ctas = steps < sms ? static_cast<int>(steps) + 1 : sms;
+  // Handing out the ends of runs costs one more small launch: from 16 steps a
+  // warp on, where the runs' ends are more than a step.
+  p.dynamic = steps >= 16.0 * kWarps * sms;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool i8 = cache->format == HDP_CACHE_INT8;
   if (cache->d == 128)
-    return i8 ? launch_for<128, HDP_CACHE_INT8>(p, nt, ctas, st) : launch_for<128, HDP_CACHE_E4M3>(p, nt, ctas, st);
-  return i8 ? launch_for<64, HDP_CACHE_INT8>(p, nt, ctas, st) : launch_for<64, HDP_CACHE_E4M3>(p, nt, ctas, st);
+    return i8 ? launch_for<128, HDP_CACHE_INT8>(p, nt, device, ctas, st) : launch_for<128, HDP_CACHE_E4M3>(p, nt, device, ctas, st);
+  return i8 ? launch_for<64, HDP_CACHE_INT8>(p, nt, device, ctas, st) : launch_for<64, HDP_CACHE_E4M3>(p, nt, device, ctas, st);
 }
