@@ -41,7 +41,13 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRingBytes = 24576;  // of each warp: 3 (d = 128) or 6 (d = 64) half blocks
+// Bytes of a warp's ring of half blocks.  More in flight streams a long run
+// better; less leaves the memory's queues shorter, and with them every other
+// access (lists, pages, query rows), which short runs wait for.  Measured at
+// 24 KB and 16 KB: one 2M-token sequence 646 and 654 us, 64 x 32 chosen blocks
+// 59 and 55 us, 16 sequences with up to 5 drafted tokens 67 and 62 us.
+template <int NT, bool SPARSE>
+constexpr int kRingBytes = NT == 1 && !SPARSE ? 24576 : 16384;
 constexpr int kMeta = 8;           // blocks whose scales and first key are kept
 constexpr float kLow = -1.0e30f;   // reference exponent before the first key
 constexpr float kLn2 = 0.6931471805599453f;
@@ -150,8 +156,9 @@ __device__ __forceinline__ SeqPlace seq_place(const CacheView& c, int i) {
   return s;
 }
 
+template <int NT, bool SPARSE>
 struct Shared {
-  unsigned char ring[kWarps][kRingBytes];
+  unsigned char ring[kWarps][kRingBytes<NT, SPARSE>];
   SeqPlace seq[kSeqs];
   Meta meta[kWarps][kMeta];
   long long pre[kThreads];  // steps before each thread's sequences
@@ -167,14 +174,14 @@ struct Cursor {
 
   __device__ __forceinline__ static int tiles_of(int n, int g) { return static_cast<int>((n * g + 8u * NT - 1) / (8u * NT)); }
   __device__ __forceinline__ static int blocks_of(const SeqPlace& s) { return max(1, static_cast<int>((s.len + (kBlock - 1u)) / kBlock)); }
-  __device__ __forceinline__ static SeqPlace place(const AttnParams& p, const Shared& sm, int i) {
-    return i < kSeqs ? sm.seq[i] : seq_place(p.c, i);
+  __device__ __forceinline__ static SeqPlace place(const AttnParams& p, const SeqPlace* kept, int i) {
+    return i < kSeqs ? kept[i] : seq_place(p.c, i);
   }
   // Steps of all units of a sequence.
   __device__ __forceinline__ static long long cost(const AttnParams& p, const SeqPlace& s) {
     return s.n ? static_cast<long long>(blocks_of(s)) * tiles_of(s.n, p.g) * p.c.hkv : 0;
   }
-  __device__ __forceinline__ void enter(const AttnParams& p, const Shared& sm, int i) {
+  __device__ __forceinline__ void enter(const AttnParams& p, const SeqPlace* kept, int i) {
     head = tile = blk = 0;
     if constexpr (SPARSE) {
       nb = p.count;
@@ -188,24 +195,24 @@ struct Cursor {
       s.n = 1;
     } else {
       seq = i;
-      s = place(p, sm, i);
+      s = place(p, kept, i);
       nb = blocks_of(s);
     }
     tiles = tiles_of(s.n, p.g);
   }
   // The sequence after this one that has rows.
-  __device__ __forceinline__ int next_seq(const AttnParams& p, const Shared& sm) const {
+  __device__ __forceinline__ int next_seq(const AttnParams& p, const SeqPlace* kept) const {
     int i = seq + 1;
-    while (i < p.c.num_seqs && place(p, sm, i).n == 0) ++i;
+    while (i < p.c.num_seqs && place(p, kept, i).n == 0) ++i;
     return i;
   }
-  __device__ __forceinline__ void next_unit(const AttnParams& p, const Shared& sm) {
+  __device__ __forceinline__ void next_unit(const AttnParams& p, const SeqPlace* kept) {
     blk = 0;
     if (++tile < tiles) return;
     tile = 0;
     if (++head < p.c.hkv) return;
-    const int i = SPARSE ? s.row0 + 1 : next_seq(p, sm);
-    if (i < (SPARSE ? p.c.rows : p.c.num_seqs)) enter(p, sm, i);
+    const int i = SPARSE ? s.row0 + 1 : next_seq(p, kept);
+    if (i < (SPARSE ? p.c.rows : p.c.num_seqs)) enter(p, kept, i);
   }
   // Skips `off` steps from the sequence's first.
   __device__ __forceinline__ void skip(long long off) {
@@ -353,13 +360,13 @@ struct Cut {
 template <int D, int FMT, int NT, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParams p) {
   constexpr int kHalf = kBlock * D;               // bytes of a block's K or V codes of one head
-  constexpr int kSlots = kRingBytes / kHalf;      // half blocks in flight
+  constexpr int kSlots = kRingBytes<NT, SPARSE> / kHalf;  // half blocks in flight
   constexpr int kKeyChunks = D / 64;              // 16-byte chunks that a lane has of a key
   constexpr int kMt = D / 16;
   constexpr int kRows = 8 * NT;
   using Cur = Cursor<SPARSE, NT>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
+  auto& sm = *reinterpret_cast<Shared<NT, SPARSE>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gr = lane >> 2, tc = lane & 3;  // fragment row group and column pair
 
@@ -413,14 +420,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
       const int head = static_cast<int>(off / (static_cast<long long>(p.count) * (per_row / p.c.hkv)));
       const int at = min(static_cast<int>(off % p.count) + lane, p.count - 1);  // of the list that comes next
       asm volatile("prefetch.global.L1 [%0];" ::"l"(p.blocks + (static_cast<long long>(row) * p.c.hkv + head) * p.count + at));
-      cur.enter(p, sm, row);
+      cur.enter(p, sm.seq, row);
       cur.skip(off);
     } else {
       const int slice = find_last(kThreads, x, [&](int s) { return sm.pre[s]; });
       long long at = sm.pre[slice];
       int i = slice * per_thread;
-      for (long long c; x - at >= (c = Cur::cost(p, Cur::place(p, sm, i))) && i + 1 < p.c.num_seqs; ++i) at += c;
-      cur.enter(p, sm, i);
+      for (long long c; x - at >= (c = Cur::cost(p, Cur::place(p, sm.seq, i))) && i + 1 < p.c.num_seqs; ++i) at += c;
+      cur.enter(p, sm.seq, i);
       cur.skip(x - at);
     }
   };
@@ -496,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
             }
           }
           if (!SPARSE && next_of < 0 && lc.last_unit(p)) {
-            next_of = lc.next_seq(p, sm);
+            next_of = lc.next_seq(p, sm.seq);
             if (next_of < p.c.num_seqs && lane < p.c.max_pages)
               next_page = __ldg(p.c.table + static_cast<long long>(next_of) * p.c.max_pages + lane);
           }
@@ -535,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
             // heads of a sequence share its pages: a list of up to 32 serves them all (its
             // visible blocks are those of the sequence's last rows)
             const bool same = !SPARSE && lc.nb <= 32 && lc.tiles == 1 && !lc.last_unit(p);
-            lc.next_unit(p, sm);
+            lc.next_unit(p, sm.seq);
             if (!same) ids_at = -1;
           }
         }
@@ -751,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
       // ---- the next unit's query rows are asked for before this one is written
       bool more = true;
       if (at < stop) {
-        cc.next_unit(p, sm);
+        cc.next_unit(p, sm.seq);
       } else {
         __syncwarp();
         more = done != loaded;
@@ -955,7 +962,7 @@ hdp_status_t launch_early(void (*kernel)(T...), dim3 grid, int threads, int smem
 template <int D, int FMT, int NT, bool SPARSE>
 hdp_status_t launch(const AttnParams& p, int device, int ctas, cudaStream_t st) {
   auto* kernel = k_cache_attention<D, FMT, NT, SPARSE>;
-  constexpr int smem = sizeof(Shared);
+  constexpr int smem = sizeof(Shared<NT, SPARSE>);
   static_assert(smem <= 232448, "shared memory of a CTA");
   static std::atomic<bool> ready[kDevices];
   if (device >= kDevices || !ready[device].load(std::memory_order_relaxed)) {

@@ -10,12 +10,17 @@
 //
 // V codes lie [channel][token] with the tokens in the order in which a 16-row
 // matrix fragment takes its k index (the attention then feeds 16-byte loads
-// straight to the tensor cores).  Each warp here has the tokens of one 16-byte
-// chunk, so the transposition is a byte shuffle between two (d = 128) or four
-// (d = 64) lanes and the chunk is stored whole; nothing goes through shared
-// memory.
+// straight to the tensor cores).  Two (d = 128) or four (d = 64) lanes here have
+// the tokens of one 16-byte chunk, so the transposition is a byte shuffle
+// between them and the chunk is stored whole; nothing goes through shared memory.
+//
+// With one token for each sequence (a decoding step) a warp has one (sequence,
+// kv head) instead, half of it the K row and half the V row: nothing but the
+// latencies of the length, the page and the old scale stands in its way, and all
+// warps of an ordinary batch run at once.
 #include <cuda_fp8.h>
 
+#include <cstring>
 #include <string>
 
 #include "kv_cache.cuh"
@@ -112,21 +117,23 @@ __device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, u
   t[3] = __byte_perm(ab1, cd1, 0x7632);
 }
 
-// Where a thread's rows and channels lie.  Pass p of a thread is token
-//   d = 128: 8 p + 2 warp + e            (e = lane / 16)
-//   d =  64: 16 p + 8 h + 2 warp + e     (e = lane / 8 % 2, h = lane / 16)
-// of the block, so warp c has exactly the tokens of V chunk c.
+// Where a thread's rows and channels lie.  8 lanes have 64 channels of a row, and
+// pass p of a thread is token
+//   d = 128: 8 p + 2 c + e         (e = lane / 8 % 2, c = 2 (warp % 2) + lane / 16; 64 channels for each two warps)
+//   d =  64: 16 p + 8 h + 2 c + e  (e = lane / 8 % 2, h = lane / 16, c = warp)
+// of the block, so 2 or 4 lanes have exactly the tokens of V chunk c, and with
+// d = 128 the next two those of the chunk beside it: whole 32-byte sectors.
 template <int D>
 struct Place {
   static constexpr int kPasses = D / 16;
-  static constexpr int kLanes = D / 8;  // lanes of a row
+  static constexpr int kLanes = 8;  // lanes of a row
   int c, e, h, ch;
   __device__ __forceinline__ Place() {
-    const int lane = threadIdx.x & 31;
-    c = threadIdx.x >> 5;
-    ch = (lane % kLanes) * 8;
-    e = (lane / kLanes) & 1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    e = (lane >> 3) & 1;
     h = D == 64 ? lane >> 4 : 0;
+    c = D == 64 ? warp : 2 * (warp & 1) + (lane >> 4);
+    ch = (lane & 7) * 8 + (D == 64 ? 0 : (warp >> 1) * 64);
   }
   __device__ __forceinline__ int token(int p) const { return D == 128 ? 8 * p + 2 * c + e : 16 * p + 8 * h + 2 * c + e; }
   // Byte of token(p) inside a channel's 64 bytes of V.
@@ -399,8 +406,12 @@ __global__ void __launch_bounds__(kThreads) k_cache_append(CacheView c, const ui
   if (threadIdx.x < D) {
     const int i = threadIdx.x;
     const float unit = FMT == HDP_CACHE_INT8 ? inv[0] : inv[0] * 0.25f;
-    float a = fminf(fminf(s_bound[0][0][i], s_bound[1][0][i]), fminf(s_bound[2][0][i], s_bound[3][0][i]));
-    float b = fmaxf(fmaxf(s_bound[0][1][i], s_bound[1][1][i]), fmaxf(s_bound[2][1][i], s_bound[3][1][i]));
+    const int w0 = D == 64 ? 0 : i / 64 * 2;  // the warps that have the channel
+    float a = fminf(s_bound[w0][0][i], s_bound[w0 + 1][0][i]), b = fmaxf(s_bound[w0][1][i], s_bound[w0 + 1][1][i]);
+    if (D == 64) {
+      a = fminf(a, fminf(s_bound[2][0][i], s_bound[3][0][i]));
+      b = fmaxf(b, fmaxf(s_bound[2][1][i], s_bound[3][1][i]));
+    }
     a = floorf(a * unit);
     b = ceilf(b * unit);
     int8_t* out = c.bounds + ph * (2 * D) + i;
@@ -412,6 +423,100 @@ __global__ void __launch_bounds__(kThreads) k_cache_append(CacheView c, const ui
     out[D] = static_cast<int8_t>(fminf(fmaxf(b, -127.f), 127.f));
   }
   if (threadIdx.x == 0) *reinterpret_cast<float2*>(c.scales + 2 * ph) = make_float2(scale[0], scale[1]);
+}
+
+// One token for each sequence.
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads) k_cache_append_one(CacheView c, const uint4* __restrict__ k,
+                                                               const uint4* __restrict__ v) {
+  constexpr int kRow = D / 8;  // lanes of a row: K in the first, V in the next
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp;
+  if (unit >= static_cast<long long>(c.num_seqs) * c.hkv) return;
+  const int seq = static_cast<int>(unit / c.hkv), head = static_cast<int>(unit - static_cast<long long>(seq) * c.hkv);
+  const int w = lane / kRow, ch = lane % kRow * 8;
+  const bool on = w < 2;
+  uint4 x = make_uint4(0, 0, 0, 0);
+  if (on) x = __ldg((w ? v : k) + static_cast<size_t>(unit) * kRow + ch / 8);
+  const long long p0 = seq_len(c, seq) - 1;
+  if (p0 < 0) return;
+  const int page = page_of(c, seq, static_cast<int>(p0 / kBlock)), t = static_cast<int>(p0 % kBlock);
+  if (page < 0) return;
+  const size_t ph = static_cast<size_t>(page) * c.hkv + head;
+  const bool fresh = t == 0;
+  uint8_t* codes = (w == 1 ? c.v : c.k) + ph * (kBlock * D);
+  int8_t* bounds = c.bounds + ph * (2 * D) + ch;
+  float before = 0.f;
+  uint2 blo = make_uint2(0, 0), bhi = blo;
+  if (!fresh && on) {
+    before = c.scales[2 * ph + w];
+    if (w == 0) {
+      blo = *reinterpret_cast<const uint2*>(bounds);
+      bhi = *reinterpret_cast<const uint2*>(bounds + D);
+    }
+  }
+  const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+  uint32_t top = max(m & 0xffffu, m >> 16);
+#pragma unroll
+  for (int o = 1; o < kRow; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool lost = top >= 0x7f80u || before != before;
+  const float scale = lost ? __int_as_float(0x7fc00000) : fmaxf(pow2i(scale_exponent<FMT>(top)), before);
+  const float inv = lost ? 1.f : __int_as_float((254 << 23) - __float_as_int(scale));
+  const bool grown = !fresh && !lost && scale != before;
+  const float ratio = grown ? before * inv : 1.f;
+
+  // The block begins: zero codes; or its scale grows: its codes rounded to it.
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    const bool grows = __shfl_sync(0xffffffffu, static_cast<int>(grown), side * kRow) != 0;
+    const float r = __shfl_sync(0xffffffffu, ratio, side * kRow);
+    if (!fresh && !grows) continue;
+    uint4* b = reinterpret_cast<uint4*>((side ? c.v : c.k) + ph * (kBlock * D));
+#pragma unroll 4
+    for (int i = lane; i < kBlock * D / 16; i += 32) {
+      uint4 y = make_uint4(0, 0, 0, 0);
+      if (!fresh) {
+        y = b[i];
+        y.x = rescale4<FMT>(y.x, r);
+        y.y = rescale4<FMT>(y.y, r);
+        y.z = rescale4<FMT>(y.z, r);
+        y.w = rescale4<FMT>(y.w, r);
+      }
+      b[i] = y;
+    }
+  }
+  __syncwarp();  // the new row goes over them
+  if (!on) return;
+  const float f[8] = {bf_lo(x.x), bf_hi(x.x), bf_lo(x.y), bf_hi(x.y), bf_lo(x.z), bf_hi(x.z), bf_lo(x.w), bf_hi(x.w)};
+  const uint2 code = make_uint2(code_pair<FMT>(f[0] * inv, f[1] * inv) | (code_pair<FMT>(f[2] * inv, f[3] * inv) << 16),
+                                code_pair<FMT>(f[4] * inv, f[5] * inv) | (code_pair<FMT>(f[6] * inv, f[7] * inv) << 16));
+  if (w == 0) {
+    *reinterpret_cast<uint2*>(codes + t * D + ch) = code;
+    const float unit_inv = FMT == HDP_CACHE_INT8 ? inv : inv * 0.25f;
+    int8_t lo[8], hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float a = floorf(f[i] * unit_inv), b = ceilf(f[i] * unit_inv);
+      if (!fresh) {
+        const uint32_t ol = (i < 4 ? blo.x : blo.y) >> (8 * (i & 3)), oh = (i < 4 ? bhi.x : bhi.y) >> (8 * (i & 3));
+        a = fminf(a, floorf(static_cast<float>(static_cast<int8_t>(ol & 0xff)) * ratio));
+        b = fmaxf(b, ceilf(static_cast<float>(static_cast<int8_t>(oh & 0xff)) * ratio));
+      }
+      lo[i] = static_cast<int8_t>(fminf(fmaxf(a, -127.f), 127.f));
+      hi[i] = static_cast<int8_t>(fminf(fmaxf(b, -127.f), 127.f));
+    }
+    uint2 pl, ph2;
+    memcpy(&pl, lo, 8);
+    memcpy(&ph2, hi, 8);
+    *reinterpret_cast<uint2*>(bounds) = pl;
+    *reinterpret_cast<uint2*>(bounds + D) = ph2;
+  } else {
+    const int byte = 16 * (t / 2 % 4) + 4 * (t / 16) + 2 * (t / 8 % 2) + t % 2;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      codes[(ch + i) * kBlock + byte] = static_cast<uint8_t>((i < 4 ? code.x : code.y) >> (8 * (i & 3)));
+  }
+  if (ch == 0) c.scales[2 * ph + w] = scale;
 }
 
 template <int FMT>
@@ -512,13 +617,20 @@ extern "C" hdp_status_t hdp_cache_append(const hdp_cache_t* cache, const int32_t
   const uint4* kp = static_cast<const uint4*>(k);
   const uint4* vp = static_cast<const uint4*>(v);
   const bool i8 = cache->format == HDP_CACHE_INT8;
+  const bool one = !cu;
+  // one token for each sequence: a warp for each (sequence, kv head), at most 2^24 * 65535 / 4 CTAs
+  const int64_t ones = (int64_t(c.num_seqs) * c.hkv + kThreads / 32 - 1) / (kThreads / 32);
+  if (one && ones > 2147483647LL) return fail(HDP_ERR_UNSUPPORTED, "hdp_cache_append: num_seqs * hkv must be below 2^33");
+  const dim3 grid = one ? dim3(static_cast<unsigned>(ones)) : g;
+  void (*kernel)(CacheView, const uint4*, const uint4*);
   if (cache->d == 128) {
-    if (i8) k_cache_append<128, HDP_CACHE_INT8><<<g, kThreads, 0, st>>>(c, kp, vp);
-    else k_cache_append<128, HDP_CACHE_E4M3><<<g, kThreads, 0, st>>>(c, kp, vp);
+    if (one) kernel = i8 ? k_cache_append_one<128, HDP_CACHE_INT8> : k_cache_append_one<128, HDP_CACHE_E4M3>;
+    else kernel = i8 ? k_cache_append<128, HDP_CACHE_INT8> : k_cache_append<128, HDP_CACHE_E4M3>;
   } else {
-    if (i8) k_cache_append<64, HDP_CACHE_INT8><<<g, kThreads, 0, st>>>(c, kp, vp);
-    else k_cache_append<64, HDP_CACHE_E4M3><<<g, kThreads, 0, st>>>(c, kp, vp);
+    if (one) kernel = i8 ? k_cache_append_one<64, HDP_CACHE_INT8> : k_cache_append_one<64, HDP_CACHE_E4M3>;
+    else kernel = i8 ? k_cache_append<64, HDP_CACHE_INT8> : k_cache_append<64, HDP_CACHE_E4M3>;
   }
+  kernel<<<grid, kThreads, 0, st>>>(c, kp, vp);
   note_launch();
   HDP_CUDA_TRY(cudaGetLastError());
   return HDP_OK;

@@ -10,10 +10,12 @@
 //
 //   k_cache_scores: 256 blocks of one (row, kv head) a CTA; a lane has 16
 //   channels of one extreme, so 16 (d = 128) or 8 lanes have a block.
-//   k_cache_top: one CTA for each (row, kv head).  The keys stay in registers;
-//   a binary search over the key's value counts the keys above it (no atomics,
-//   so many equal keys cost nothing), and ballots give each chosen block its
-//   place in ascending order.
+//   k_cache_top: one CTA for each (row, kv head), a cluster of 8 for more than
+//   4,096 blocks.  The keys stay in registers; a binary search over the key's
+//   value counts the keys above it (no atomics, so many equal keys cost
+//   nothing), and ballots give each chosen block its place in ascending order.
+#include <cooperative_groups.h>
+
 #include <string>
 
 #include "kv_cache.cuh"
@@ -73,10 +75,18 @@ __global__ void __launch_bounds__(kScoreThreads) k_cache_scores(const SelectPara
   if (!row_place(p.c, row, seq, have)) return;
   if (have <= p.count || chunk * kScoreBlocks >= have) return;  // all are chosen, or none here
 
-  // pages first: their latency hides behind the query's
+  // The bounds are asked for first: their latency hides behind the query's work.
   const int b = chunk * kScoreBlocks + warp * 32 + lane;
   const int page = b < have ? page_of(p.c, seq, b) : -1;
   const size_t ph = static_cast<size_t>(max(page, 0)) * p.c.hkv + head;
+  const int part = lane % kLanes;  // 16 channels of one extreme
+  uint4 x[kLanes];
+#pragma unroll
+  for (int i = 0; i < kLanes; ++i) {  // block i of this group of lanes: lane (group, i) keeps its sum
+    const int pg = __shfl_sync(0xffffffffu, page, (lane & ~(kLanes - 1)) + i);
+    x[i] = pg >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.c.bounds + (static_cast<size_t>(pg) * p.c.hkv + head) * (2 * D)) + part)
+                   : make_uint4(0, 0, 0, 0);
+  }
   const float scale = page >= 0 ? __ldg(p.c.scales + 2 * ph) : 0.f;
 
   const __nv_bfloat16* q = p.q + (static_cast<size_t>(row) * p.hq + head * p.g) * D;
@@ -111,8 +121,6 @@ __global__ void __launch_bounds__(kScoreThreads) k_cache_scores(const SelectPara
   }
   __syncthreads();
 
-  // this lane's 16 channels of one extreme
-  const int part = lane % kLanes;
   int qr[8];
   {
     const int4* src = reinterpret_cast<const int4*>(&s_q[0][0] + part * 16);
@@ -127,13 +135,6 @@ __global__ void __launch_bounds__(kScoreThreads) k_cache_scores(const SelectPara
     qr[7] = c.w;
   }
   int mine = 0;
-  uint4 x[kLanes];
-#pragma unroll
-  for (int i = 0; i < kLanes; ++i) {  // block i of this group of lanes: lane (group, i) keeps its sum
-    const int pg = __shfl_sync(0xffffffffu, page, (lane & ~(kLanes - 1)) + i);
-    x[i] = pg >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.c.bounds + (static_cast<size_t>(pg) * p.c.hkv + head) * (2 * D)) + part)
-                   : make_uint4(0, 0, 0, 0);
-  }
 #pragma unroll
   for (int i = 0; i < kLanes; ++i) {
     int u = dp2a_lo(qr[0], x[i].x, 0);
@@ -156,118 +157,188 @@ __global__ void __launch_bounds__(kScoreThreads) k_cache_scores(const SelectPara
   }
 }
 
-// ITEMS keys of a thread in registers (ITEMS * 1024 blocks at most); 0: the
-// keys are read again for each step.
+// Chooses the `count` largest of a CTA's keys, the earlier of equal ones, and
+// calls emit(place, i) for each of a thread's that is chosen.  Item i of a
+// thread comes after all items of the warps before its own, and after items of
+// its warp with a smaller (i, lane).  key_at(i) is its key, has(i) whether there
+// is one; at least `count` of them are there.
+struct TopShared {
+  int count[2][32];
+  uint32_t low[32], high[32];
+};
+template <class K, class H, class E>
+__device__ __forceinline__ void choose(TopShared& sm, int items, int count, int forced, K key_at, H has, E emit) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t low = 0xffffffffu, high = 0;
+#pragma unroll
+  for (int i = 0; i < items; ++i) {
+    if (has(i)) {
+      const uint32_t k = key_at(i);
+      low = min(low, k);
+      high = max(high, k == kForced ? 0u : k);
+    }
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  if (lane == 0) {
+    sm.low[warp] = low;
+    sm.high[warp] = high;
+  }
+  __syncthreads();
+  low = __reduce_min_sync(0xffffffffu, sm.low[lane]);
+  high = __reduce_max_sync(0xffffffffu, sm.high[lane]);
+  // the largest x with at least `count` keys >= x: between low (all of them)
+  // and the largest key that is not forced, unless the forced ones are enough
+  if (forced >= count) low = high = kForced;
+  int turn = 0;
+  while (low < high) {
+    const uint32_t mid = low + ((high - low) >> 1) + ((high - low) & 1);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < items; ++i) n += has(i) && key_at(i) >= mid;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) sm.count[turn][warp] = n;
+    __syncthreads();
+    n = __reduce_add_sync(0xffffffffu, sm.count[turn][lane]);
+    turn ^= 1;
+    if (n == count) {  // exactly these
+      low = mid;
+      break;
+    }
+    if (n > count) low = mid;
+    else high = mid - 1;
+  }
+
+  // keys above it are chosen, and of those equal to it the first ones (if the
+  // search ended early, all of them)
+  int above = 0, equal = 0;
+#pragma unroll
+  for (int i = 0; i < items; ++i) {
+    const bool in = has(i);
+    const uint32_t k = key_at(i);
+    above += __popc(__ballot_sync(0xffffffffu, in && k > low));
+    equal += __popc(__ballot_sync(0xffffffffu, in && k == low));
+  }
+  __syncthreads();  // the search's last counts have been read
+  if (lane == 0) {
+    sm.count[0][warp] = above;
+    sm.count[1][warp] = equal;
+  }
+  __syncthreads();
+  const int a = sm.count[0][lane], e = sm.count[1][lane];
+  const int take = count - __reduce_add_sync(0xffffffffu, a);  // of the equal ones
+  int before_above = __reduce_add_sync(0xffffffffu, lane < warp ? a : 0);
+  int before_equal = __reduce_add_sync(0xffffffffu, lane < warp ? e : 0);
+  const unsigned under = (1u << lane) - 1;
+#pragma unroll
+  for (int i = 0; i < items; ++i) {
+    const bool in = has(i);
+    const uint32_t k = key_at(i);
+    const unsigned ma = __ballot_sync(0xffffffffu, in && k > low), me = __ballot_sync(0xffffffffu, in && k == low);
+    const int ra = before_above + __popc(ma & under), re = before_equal + __popc(me & under);
+    if (in && (k > low || (k == low && re < take))) emit(ra + min(re, take), i);
+    before_above += __popc(ma);
+    before_equal += __popc(me);
+  }
+}
+
+// Forced keys: the first p.first and the last p.last of `have` > p.count blocks.
+__device__ __forceinline__ int forced_in(const SelectParams& p, int have, int from, int to) {
+  return max(0, min(to, p.first) - from) + max(0, to - max(from, have - p.last));
+}
+
+// One CTA for each (row, kv head).  ITEMS keys of a thread in registers (ITEMS *
+// 1024 blocks at most); 0: the keys are read again for each step.
 template <int ITEMS>
 __global__ void __launch_bounds__(kTopThreads) k_cache_top(const SelectParams p) {
-  __shared__ int s_count[2][32];
-  __shared__ uint32_t s_low[32], s_high[32];
+  __shared__ TopShared sm;
   const int row = blockIdx.x / p.c.hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   int seq, have;
-  if (!row_place(p.c, row, seq, have)) return;
+  const bool live = row_place(p.c, row, seq, have);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!live) return;
   int32_t* out = p.out + static_cast<size_t>(blockIdx.x) * p.count;
   if (have <= p.count) {
     for (int i = threadIdx.x; i < p.count; i += kTopThreads) out[i] = i < have ? i : -1;
     return;
   }
   const uint32_t* keys = p.keys + static_cast<size_t>(blockIdx.x) * p.c.max_pages;
-  // a warp has a run of `items` * 32 keys
-  const int items = (have + kTopThreads - 1) / kTopThreads;
+  const int items = (have + kTopThreads - 1) / kTopThreads;  // a warp has a run of items * 32 keys
   const int base = warp * items * 32 + lane;
-  uint32_t key[ITEMS ? ITEMS : 1];
+  const int forced = forced_in(p, have, 0, have);
+  auto has = [&](int i) { return i < items && base + i * 32 < have; };
+  auto emit = [&](int at, int i) { out[at] = base + i * 32; };
   if constexpr (ITEMS > 0) {
+    uint32_t key[ITEMS];
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) key[i] = i < items && base + i * 32 < have ? __ldcg(keys + base + i * 32) : 0u;
-  }
-  // key i of this thread; `in` tells whether there is one
-  auto at = [&](int i) { return __ldcg(keys + base + i * 32); };
-
-  uint32_t low = 0xffffffffu, high = 0;
-  if constexpr (ITEMS > 0) {
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      if (i < items && base + i * 32 < have) {
-        low = min(low, key[i]);
-        high = max(high, key[i]);
-      }
-    }
+    for (int i = 0; i < ITEMS; ++i) key[i] = has(i) ? __ldcg(keys + base + i * 32) : 0u;
+    choose(sm, ITEMS, p.count, forced, [&](int i) { return key[i]; }, has, emit);
   } else {
-    for (int i = 0; i < items && base + i * 32 < have; ++i) {
-      low = min(low, at(i));
-      high = max(high, at(i));
-    }
+    choose(sm, items, p.count, forced, [&](int i) { return has(i) ? __ldcg(keys + base + i * 32) : 0u; }, has, emit);
   }
-  low = __reduce_min_sync(0xffffffffu, low);
-  high = __reduce_max_sync(0xffffffffu, high);
-  if (lane == 0) {
-    s_low[warp] = low;
-    s_high[warp] = high;
-  }
-  __syncthreads();
-  low = __reduce_min_sync(0xffffffffu, s_low[lane]);
-  high = __reduce_max_sync(0xffffffffu, s_high[lane]);
+}
 
-  // the largest x with at least `count` keys >= x: between low (all of them) and high
-  int turn = 0;
-  while (low < high) {
-    const uint32_t mid = low + ((high - low) >> 1) + ((high - low) & 1);
-    int n = 0;
-    if constexpr (ITEMS > 0) {
+// The same for many blocks: a cluster of 8 CTAs for each (row, kv head).  Each
+// chooses `count` of its eighth, into the shared memory of the first, which
+// chooses among those: a step of the search then has 4 keys of a thread to
+// count instead of 32, and no CTA waits for another during it.
+constexpr int kTopCtas = 8;
+constexpr int kTopMost = 512;  // largest count
+__global__ void __cluster_dims__(kTopCtas, 1, 1) __launch_bounds__(kTopThreads) k_cache_top_cluster(const SelectParams p) {
+  namespace cg = cooperative_groups;
+  constexpr int kItems = 4;
+  __shared__ TopShared sm;
+  __shared__ uint32_t s_key[kTopCtas * kTopMost];
+  __shared__ int s_block[kTopCtas * kTopMost];
+  __shared__ int s_n[kTopCtas];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank()), unit = blockIdx.x / kTopCtas;
+  const int row = unit / p.c.hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int seq, have;
+  const bool live = row_place(p.c, row, seq, have);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!live) return;  // the whole cluster
+  int32_t* out = p.out + static_cast<size_t>(unit) * p.count;
+  if (have <= p.count) {
+    if (rank == 0)
+      for (int i = threadIdx.x; i < p.count; i += kTopThreads) out[i] = i < have ? i : -1;
+    return;
+  }
+  const uint32_t* keys = p.keys + static_cast<size_t>(unit) * p.c.max_pages;
+  const int each = (have + kTopCtas - 1) / kTopCtas;  // at most kItems * kTopThreads
+  const int from = min(have, rank * each), to = min(have, from + each), n = to - from;
+  const int items = (n + kTopThreads - 1) / kTopThreads;
+  const int base = from + warp * items * 32 + lane;
+  uint32_t key[kItems];
+  auto has = [&](int i) { return i < items && base + i * 32 < to; };
 #pragma unroll
-      for (int i = 0; i < ITEMS; ++i) n += key[i] >= mid;  // mid > low >= 0: padding (0) never counts
-    } else {
-      for (int i = 0; i < items && base + i * 32 < have; ++i) n += at(i) >= mid;
-    }
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) s_count[turn][warp] = n;
-    __syncthreads();
-    n = __reduce_add_sync(0xffffffffu, s_count[turn][lane]);
-    turn ^= 1;
-    if (n >= p.count) low = mid;
-    else high = mid - 1;
-  }
-
-  // keys above it are chosen, and of those equal to it the first ones
-  int above = 0, equal = 0;
-  auto count_at = [&](int i, uint32_t k) {
-    const bool in = i < items && base + i * 32 < have;
-    above += __popc(__ballot_sync(0xffffffffu, in && k > low));
-    equal += __popc(__ballot_sync(0xffffffffu, in && k == low));
+  for (int i = 0; i < kItems; ++i) key[i] = has(i) ? __ldcg(keys + base + i * 32) : 0u;
+  uint32_t* to_key = cluster.map_shared_rank(s_key, 0) + rank * kTopMost;
+  int* to_block = cluster.map_shared_rank(s_block, 0) + rank * kTopMost;
+  auto pass_on = [&](int at, int i) {
+    to_key[at] = key[i];
+    to_block[at] = base + i * 32;
   };
-  if constexpr (ITEMS > 0) {
+  cluster.sync();  // the first CTA has begun
+  if (n <= p.count) {
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) count_at(i, key[i]);
+    for (int i = 0; i < kItems; ++i)
+      if (has(i)) pass_on(base + i * 32 - from, i);
   } else {
-    for (int i = 0; i < items; ++i) count_at(i, base + i * 32 < have ? at(i) : 0u);
+    choose(sm, kItems, p.count, forced_in(p, have, from, to), [&](int i) { return key[i]; }, has, pass_on);
   }
-  __syncthreads();  // the search's last counts have been read
-  if (lane == 0) {
-    s_count[0][warp] = above;
-    s_count[1][warp] = equal;
-  }
-  __syncthreads();
-  const int a = s_count[0][lane], e = s_count[1][lane];
-  const int total_above = __reduce_add_sync(0xffffffffu, a);
-  int before_above = __reduce_add_sync(0xffffffffu, lane < warp ? a : 0);
-  int before_equal = __reduce_add_sync(0xffffffffu, lane < warp ? e : 0);
-  const int take = p.count - total_above;  // of the equal ones
-  const unsigned under = (1u << lane) - 1;
-  auto place = [&](int i, uint32_t k) {
-    const bool in = i < items && base + i * 32 < have;
-    const unsigned ma = __ballot_sync(0xffffffffu, in && k > low), me = __ballot_sync(0xffffffffu, in && k == low);
-    const int ra = before_above + __popc(ma & under), re = before_equal + __popc(me & under);
-    if (in && (k > low || (k == low && re < take))) out[ra + min(re, take)] = base + i * 32;
-    before_above += __popc(ma);
-    before_equal += __popc(me);
-  };
-  if constexpr (ITEMS > 0) {
+  if (threadIdx.x == 0) cluster.map_shared_rank(s_n, 0)[rank] = min(n, p.count);
+  cluster.sync();
+  if (rank != 0) return;
+  // slots of kTopMost for each CTA, in the order of the blocks
+  const int at = warp * (kItems * 32) + lane;
+  auto chosen = [&](int i) { return (at + i * 32) % kTopMost < s_n[(at + i * 32) / kTopMost]; };
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) place(i, key[i]);
-  } else {
-    for (int i = 0; i < items; ++i) place(i, base + i * 32 < have ? at(i) : 0u);
-  }
+  for (int i = 0; i < kItems; ++i) key[i] = chosen(i) ? s_key[at + i * 32] : 0u;
+  choose(sm, kItems, p.count, forced_in(p, have, 0, have), [&](int i) { return key[i]; }, chosen,
+         [&](int place, int i) { out[place] = s_block[at + i * 32]; });
 }
 
 hdp_status_t select_bytes(const CacheView& c, size_t* bytes) {
@@ -331,7 +402,7 @@ extern "C" hdp_status_t hdp_cache_select(const hdp_cache_t* cache, const int32_t
   else k_cache_scores<64><<<units * chunks, kScoreThreads, 0, st>>>(p, chunks);
   note_launch();
   HDP_CUDA_TRY(cudaGetLastError());
-  cudaLaunchAttribute attr;
+  cudaLaunchAttribute attr;  // the launch overlaps the scores; the kernel waits for them
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
@@ -340,9 +411,17 @@ extern "C" hdp_status_t hdp_cache_select(const hdp_cache_t* cache, const int32_t
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cache->max_pages <= 4 * kTopThreads) HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_cache_top<4>, p));
-  else if (cache->max_pages <= 32 * kTopThreads) HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_cache_top<32>, p));
-  else HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_cache_top<0>, p));
+  // One CTA up to 4,096 blocks, where its search counts 4 keys a thread; a
+  // cluster beyond (32,768 blocks, 8 heads: 37.6 us with one CTA of 32 keys a
+  // thread), as long as its candidates fit and its grid is in range.
+  if (cache->max_pages <= 4 * kTopThreads) {
+    HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_cache_top<4>, p));
+  } else if (cache->max_pages <= 32 * kTopThreads && count <= kTopMost && units <= 2147483647u / kTopCtas) {
+    cfg.gridDim = dim3(units * kTopCtas);
+    HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_cache_top_cluster, p));
+  } else {
+    HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_cache_top<0>, p));
+  }
   note_launch();
   return HDP_OK;
 }
