@@ -1,8 +1,9 @@
 // Writing rows into the 8-bit cache and reading them back.
 //
-// One CTA has one (block of 64 tokens, kv head): 128 threads hold its new K and
-// V rows in registers (16 bytes = 8 channels of a row each, d / 16 rows), so
-// the largest magnitude, the scale, the bounds and the codes come from one read.
+// One CTA has the new rows of one (block of 64 tokens, kv head): 128 threads hold
+// its K, then its V rows in registers (16 bytes = 8 channels of a row each, d / 16
+// rows), so the largest magnitude, the scale, the bounds and the codes come from
+// one read.
 //
 // The scale is 2^e with the smallest e that fits the largest magnitude ever
 // written, so x / s is a shift of the exponent and the code is the only
@@ -71,7 +72,8 @@ constexpr int kThreads = 128;
 template <int FMT>
 __device__ __forceinline__ uint32_t code_pair(float a, float b) {
   if constexpr (FMT == HDP_CACHE_INT8) {
-    return (static_cast<uint32_t>(__float2int_rn(a)) & 0xffu) | ((static_cast<uint32_t>(__float2int_rn(b)) & 0xffu) << 8);
+    // 1.5 * 2^23 + x: the sum is rounded to a whole number, ties to even, and its low byte is the code
+    return __byte_perm(__float_as_uint(a + 12582912.f), __float_as_uint(b + 12582912.f), 0x0040) & 0xffffu;
   } else {
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   }
@@ -80,8 +82,9 @@ __device__ __forceinline__ uint32_t code_pair(float a, float b) {
 template <int FMT>
 __device__ __forceinline__ float2 value_pair(uint32_t two) {
   if constexpr (FMT == HDP_CACHE_INT8) {
-    return make_float2(static_cast<float>(static_cast<int8_t>(two & 0xff)),
-                       static_cast<float>(static_cast<int8_t>((two >> 8) & 0xff)));
+    const uint32_t u = two ^ 0x8080u;  // code + 128; 0x4b000000 | u is 2^23 + u
+    return make_float2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)) - 8388736.f,
+                       __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441)) - 8388736.f);
   } else {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xffff), __NV_E4M3);
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
@@ -104,6 +107,7 @@ __device__ __forceinline__ int scale_exponent(uint32_t abs_bits) {
   return max(e, -126);
 }
 
+__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); }
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
@@ -117,23 +121,23 @@ __device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, u
   t[3] = __byte_perm(ab1, cd1, 0x7632);
 }
 
-// Where a thread's rows and channels lie.  8 lanes have 64 channels of a row, and
-// pass p of a thread is token
-//   d = 128: 8 p + 2 c + e         (e = lane / 8 % 2, c = 2 (warp % 2) + lane / 16; 64 channels for each two warps)
-//   d =  64: 16 p + 8 h + 2 c + e  (e = lane / 8 % 2, h = lane / 16, c = warp)
-// of the block, so 2 or 4 lanes have exactly the tokens of V chunk c, and with
-// d = 128 the next two those of the chunk beside it: whole 32-byte sectors.
-template <int D>
+// Where a thread's rows and channels lie: pass p of a thread has 8 channels of
+// token
+//   d = 128: 8 p + 2 c + e
+//   d =  64: 16 p + 8 h + 2 c + e
+// of the block, so 2 or 4 lanes have exactly the tokens of V chunk c.  With
+// d = 128, either 16 lanes have a row (WIDE, c = warp: whole rows), or 8 have
+// half of one and the next lanes the chunk beside it (whole 32-byte sectors of V).
+template <int D, bool WIDE>
 struct Place {
-  static constexpr int kPasses = D / 16;
-  static constexpr int kLanes = 8;  // lanes of a row
+  static constexpr int kLanes = D == 128 && WIDE ? 16 : 8;  // lanes of a row
   int c, e, h, ch;
   __device__ __forceinline__ Place() {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    e = (lane >> 3) & 1;
+    e = lane / kLanes & 1;
     h = D == 64 ? lane >> 4 : 0;
-    c = D == 64 ? warp : 2 * (warp & 1) + (lane >> 4);
-    ch = (lane & 7) * 8 + (D == 64 ? 0 : (warp >> 1) * 64);
+    c = D == 64 || WIDE ? warp : 2 * (warp & 1) + (lane >> 4);
+    ch = lane % kLanes * 8 + (D == 64 || WIDE ? 0 : (warp >> 1) * 64);
   }
   __device__ __forceinline__ int token(int p) const { return D == 128 ? 8 * p + 2 * c + e : 16 * p + 8 * h + 2 * c + e; }
   // Byte of token(p) inside a channel's 64 bytes of V.
@@ -145,15 +149,15 @@ struct Place {
 
 // Row-wise codes w[p][2] (8 channels of token(p)) to whole 16-byte chunks of
 // channels (out[x] belongs to channel v_channel(x)) and back.
-template <int D>
-__device__ __forceinline__ void to_chunks(const Place<D>& pl, const uint32_t (&w)[Place<D>::kPasses][2],
+template <int D, bool W>
+__device__ __forceinline__ void to_chunks(const Place<D, W>& pl, const uint32_t (&w)[D / 16][2],
                                           uint32_t (&out)[D / 32][4]) {
-  constexpr int P = Place<D>::kPasses;
+  constexpr int P = D / 16;
   uint32_t lo[P], hi[P];  // of this lane's four channels: tokens with e = 0 and e = 1
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const uint32_t mine = pl.e ? w[p][1] : w[p][0];
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, pl.e ? w[p][0] : w[p][1], Place<D>::kLanes);
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, pl.e ? w[p][0] : w[p][1], Place<D, W>::kLanes);
     lo[p] = pl.e ? got : mine;
     hi[p] = pl.e ? mine : got;
   }
@@ -174,15 +178,15 @@ __device__ __forceinline__ void to_chunks(const Place<D>& pl, const uint32_t (&w
   }
 }
 
-template <int D>
-__device__ __forceinline__ int v_channel(const Place<D>& pl, int x) {
+template <int D, bool W>
+__device__ __forceinline__ int v_channel(const Place<D, W>& pl, int x) {
   return pl.ch + 4 * pl.e + (D == 64 ? 2 * pl.h : 0) + x;
 }
 
-template <int D>
-__device__ __forceinline__ void from_chunks(const Place<D>& pl, const uint32_t (&in)[D / 32][4],
-                                            uint32_t (&w)[Place<D>::kPasses][2]) {
-  constexpr int P = Place<D>::kPasses;
+template <int D, bool W>
+__device__ __forceinline__ void from_chunks(const Place<D, W>& pl, const uint32_t (&in)[D / 32][4],
+                                            uint32_t (&w)[D / 16][2]) {
+  constexpr int P = D / 16;
   uint32_t lo[P], hi[P];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -204,7 +208,7 @@ __device__ __forceinline__ void from_chunks(const Place<D>& pl, const uint32_t (
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const uint32_t mine = pl.e ? hi[p] : lo[p];
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, pl.e ? lo[p] : hi[p], Place<D>::kLanes);
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, pl.e ? lo[p] : hi[p], Place<D, W>::kLanes);
     w[p][0] = pl.e ? got : mine;
     w[p][1] = pl.e ? mine : got;
   }
@@ -250,179 +254,157 @@ __device__ __forceinline__ bool touched_block(const CacheView& c, int slot, Touc
   return true;
 }
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads) k_cache_append(CacheView c, const uint4* __restrict__ k,
-                                                           const uint4* __restrict__ v) {
-  constexpr int P = Place<D>::kPasses;
-  __shared__ uint32_t s_amax[2][4];
-  __shared__ float s_bound[4][2][D];
-  Touched t;
-  if (!touched_block(c, blockIdx.x, t)) return;
-  const int head = blockIdx.y;
-  const int page = page_of(c, t.seq, t.block);
-  if (page < 0) return;
-  const Place<D> pl;
+// The new K rows (W = 0) or V rows (W = 1) of one (block, kv head).
+template <int D, int FMT, int W>
+__device__ __forceinline__ void append_rows(const CacheView& c, const Touched& t, int page, int head,
+                                            const uint4* __restrict__ rows) {
+  constexpr int P = D / 16;
+  using Pl = Place<D, W == 0>;
+  __shared__ uint32_t s_amax[4];
+  __shared__ float s_bound[W == 0 ? 4 : 1][2][D];
+  const Pl pl;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const size_t ph = static_cast<size_t>(page) * c.hkv + head;
-
-  uint4 x[2][P];
+  uint4 x[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const int r = pl.token(p) - t.first;
     const size_t at = ((static_cast<size_t>(t.row) + r) * c.hkv + head) * (D / 8) + pl.ch / 8;
-    const bool in = r >= 0 && r < t.count;
-    x[0][p] = in ? __ldg(k + at) : make_uint4(0, 0, 0, 0);
-    x[1][p] = in ? __ldg(v + at) : make_uint4(0, 0, 0, 0);
+    x[p] = r >= 0 && r < t.count ? __ldg(rows + at) : make_uint4(0, 0, 0, 0);
   }
-  const float2 old = t.fresh ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(c.scales + 2 * ph);
+  const float before = t.fresh ? 0.f : c.scales[2 * ph + W];
 
   // Largest magnitudes, as bf16 bits: their order is the values' order, with
   // infinity and NaN (>= 0x7f80) on top.
+  uint32_t m = 0;
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    uint32_t m = 0;
+  for (int p = 0; p < P; ++p)
+    m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[p].x & 0x7fff7fffu, x[p].y & 0x7fff7fffu),
+                             __vmaxu2(x[p].z & 0x7fff7fffu, x[p].w & 0x7fff7fffu)));
+  uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+  if (lane == 0) s_amax[warp] = top;
+  if constexpr (W == 0) {  // channel-wise minimum and maximum
+    const __nv_bfloat162 inf = __halves2bfloat162(__ushort_as_bfloat16(0x7f80), __ushort_as_bfloat16(0x7f80));
+    __nv_bfloat162 lo[4] = {inf, inf, inf, inf}, hi[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) hi[i] = __hneg2(inf);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[w][p].x & 0x7fff7fffu, x[w][p].y & 0x7fff7fffu),
-                               __vmaxu2(x[w][p].z & 0x7fff7fffu, x[w][p].w & 0x7fff7fffu)));
-    }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-    if (lane == 0) s_amax[w][warp] = top;
-  }
-  // Channel-wise minimum and maximum of the new K rows.
-  float lo[8], hi[8];
+      const int r = pl.token(p) - t.first;
+      if (r >= 0 && r < t.count) {
+        const uint32_t q[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo[i] = __int_as_float(0x7f800000);
-    hi[i] = -lo[i];
-  }
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int r = pl.token(p) - t.first;
-    if (r >= 0 && r < t.count) {
-      const uint32_t q[4] = {x[0][p].x, x[0][p].y, x[0][p].z, x[0][p].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo[2 * i] = fminf(lo[2 * i], bf_lo(q[i]));
-        hi[2 * i] = fmaxf(hi[2 * i], bf_lo(q[i]));
-        lo[2 * i + 1] = fminf(lo[2 * i + 1], bf_hi(q[i]));
-        hi[2 * i + 1] = fmaxf(hi[2 * i + 1], bf_hi(q[i]));
+        for (int i = 0; i < 4; ++i) {
+          lo[i] = __hmin2(lo[i], as_bf2(q[i]));
+          hi[i] = __hmax2(hi[i], as_bf2(q[i]));
+        }
       }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-    for (int o = Place<D>::kLanes; o < 32; o *= 2) {
-      lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
-      hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+      for (int o = Pl::kLanes; o < 32; o *= 2) {
+        lo[i] = __hmin2(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+        hi[i] = __hmax2(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+      }
     }
-  }
-  if (lane < Place<D>::kLanes) {
+    if (lane < Pl::kLanes) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      s_bound[warp][0][pl.ch + i] = lo[i];
-      s_bound[warp][1][pl.ch + i] = hi[i];
+      for (int i = 0; i < 4; ++i) {
+        *reinterpret_cast<float2*>(&s_bound[warp][0][pl.ch + 2 * i]) = __bfloat1622float2(lo[i]);
+        *reinterpret_cast<float2*>(&s_bound[warp][1][pl.ch + 2 * i]) = __bfloat1622float2(hi[i]);
+      }
     }
   }
   __syncthreads();
 
-  float scale[2], inv[2], ratio[2];
-  bool grown[2];
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const uint32_t top = max(max(s_amax[w][0], s_amax[w][1]), max(s_amax[w][2], s_amax[w][3]));
-    const float before = w ? old.y : old.x;
-    const int e = scale_exponent<FMT>(top);
-    const bool lost = top >= 0x7f80u || (!t.fresh && before != before);
-    const float need = lost ? 0.f : pow2i(e);
-    scale[w] = lost ? __int_as_float(0x7fc00000) : fmaxf(need, before);
-    // 1 / scale: the scale is a power of two, so its exponent changes sign
-    inv[w] = lost ? 1.f : __int_as_float((254 << 23) - __float_as_int(scale[w]));
-    grown[w] = !t.fresh && !lost && scale[w] != before;
-    ratio[w] = grown[w] ? before * inv[w] : 1.f;
-  }
+  top = max(max(s_amax[0], s_amax[1]), max(s_amax[2], s_amax[3]));
+  const bool lost = top >= 0x7f80u || before != before;
+  const float scale = lost ? __int_as_float(0x7fc00000) : fmaxf(pow2i(scale_exponent<FMT>(top)), before);
+  // 1 / scale: the scale is a power of two, so its exponent changes sign
+  const float inv = lost ? 1.f : __int_as_float((254 << 23) - __float_as_int(scale));
+  const bool grown = !t.fresh && !lost && scale != before;
+  const float ratio = grown ? before * inv : 1.f;
 
-  uint8_t* kb = c.k + ph * (kBlock * D);
-  uint8_t* vb = c.v + ph * (kBlock * D);
+  uint8_t* block = (W ? c.v : c.k) + ph * (kBlock * D);
   // A larger scale: the codes that are there are rounded to it (every byte of
   // the block is one, written or zero).
-  if (grown[0] || grown[1]) {
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      if (!grown[w]) continue;
-      uint4* b = reinterpret_cast<uint4*>(w ? vb : kb);
-      for (int i = threadIdx.x; i < kBlock * D / 16; i += kThreads) {
-        uint4 y = b[i];
-        y.x = rescale4<FMT>(y.x, ratio[w]);
-        y.y = rescale4<FMT>(y.y, ratio[w]);
-        y.z = rescale4<FMT>(y.z, ratio[w]);
-        y.w = rescale4<FMT>(y.w, ratio[w]);
-        b[i] = y;
-      }
+  if (grown) {
+    uint4* b = reinterpret_cast<uint4*>(block);
+    for (int i = threadIdx.x; i < kBlock * D / 16; i += kThreads) {
+      uint4 y = b[i];
+      y.x = rescale4<FMT>(y.x, ratio);
+      y.y = rescale4<FMT>(y.y, ratio);
+      y.z = rescale4<FMT>(y.z, ratio);
+      y.w = rescale4<FMT>(y.w, ratio);
+      b[i] = y;
     }
     __syncthreads();  // the new rows go over them
   }
 
   uint32_t code[P][2];
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
+  for (int p = 0; p < P; ++p) {
+    const uint4 y = x[p];
+    code[p][0] = code_pair<FMT>(bf_lo(y.x) * inv, bf_hi(y.x) * inv) | (code_pair<FMT>(bf_lo(y.y) * inv, bf_hi(y.y) * inv) << 16);
+    code[p][1] = code_pair<FMT>(bf_lo(y.z) * inv, bf_hi(y.z) * inv) | (code_pair<FMT>(bf_lo(y.w) * inv, bf_hi(y.w) * inv) << 16);
+  }
+  if constexpr (W == 0) {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const float s = inv[w];
-      const uint4 y = x[w][p];
-      code[p][0] = code_pair<FMT>(bf_lo(y.x) * s, bf_hi(y.x) * s) | (code_pair<FMT>(bf_lo(y.y) * s, bf_hi(y.y) * s) << 16);
-      code[p][1] = code_pair<FMT>(bf_lo(y.z) * s, bf_hi(y.z) * s) | (code_pair<FMT>(bf_lo(y.w) * s, bf_hi(y.w) * s) << 16);
+      const int r = pl.token(p) - t.first;
+      if (t.fresh || (r >= 0 && r < t.count))
+        *reinterpret_cast<uint2*>(block + pl.token(p) * D + pl.ch) = make_uint2(code[p][0], code[p][1]);
     }
-    if (w == 0) {
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int r = pl.token(p) - t.first;
-        if (t.fresh || (r >= 0 && r < t.count))
-          *reinterpret_cast<uint2*>(kb + pl.token(p) * D + pl.ch) = make_uint2(code[p][0], code[p][1]);
+    // Bounds, in whole units (one K scale, four for e4m3): rounding outwards
+    // nests, so a change of unit loses nothing but the finer grid.
+    if (threadIdx.x < D) {
+      const int i = threadIdx.x;
+      const float unit = FMT == HDP_CACHE_INT8 ? inv : inv * 0.25f;
+      float a = fminf(fminf(s_bound[0][0][i], s_bound[1][0][i]), fminf(s_bound[2][0][i], s_bound[3][0][i]));
+      float b = fmaxf(fmaxf(s_bound[0][1][i], s_bound[1][1][i]), fmaxf(s_bound[2][1][i], s_bound[3][1][i]));
+      a = floorf(a * unit);
+      b = ceilf(b * unit);
+      int8_t* out = c.bounds + ph * (2 * D) + i;
+      if (!t.fresh) {
+        a = fminf(a, floorf(static_cast<float>(out[0]) * ratio));
+        b = fmaxf(b, ceilf(static_cast<float>(out[D]) * ratio));
       }
-    } else if (t.fresh) {
-      uint32_t chunk[D / 32][4];
-      to_chunks<D>(pl, code, chunk);
+      out[0] = static_cast<int8_t>(fminf(fmaxf(a, -127.f), 127.f));
+      out[D] = static_cast<int8_t>(fminf(fmaxf(b, -127.f), 127.f));
+    }
+  } else if (t.fresh) {
+    uint32_t chunk[D / 32][4];
+    to_chunks(pl, code, chunk);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-        *reinterpret_cast<uint4*>(vb + v_channel<D>(pl, i) * kBlock + pl.c * 16) =
-            make_uint4(chunk[i][0], chunk[i][1], chunk[i][2], chunk[i][3]);
-    } else {
+    for (int i = 0; i < D / 32; ++i)
+      *reinterpret_cast<uint4*>(block + v_channel(pl, i) * kBlock + pl.c * 16) =
+          make_uint4(chunk[i][0], chunk[i][1], chunk[i][2], chunk[i][3]);
+  } else {
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int r = pl.token(p) - t.first;
-        if (r >= 0 && r < t.count) {
+    for (int p = 0; p < P; ++p) {
+      const int r = pl.token(p) - t.first;
+      if (r >= 0 && r < t.count) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            vb[(pl.ch + i) * kBlock + pl.v_byte(p)] = static_cast<uint8_t>(code[p][i >> 2] >> (8 * (i & 3)));
-        }
+        for (int i = 0; i < 8; ++i)
+          block[(pl.ch + i) * kBlock + pl.v_byte(p)] = static_cast<uint8_t>(code[p][i >> 2] >> (8 * (i & 3)));
       }
     }
   }
+  if (threadIdx.x == 0) c.scales[2 * ph + W] = scale;
+}
 
-  // Bounds, in whole units (one K scale, four for e4m3): rounding outwards
-  // nests, so a change of unit loses nothing but the finer grid.
-  if (threadIdx.x < D) {
-    const int i = threadIdx.x;
-    const float unit = FMT == HDP_CACHE_INT8 ? inv[0] : inv[0] * 0.25f;
-    const int w0 = D == 64 ? 0 : i / 64 * 2;  // the warps that have the channel
-    float a = fminf(s_bound[w0][0][i], s_bound[w0 + 1][0][i]), b = fmaxf(s_bound[w0][1][i], s_bound[w0 + 1][1][i]);
-    if (D == 64) {
-      a = fminf(a, fminf(s_bound[2][0][i], s_bound[3][0][i]));
-      b = fmaxf(b, fmaxf(s_bound[2][1][i], s_bound[3][1][i]));
-    }
-    a = floorf(a * unit);
-    b = ceilf(b * unit);
-    int8_t* out = c.bounds + ph * (2 * D) + i;
-    if (!t.fresh) {
-      a = fminf(a, floorf(static_cast<float>(out[0]) * ratio[0]));
-      b = fmaxf(b, ceilf(static_cast<float>(out[D]) * ratio[0]));
-    }
-    out[0] = static_cast<int8_t>(fminf(fmaxf(a, -127.f), 127.f));
-    out[D] = static_cast<int8_t>(fminf(fmaxf(b, -127.f), 127.f));
-  }
-  if (threadIdx.x == 0) *reinterpret_cast<float2*>(c.scales + 2 * ph) = make_float2(scale[0], scale[1]);
+// K, then V: one of them in registers at a time leaves room for 7 CTAs an SM (83K
+// prompt tokens, 8 heads of 128, int8: 85 us; both at once 93, a CTA for each 91).
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads) k_cache_append(CacheView c, const uint4* __restrict__ k,
+                                                           const uint4* __restrict__ v) {
+  Touched t;
+  if (!touched_block(c, blockIdx.x, t)) return;
+  const int page = page_of(c, t.seq, t.block);
+  if (page < 0) return;
+  append_rows<D, FMT, 0>(c, t, page, blockIdx.y, k);
+  append_rows<D, FMT, 1>(c, t, page, blockIdx.y, v);
 }
 
 // One token for each sequence.
@@ -528,7 +510,7 @@ __device__ __forceinline__ uint32_t bf16_pair(uint32_t two, float s) {
 
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads) k_cache_read(CacheView c, uint4* __restrict__ k, uint4* __restrict__ v) {
-  constexpr int P = Place<D>::kPasses;
+  constexpr int P = D / 16;
   Touched t;
   const bool any = touched_block(c, blockIdx.x, t);
   const int head = blockIdx.y;
@@ -538,7 +520,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_read(CacheView c, uint4* __r
   }
   if (!any) return;
   const int page = page_of(c, t.seq, t.block);
-  const Place<D> pl;
+  const Place<D, true> pl;
   uint32_t code[2][P][2] = {};
   float2 scale = make_float2(0.f, 0.f);
   if (page >= 0) {
@@ -548,7 +530,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_read(CacheView c, uint4* __r
     uint32_t chunk[D / 32][4];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const uint4 y = __ldg(reinterpret_cast<const uint4*>(vb + v_channel<D>(pl, i) * kBlock + pl.c * 16));
+      const uint4 y = __ldg(reinterpret_cast<const uint4*>(vb + v_channel(pl, i) * kBlock + pl.c * 16));
       chunk[i][0] = y.x;
       chunk[i][1] = y.y;
       chunk[i][2] = y.z;
@@ -564,7 +546,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_read(CacheView c, uint4* __r
       }
     }
     scale = __ldg(reinterpret_cast<const float2*>(c.scales + 2 * ph));
-    from_chunks<D>(pl, chunk, code[1]);
+    from_chunks(pl, chunk, code[1]);
   }
 #pragma unroll
   for (int w = 0; w < 2; ++w) {

@@ -63,7 +63,7 @@ __device__ __forceinline__ int dp2a_hi(int a, int b, int c) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kScoreThreads) k_cache_scores(const SelectParams p, int chunks) {
+__global__ void __launch_bounds__(kScoreThreads, 4) k_cache_scores(const SelectParams p, int chunks) {
   constexpr int kLanes = D / 8;  // of a block: D / 16 for each extreme
   __shared__ __align__(16) int16_t s_q[2][D];  // sums of min(c, 0) and of max(c, 0)
   __shared__ uint32_t s_top[kScoreThreads / 32];
@@ -80,13 +80,17 @@ __global__ void __launch_bounds__(kScoreThreads) k_cache_scores(const SelectPara
   const int page = b < have ? page_of(p.c, seq, b) : -1;
   const size_t ph = static_cast<size_t>(max(page, 0)) * p.c.hkv + head;
   const int part = lane % kLanes;  // 16 channels of one extreme
-  uint4 x[kLanes];
+  constexpr int kAhead = 8;  // blocks of a group of lanes in flight; lane (group, i) keeps block i's sum
+  uint4 x[kAhead];
+  auto fetch = [&](int first) {
 #pragma unroll
-  for (int i = 0; i < kLanes; ++i) {  // block i of this group of lanes: lane (group, i) keeps its sum
-    const int pg = __shfl_sync(0xffffffffu, page, (lane & ~(kLanes - 1)) + i);
-    x[i] = pg >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.c.bounds + (static_cast<size_t>(pg) * p.c.hkv + head) * (2 * D)) + part)
-                   : make_uint4(0, 0, 0, 0);
-  }
+    for (int i = 0; i < kAhead; ++i) {
+      const int pg = __shfl_sync(0xffffffffu, page, (lane & ~(kLanes - 1)) + first + i);
+      x[i] = pg >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.c.bounds + (static_cast<size_t>(pg) * p.c.hkv + head) * (2 * D)) + part)
+                     : make_uint4(0, 0, 0, 0);
+    }
+  };
+  fetch(0);
   const float scale = page >= 0 ? __ldg(p.c.scales + 2 * ph) : 0.f;
 
   const __nv_bfloat16* q = p.q + (static_cast<size_t>(row) * p.hq + head * p.g) * D;
@@ -136,7 +140,10 @@ __global__ void __launch_bounds__(kScoreThreads) k_cache_scores(const SelectPara
   }
   int mine = 0;
 #pragma unroll
-  for (int i = 0; i < kLanes; ++i) {
+  for (int first = 0; first < kLanes; first += kAhead) {
+    if (first) fetch(first);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
     int u = dp2a_lo(qr[0], x[i].x, 0);
     u = dp2a_hi(qr[1], x[i].x, u);
     u = dp2a_lo(qr[2], x[i].y, u);
@@ -147,7 +154,8 @@ __global__ void __launch_bounds__(kScoreThreads) k_cache_scores(const SelectPara
     u = dp2a_hi(qr[7], x[i].w, u);
 #pragma unroll
     for (int s = 1; s < kLanes; s *= 2) u += __shfl_xor_sync(0xffffffffu, u, s);
-    if (part == i) mine = u;
+    if (part == first + i) mine = u;
+  }
   }
   if (b < have) {
     uint32_t key = scale == scale ? key_of(static_cast<float>(mine) * scale) : kNanKey;
@@ -163,10 +171,10 @@ __global__ void __launch_bounds__(kScoreThreads) k_cache_scores(const SelectPara
 // its warp with a smaller (i, lane).  key_at(i) is its key, has(i) whether there
 // is one; at least `count` of them are there.
 struct TopShared {
-  int count[2][32];
+  int4 count[2][32];
   uint32_t low[32], high[32];
 };
-template <class K, class H, class E>
+template <bool PACK, class K, class H, class E>
 __device__ __forceinline__ void choose(TopShared& sm, int items, int count, int forced, K key_at, H has, E emit) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t low = 0xffffffffu, high = 0;
@@ -191,22 +199,53 @@ __device__ __forceinline__ void choose(TopShared& sm, int items, int count, int 
   // and the largest key that is not forced, unless the forced ones are enough
   if (forced >= count) low = high = kForced;
   int turn = 0;
-  while (low < high) {
-    const uint32_t mid = low + ((high - low) >> 1) + ((high - low) & 1);
-    int n = 0;
+  bool found = false;
+  while (low < high && !found) {
+    // three cuts at once: a step costs its barrier and reductions more than its counting
+    const uint32_t d = high - low, q = d >> 2;
+    const uint32_t m2 = low + (d >> 1) + (d & 1), m1 = max(low + q, low + 1), m3 = max(m2, high - q);
+    int n12 = 0, n3 = 0;  // counts of a CTA's keys fit 16 bits (PACK), so two share a word
+    int n2 = 0;
 #pragma unroll
-    for (int i = 0; i < items; ++i) n += has(i) && key_at(i) >= mid;
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) sm.count[turn][warp] = n;
-    __syncthreads();
-    n = __reduce_add_sync(0xffffffffu, sm.count[turn][lane]);
-    turn ^= 1;
-    if (n == count) {  // exactly these
-      low = mid;
-      break;
+    for (int i = 0; i < items; ++i) {
+      const uint32_t k = has(i) ? key_at(i) : 0u;  // cuts are above low, so above 0
+      n12 += k >= m1;
+      n2 += k >= m2;
+      n3 += k >= m3;
     }
-    if (n > count) low = mid;
-    else high = mid - 1;
+    if (PACK) {
+      n12 = __reduce_add_sync(0xffffffffu, n12 | n2 << 16);
+    } else {
+      n12 = __reduce_add_sync(0xffffffffu, n12);
+      n2 = __reduce_add_sync(0xffffffffu, n2);
+    }
+    n3 = __reduce_add_sync(0xffffffffu, n3);
+    if (lane == 0) sm.count[turn][warp] = make_int4(n12, n2, n3, 0);
+    __syncthreads();
+    const int4 c = sm.count[turn][lane];
+    turn ^= 1;
+    int c1 = __reduce_add_sync(0xffffffffu, c.x), c2;
+    if (PACK) {
+      c2 = static_cast<int>(static_cast<unsigned>(c1) >> 16);
+      c1 &= 0xffff;
+    } else {
+      c2 = __reduce_add_sync(0xffffffffu, c.y);
+    }
+    const int c3 = __reduce_add_sync(0xffffffffu, c.z);
+    if (c3 >= count) {
+      low = m3;
+      found = c3 == count;  // exactly these
+    } else if (c2 >= count) {
+      low = m2;
+      high = m3 - 1;
+      found = c2 == count;
+    } else if (c1 >= count) {
+      low = m1;
+      high = m2 - 1;
+      found = c1 == count;
+    } else {
+      high = m1 - 1;
+    }
   }
 
   // keys above it are chosen, and of those equal to it the first ones (if the
@@ -220,12 +259,9 @@ __device__ __forceinline__ void choose(TopShared& sm, int items, int count, int 
     equal += __popc(__ballot_sync(0xffffffffu, in && k == low));
   }
   __syncthreads();  // the search's last counts have been read
-  if (lane == 0) {
-    sm.count[0][warp] = above;
-    sm.count[1][warp] = equal;
-  }
+  if (lane == 0) sm.count[0][warp] = make_int4(above, equal, 0, 0);
   __syncthreads();
-  const int a = sm.count[0][lane], e = sm.count[1][lane];
+  const int a = sm.count[0][lane].x, e = sm.count[0][lane].y;
   const int take = count - __reduce_add_sync(0xffffffffu, a);  // of the equal ones
   int before_above = __reduce_add_sync(0xffffffffu, lane < warp ? a : 0);
   int before_equal = __reduce_add_sync(0xffffffffu, lane < warp ? e : 0);
@@ -273,9 +309,9 @@ __global__ void __launch_bounds__(kTopThreads) k_cache_top(const SelectParams p)
     uint32_t key[ITEMS];
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) key[i] = has(i) ? __ldcg(keys + base + i * 32) : 0u;
-    choose(sm, ITEMS, p.count, forced, [&](int i) { return key[i]; }, has, emit);
+    choose<true>(sm, ITEMS, p.count, forced, [&](int i) { return key[i]; }, has, emit);
   } else {
-    choose(sm, items, p.count, forced, [&](int i) { return has(i) ? __ldcg(keys + base + i * 32) : 0u; }, has, emit);
+    choose<false>(sm, items, p.count, forced, [&](int i) { return has(i) ? __ldcg(keys + base + i * 32) : 0u; }, has, emit);
   }
 }
 
@@ -327,7 +363,7 @@ __global__ void __cluster_dims__(kTopCtas, 1, 1) __launch_bounds__(kTopThreads) 
     for (int i = 0; i < kItems; ++i)
       if (has(i)) pass_on(base + i * 32 - from, i);
   } else {
-    choose(sm, kItems, p.count, forced_in(p, have, from, to), [&](int i) { return key[i]; }, has, pass_on);
+    choose<true>(sm, kItems, p.count, forced_in(p, have, from, to), [&](int i) { return key[i]; }, has, pass_on);
   }
   if (threadIdx.x == 0) cluster.map_shared_rank(s_n, 0)[rank] = min(n, p.count);
   cluster.sync();
@@ -337,7 +373,7 @@ __global__ void __cluster_dims__(kTopCtas, 1, 1) __launch_bounds__(kTopThreads) 
   auto chosen = [&](int i) { return (at + i * 32) % kTopMost < s_n[(at + i * 32) / kTopMost]; };
 #pragma unroll
   for (int i = 0; i < kItems; ++i) key[i] = chosen(i) ? s_key[at + i * 32] : 0u;
-  choose(sm, kItems, p.count, forced_in(p, have, 0, have), [&](int i) { return key[i]; }, chosen,
+  choose<true>(sm, kItems, p.count, forced_in(p, have, 0, have), [&](int i) { return key[i]; }, chosen,
          [&](int place, int i) { out[place] = s_block[at + i * 32]; });
 }
 
