@@ -9,6 +9,7 @@ not load the library; the first call does, and fails loudly if it is absent.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 
 from .binding import (  # noqa: F401
@@ -105,18 +106,16 @@ def attention_backward(plan: Plan, q, k, v, o, lse, dout, scale: float | None = 
     return dq, dk, dv
 
 
-_cache_ws_bytes: dict = {}
+_HERE = contextlib.nullcontext()
 
 
 def _pool(stream, cache):
     """The stream whose memory pool a call's tensors come from: what is freed after the call is only given out again in
     that stream's order."""
-    import contextlib
-
+    if stream is None:
+        return _HERE
     import torch
 
-    if stream is None:
-        return contextlib.nullcontext()
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=cache.device)
     return torch.cuda.stream(stream)
@@ -133,13 +132,11 @@ def cache_read(cache: KVCache, page_table, lens, rows: int, cu=None, stream=None
     call on another stream than the current one returns belong to that stream."""
     import torch
 
-    if stream is not None:
-        with _pool(stream, cache):
-            k, v = (torch.empty((rows, cache.hkv, cache.d), dtype=torch.bfloat16, device=cache.device) for _ in "kv")
-    else:
+    s = cache._with(page_table, lens, cu, rows)
+    with _pool(stream, cache):
         k = torch.empty((rows, cache.hkv, cache.d), dtype=torch.bfloat16, device=cache.device)
         v = torch.empty_like(k)
-    hdp_cache_read(cache, page_table, lens, k, v, cu=cu, stream=stream)
+    cache._call("hdp_cache_read", stream, s, None if cu is None else cu.data_ptr(), rows, k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -149,16 +146,14 @@ def cache_select(cache: KVCache, page_table, lens, q, count: int, cu=None, keep_
     bf16 and kv head: int32 [rows][hkv][count], ascending, -1 behind the last."""
     import torch
 
-    rows, hkv = q.shape[0], cache.hkv
-    nbytes = (rows * hkv * page_table.shape[1] * 4 + 255) // 256 * 256  # hdp_cache_select_workspace_bytes
-    if stream is not None:
-        with _pool(stream, cache):
-            blocks = torch.empty((rows, hkv, count), dtype=torch.int32, device=cache.device)
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
-    else:
-        blocks = torch.empty((rows, hkv, count), dtype=torch.int32, device=cache.device)
+    rows, hq = cache._rows_of(q, "q")
+    s = cache._with(page_table, lens, cu, rows)
+    nbytes = (rows * cache.hkv * page_table.shape[1] * 4 + 255) // 256 * 256  # hdp_cache_select_workspace_bytes
+    with _pool(stream, cache):
+        blocks = torch.empty((rows, cache.hkv, count), dtype=torch.int32, device=cache.device)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
-    hdp_cache_select(cache, page_table, lens, q, keep_first, keep_last, ws, blocks, cu=cu, stream=stream)
+    cache._call("hdp_cache_select", stream, s, None if cu is None else cu.data_ptr(), rows, q.data_ptr(), hq, count,
+                keep_first, keep_last, ws.data_ptr(), nbytes, blocks.data_ptr())
     return blocks
 
 
@@ -168,21 +163,18 @@ def cache_attention(cache: KVCache, page_table, lens, q, cu=None, blocks=None, s
     blocks only; returns (o bf16 [rows][hq][d], lse fp32 [hq][rows])."""
     import torch
 
-    rows, hq, d = q.shape
+    rows, hq = cache._rows_of(q, "q")
+    s = cache._with(page_table, lens, cu, rows)
+    count, list_ptr = cache._blocks_of(blocks, rows)
     if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    device = cache.device
-    nbytes = _cache_ws_bytes.get((device, d))
+        scale = 1.0 / math.sqrt(cache.d)
+    nbytes = cache._attention_bytes
     if nbytes is None:
-        nbytes = _cache_ws_bytes[device, d] = hdp_cache_attention_workspace_bytes(cache, hq)
-    if stream is not None:
-        with _pool(stream, cache):
-            o = torch.empty_like(q)
-            lse = torch.empty((hq, rows), dtype=torch.float32, device=device)
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    else:
+        nbytes = cache._attention_bytes = hdp_cache_attention_workspace_bytes(cache, hq)
+    with _pool(stream, cache):
         o = torch.empty_like(q)
-        lse = torch.empty((hq, rows), dtype=torch.float32, device=device)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    hdp_cache_attention(cache, page_table, lens, q, scale, ws, o, lse, cu=cu, blocks=blocks, stream=stream)
+        lse = torch.empty((hq, rows), dtype=torch.float32, device=cache.device)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+    cache._call("hdp_cache_attention", stream, s, None if cu is None else cu.data_ptr(), rows, q.data_ptr(), hq, scale,
+                list_ptr, count, ws.data_ptr(), nbytes, o.data_ptr(), lse.data_ptr())
     return o, lse

@@ -371,11 +371,8 @@ class KVCache:
         if format not in (HDP_CACHE_E4M3, HDP_CACHE_INT8):
             raise ValueError("format must be HDP_CACHE_E4M3 or HDP_CACHE_INT8")
         self.k, self.v, self.scales, self.bounds, self.format = k, v, scales, bounds, int(format)
-        self.num_pages, self.hkv, self.d, self._dev = pages, hkv, d, dev
-
-    @property
-    def device(self):
-        return self.k.device
+        self.num_pages, self.hkv, self.d, self._dev, self.device = pages, hkv, d, dev, k.device
+        self._attention_bytes = _attention_bytes.get((dev, d))
 
     @classmethod
     def empty(cls, num_pages: int, hkv: int, d: int, format: int, device="cuda"):
@@ -403,6 +400,24 @@ class KVCache:
         return _CACHE_FORMAT.pack(self.k.data_ptr(), self.v.data_ptr(), self.scales.data_ptr(), self.bounds.data_ptr(),
                                   self.num_pages, self.hkv, self.d, self.format, page_table.data_ptr(),
                                   lens.data_ptr(), n, columns)
+
+    def _rows_of(self, q, name):
+        """(rows, hq) of q [rows][hq][d] bf16."""
+        import torch
+
+        rows, hq = q.shape[0], q.shape[1] if q.dim() == 3 else -1
+        _tensor(q, name, torch.bfloat16, (rows, hq, self.d), self._dev)
+        return rows, hq
+
+    def _blocks_of(self, blocks, rows):
+        """(count, address) of a block list."""
+        import torch
+
+        if blocks is None:
+            return 0, None
+        count = blocks.shape[-1]
+        _tensor(blocks, "blocks", torch.int32, (rows, self.hkv, count), self._dev)
+        return count, blocks.data_ptr()
 
     def _call(self, name, stream, *args):
         """Runs an entry point with the cache's device current, on `stream` or that device's current one."""
@@ -455,6 +470,9 @@ def hdp_cache_read(cache: KVCache, page_table, lens, k, v, cu=None, stream=None)
                 None if cu is None else cu.data_ptr(), rows, k.data_ptr(), v.data_ptr())
 
 
+_attention_bytes: dict = {}  # (device, d): it depends on nothing else
+
+
 def hdp_cache_attention_workspace_bytes(cache: KVCache, hq: int) -> int:
     import torch
 
@@ -463,6 +481,7 @@ def hdp_cache_attention_workspace_bytes(cache: KVCache, hq: int) -> int:
     with torch.cuda.device(cache._dev):
         _check(load().hdp_cache_attention_workspace_bytes(s, hq, ctypes.byref(n)),
                "hdp_cache_attention_workspace_bytes")
+    _attention_bytes[cache._dev, cache.d] = n.value
     return n.value
 
 
@@ -472,17 +491,11 @@ def hdp_cache_attention(cache: KVCache, page_table, lens, q, scale: float, works
     given) into o (like q) and lse [hq][rows] float32."""
     import torch
 
-    rows, hq = q.shape[0], q.shape[1] if q.dim() == 3 else -1
-    shape = (rows, hq, cache.d)
-    _tensor(q, "q", torch.bfloat16, shape, cache._dev)
-    _tensor(o, "o", torch.bfloat16, shape, cache._dev)
+    rows, hq = cache._rows_of(q, "q")
+    _tensor(o, "o", torch.bfloat16, (rows, hq, cache.d), cache._dev)
     _tensor(lse, "lse", torch.float32, (hq, rows), cache._dev)
     _tensor(workspace, "workspace", torch.uint8, (workspace.numel(),), cache._dev)
-    count, list_ptr = 0, None
-    if blocks is not None:
-        count = blocks.shape[-1]
-        _tensor(blocks, "blocks", torch.int32, (rows, cache.hkv, count), cache._dev)
-        list_ptr = blocks.data_ptr()
+    count, list_ptr = cache._blocks_of(blocks, rows)
     cache._call("hdp_cache_attention", stream, cache._with(page_table, lens, cu, rows),
                 None if cu is None else cu.data_ptr(), rows, q.data_ptr(), hq, scale, list_ptr, count,
                 workspace.data_ptr(), workspace.numel(), o.data_ptr(), lse.data_ptr())
@@ -500,14 +513,12 @@ def hdp_cache_select(cache: KVCache, page_table, lens, q, keep_first: int, keep_
     """Chooses blocks for each row of q [rows][hq][d] bf16 and kv head into blocks int32 [rows][hkv][count]."""
     import torch
 
-    rows, hq = q.shape[0], q.shape[1] if q.dim() == 3 else -1
-    _tensor(q, "q", torch.bfloat16, (rows, hq, cache.d), cache._dev)
-    count = blocks.shape[-1]
-    _tensor(blocks, "blocks", torch.int32, (rows, cache.hkv, count), cache._dev)
+    rows, hq = cache._rows_of(q, "q")
+    count, list_ptr = cache._blocks_of(blocks, rows)
     _tensor(workspace, "workspace", torch.uint8, (workspace.numel(),), cache._dev)
     cache._call("hdp_cache_select", stream, cache._with(page_table, lens, cu, rows),
                 None if cu is None else cu.data_ptr(), rows, q.data_ptr(), hq, count, keep_first, keep_last,
-                workspace.data_ptr(), workspace.numel(), blocks.data_ptr())
+                workspace.data_ptr(), workspace.numel(), list_ptr)
 
 
 # ---------------------------------------------------------------- cost models (host arithmetic)
