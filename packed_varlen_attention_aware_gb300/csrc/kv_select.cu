@@ -8,14 +8,14 @@
 // products whatever the group's size is, and the choice does not depend on the
 // order of summation.  HBM bounds the scores (1/64 of the cache's bytes).
 //
-//   k_cache_scores: 256 blocks of one (row, kv head) a CTA; a lane has 16
-//   channels of one extreme, so 16 (d = 128) or 8 lanes have a block.
-//   k_cache_top: one CTA for each (row, kv head), a cluster of 8 for more than
-//   4,096 blocks.  The keys stay in registers; a binary search over the key's
-//   value counts the keys above it (no atomics, so many equal keys cost
-//   nothing), and ballots give each chosen block its place in ascending order.
+//   Up to 32,768 blocks (2M tokens) and a count of 512, one kernel scores and
+//   chooses, a cluster of CTAs for each (row, kv head); beyond, the scores go
+//   through memory.  The choice is a search over the key's value that counts the
+//   keys above three cuts at a time (no atomics, so many equal keys cost
+//   nothing); ballots then give each chosen block its place in ascending order.
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <string>
 
 #include "kv_cache.cuh"
@@ -62,72 +62,71 @@ __device__ __forceinline__ int dp2a_hi(int a, int b, int c) {
   return r;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kScoreThreads, 4) k_cache_scores(const SelectParams p, int chunks) {
-  constexpr int kLanes = D / 8;  // of a block: D / 16 for each extreme
-  __shared__ __align__(16) int16_t s_q[2][D];  // sums of min(c, 0) and of max(c, 0)
-  __shared__ uint32_t s_top[kScoreThreads / 32];
-  const int unit = blockIdx.x / chunks, chunk = blockIdx.x - unit * chunks;
-  const int row = unit / p.c.hkv, head = unit - row * p.c.hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int seq, have;
-  if (!row_place(p.c, row, seq, have)) return;
-  if (have <= p.count || chunk * kScoreBlocks >= have) return;  // all are chosen, or none here
-
-  // The bounds are asked for first: their latency hides behind the query's work.
-  const int b = chunk * kScoreBlocks + warp * 32 + lane;
-  const int page = b < have ? page_of(p.c, seq, b) : -1;
-  const size_t ph = static_cast<size_t>(max(page, 0)) * p.c.hkv + head;
-  const int part = lane % kLanes;  // 16 channels of one extreme
-  constexpr int kAhead = 8;  // blocks of a group of lanes in flight; lane (group, i) keeps block i's sum
+// Scores of one (row, kv head) by a CTA of THREADS threads: a warp has 32 blocks
+// at a time, a lane 16 channels of one extreme, so 16 (d = 128) or 8 lanes have
+// a block.
+template <int D, int THREADS>
+struct Scorer {
+  static constexpr int kLanes = D / 8;  // of a block: D / 16 for each extreme
+  static constexpr int kAhead = 8;      // blocks of a group of lanes in flight
+  struct Shared {
+    int16_t __align__(16) q[2][D];  // sums over the group's heads of min(c, 0) and of max(c, 0)
+    uint32_t top[THREADS / 32];
+  };
+  const SelectParams& p;
+  int seq, have, head, lane, part;
+  int qr[8];  // this lane's 16 channels of q
   uint4 x[kAhead];
-  auto fetch = [&](int first) {
+  int page;
+
+  __device__ __forceinline__ Scorer(const SelectParams& p, int seq, int have, int head)
+      : p(p), seq(seq), have(have), head(head), lane(threadIdx.x & 31), part(lane % kLanes) {}
+  // Page of block b0 + lane.
+  __device__ __forceinline__ int page_at(int b0) const { return b0 + lane < have ? page_of(p.c, seq, b0 + lane) : -1; }
+  // Asks for blocks first .. first + kAhead - 1 of each group of lanes.
+  __device__ __forceinline__ void fetch(int first) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int pg = __shfl_sync(0xffffffffu, page, (lane & ~(kLanes - 1)) + first + i);
       x[i] = pg >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.c.bounds + (static_cast<size_t>(pg) * p.c.hkv + head) * (2 * D)) + part)
                      : make_uint4(0, 0, 0, 0);
     }
-  };
-  fetch(0);
-  const float scale = page >= 0 ? __ldg(p.c.scales + 2 * ph) : 0.f;
-
-  const __nv_bfloat16* q = p.q + (static_cast<size_t>(row) * p.hq + head * p.g) * D;
-  uint32_t top = 0;
-  for (int i = threadIdx.x; i < p.g * D / 8; i += kScoreThreads) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(q) + i);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
-      top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-    }
   }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) s_top[warp] = top;
-  __syncthreads();
-  if (threadIdx.x < D) {
+  // Rounds the group's query rows to whole numbers (all threads).
+  __device__ __forceinline__ void query(Shared& sm, int row) {
+    const __nv_bfloat16* q = p.q + (static_cast<size_t>(row) * p.hq + head * p.g) * D;
+    uint32_t top = 0;
+    for (int i = threadIdx.x; i < p.g * D / 8; i += THREADS) {
+      const uint4 y = __ldg(reinterpret_cast<const uint4*>(q) + i);
+      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int w = 0; w < kScoreThreads / 32; ++w) top = max(top, s_top[w]);
-    // the smallest 2^e, e >= -126, with the largest magnitude at most 127 * 2^e (127 = 1.984375 * 2^6)
-    const int e = max(static_cast<int>(top >> 7) - 127 - 6 + ((top & 0x7f) > 0x7e), -126);
-    const float down = pow2i(-e);
-    int neg = 0, pos = 0;
-    for (int h = 0; h < p.g; ++h) {
-      const float x = __bfloat162float(q[h * D + threadIdx.x]);
-      const int c = (__float_as_uint(x) & 0x7fffffffu) < 0x7f800000u ? __float2int_rn(x * down) : 0;
-      neg += min(c, 0);
-      pos += max(c, 0);
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
+        top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+      }
     }
-    s_q[0][threadIdx.x] = static_cast<int16_t>(neg);
-    s_q[1][threadIdx.x] = static_cast<int16_t>(pos);
-  }
-  __syncthreads();
-
-  int qr[8];
-  {
-    const int4* src = reinterpret_cast<const int4*>(&s_q[0][0] + part * 16);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) sm.top[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x < D) {
+#pragma unroll
+      for (int w = 0; w < THREADS / 32; ++w) top = max(top, sm.top[w]);
+      // the smallest 2^e, e >= -126, with the largest magnitude at most 127 * 2^e (127 = 1.984375 * 2^6)
+      const int e = max(static_cast<int>(top >> 7) - 127 - 6 + ((top & 0x7f) > 0x7e), -126);
+      const float down = pow2i(-e);
+      int neg = 0, pos = 0;
+#pragma unroll 4
+      for (int h = 0; h < p.g; ++h) {
+        const float y = __bfloat162float(q[h * D + threadIdx.x]);
+        const int c = (__float_as_uint(y) & 0x7fffffffu) < 0x7f800000u ? __float2int_rn(y * down) : 0;
+        neg += min(c, 0);
+        pos += max(c, 0);
+      }
+      sm.q[0][threadIdx.x] = static_cast<int16_t>(neg);
+      sm.q[1][threadIdx.x] = static_cast<int16_t>(pos);
+    }
+    __syncthreads();
+    const int4* src = reinterpret_cast<const int4*>(&sm.q[0][0] + part * 16);
     const int4 a = src[0], c = src[1];
     qr[0] = a.x;
     qr[1] = a.y;
@@ -138,31 +137,73 @@ __global__ void __launch_bounds__(kScoreThreads, 4) k_cache_scores(const SelectP
     qr[6] = c.z;
     qr[7] = c.w;
   }
-  int mine = 0;
+  // Key of block b0 + lane; its pages are in `page`, its first blocks asked for.
+  __device__ __forceinline__ uint32_t key(int b0) {
+    const float scale = page >= 0 ? __ldg(p.c.scales + 2 * (static_cast<size_t>(page) * p.c.hkv + head)) : 0.f;
+    int mine = 0;
 #pragma unroll
-  for (int first = 0; first < kLanes; first += kAhead) {
-    if (first) fetch(first);
+    for (int first = 0; first < kLanes; first += kAhead) {
+      if (first) fetch(first);
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    int u = dp2a_lo(qr[0], x[i].x, 0);
-    u = dp2a_hi(qr[1], x[i].x, u);
-    u = dp2a_lo(qr[2], x[i].y, u);
-    u = dp2a_hi(qr[3], x[i].y, u);
-    u = dp2a_lo(qr[4], x[i].z, u);
-    u = dp2a_hi(qr[5], x[i].z, u);
-    u = dp2a_lo(qr[6], x[i].w, u);
-    u = dp2a_hi(qr[7], x[i].w, u);
+      for (int i = 0; i < kAhead; ++i) {  // lane (group, first + i) keeps that block's sum
+        int u = dp2a_lo(qr[0], x[i].x, 0);
+        u = dp2a_hi(qr[1], x[i].x, u);
+        u = dp2a_lo(qr[2], x[i].y, u);
+        u = dp2a_hi(qr[3], x[i].y, u);
+        u = dp2a_lo(qr[4], x[i].z, u);
+        u = dp2a_hi(qr[5], x[i].z, u);
+        u = dp2a_lo(qr[6], x[i].w, u);
+        u = dp2a_hi(qr[7], x[i].w, u);
 #pragma unroll
-    for (int s = 1; s < kLanes; s *= 2) u += __shfl_xor_sync(0xffffffffu, u, s);
-    if (part == first + i) mine = u;
+        for (int s = 1; s < kLanes; s *= 2) u += __shfl_xor_sync(0xffffffffu, u, s);
+        if (part == first + i) mine = u;
+      }
+    }
+    const int b = b0 + lane;
+    if (b < p.first || b >= have - p.last) return kForced;
+    if (page < 0) return 0;
+    return scale == scale ? key_of(static_cast<float>(mine) * scale) : kNanKey;
   }
+  // put(block, key) for this warp's blocks b0 .. b0 + 31, b0 + step .., below `to`.
+  template <class P>
+  __device__ __forceinline__ void all(Shared& sm, int row, int b0, int step, int to, P put) {
+    if (b0 < to) {
+      page = page_at(b0);
+      fetch(0);  // its latency hides behind the query's work
+    }
+    query(sm, row);
+    for (; b0 < to; b0 += step) {
+      const bool more = to - b0 > step;
+      const int next_page = more ? page_at(b0 + step) : -1;
+      const uint32_t k = key(b0);
+      if (b0 + lane < to) put(b0 + lane, k);
+      page = next_page;
+      if (more) fetch(0);
+    }
   }
-  if (b < have) {
-    uint32_t key = scale == scale ? key_of(static_cast<float>(mine) * scale) : kNanKey;
-    if (page < 0) key = 0;
-    if (b < p.first || b >= have - p.last) key = kForced;
-    p.keys[(static_cast<size_t>(row) * p.c.hkv + head) * p.c.max_pages + b] = key;
-  }
+};
+
+// Keys into memory: a CTA has 256 blocks of a (row, kv head).  Each warp's chain
+// of waits (length, pages, bounds twice) bounds it, not their number: 32 warps an
+// SM with 8 blocks of a lane group in flight took 16.5 us for 32,768 blocks of 8
+// heads (67 MB), 20 warps with 16 blocks 17.8, loops over more blocks 18 to 40.
+template <int D>
+__global__ void __launch_bounds__(kScoreThreads, 4) k_cache_scores(const SelectParams p, int chunks) {
+  using S = Scorer<D, kScoreThreads>;
+  __shared__ typename S::Shared sm;
+  const int unit = blockIdx.x / chunks, chunk = blockIdx.x - unit * chunks;
+  const int row = unit / p.c.hkv, head = unit - row * p.c.hkv;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int seq, have;
+  if (!row_place(p.c, row, seq, have)) return;
+  if (have <= p.count || chunk * kScoreBlocks >= have) return;  // all are chosen, or none here
+  S s(p, seq, have, head);
+  const int b0 = chunk * kScoreBlocks + (threadIdx.x >> 5) * 32;
+  s.page = s.page_at(b0);
+  s.fetch(0);  // its latency hides behind the query's work
+  s.query(sm, row);
+  const uint32_t key = s.key(b0);
+  if (b0 + s.lane < have) p.keys[(static_cast<size_t>(row) * p.c.hkv + head) * p.c.max_pages + b0 + s.lane] = key;
 }
 
 // Chooses the `count` largest of a CTA's keys, the earlier of equal ones, and
@@ -283,9 +324,95 @@ __device__ __forceinline__ int forced_in(const SelectParams& p, int have, int fr
   return max(0, min(to, p.first) - from) + max(0, to - max(from, have - p.last));
 }
 
-// One CTA for each (row, kv head).  ITEMS keys of a thread in registers (ITEMS *
-// 1024 blocks at most); 0: the keys are read again for each step.
-template <int ITEMS>
+// Scores (unless they are in memory) and choice, up to kSelectBlocks blocks a CTA:
+// a cluster of 1 to 8 CTAs has a (row, kv head), each a run of its blocks, whose
+// keys stay in shared memory and then in registers.  Each chooses `count` of its own, into
+// the shared memory of the first, which chooses among those; no CTA waits for
+// another during a search.
+constexpr int kSelectBlocks = 4 * kTopThreads;
+constexpr int kTopCtas = 8;
+constexpr int kTopMost = 512;  // largest count for a cluster
+template <int D>
+__global__ void __launch_bounds__(kTopThreads) k_cache_select(const SelectParams p, int ctas, bool scored) {
+  namespace cg = cooperative_groups;
+  using S = Scorer<D, kTopThreads>;
+  constexpr int kItems = kSelectBlocks / kTopThreads;
+  __shared__ typename S::Shared s_query;
+  __shared__ TopShared s_top;
+  __shared__ union {
+    uint32_t keys[kSelectBlocks];
+    struct {
+      uint32_t key[kTopCtas * kTopMost];
+      int block[kTopCtas * kTopMost];
+    } passed;
+  } sm;
+  __shared__ int s_n[kTopCtas];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int unit = blockIdx.x / ctas, rank = blockIdx.x - unit * ctas;
+  const int row = unit / p.c.hkv, head = unit - row * p.c.hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int seq, have;
+  const bool live = row_place(p.c, row, seq, have);
+  if (scored) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!live) return;  // the whole cluster
+  int32_t* out = p.out + static_cast<size_t>(unit) * p.count;
+  if (have <= p.count) {
+    if (rank == 0)
+      for (int i = threadIdx.x; i < p.count; i += kTopThreads) out[i] = i < have ? i : -1;
+    return;
+  }
+  const int each = ((have + ctas - 1) / ctas + 31) / 32 * 32;  // at most kSelectBlocks
+  const int from = min(have, rank * each), to = min(have, from + each), n = to - from;
+
+  if (!scored) {
+    S s(p, seq, have, head);
+    s.all(s_query, row, from + warp * 32, kTopThreads, to, [&](int b, uint32_t k) { sm.keys[b - from] = k; });
+    __syncthreads();
+  }
+  const uint32_t* keys = p.keys + static_cast<size_t>(unit) * p.c.max_pages + from;
+  const int items = (n + kTopThreads - 1) / kTopThreads;  // a warp has a run of items * 32 keys
+  const int base = warp * items * 32 + lane;
+  auto has = [&](int i) { return i < items && base + i * 32 < n; };
+  uint32_t key[kItems];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) key[i] = !has(i) ? 0u : scored ? __ldcg(keys + base + i * 32) : sm.keys[base + i * 32];
+  auto key_at = [&](int i) { return key[i]; };
+  const int forced = forced_in(p, have, from, to);
+  if (ctas == 1) {
+    choose<true>(s_top, kItems, p.count, forced, key_at, has, [&](int at, int i) { out[at] = base + i * 32; });
+    return;
+  }
+  uint32_t* to_key = cluster.map_shared_rank(sm.passed.key, 0) + rank * kTopMost;
+  int* to_block = cluster.map_shared_rank(sm.passed.block, 0) + rank * kTopMost;
+  auto pass_on = [&](int at, int i) {
+    to_key[at] = key[i];
+    to_block[at] = from + base + i * 32;
+  };
+  cluster.sync();  // the first CTA has its keys in registers
+  if (n <= p.count) {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+      if (has(i)) pass_on(base + i * 32, i);
+  } else {
+    choose<true>(s_top, kItems, p.count, forced, key_at, has, pass_on);
+  }
+  if (threadIdx.x == 0) cluster.map_shared_rank(s_n, 0)[rank] = min(n, p.count);
+  cluster.sync();
+  if (rank != 0) return;
+  // slots of kTopMost for each CTA, in the order of the blocks
+  const int at = warp * (kItems * 32) + lane;
+  auto passed = [&](int i) {
+    const int x = at + i * 32, c = x / kTopMost;
+    return c < ctas && x % kTopMost < s_n[c];
+  };
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) key[i] = passed(i) ? sm.passed.key[at + i * 32] : 0u;
+  choose<true>(s_top, kItems, p.count, forced_in(p, have, 0, have), key_at, passed,
+               [&](int place, int i) { out[place] = sm.passed.block[at + i * 32]; });
+}
+
+// The choice among keys in memory, for more blocks or a larger count than a
+// cluster takes; they are read again for each step of the search.
 __global__ void __launch_bounds__(kTopThreads) k_cache_top(const SelectParams p) {
   __shared__ TopShared sm;
   const int row = blockIdx.x / p.c.hkv;
@@ -300,86 +427,27 @@ __global__ void __launch_bounds__(kTopThreads) k_cache_top(const SelectParams p)
     return;
   }
   const uint32_t* keys = p.keys + static_cast<size_t>(blockIdx.x) * p.c.max_pages;
-  const int items = (have + kTopThreads - 1) / kTopThreads;  // a warp has a run of items * 32 keys
+  const int items = (have + kTopThreads - 1) / kTopThreads;
   const int base = warp * items * 32 + lane;
-  const int forced = forced_in(p, have, 0, have);
   auto has = [&](int i) { return i < items && base + i * 32 < have; };
-  auto emit = [&](int at, int i) { out[at] = base + i * 32; };
-  if constexpr (ITEMS > 0) {
-    uint32_t key[ITEMS];
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) key[i] = has(i) ? __ldcg(keys + base + i * 32) : 0u;
-    choose<true>(sm, ITEMS, p.count, forced, [&](int i) { return key[i]; }, has, emit);
-  } else {
-    choose<false>(sm, items, p.count, forced, [&](int i) { return has(i) ? __ldcg(keys + base + i * 32) : 0u; }, has, emit);
-  }
+  choose<false>(sm, items, p.count, forced_in(p, have, 0, have),
+                [&](int i) { return has(i) ? __ldcg(keys + base + i * 32) : 0u; }, has,
+                [&](int at, int i) { out[at] = base + i * 32; });
 }
 
-// The same for many blocks: a cluster of 8 CTAs for each (row, kv head).  Each
-// chooses `count` of its eighth, into the shared memory of the first, which
-// chooses among those: a step of the search then has 4 keys of a thread to
-// count instead of 32, and no CTA waits for another during it.
-constexpr int kTopCtas = 8;
-constexpr int kTopMost = 512;  // largest count
-__global__ void __cluster_dims__(kTopCtas, 1, 1) __launch_bounds__(kTopThreads) k_cache_top_cluster(const SelectParams p) {
-  namespace cg = cooperative_groups;
-  constexpr int kItems = 4;
-  __shared__ TopShared sm;
-  __shared__ uint32_t s_key[kTopCtas * kTopMost];
-  __shared__ int s_block[kTopCtas * kTopMost];
-  __shared__ int s_n[kTopCtas];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = static_cast<int>(cluster.block_rank()), unit = blockIdx.x / kTopCtas;
-  const int row = unit / p.c.hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int seq, have;
-  const bool live = row_place(p.c, row, seq, have);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!live) return;  // the whole cluster
-  int32_t* out = p.out + static_cast<size_t>(unit) * p.count;
-  if (have <= p.count) {
-    if (rank == 0)
-      for (int i = threadIdx.x; i < p.count; i += kTopThreads) out[i] = i < have ? i : -1;
-    return;
-  }
-  const uint32_t* keys = p.keys + static_cast<size_t>(unit) * p.c.max_pages;
-  const int each = (have + kTopCtas - 1) / kTopCtas;  // at most kItems * kTopThreads
-  const int from = min(have, rank * each), to = min(have, from + each), n = to - from;
-  const int items = (n + kTopThreads - 1) / kTopThreads;
-  const int base = from + warp * items * 32 + lane;
-  uint32_t key[kItems];
-  auto has = [&](int i) { return i < items && base + i * 32 < to; };
-#pragma unroll
-  for (int i = 0; i < kItems; ++i) key[i] = has(i) ? __ldcg(keys + base + i * 32) : 0u;
-  uint32_t* to_key = cluster.map_shared_rank(s_key, 0) + rank * kTopMost;
-  int* to_block = cluster.map_shared_rank(s_block, 0) + rank * kTopMost;
-  auto pass_on = [&](int at, int i) {
-    to_key[at] = key[i];
-    to_block[at] = base + i * 32;
-  };
-  cluster.sync();  // the first CTA has begun
-  if (n <= p.count) {
-#pragma unroll
-    for (int i = 0; i < kItems; ++i)
-      if (has(i)) pass_on(base + i * 32 - from, i);
-  } else {
-    choose<true>(sm, kItems, p.count, forced_in(p, have, from, to), [&](int i) { return key[i]; }, has, pass_on);
-  }
-  if (threadIdx.x == 0) cluster.map_shared_rank(s_n, 0)[rank] = min(n, p.count);
-  cluster.sync();
-  if (rank != 0) return;
-  // slots of kTopMost for each CTA, in the order of the blocks
-  const int at = warp * (kItems * 32) + lane;
-  auto chosen = [&](int i) { return (at + i * 32) % kTopMost < s_n[(at + i * 32) / kTopMost]; };
-#pragma unroll
-  for (int i = 0; i < kItems; ++i) key[i] = chosen(i) ? s_key[at + i * 32] : 0u;
-  choose<true>(sm, kItems, p.count, forced_in(p, have, 0, have), [&](int i) { return key[i]; }, chosen,
-         [&](int place, int i) { out[place] = s_block[at + i * 32]; });
+// CTAs of k_cache_select for a (row, kv head): enough for the blocks, and as many
+// as leave no more than one for each SM; 0: not for this size.
+int select_ctas(int64_t units, int max_pages, int count) {
+  const int least = (max_pages + kSelectBlocks - 1) / kSelectBlocks;
+  int ctas = 1;
+  while (ctas < least) ctas *= 2;
+  if (ctas > kTopCtas || (ctas > 1 && count > kTopMost) || units * ctas > 2147483647LL) return 0;
+  while (ctas < kTopCtas && count <= kTopMost && units * ctas * 2 <= 152 && max_pages > ctas * kTopThreads) ctas *= 2;
+  return ctas;
 }
 
-hdp_status_t select_bytes(const CacheView& c, size_t* bytes) {
-  *bytes = (static_cast<size_t>(c.rows) * c.hkv * c.max_pages * sizeof(uint32_t) + 255) & ~size_t(255);
-  return HDP_OK;
+size_t select_bytes(int64_t rows, int hkv, int max_pages) {
+  return (static_cast<size_t>(rows) * hkv * max_pages * sizeof(uint32_t) + 255) & ~size_t(255);
 }
 
 }  // namespace
@@ -391,11 +459,8 @@ extern "C" hdp_status_t hdp_cache_select_workspace_bytes(const hdp_cache_t* cach
   if (!cache || !bytes) return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_select_workspace_bytes: NULL argument");
   if (cache->hkv < 1 || cache->max_pages < 1 || rows < 0 || rows > 2147483647LL)
     return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_select_workspace_bytes: need hkv >= 1, max_pages >= 1, 0 <= rows < 2^31");
-  CacheView c = {};
-  c.rows = static_cast<int>(rows);
-  c.hkv = cache->hkv;
-  c.max_pages = cache->max_pages;
-  return select_bytes(c, bytes);
+  *bytes = select_bytes(rows, cache->hkv, cache->max_pages);
+  return HDP_OK;
 }
 
 extern "C" hdp_status_t hdp_cache_select(const hdp_cache_t* cache, const int32_t* cu, int64_t rows, const void* q,
@@ -414,11 +479,9 @@ extern "C" hdp_status_t hdp_cache_select(const hdp_cache_t* cache, const int32_t
   if (!q || !blocks) return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_select: NULL argument");
   if (reinterpret_cast<uintptr_t>(q) & 15)
     return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_select: q must be 16-byte aligned");
-  const int chunks = (cache->max_pages + kScoreBlocks - 1) / kScoreBlocks;
-  if (rows * cache->hkv > 2147483647LL / chunks)
+  if (rows * cache->hkv > 2147483647LL / ((cache->max_pages + kScoreBlocks - 1) / kScoreBlocks))
     return fail(HDP_ERR_UNSUPPORTED, "hdp_cache_select: rows * hkv * max_pages / 256 must be below 2^31");
-  size_t need = 0;
-  select_bytes(p.c, &need);
+  const size_t need = select_bytes(rows, cache->hkv, cache->max_pages);
   if (!workspace || workspace_bytes < need)
     return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_select: workspace too small (need " + std::to_string(need) + " bytes)");
   if (reinterpret_cast<uintptr_t>(workspace) & 255)
@@ -433,31 +496,38 @@ extern "C" hdp_status_t hdp_cache_select(const hdp_cache_t* cache, const int32_t
   p.first = keep_first;
   p.last = keep_last;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned units = static_cast<unsigned>(rows * cache->hkv);
-  if (cache->d == 128) k_cache_scores<128><<<units * chunks, kScoreThreads, 0, st>>>(p, chunks);
-  else k_cache_scores<64><<<units * chunks, kScoreThreads, 0, st>>>(p, chunks);
-  note_launch();
-  HDP_CUDA_TRY(cudaGetLastError());
-  cudaLaunchAttribute attr;  // the launch overlaps the scores; the kernel waits for them
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  const int64_t units = rows * cache->hkv;
+  const int ctas = select_ctas(units, cache->max_pages, count);
+  // Few long rows: the scores want every SM, the choice has 8 CTAs for each head
+  // at most (32,768 blocks, 8 heads: 41 us from one kernel).
+  const bool scored = !ctas || (units * ctas < 100 && cache->max_pages > 2 * kTopThreads);
+  if (scored) {
+    const int chunks = (cache->max_pages + kScoreBlocks - 1) / kScoreBlocks;
+    const unsigned grid = static_cast<unsigned>(units * chunks);
+    if (cache->d == 128) k_cache_scores<128><<<grid, kScoreThreads, 0, st>>>(p, chunks);
+    else k_cache_scores<64><<<grid, kScoreThreads, 0, st>>>(p, chunks);
+    note_launch();
+    HDP_CUDA_TRY(cudaGetLastError());
+  }
+  cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(units);
   cfg.blockDim = dim3(kTopThreads);
   cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  // One CTA up to 4,096 blocks, where its search counts 4 keys a thread; a
-  // cluster beyond (32,768 blocks, 8 heads: 37.6 us with one CTA of 32 keys a
-  // thread), as long as its candidates fit and its grid is in range.
-  if (cache->max_pages <= 4 * kTopThreads) {
-    HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_cache_top<4>, p));
-  } else if (cache->max_pages <= 32 * kTopThreads && count <= kTopMost && units <= 2147483647u / kTopCtas) {
-    cfg.gridDim = dim3(units * kTopCtas);
-    HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_cache_top_cluster, p));
-  } else {
-    HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_cache_top<0>, p));
+  cfg.attrs = attr;
+  if (ctas) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = ctas;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
   }
+  if (scored) {  // the launch overlaps the scores; the kernel waits for them
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(units * std::max(1, ctas)));
+  if (!ctas) HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_cache_top, p));
+  else HDP_CUDA_TRY(cudaLaunchKernelEx(&cfg, cache->d == 128 ? k_cache_select<128> : k_cache_select<64>, p, ctas, scored));
   note_launch();
   return HDP_OK;
 }
