@@ -76,6 +76,7 @@ def test_attention_refusals(lib):
                 dict(blocks=V(256), count=0), dict(blocks=V(256), count=-1), dict(q=None), dict(o=None), dict(lse=None),
                 dict(q=V(264)), dict(o=V(264))):
         assert _attend(lib, c, **bad) == INVALID, bad
+    assert _attend(lib, _cache(hkv=1), rows=1 << 30, hq=4) == UNSUPPORTED
     n = ctypes.c_size_t()
     assert lib.hdp_cache_attention_workspace_bytes(None, 4, ctypes.byref(n)) == INVALID
     assert lib.hdp_cache_attention_workspace_bytes(c, 3, ctypes.byref(n)) == INVALID

@@ -218,6 +218,40 @@ def test_read_gives_code_times_scale(fmt, d, hkv):
     assert (k[:3] == 0).all() and (v[:3] == 0).all() and np.array_equal(_f64(k[3:]), ref.sequence(table[0], 130)[0])
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_rows_before_the_sequence_and_of_empty_sequences_are_not_written(fmt):
+    cache = _filled(3, 2, 64, fmt)
+    ref = _oracle(cache)
+    table = np.array([[1, -7], [2, 0]], np.int32)
+    k, v = _bf16((8, 2, 64), 1), _bf16((8, 2, 64), 2)
+    pkg.cache_append(cache, _i32(table), _i32([0, 3]), k.cuda(), v.cuda(), cu=_i32([0, 2, 8]))
+    pkg.cache_append(cache, _i32(table), _i32([0, 4]), k[:2].cuda(), v[:2].cuda())  # one of an empty sequence
+    pkg.hdp_device_status()
+    ref.append(table[1:], [3], _f64(k[5:]), _f64(v[5:]), [0, 3])  # the last three of six rows
+    ref.append(table[1:], [4], _f64(k[1:2]), _f64(v[1:2]), [0, 1])
+    got = _oracle(cache)
+    for name in ("scales", "bounds", "k", "v"):
+        assert np.array_equal(getattr(got, name), getattr(ref, name)), name
+
+
+def test_page_shared_by_two_sequences_and_rows_written_twice():
+    """A common prefix page read by both sequences; the second half of a draft overwritten with other tokens reads as
+    those, within the larger scale that the first left."""
+    cache = pkg.KVCache.empty(4, 1, 64, 1)
+    table = _i32([[0, 1], [0, 2]])
+    prefix = _bf16((64, 1, 64), 1).cuda()
+    pkg.cache_append(cache, table[:1], _i32([64]), prefix, prefix, cu=_i32([0, 64]))
+    tail = _bf16((2, 1, 64), 2).cuda()
+    pkg.cache_append(cache, table, _i32([65, 65]), tail, tail)
+    k, _ = pkg.cache_read(cache, table, _i32([65, 65]), 130, cu=_i32([0, 65, 130]))
+    assert torch.equal(k[:64], k[65:129]) and not torch.equal(k[64], k[129])
+    pkg.cache_append(cache, table, _i32([66, 66]), tail * 64, tail * 64)
+    pkg.cache_append(cache, table, _i32([66, 66]), tail, tail)
+    k, _ = pkg.cache_read(cache, table, _i32([66, 66]), 2)
+    step = cache.scales[[1, 2], :, 0][..., None]
+    assert ((k.float() - tail.float()).abs() <= step / 2).all() and (step > 0.25).all()
+
+
 # ---------------------------------------------------------------- attention
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -264,6 +298,68 @@ def test_long_sequences_are_split_and_joined(fmt, hq, hkv, d, lens):
     for _ in range(3):
         o2, lse2 = pkg.cache_attention(*args)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("fmt,hq,hkv,d,lens,new", [
+    (1, 16, 8, 64, [600000, 130, 250001, 64, 7000], 1), (0, 8, 8, 128, [200000, 100100], 1), (0, 8, 4, 64, [400000, 90000], 5)])
+def test_runs_whose_ends_are_handed_out(fmt, hq, hkv, d, lens, new):
+    """More than 20 blocks for each warp of the device: pieces of runs go to whoever comes free, with the same result
+    every time; against PyTorch in 64 bits on the values that the cache holds."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    need = [(l + 63) // 64 for l in lens]
+    pages = sum(need)
+    order = torch.randperm(pages, generator=g, device="cuda").int()
+    table = torch.zeros((len(lens), max(need)), dtype=torch.int32, device="cuda")
+    for i, m in enumerate(need):
+        table[i, :m] = order[sum(need[:i]):sum(need[:i]) + m]
+    cache = pkg.KVCache.empty(pages, hkv, d, fmt)
+    for t in (cache.k, cache.v):
+        x = torch.randint(-90, 91, t.shape, generator=g, device="cuda", dtype=torch.int8)
+        t.copy_(x.view(torch.uint8) if fmt else (x.float() * 3).to(torch.float8_e4m3fn).view(torch.uint8))
+    cache.scales.copy_(torch.exp2(torch.randint(-8, -5, cache.scales.shape, generator=g, device="cuda").float()))
+    rows = len(lens) * new
+    q = torch.randn((rows, hq, d), generator=g, device="cuda").bfloat16()
+    cu = None if new == 1 else _i32(np.arange(len(lens) + 1) * new)
+    dl = _i32(lens)
+    o, lse = pkg.cache_attention(cache, table, dl, q, cu=cu)
+    pkg.hdp_device_status()
+    for _ in range(4):
+        o2, lse2 = pkg.cache_attention(cache, table, dl, q, cu=cu)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    whole = _i32(np.concatenate([[0], np.cumsum(lens)]))
+    k, v = pkg.cache_read(cache, table, dl, sum(lens), cu=whole)
+    grp = hq // hkv
+    for i, l in enumerate(lens):
+        for h in range(hkv):
+            kh, vh = (x[sum(lens[:i]):sum(lens[:i]) + l, h].double() for x in (k, v))
+            for r in range(new):
+                seen = l - new + 1 + r
+                qq = q[i * new + r, h * grp:(h + 1) * grp].double()
+                sc = qq @ kh[:seen].T * d ** -0.5
+                p = sc.softmax(1)
+                ref, a = p @ vh[:seen], p @ vh[:seen].abs()
+                ds = 2.0 ** -16 * (qq.abs() @ kh[:seen].abs().T * d ** -0.5).amax(1)
+                err = (o[i * new + r, h * grp:(h + 1) * grp].double() - ref).abs()
+                # as in _check_attention, with scales s of 2^-8 to 2^-6 and codes up to 270: where p s < 2^-13 max(p s),
+                # p < 2^-11 max p
+                top = p.amax(1, keepdim=True)
+                z = top * 2.0 ** -6 * (p < 2.0 ** -11 * top).double().sum(1, keepdim=True) * 270
+                tol = 2.0 ** -8 * ref.abs() + (2.0 ** -10 + 2.0 ** -18 + 2 * ds[:, None]) * a + 2.0 ** -23 * z
+                assert (err <= tol).all(), (i, h, r, float((err - tol).max()))
+                want = torch.logsumexp(sc, 1)
+                got = lse[h * grp:(h + 1) * grp, i * new + r].double()
+                assert ((got - want).abs() <= ds + 2.0 ** -20 * want.abs().clamp(min=1)).all()
+
+
+def test_many_rows_of_one_sequence():
+    """A prompt's rows all at once: 88 tiles of query rows over one cache."""
+    lens, new = [700, 40], [700, 3]
+    cache, table, ref = _random_cache(lens, 2, 64, 1, 15)
+    cu = np.array([0, 700, 703])
+    q = _bf16((703, 4, 64), 16)
+    o, lse = pkg.cache_attention(cache, _i32(table), _i32(lens), q.cuda(), cu=_i32(cu))
+    pkg.hdp_device_status()
+    _check_attention(o, lse, ref.attention(table, lens, _f64(q), cu, 0.125))
 
 
 def test_many_sequences_against_one_at_a_time():
@@ -396,6 +492,32 @@ def test_select_among_many_blocks(blocks, count):
     score[:3] = score[-4:] = float("inf")
     want = score.sort(descending=True, stable=True).indices[:count].sort().values
     assert torch.equal(got[0, 0].cpu().long(), want)
+
+
+@pytest.mark.parametrize("blocks,rows,count", [(3000, 30, 100), (20000, 30, 512), (1500, 140, 64), (6000, 30, 600)])
+def test_select_for_many_rows(blocks, rows, count):
+    """Rows enough to fill the device: scores and choice in one kernel, 1 to 8 CTAs a row; a count beyond what they
+    take goes through memory."""
+    d = 64
+    g = torch.Generator().manual_seed(blocks)
+    bounds = torch.randint(-90, 91, (blocks, 1, 2, d), generator=g).sort(2).values.to(torch.int8)
+    scales = torch.exp2(torch.randint(-1, 1, (blocks, 1, 2), generator=g).float())
+    cache = pkg.KVCache(torch.empty((blocks, 1, 64, d), dtype=torch.uint8, device="cuda"),
+                        torch.empty((blocks, 1, d, 64), dtype=torch.uint8, device="cuda"), scales.cuda(), bounds.cuda(), 0)
+    table = torch.randperm(blocks, generator=g).to(torch.int32)[None]
+    q = torch.randint(-127, 128, (rows, 3, d), generator=g).to(torch.bfloat16)
+    q[:, 0, 0] = 127  # whole numbers that the rounding of q leaves alone
+    length = blocks * 64 - 20
+    got = pkg.cache_select(cache, table.cuda(), _i32([length]), q.cuda(), count, cu=_i32([0, rows]), keep_first=2, keep_last=3)
+    pkg.hdp_device_status()
+    bd, sc = bounds[table[0].long(), 0].long(), scales[table[0].long(), 0, 0]
+    for r in range(rows):
+        have = (length - rows + r) // 64 + 1
+        x = q[r].long()
+        score = (bd[:have, 1] @ x.clamp(min=0).sum(0) + bd[:have, 0] @ x.clamp(max=0).sum(0)).float() * sc[:have]
+        score[:2] = score[have - 3:] = float("inf")
+        want = score.sort(descending=True, stable=True).indices[:count].sort().values
+        assert torch.equal(got[r, 0].cpu().long(), want), r
 
 
 @pytest.mark.parametrize("fmt", FMTS)
