@@ -79,6 +79,18 @@ __device__ __forceinline__ uint32_t code_pair(float a, float b) {
   }
 }
 
+// Four codes in a word.
+template <int FMT>
+__device__ __forceinline__ uint32_t code_quad(float a, float b, float c, float d) {
+  if constexpr (FMT == HDP_CACHE_INT8) {
+    const uint32_t ab = __byte_perm(__float_as_uint(a + 12582912.f), __float_as_uint(b + 12582912.f), 0x0040);
+    const uint32_t cd = __byte_perm(__float_as_uint(c + 12582912.f), __float_as_uint(d + 12582912.f), 0x0040);
+    return __byte_perm(ab, cd, 0x5410);
+  } else {
+    return __byte_perm(code_pair<FMT>(a, b), code_pair<FMT>(c, d), 0x5410);
+  }
+}
+
 template <int FMT>
 __device__ __forceinline__ float2 value_pair(uint32_t two) {
   if constexpr (FMT == HDP_CACHE_INT8) {
@@ -95,7 +107,7 @@ __device__ __forceinline__ float2 value_pair(uint32_t two) {
 template <int FMT>
 __device__ __forceinline__ uint32_t rescale4(uint32_t x, float ratio) {
   const float2 a = value_pair<FMT>(x), b = value_pair<FMT>(x >> 16);
-  return code_pair<FMT>(a.x * ratio, a.y * ratio) | (code_pair<FMT>(b.x * ratio, b.y * ratio) << 16);
+  return code_quad<FMT>(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
 }
 
 // Exponent of the smallest power of two 2^e, e >= -126, with |x| <= M 2^e, for
@@ -108,6 +120,7 @@ __device__ __forceinline__ int scale_exponent(uint32_t abs_bits) {
 }
 
 __device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); }
+__device__ __forceinline__ uint32_t bits(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); }
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
@@ -261,7 +274,7 @@ __device__ __forceinline__ void append_rows(const CacheView& c, const Touched& t
   constexpr int P = D / 16;
   using Pl = Place<D, W == 0>;
   __shared__ uint32_t s_amax[4];
-  __shared__ float s_bound[W == 0 ? 4 : 1][2][D];
+  __shared__ __align__(16) __nv_bfloat16 s_bound[W == 0 ? 4 : 1][2][D];
   const Pl pl;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const size_t ph = static_cast<size_t>(page) * c.hkv + head;
@@ -275,15 +288,10 @@ __device__ __forceinline__ void append_rows(const CacheView& c, const Touched& t
   const float before = t.fresh ? 0.f : c.scales[2 * ph + W];
 
   // Largest magnitudes, as bf16 bits: their order is the values' order, with
-  // infinity and NaN (>= 0x7f80) on top.
+  // infinity and NaN (>= 0x7f80) on top.  K takes them from the channel-wise
+  // minimum and maximum, which keep a NaN.
   uint32_t m = 0;
-#pragma unroll
-  for (int p = 0; p < P; ++p)
-    m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[p].x & 0x7fff7fffu, x[p].y & 0x7fff7fffu),
-                             __vmaxu2(x[p].z & 0x7fff7fffu, x[p].w & 0x7fff7fffu)));
-  uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-  if (lane == 0) s_amax[warp] = top;
-  if constexpr (W == 0) {  // channel-wise minimum and maximum
+  if constexpr (W == 0) {
     const __nv_bfloat162 inf = __halves2bfloat162(__ushort_as_bfloat16(0x7f80), __ushort_as_bfloat16(0x7f80));
     __nv_bfloat162 lo[4] = {inf, inf, inf, inf}, hi[4];
 #pragma unroll
@@ -295,8 +303,8 @@ __device__ __forceinline__ void append_rows(const CacheView& c, const Touched& t
         const uint32_t q[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          lo[i] = __hmin2(lo[i], as_bf2(q[i]));
-          hi[i] = __hmax2(hi[i], as_bf2(q[i]));
+          lo[i] = __hmin2_nan(lo[i], as_bf2(q[i]));
+          hi[i] = __hmax2_nan(hi[i], as_bf2(q[i]));
         }
       }
     }
@@ -304,18 +312,24 @@ __device__ __forceinline__ void append_rows(const CacheView& c, const Touched& t
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
       for (int o = Pl::kLanes; o < 32; o *= 2) {
-        lo[i] = __hmin2(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
-        hi[i] = __hmax2(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+        lo[i] = __hmin2_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+        hi[i] = __hmax2_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
       }
+      // a warp may have no row at all: +inf and -inf say nothing then
+      if (__hgt2_mask(lo[i], hi[i]) == 0u) m = __vmaxu2(m, __vmaxu2(bits(lo[i]) & 0x7fff7fffu, bits(hi[i]) & 0x7fff7fffu));
     }
     if (lane < Pl::kLanes) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        *reinterpret_cast<float2*>(&s_bound[warp][0][pl.ch + 2 * i]) = __bfloat1622float2(lo[i]);
-        *reinterpret_cast<float2*>(&s_bound[warp][1][pl.ch + 2 * i]) = __bfloat1622float2(hi[i]);
-      }
+      *reinterpret_cast<uint4*>(&s_bound[warp][0][pl.ch]) = make_uint4(bits(lo[0]), bits(lo[1]), bits(lo[2]), bits(lo[3]));
+      *reinterpret_cast<uint4*>(&s_bound[warp][1][pl.ch]) = make_uint4(bits(hi[0]), bits(hi[1]), bits(hi[2]), bits(hi[3]));
     }
+  } else {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[p].x & 0x7fff7fffu, x[p].y & 0x7fff7fffu),
+                               __vmaxu2(x[p].z & 0x7fff7fffu, x[p].w & 0x7fff7fffu)));
   }
+  uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+  if (lane == 0) s_amax[warp] = top;
   __syncthreads();
 
   top = max(max(s_amax[0], s_amax[1]), max(s_amax[2], s_amax[3]));
@@ -346,8 +360,8 @@ __device__ __forceinline__ void append_rows(const CacheView& c, const Touched& t
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const uint4 y = x[p];
-    code[p][0] = code_pair<FMT>(bf_lo(y.x) * inv, bf_hi(y.x) * inv) | (code_pair<FMT>(bf_lo(y.y) * inv, bf_hi(y.y) * inv) << 16);
-    code[p][1] = code_pair<FMT>(bf_lo(y.z) * inv, bf_hi(y.z) * inv) | (code_pair<FMT>(bf_lo(y.w) * inv, bf_hi(y.w) * inv) << 16);
+    code[p][0] = code_quad<FMT>(bf_lo(y.x) * inv, bf_hi(y.x) * inv, bf_lo(y.y) * inv, bf_hi(y.y) * inv);
+    code[p][1] = code_quad<FMT>(bf_lo(y.z) * inv, bf_hi(y.z) * inv, bf_lo(y.w) * inv, bf_hi(y.w) * inv);
   }
   if constexpr (W == 0) {
 #pragma unroll
@@ -361,10 +375,9 @@ __device__ __forceinline__ void append_rows(const CacheView& c, const Touched& t
     if (threadIdx.x < D) {
       const int i = threadIdx.x;
       const float unit = FMT == HDP_CACHE_INT8 ? inv : inv * 0.25f;
-      float a = fminf(fminf(s_bound[0][0][i], s_bound[1][0][i]), fminf(s_bound[2][0][i], s_bound[3][0][i]));
-      float b = fmaxf(fmaxf(s_bound[0][1][i], s_bound[1][1][i]), fmaxf(s_bound[2][1][i], s_bound[3][1][i]));
-      a = floorf(a * unit);
-      b = ceilf(b * unit);
+      const __nv_bfloat16 lo = __hmin(__hmin(s_bound[0][0][i], s_bound[1][0][i]), __hmin(s_bound[2][0][i], s_bound[3][0][i]));
+      const __nv_bfloat16 hi = __hmax(__hmax(s_bound[0][1][i], s_bound[1][1][i]), __hmax(s_bound[2][1][i], s_bound[3][1][i]));
+      float a = floorf(__bfloat162float(lo) * unit), b = ceilf(__bfloat162float(hi) * unit);
       int8_t* out = c.bounds + ph * (2 * D) + i;
       if (!t.fresh) {
         a = fminf(a, floorf(static_cast<float>(out[0]) * ratio));
@@ -470,8 +483,8 @@ __global__ void __launch_bounds__(kThreads) k_cache_append_one(CacheView c, cons
   __syncwarp();  // the new row goes over them
   if (!on) return;
   const float f[8] = {bf_lo(x.x), bf_hi(x.x), bf_lo(x.y), bf_hi(x.y), bf_lo(x.z), bf_hi(x.z), bf_lo(x.w), bf_hi(x.w)};
-  const uint2 code = make_uint2(code_pair<FMT>(f[0] * inv, f[1] * inv) | (code_pair<FMT>(f[2] * inv, f[3] * inv) << 16),
-                                code_pair<FMT>(f[4] * inv, f[5] * inv) | (code_pair<FMT>(f[6] * inv, f[7] * inv) << 16));
+  const uint2 code = make_uint2(code_quad<FMT>(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                                code_quad<FMT>(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
   if (w == 0) {
     *reinterpret_cast<uint2*>(codes + t * D + ch) = code;
     const float unit_inv = FMT == HDP_CACHE_INT8 ? inv : inv * 0.25f;
