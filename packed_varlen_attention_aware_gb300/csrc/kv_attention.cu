@@ -142,6 +142,12 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t x) {
 
 constexpr int kSeqs = 512;  // sequences whose places are kept in shared memory
 
+template <int FMT>
+__device__ __forceinline__ uint4 without_nan(uint4 x) {
+  return make_uint4(without_nan<FMT>(x.x), without_nan<FMT>(x.y), without_nan<FMT>(x.z), without_nan<FMT>(x.w));
+}
+__device__ __forceinline__ uint32_t word(const uint4& x, int k) { return k == 0 ? x.x : k == 1 ? x.y : k == 2 ? x.z : x.w; }
+
 // A sequence's rows in the call, its tokens, and the position of its first row.
 struct SeqPlace {
   int row0, n, len, p0;
@@ -364,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
   constexpr int kKeyChunks = D / 64;              // 16-byte chunks that a lane has of a key
   constexpr int kMt = D / 16;
   constexpr int kRows = 8 * NT;
+  constexpr int kTogether = 2;  // 16-row tiles whose chains of products are interleaved
   using Cur = Cursor<SPARSE, NT>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   auto& sm = *reinterpret_cast<Shared<NT, SPARSE>*>(smem_raw);
@@ -646,22 +653,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
           const uint4* kx = reinterpret_cast<const uint4*>(sm.ring[warp] + slot * kHalf) + lane;
           float s[NT][4][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 4; i += kTogether) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int h = 0; h < kTogether; ++h)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) s[t][i][k] = 0.f;
+              for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[t][i + h][k] = 0.f;
 #pragma unroll
             for (int j = 0; j < kKeyChunks; ++j) {
-              const uint4 u = kx[((2 * i) * kKeyChunks + j) * 32], w = kx[((2 * i + 1) * kKeyChunks + j) * 32];
-              const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+              uint4 u[kTogether], w[kTogether];
+#pragma unroll
+              for (int h = 0; h < kTogether; ++h) {
+                u[h] = kx[((2 * (i + h)) * kKeyChunks + j) * 32];
+                w[h] = kx[((2 * (i + h) + 1) * kKeyChunks + j) * 32];
+              }
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                uint32_t a0, a1, a2, a3;
-                decode4<FMT>(uw[k], a0, a2);
-                decode4<FMT>(ww[k], a1, a3);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) mma16816(s[t][i], a0, a1, a2, a3, qf[t][j * 4 + k][0], qf[t][j * 4 + k][1]);
+                for (int h = 0; h < kTogether; ++h) {
+                  uint32_t a0, a1, a2, a3;
+                  decode4<FMT>(word(u[h], k), a0, a2);
+                  decode4<FMT>(word(w[h], k), a1, a3);
+#pragma unroll
+                  for (int t = 0; t < NT; ++t)
+                    mma16816(s[t][i + h], a0, a1, a2, a3, qf[t][j * 4 + k][0], qf[t][j * 4 + k][1]);
+                }
               }
             }
           }
@@ -726,23 +743,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
         if (seen) {
           const uint4* vx = reinterpret_cast<const uint4*>(sm.ring[warp] + slot * kHalf) + lane;
 #pragma unroll
-          for (int i = 0; i < kMt; ++i) {
-            const uint4 u = vx[(2 * i) * 32], w = vx[(2 * i + 1) * 32];
-            uint32_t uw[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
-            if (masked) {
+          for (int i = 0; i < kMt; i += kTogether) {
+            uint4 u[kTogether], w[kTogether];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uw[k] = without_nan<FMT>(uw[k]);
-                ww[k] = without_nan<FMT>(ww[k]);
+            for (int h = 0; h < kTogether; ++h) {
+              u[h] = vx[(2 * (i + h)) * 32];
+              w[h] = vx[(2 * (i + h) + 1) * 32];
+              if (masked) {
+                u[h] = without_nan<FMT>(u[h]);
+                w[h] = without_nan<FMT>(w[h]);
               }
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              uint32_t a0, a1, a2, a3;
-              decode4<FMT>(uw[k], a0, a2);
-              decode4<FMT>(ww[k], a1, a3);
 #pragma unroll
-              for (int t = 0; t < NT; ++t) mma16816(acc[t][i], a0, a1, a2, a3, pf[t][k][0], pf[t][k][1]);
+              for (int h = 0; h < kTogether; ++h) {
+                uint32_t a0, a1, a2, a3;
+                decode4<FMT>(word(u[h], k), a0, a2);
+                decode4<FMT>(word(w[h], k), a1, a3);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma16816(acc[t][i + h], a0, a1, a2, a3, pf[t][k][0], pf[t][k][1]);
+              }
             }
           }
         }
