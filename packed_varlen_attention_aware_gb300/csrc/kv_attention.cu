@@ -856,6 +856,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
     }
     copies_wait<0>();
   }
+  // Even a call without work ends after the kernels in front of it: what comes
+  // next in the stream (another thread's kernel, perhaps) waits for this one only.
+  if (p.dynamic) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
@@ -866,64 +869,105 @@ __global__ void k_cache_attention_start(const AttnParams p) {
 }
 
 // Joins the parts of units that several pieces share.  A CTA has every n-th
-// open unit (n CTAs): its warps take rows of up to kAlone parts in turn, and
-// share those of larger units (a 2M-token sequence leaves several hundred parts
-// for each head), all rows at once.
+// open unit (n CTAs), and its warps take rows of up to kAlone parts in turn.  A
+// 2M-token sequence leaves 600 parts for each of its few heads: the rows of such
+// units are dealt to all CTAs, whose warps then share a row's parts (that call:
+// 646 us with each unit's CTA joining its rows itself, 636 us so).
 constexpr int kJoinWarps = 16;
 template <int D, int NT>
 __global__ void __launch_bounds__(kJoinWarps * 32, 1) k_cache_attention_join(const AttnParams p, int pieces) {
   constexpr int kRows = 8 * NT;
-  constexpr int kAlone = 48;
+  constexpr int kAlone = 48;  // most parts of a row that a warp joins alone
+  constexpr int kFew = 256;   // most parts of rows that a CTA joins at once
+  // Two units share at most one piece, so n units of more than kAlone parts take
+  // more than n (kAlone - 1) pieces; of the others a CTA has one for each
+  // gridDim.x pieces.  The host keeps both below this.
+  constexpr int kMostShared = 192;
   constexpr int V = D / 32;
-  static_assert(kRows <= kJoinWarps, "a warp for each row");
   __shared__ __align__(16) float s_x[kJoinWarps][D];
   __shared__ float s_lse[kJoinWarps];
+  __shared__ int4 s_shared[kMostShared][2], s_own[kMostShared][2];  // shared units, and this CTA's others
+  __shared__ int s_n, s_own_n;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) s_n = s_own_n = 0;
+  __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int made = __ldcg(p.head + (p.dynamic ? 0 : 2));
-  int nth = 0;
-  for (int base = blockIdx.x; base < pieces; base += gridDim.x * 32) {
-    const int mine = min(base + lane * static_cast<int>(gridDim.x), pieces - 1);
-    const int4 a = __ldcg(reinterpret_cast<const int4*>(p.open + mine));  // before `made` is here
-    const int4 b = __ldcg(reinterpret_cast<const int4*>(p.open + mine) + 1);
-    if (base >= made) break;
-    unsigned todo = __ballot_sync(0xffffffffu, base + lane * gridDim.x < min(pieces, made) && a.x != 0);
-    while (todo) {
-      const int bit = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const int m = __shfl_sync(0xffffffffu, a.x, bit), e = __shfl_sync(0xffffffffu, a.y, bit);
-      const int row0 = __shfl_sync(0xffffffffu, a.z, bit), head = __shfl_sync(0xffffffffu, a.w, bit);
-      const int nrows = __shfl_sync(0xffffffffu, b.x, bit), rr0 = __shfl_sync(0xffffffffu, b.y, bit);
-      auto at = [&](int k, int r) { return (static_cast<size_t>(e + k) * 2 + (k == 0 ? 1 : 0)) * kRows + r; };
-      float x[V];
-      if (m <= kAlone) {
-        for (int r = 0; r < nrows; ++r) {
-          if (nth++ % kJoinWarps != warp) continue;
-          const float lse2 = join_row<D>(
-              m, lane, x, [&](int k) { return __ldcg(p.part_lse + at(k, r)); },
-              [&](int k) { return p.part + at(k, r) * D; });
-          write_o<D>(p, row0, head, rr0 + r, x, lse2 * kLn2, lane);
-        }
-        continue;
-      }
-      // `each` warps have one row, a run of its parts each
-      const int each = kJoinWarps >> (32 - __clz(nrows - 1));
-      const int r = warp / each, run = warp - r * each;
-      if (r < nrows) {
-        const int k0 = static_cast<int>(static_cast<long long>(m) * run / each);
-        const int k1 = static_cast<int>(static_cast<long long>(m) * (run + 1) / each);
-        const float part = join_row<D>(
-            k1 - k0, lane, x, [&](int k) { return __ldcg(p.part_lse + at(k0 + k, r)); },
-            [&](int k) { return p.part + at(k0 + k, r) * D; });
+  const int made = min(pieces, __ldcg(p.head + (p.dynamic ? 0 : 2)));
+  auto at = [&](int e, int k, int r) { return (static_cast<size_t>(e + k) * 2 + (k == 0 ? 1 : 0)) * kRows + r; };
+
+  // This CTA's open units, and all shared ones where the units are listed as they
+  // came; where each piece has an entry (1,216 of them, which 152 CTAs reading all
+  // would take 4 us for), a CTA keeps to its own.
+  const int stride = p.dynamic ? 1 : gridDim.x, origin = p.dynamic ? 0 : blockIdx.x;
+  constexpr int kScan = 2;
+  for (int base = 0; base == 0 || origin + base * stride < made; base += kScan * kJoinWarps * 32) {
+    int4 a[kScan], b[kScan];  // the first loads do not wait for the units' number
 #pragma unroll
-        for (int i = 0; i < V; ++i) s_x[warp][lane * V + i] = x[i];
+    for (int u = 0; u < kScan; ++u) {
+      const int i = origin + (base + u * kJoinWarps * 32 + static_cast<int>(threadIdx.x)) * stride;
+      a[u] = b[u] = make_int4(0, 0, 0, 0);
+      if (i < pieces) {
+        a[u] = __ldcg(reinterpret_cast<const int4*>(p.open + i));
+        b[u] = __ldcg(reinterpret_cast<const int4*>(p.open + i) + 1);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kScan; ++u) {
+      const int i = origin + (base + u * kJoinWarps * 32 + static_cast<int>(threadIdx.x)) * stride;
+      if (i >= made || a[u].x == 0) continue;
+      const bool shared = a[u].x > kAlone;
+      if (!shared && i % gridDim.x != blockIdx.x) continue;
+      const int n = atomicAdd(shared ? &s_n : &s_own_n, 1);
+      if (n >= kMostShared) continue;  // cannot be (see there)
+      int4* to = shared ? s_shared[n] : s_own[n];
+      to[0] = a[u];
+      to[1] = b[u];
+    }
+  }
+  __syncthreads();
+
+  const int own = min(s_own_n, kMostShared);
+  int nth = 0;
+  for (int q = 0; q < own; ++q) {
+    const int4 a = s_own[q][0], b = s_own[q][1];
+    for (int r = 0; r < b.x; ++r) {
+      if (nth++ % kJoinWarps != warp) continue;
+      float x[V];
+      const float lse2 = join_row<D>(
+          a.x, lane, x, [&](int k) { return __ldcg(p.part_lse + at(a.y, k, r)); },
+          [&](int k) { return p.part + at(a.y, k, r) * D; });
+      write_o<D>(p, a.z, a.w, b.y + r, x, lse2 * kLn2, lane);
+    }
+  }
+
+  const int n = min(s_n, kMostShared);
+  for (int q = 0; q < n; ++q) {
+    const int4 a = s_shared[q][0], b = s_shared[q][1];
+    const int m = a.x, e = a.y, nrows = b.x;
+    int rank = 0;  // of its first piece: the same in every CTA, whose lists differ in order
+    for (int z = lane; z < n; z += 32) rank += s_shared[z][0].y < e;
+    rank = __reduce_add_sync(0xffffffffu, rank);
+    // rows that a CTA joins at once, and warps for each
+    const int rows = m > kFew ? 1 : min(kJoinWarps, 1 << (32 - __clz(nrows - 1)) % 32), each = kJoinWarps / rows;
+    const int nr = warp / each, run = warp - nr * each;
+    for (int r0 = 0; r0 < nrows; r0 += rows) {
+      if (p.dynamic && (rank * nrows + r0) % static_cast<int>(gridDim.x) != static_cast<int>(blockIdx.x)) continue;
+      const int r = r0 + nr;
+      float x[V];
+      if (r < nrows) {
+        const int k0 = m * run / each, k1 = m * (run + 1) / each;
+        const float part = join_row<D>(
+            k1 - k0, lane, x, [&](int k) { return __ldcg(p.part_lse + at(e, k0 + k, r)); },
+            [&](int k) { return p.part + at(e, k0 + k, r) * D; });
+#pragma unroll
+        for (int v = 0; v < V; ++v) s_x[warp][lane * V + v] = x[v];
         if (lane == 0) s_lse[warp] = part;
       }
       __syncthreads();
       if (r < nrows && run == 0) {
         const float lse2 = join_row<D>(each, lane, x, [&](int k) { return s_lse[warp + k]; },
                                        [&](int k) { return &s_x[warp + k][0]; });
-        write_o<D>(p, row0, head, rr0 + r, x, lse2 * kLn2, lane);
+        write_o<D>(p, a.z, a.w, b.y + r, x, lse2 * kLn2, lane);
       }
       __syncthreads();  // the sums have been read
     }
@@ -991,6 +1035,8 @@ hdp_status_t launch(const AttnParams& p, int device, int ctas, cudaStream_t st) 
     if (device < kDevices) ready[device].store(true, std::memory_order_relaxed);
   }
   const int pieces = ctas * kWarps * (p.dynamic ? 1 + kMorePieces : 1);
+  if (pieces > 47 * 192)  // k_cache_attention_join's lists; a device of over 188 SMs
+    return fail(HDP_ERR_UNSUPPORTED, "hdp_cache_attention: too many SMs");
   if (p.dynamic) {
     k_cache_attention_start<<<1, 32, 0, st>>>(p);
     note_launch();

@@ -326,6 +326,22 @@ def test_runs_whose_ends_are_handed_out(fmt, hq, hkv, d, lens, new):
     for _ in range(4):
         o2, lse2 = pkg.cache_attention(cache, table, dl, q, cu=cu)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    # captured and replayed, beside an eager call on another stream, and with other queries in place
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    q_in = q.clone()
+    with torch.cuda.graph(graph):
+        og, lg = pkg.cache_attention(cache, table, dl, q_in, cu=cu)
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        graph.replay()
+        o2, lse2 = pkg.cache_attention(cache, table, dl, q, cu=cu, stream=side)
+        side.synchronize()
+        torch.cuda.current_stream().synchronize()
+        assert torch.equal(o, og) and torch.equal(lse, lg) and torch.equal(o, o2) and torch.equal(lse, lse2)
+    q_in.copy_(-q)
+    graph.replay()
+    o2, lse2 = pkg.cache_attention(cache, table, dl, -q, cu=cu)
+    assert torch.equal(o2, og) and torch.equal(lse2, lg) and not torch.equal(o, og)
     whole = _i32(np.concatenate([[0], np.cumsum(lens)]))
     k, v = pkg.cache_read(cache, table, dl, sum(lens), cu=whole)
     grp = hq // hkv
@@ -590,6 +606,42 @@ def test_pages_and_lengths_outside_are_reported_and_never_touched():
     assert (b == _i32([0, 2, 3])).all()
     with pytest.raises(pkg.HdpError):
         pkg.hdp_device_status()
+
+
+def test_two_threads_on_one_stream():
+    """Calls from two threads interleave on the default stream; each has its own workspace."""
+    import threading
+
+    lens = [120000, 90000]
+    pages = sum((l + 63) // 64 for l in lens)
+    cache = pkg.KVCache.empty(pages, 8, 64, 1)
+    cache.k.random_(0, 256)
+    cache.v.random_(0, 256)
+    cache.scales.fill_(2.0 ** -6)
+    cache.bounds.random_(-100, 100)
+    table = torch.zeros((2, 1875), dtype=torch.int32, device="cuda")
+    table[0] = torch.arange(1875)
+    table[1, :1407] = torch.arange(1875, pages)
+    qs = [_bf16((2, 16, 64), i).cuda() for i in range(2)]
+    dl = _i32(lens)
+    want = [(*pkg.cache_attention(cache, table, dl, q), pkg.cache_select(cache, table, dl, q, 50)) for q in qs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def many(i):
+        for _ in range(60):
+            got = (*pkg.cache_attention(cache, table, dl, qs[i]), pkg.cache_select(cache, table, dl, qs[i], 50))
+            torch.cuda.current_stream().synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=many, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    pkg.hdp_device_status()
 
 
 def test_another_stream_and_no_rows():
