@@ -322,7 +322,7 @@ typedef struct {
  * outside [0, num_pages) is never touched (its tokens are not written, read
  * as zeros, and are masked in the attention); both are reported by the next
  * hdp_device_status as INVALID_ARGUMENT.  Table entries beyond a sequence's
- * last block are not read.
+ * last block may hold anything.
  * Host-side errors: INVALID_ARGUMENT for NULL pointers, sizes, alignment and
  * workspaces; UNSUPPORTED for a d other than 64 and 128.
  */

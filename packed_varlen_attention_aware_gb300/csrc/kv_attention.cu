@@ -20,15 +20,21 @@
 //   likewise.  The codes become fp16 exactly (int8 by the exponent of 1024,
 //   e4m3 by the conversion instruction); the cache's order of bytes is the
 //   fragments' order.  The query row is shifted by a power of two to
-//   [2^14, 2^15), which is exact in fp16 down to 2^-38 of its largest element
+//   [2^14, 2^15), which is exact in fp16 down to 2^-31 of its largest element
 //   (below, the error is at most 2^-39 of it).  P <= 1 is rounded to fp16:
-//   half a step is 2^-12 of a probability (2^-25 absolute below 2^-14), 1/16 of
+//   half a step is 2^-11 of a probability (2^-25 absolute below 2^-14), 1/8 of
 //   the bf16 rounding of the output.  All sums are fp32.
 //   Softmax.  The reference exponents are whole numbers: m of the row sum, M of
 //   the output, which also takes in the V scales' exponents; every rescaling is
 //   then by a power of two, and blocks with very different V scales lose nothing.
 //   Joining.  A piece leaves a normalised (O, LSE) for a unit that it shares with
 //   its neighbours; a second small kernel joins them in the order of the keys.
+//
+// Measured (one GB300, in a captured graph): one token over 2M cached ones, 8 kv
+// heads of 128, 628 to 636 us (4.3 GB, 6.8 TB/s); 64 sequences of 256 to 29K
+// tokens 147 us (843 MB, 5.7 TB/s: while the runs stream, a block takes a warp
+// 5.2K cycles, 7.2 TB/s; the rest is the start and the ends); 64 x 32 chosen
+// blocks 56 us (270 MB).
 #include <cuda_fp16.h>
 
 #include <atomic>
