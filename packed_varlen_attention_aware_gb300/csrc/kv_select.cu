@@ -209,15 +209,22 @@ __global__ void __launch_bounds__(kScoreThreads, 4) k_cache_scores(const SelectP
 // Chooses the `count` largest of a CTA's keys, the earlier of equal ones, and
 // calls emit(place, i) for each of a thread's that is chosen.  Item i of a
 // thread comes after all items of the warps before its own, and after items of
-// its warp with a smaller (i, lane).  key_at(i) is its key, has(i) whether there
-// is one; at least `count` of them are there.
+// its warp with a smaller (i, lane).  key_at(i) is its key or 0, has(i) whether
+// there is one; at least `count` of them are there.
+// The first WARPS warps of the CTA take part (32,768 blocks, 8 heads: 31 us with
+// 16 warps and 8 keys a thread, 32 with 32, 35 with 8).
 struct TopShared {
   int4 count[2][32];
   uint32_t low[32], high[32];
 };
-template <bool PACK, class K, class H, class E>
+template <int WARPS>
+__device__ __forceinline__ void warps_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+}
+template <int WARPS, bool PACK, class K, class H, class E>
 __device__ __forceinline__ void choose(TopShared& sm, int items, int count, int forced, K key_at, H has, E emit) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool one = lane < WARPS;  // this lane has a warp's entry to add up
   uint32_t low = 0xffffffffu, high = 0;
 #pragma unroll
   for (int i = 0; i < items; ++i) {
@@ -233,9 +240,9 @@ __device__ __forceinline__ void choose(TopShared& sm, int items, int count, int 
     sm.low[warp] = low;
     sm.high[warp] = high;
   }
-  __syncthreads();
-  low = __reduce_min_sync(0xffffffffu, sm.low[lane]);
-  high = __reduce_max_sync(0xffffffffu, sm.high[lane]);
+  warps_sync<WARPS>();
+  low = __reduce_min_sync(0xffffffffu, one ? sm.low[lane] : 0xffffffffu);
+  high = __reduce_max_sync(0xffffffffu, one ? sm.high[lane] : 0u);
   // the largest x with at least `count` keys >= x: between low (all of them)
   // and the largest key that is not forced, unless the forced ones are enough
   if (forced >= count) low = high = kForced;
@@ -249,7 +256,7 @@ __device__ __forceinline__ void choose(TopShared& sm, int items, int count, int 
     int n2 = 0;
 #pragma unroll
     for (int i = 0; i < items; ++i) {
-      const uint32_t k = has(i) ? key_at(i) : 0u;  // cuts are above low, so above 0
+      const uint32_t k = key_at(i);  // a missing key is 0, and cuts are above low, so above 0
       n12 += k >= m1;
       n2 += k >= m2;
       n3 += k >= m3;
@@ -262,8 +269,8 @@ __device__ __forceinline__ void choose(TopShared& sm, int items, int count, int 
     }
     n3 = __reduce_add_sync(0xffffffffu, n3);
     if (lane == 0) sm.count[turn][warp] = make_int4(n12, n2, n3, 0);
-    __syncthreads();
-    const int4 c = sm.count[turn][lane];
+    warps_sync<WARPS>();
+    const int4 c = one ? sm.count[turn][lane] : make_int4(0, 0, 0, 0);
     turn ^= 1;
     int c1 = __reduce_add_sync(0xffffffffu, c.x), c2;
     if (PACK) {
@@ -299,10 +306,10 @@ __device__ __forceinline__ void choose(TopShared& sm, int items, int count, int 
     above += __popc(__ballot_sync(0xffffffffu, in && k > low));
     equal += __popc(__ballot_sync(0xffffffffu, in && k == low));
   }
-  __syncthreads();  // the search's last counts have been read
+  warps_sync<WARPS>();  // the search's last counts have been read
   if (lane == 0) sm.count[0][warp] = make_int4(above, equal, 0, 0);
-  __syncthreads();
-  const int a = sm.count[0][lane].x, e = sm.count[0][lane].y;
+  warps_sync<WARPS>();
+  const int a = one ? sm.count[0][lane].x : 0, e = one ? sm.count[0][lane].y : 0;
   const int take = count - __reduce_add_sync(0xffffffffu, a);  // of the equal ones
   int before_above = __reduce_add_sync(0xffffffffu, lane < warp ? a : 0);
   int before_equal = __reduce_add_sync(0xffffffffu, lane < warp ? e : 0);
@@ -330,13 +337,14 @@ __device__ __forceinline__ int forced_in(const SelectParams& p, int have, int fr
 // the shared memory of the first, which chooses among those; no CTA waits for
 // another during a search.
 constexpr int kSelectBlocks = 4 * kTopThreads;
+constexpr int kChooseWarps = 16;
 constexpr int kTopCtas = 8;
 constexpr int kTopMost = 512;  // largest count for a cluster
 template <int D>
 __global__ void __launch_bounds__(kTopThreads) k_cache_select(const SelectParams p, int ctas, bool scored) {
   namespace cg = cooperative_groups;
   using S = Scorer<D, kTopThreads>;
-  constexpr int kItems = kSelectBlocks / kTopThreads;
+  constexpr int kItems = kSelectBlocks / (kChooseWarps * 32);
   __shared__ typename S::Shared s_query;
   __shared__ TopShared s_top;
   __shared__ union {
@@ -370,16 +378,24 @@ __global__ void __launch_bounds__(kTopThreads) k_cache_select(const SelectParams
     __syncthreads();
   }
   const uint32_t* keys = p.keys + static_cast<size_t>(unit) * p.c.max_pages + from;
-  const int items = (n + kTopThreads - 1) / kTopThreads;  // a warp has a run of items * 32 keys
+  // The choice is up to kChooseWarps warps, which have a run of items * 32 keys each.
+  const bool on = warp < kChooseWarps;
+  const int items = (n + kChooseWarps * 32 - 1) / (kChooseWarps * 32);
   const int base = warp * items * 32 + lane;
-  auto has = [&](int i) { return i < items && base + i * 32 < n; };
   uint32_t key[kItems];
+  unsigned there = 0;  // bit i: item i is one
 #pragma unroll
-  for (int i = 0; i < kItems; ++i) key[i] = !has(i) ? 0u : scored ? __ldcg(keys + base + i * 32) : sm.keys[base + i * 32];
+  for (int i = 0; i < kItems; ++i) {
+    const bool in = on && i < items && base + i * 32 < n;
+    there |= static_cast<unsigned>(in) << i;
+    key[i] = !in ? 0u : scored ? __ldcg(keys + base + i * 32) : sm.keys[base + i * 32];
+  }
   auto key_at = [&](int i) { return key[i]; };
+  auto has = [&](int i) { return (there >> i & 1) != 0; };
   const int forced = forced_in(p, have, from, to);
   if (ctas == 1) {
-    choose<true>(s_top, kItems, p.count, forced, key_at, has, [&](int at, int i) { out[at] = base + i * 32; });
+    if (on)
+      choose<kChooseWarps, true>(s_top, kItems, p.count, forced, key_at, has, [&](int at, int i) { out[at] = base + i * 32; });
     return;
   }
   uint32_t* to_key = cluster.map_shared_rank(sm.passed.key, 0) + rank * kTopMost;
@@ -389,26 +405,30 @@ __global__ void __launch_bounds__(kTopThreads) k_cache_select(const SelectParams
     to_block[at] = from + base + i * 32;
   };
   cluster.sync();  // the first CTA has its keys in registers
-  if (n <= p.count) {
+  if (on) {
+    if (n <= p.count) {
 #pragma unroll
-    for (int i = 0; i < kItems; ++i)
-      if (has(i)) pass_on(base + i * 32, i);
-  } else {
-    choose<true>(s_top, kItems, p.count, forced, key_at, has, pass_on);
+      for (int i = 0; i < kItems; ++i)
+        if (has(i)) pass_on(base + i * 32, i);
+    } else {
+      choose<kChooseWarps, true>(s_top, kItems, p.count, forced, key_at, has, pass_on);
+    }
   }
   if (threadIdx.x == 0) cluster.map_shared_rank(s_n, 0)[rank] = min(n, p.count);
   cluster.sync();
-  if (rank != 0) return;
+  if (rank != 0 || !on) return;
   // slots of kTopMost for each CTA, in the order of the blocks
   const int at = warp * (kItems * 32) + lane;
-  auto passed = [&](int i) {
-    const int x = at + i * 32, c = x / kTopMost;
-    return c < ctas && x % kTopMost < s_n[c];
-  };
+  there = 0;
 #pragma unroll
-  for (int i = 0; i < kItems; ++i) key[i] = passed(i) ? sm.passed.key[at + i * 32] : 0u;
-  choose<true>(s_top, kItems, p.count, forced_in(p, have, 0, have), key_at, passed,
-               [&](int place, int i) { out[place] = sm.passed.block[at + i * 32]; });
+  for (int i = 0; i < kItems; ++i) {
+    const int x = at + i * 32, c = x / kTopMost;
+    const bool in = c < ctas && x % kTopMost < s_n[c];
+    there |= static_cast<unsigned>(in) << i;
+    key[i] = in ? sm.passed.key[x] : 0u;
+  }
+  choose<kChooseWarps, true>(s_top, kItems, p.count, forced_in(p, have, 0, have), key_at, has,
+                             [&](int place, int i) { out[place] = sm.passed.block[at + i * 32]; });
 }
 
 // The choice among keys in memory, for more blocks or a larger count than a
@@ -430,7 +450,7 @@ __global__ void __launch_bounds__(kTopThreads) k_cache_top(const SelectParams p)
   const int items = (have + kTopThreads - 1) / kTopThreads;
   const int base = warp * items * 32 + lane;
   auto has = [&](int i) { return i < items && base + i * 32 < have; };
-  choose<false>(sm, items, p.count, forced_in(p, have, 0, have),
+  choose<kTopThreads / 32, false>(sm, items, p.count, forced_in(p, have, 0, have),
                 [&](int i) { return has(i) ? __ldcg(keys + base + i * 32) : 0u; }, has,
                 [&](int at, int i) { out[at] = base + i * 32; });
 }
