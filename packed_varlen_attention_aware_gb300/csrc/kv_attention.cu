@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) issue();
 
-    int slot = 0, meta_at = 0, at_piece = piece;
+    int slot = 0, meta_at = 0, at_piece = run * cut.pieces;  // (the copies may be in a later piece already)
     long long at = start;
     uint4 qx[NT][kMt / 2];  // raw query rows of cc's unit, this lane's channels
     auto fetch_q = [&]() {

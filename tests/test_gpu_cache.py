@@ -367,6 +367,55 @@ def test_runs_whose_ends_are_handed_out(fmt, hq, hkv, d, lens, new):
                 assert ((got - want).abs() <= ds + 2.0 ** -20 * want.abs().clamp(min=1)).all()
 
 
+def _poisoned(cache, table, lens, q, scale, cu=None, blocks=None):
+    """The call with a workspace and outputs of garbage (0x7f7f7f7f is a large float)."""
+    rows, hq, d = q.shape
+    ws = torch.full((pkg.hdp_cache_attention_workspace_bytes(cache, hq),), 0x7f, dtype=torch.uint8, device="cuda")
+    o, lse = torch.full_like(q, 1e30), torch.full((hq, rows), 1e30, device="cuda")
+    pkg.hdp_cache_attention(cache, table, lens, q, scale, ws, o, lse, cu=cu, blocks=blocks)
+    pkg.hdp_device_status()
+    return o, lse
+
+
+@pytest.mark.parametrize("blocks", [3048, 3053, 3061, 3090])
+def test_a_last_run_of_few_blocks(blocks):
+    """On 152 SMs the last warp with work has 1 to 3 blocks, fewer than its copies run ahead: it goes on to pieces of
+    other runs before its own is done."""
+    length, hkv, d = blocks * 64 - 3, 8, 64
+    g = torch.Generator(device="cuda").manual_seed(blocks)
+    cache = pkg.KVCache.empty(blocks, hkv, d, 1)
+    for t in (cache.k, cache.v):
+        t.copy_(torch.randint(-90, 91, t.shape, generator=g, device="cuda", dtype=torch.int8).view(torch.uint8))
+    cache.scales.fill_(2.0 ** -7)
+    table = torch.randperm(blocks, generator=g, device="cuda").int()[None]
+    q = torch.randn((1, hkv, d), generator=g, device="cuda").bfloat16()
+    o, lse = _poisoned(cache, table, _i32([length]), q, 0.125)
+    k, v = pkg.cache_read(cache, table, _i32([length]), length, cu=_i32([0, length]))
+    for h in range(hkv):
+        sc = k[:, h].double() @ q[0, h].double() * 0.125
+        p = sc.softmax(0)
+        want = torch.logsumexp(sc, 0)
+        ds = 2.0 ** -16 * (k[:, h].double().abs() @ q[0, h].double().abs() * 0.125).max()
+        assert (lse[h, 0].double() - want).abs() <= ds + 2.0 ** -20 * want.abs()
+        # as in _check_attention; all keys below 2^-13 of the largest probability or not, one scale
+        a, z = p @ v[:, h].double().abs(), p.max() * (p < 2.0 ** -13 * p.max()).sum() * 90 * 2.0 ** -7
+        ref = p @ v[:, h].double()
+        assert ((o[0, h].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -10 + 2.0 ** -18 + 2 * ds) * a + 2.0 ** -23 * z).all()
+
+
+@pytest.mark.parametrize("count", [200, 203, 207, 252])
+def test_a_last_run_of_few_list_entries(count):
+    lens = [int(x) for x in np.random.default_rng(count).integers(0, 140, 165)]
+    lens[-1] = 65
+    cache, table, ref = _random_cache(lens, 4, 64, 0, 7)
+    q = _bf16((165, 48, 64), 8)
+    blocks = np.full((165, 4, count), -1, np.int32)
+    blocks[:, :, 0], blocks[:, :, 1], blocks[:, :, count - 1] = 0, 1, 2
+    blocks[:, 1, 0] = -1
+    o, lse = _poisoned(cache, _i32(table), _i32(lens), q.cuda(), 0.125, blocks=_i32(blocks))
+    _check_attention(o, lse, ref.attention(table, lens, _f64(q), np.arange(166), 0.125, blocks))
+
+
 def test_many_rows_of_one_sequence():
     """A prompt's rows all at once: 88 tiles of query rows over one cache."""
     lens, new = [700, 40], [700, 3]
