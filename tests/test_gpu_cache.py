@@ -808,3 +808,59 @@ def test_prompt_then_decoding_steps_in_a_graph():
     assert torch.equal(still[0], still2[0]) and torch.equal(still[1], still2[1])
     assert all(torch.equal(a, b) for a, b in zip(full, outs)) and want_still[0].shape == still[0].shape
     pkg.hdp_device_status()
+
+
+# ---------------------------------------------------------------- drawn calls
+
+@pytest.mark.parametrize("seed", [3304] + list(range(40)))
+def test_drawn_calls(seed):
+    """Everything at once on drawn shapes: several appends (prompts, chunks, single tokens, scales that grow), then
+    attention, the choice of blocks, attention over them and reading back, for drawn numbers of rows."""
+    import random
+
+    r, rng = random.Random(seed), np.random.default_rng(seed)
+    fmt, d, hkv = r.choice(FMTS), r.choice([64, 128]), r.choice([1, 1, 2, 3, 4, 8])
+    hq, n = hkv * r.choice([1, 2, 3, 4, 5, 7, 8, 12, 16, 17, 33]), r.choice([1, 1, 2, 3, 5, 9, 40])
+    top = r.choice([3, 70, 300, 1500]) if n > 3 else r.choice([1, 65, 300, 3000, 9000])
+    lens = [r.choice([0, 1, 63, 64, 65, r.randint(0, top), r.randint(0, top)]) for _ in range(n)]
+    pages, table = _table([max(l, 1) for l in lens], rng, spare=r.randint(0, 3), columns=r.randint(0, 60))
+    cache = _filled(pages, hkv, d, fmt, byte=r.randint(0, 126))
+    ref, tb = _oracle(cache), _i32(table)
+    now, step = [0] * n, 0
+    while now != lens:
+        new = [min(l - c, r.choice([0, 1, 1, 5, 64, 100, 10000])) for l, c in zip(lens, now)]
+        if not sum(new):
+            continue
+        step += 1
+        now = [c + m for c, m in zip(now, new)]
+        cu = np.concatenate([[0], np.cumsum(new)])
+        k, v = (_bf16((int(cu[-1]), hkv, d), seed + 50 * step + w, 2.0 ** r.randint(-4, 4)) for w in range(2))
+        pkg.cache_append(cache, tb, _i32(now), k.cuda(), v.cuda(), cu=_i32(cu))
+        ref.append(table, now, _f64(k), _f64(v), cu)
+    got = _oracle(cache)
+    used = sorted({int(table[i, b]) for i, l in enumerate(lens) for b in range((l + 63) // 64)})
+    for name in ("scales", "bounds", "k", "v"):
+        assert np.array_equal(getattr(got, name)[used], getattr(ref, name)[used]), name
+
+    single = r.random() < 0.3
+    new = [1] * n if single else [r.choice([0, 1, 1, 2, 3, 9, r.randint(0, l + 2) if l < 100 else 4]) for l in lens]
+    new[0] = max(new[0], 1)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    rows = int(cu[-1])
+    q, cud, scale = _bf16((rows, hq, d), seed + 3, r.choice([0.3, 1, 3])), None if single else _i32(cu), d ** -0.5
+    o, lse = _poisoned(cache, tb, _i32(lens), q.cuda(), scale, cu=cud)
+    _check_attention(o, lse, ref.attention(table, lens, _f64(q), cu, scale), "all")
+    count = r.choice([1, 2, 3, 8, 40, 200])
+    first = r.randint(0, min(2, count))
+    last = r.randint(0, min(2, count - first))
+    b = pkg.cache_select(cache, tb, _i32(lens), q.cuda(), count, cu=cud, keep_first=first, keep_last=last)
+    want = ref.select(table, lens, _f64(q), cu, count, first, last)
+    assert np.array_equal(b.cpu().numpy(), want)
+    o, lse = _poisoned(cache, tb, _i32(lens), q.cuda(), scale, cu=cud, blocks=b)
+    _check_attention(o, lse, ref.attention(table, lens, _f64(q), cu, scale, want), "chosen")
+    k, v = pkg.cache_read(cache, tb, _i32(lens), rows, cu=cud)
+    for i, l in enumerate(lens):
+        none = max(0, new[i] - l)
+        for x, y in zip((k, v), ref.sequence(table[i], l)):
+            assert np.array_equal(_f64(x[cu[i] + none:cu[i + 1]]), y[l - new[i] + none:]) and (x[cu[i]:cu[i] + none] == 0).all()
+    pkg.hdp_device_status()
