@@ -24,11 +24,15 @@
 //   (below, the error is at most 2^-39 of it).  P <= 1 is rounded to fp16:
 //   half a step is 2^-11 of a probability (2^-25 absolute below 2^-14), 1/8 of
 //   the bf16 rounding of the output.  All sums are fp32.
-//   Softmax.  The reference exponents are whole numbers: m of the row sum, M of
-//   the output, which also takes in the V scales' exponents; every rescaling is
-//   then by a power of two, and blocks with very different V scales lose nothing.
-//   Joining.  A piece leaves a normalised (O, LSE) for a unit that it shares with
-//   its neighbours; a second small kernel joins them in the order of the keys.
+//   Softmax.  The row sum's reference is a whole number of bits, m.  The output's
+//   takes in the V scales' exponents as well and is kept as its distance `gap` from
+//   m: that stays small (-126 to 122) whatever the scores are, where the sum of the
+//   two would lose it from 2^24 on.  Every rescaling is by a power of two, and
+//   blocks with very different V scales lose nothing.
+//   Joining.  A piece leaves a normalised O and its (m, row sum) for a unit that
+//   it shares with its neighbours, not their LSE, which for the same reason could
+//   not tell the row sums of large scores apart; a second small kernel joins them
+//   in the order of the keys.
 //
 // Measured (one GB300, in a captured graph): one token over 2M cached ones, 8 kv
 // heads of 128, 628 to 636 us (4.3 GB, 6.8 TB/s); 64 sequences of 256 to 29K
@@ -55,7 +59,7 @@ constexpr int kThreads = kWarps * 32;
 template <int NT, bool SPARSE>
 constexpr int kRingBytes = NT == 1 && !SPARSE ? 24576 : 16384;
 constexpr int kMeta = 8;           // blocks whose scales and first key are kept
-constexpr float kLow = -1.0e30f;   // reference exponent before the first key
+constexpr float kLow = -3.402823466e38f;  // reference exponent before the first key: below every finite score
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct Meta {
@@ -78,11 +82,11 @@ struct AttnParams {
   const int32_t* blocks;
   int count, hq, g;
   float scale_log2;
-  bool dynamic;     // the ends of the runs are handed out through the counter
-  float* part;      // [pieces][2][rows of a tile][d]: of a unit begun before the piece, and of one begun in it
-  float* part_lse;  // [pieces][2][rows of a tile]
-  Open* open;       // [pieces]: one for each piece, or, with a counter, as they come
-  int* head;        // [0] entries of open (dynamic), [1] next ticket, [2] entries of open (static)
+  bool dynamic;      // the ends of the runs are handed out through the counter
+  float* part;       // [pieces][2][rows of a tile][d]: of a unit begun before the piece, and of one begun in it
+  float2* part_sum;  // [pieces][2][rows of a tile]: m, sum of 2^(score - m)
+  Open* open;        // [pieces]: one for each piece, or, with a counter, as they come
+  int* head;         // [0] entries of open (dynamic), [1] next ticket, [2] entries of open (static)
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -261,29 +265,33 @@ __device__ __forceinline__ void write_o(const AttnParams& p, int row0, int head,
   if (lane == 0) p.lse[static_cast<long long>(h) * p.c.rows + t] = lse;
 }
 
-// Joins `m` normalised partials of one row (lse in bits of 2) in their order:
-// x = sum 2^(lse_k - L) o_k, L = log2 sum 2^lse_k.  o_at(k) points at the row.
-template <int D, class L, class O>
-__device__ __forceinline__ float join_row(int m, int lane, float (&x)[D / 32], L lse_at, O o_at) {
+// Joins `m` normalised partials of one row in their order: with (r, l) = sum_at(k),
+// x = sum 2^(r_k - R) l_k o_k / L, R = max r_k, L = sum 2^(r_k - R) l_k.  Returns (R, L).
+template <int D, class S, class O>
+__device__ __forceinline__ float2 join_row(int m, int lane, float (&x)[D / 32], S sum_at, O o_at) {
   constexpr int V = D / 32;
   constexpr int kAhead = 16;  // partial rows in flight
-  const float low = -__int_as_float(0x7f800000);
-  float top = low, sum = 0.f;
+  float top = kLow, sum = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) x[i] = 0.f;
   for (int base = 0; base < m; base += 32) {
     const int here = min(32, m - base);
-    const float l = lane < here ? lse_at(base + lane) : low;
-    float t = l;
+    const float2 l = lane < here ? sum_at(base + lane) : make_float2(kLow, 0.f);
+    float t = l.x;
 #pragma unroll
     for (int s = 16; s; s >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
     t = fmaxf(t, top);
-    const float ref = t == low ? 0.f : t;  // no key so far: every weight is 2^-inf = 0 (a NaN stays one)
-    const float w = exp2_approx(l - ref), old = exp2_approx(top - ref);
-    top = t;
-    sum *= old;
+    float w = l.y * exp2_approx(l.x - t), all = w;
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] *= old;
+    for (int s = 16; s; s >>= 1) all += __shfl_xor_sync(0xffffffffu, all, s);
+    const float old = sum * exp2_approx(top - t);
+    top = t;
+    sum = old + all;
+    // x stays normalised, so it is no larger than the largest V
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key so far: o = 0
+    w *= inv;
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] *= old * inv;
     for (int k = 0; k < here; k += kAhead) {
       float y[kAhead][V];
 #pragma unroll
@@ -305,17 +313,17 @@ __device__ __forceinline__ float join_row(int m, int lane, float (&x)[D / 32], L
       for (int u = 0; u < kAhead; ++u) {
         const float f = __shfl_sync(0xffffffffu, w, (k + u) & 31);
         const float g = k + u < here ? f : 0.f;
-        sum += g;
 #pragma unroll
         for (int i = 0; i < V; ++i) x[i] = k + u < here ? fmaf(g, y[u][i], x[i]) : x[i];
       }
     }
   }
-  if (sum == 0.f) return low;  // no key in any of them: o = 0
-  const float inv = 1.f / sum;
-#pragma unroll
-  for (int i = 0; i < V; ++i) x[i] *= inv;
-  return top + log2f(sum);
+  return make_float2(top, sum);
+}
+
+// Natural logarithm of sum 2^m.
+__device__ __forceinline__ float lse_of(float m, float sum) {
+  return sum == 0.f ? -__int_as_float(0x7f800000) : (m + log2f(sum)) * kLn2;
 }
 
 // How the flat order of `total` steps is cut.  `used` warps of each CTA have a
@@ -633,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
       }
       const int low_pos = cc.first_pos(p.g);
 
-      float acc[NT][kMt][4], m[NT][2], M[NT][2], l[NT][2];
+      float acc[NT][kMt][4], m[NT][2], gap[NT][2], l[NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -642,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
           for (int k = 0; k < 4; ++k) acc[t][i][k] = 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          m[t][k] = M[t][k] = kLow;
+          m[t][k] = gap[t][k] = kLow;
           l[t][k] = 0.f;
         }
       }
@@ -711,10 +719,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
               const float c = none ? 0.f : ceilf(top[k]);
               ref[k] = c;
               const float m1 = none ? m[t][k] : fmaxf(m[t][k], c);
-              const float M1 = none ? M[t][k] : fmaxf(M[t][k], c + lsv);
-              l[t][k] *= exp2_approx(m[t][k] - m1);
-              const float up = exp2_approx(M[t][k] - M1);
-              if (M1 != M[t][k]) {
+              const float down = m[t][k] - m1;
+              const float gap1 = none ? gap[t][k] : fmaxf(gap[t][k] + down, (c - m1) + lsv);
+              l[t][k] *= exp2_approx(down);
+              const float up = exp2_approx(down + (gap[t][k] - gap1));
+              if (up != 1.f) {
 #pragma unroll
                 for (int i = 0; i < kMt; ++i) {
                   acc[t][i][k] *= up;
@@ -722,9 +731,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
                 }
               }
               m[t][k] = m1;
-              M[t][k] = M1;
+              gap[t][k] = gap1;
               const float fl = none ? 0.f : exp2_approx(c - m1);
-              f[k] = none ? 0.f : exp2_approx(c + lsv - M1);
+              f[k] = none ? 0.f : exp2_approx((c - m1) + (lsv - gap1));
               float sum = 0.f;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -803,14 +812,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
       const size_t part_at = (static_cast<size_t>(this_piece) * 2 + (begins ? 1 : 0)) * kRows;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float inv[2], lse2[2];
+        float inv[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
 #pragma unroll
           for (int d = 4; d < 32; d *= 2) l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], d);
           const bool none = l[t][k] == 0.f;
-          inv[k] = none ? 0.f : exp2_approx(M[t][k] - m[t][k]) / l[t][k];
-          lse2[k] = none ? -__int_as_float(0x7f800000) : m[t][k] + log2f(l[t][k]);
+          inv[k] = none ? 0.f : exp2_approx(gap[t][k]) / l[t][k];
         }
         if (whole) {
           const int r = t * 8 + gr;
@@ -832,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
             const int rc = t * 8 + 2 * tc + k;
             if (gr == 0 && rc < nrows && live) {
               const unsigned tk = static_cast<unsigned>(rr0 + rc) / p.g;
-              p.lse[(static_cast<long long>(head) * p.g + (rr0 + rc - tk * p.g)) * p.c.rows + row0 + tk] = lse2[k] * kLn2;
+              p.lse[(static_cast<long long>(head) * p.g + (rr0 + rc - tk * p.g)) * p.c.rows + row0 + tk] = lse_of(m[t][k], l[t][k]);
             }
           }
         } else {
@@ -843,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
 #pragma unroll
               for (int i = 0; i < kMt; ++i)
                 p.part[(part_at + r) * D + i * 16 + (k >> 1) * 8 + gr] = acc[t][i][k] * inv[k & 1];
-              if (gr == 0 && k < 2) p.part_lse[part_at + r] = lse2[k & 1];
+              if (gr == 0 && k < 2) p.part_sum[part_at + r] = make_float2(m[t][k & 1], l[t][k & 1]);
             }
           }
         }
@@ -891,7 +899,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 1) k_cache_attention_join(con
   constexpr int kMostShared = 192;
   constexpr int V = D / 32;
   __shared__ __align__(16) float s_x[kJoinWarps][D];
-  __shared__ float s_lse[kJoinWarps];
+  __shared__ float2 s_sum[kJoinWarps];
   __shared__ int4 s_shared[kMostShared][2], s_own[kMostShared][2];  // shared units, and this CTA's others
   __shared__ int s_n, s_own_n;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -939,10 +947,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 1) k_cache_attention_join(con
     for (int r = 0; r < b.x; ++r) {
       if (nth++ % kJoinWarps != warp) continue;
       float x[V];
-      const float lse2 = join_row<D>(
-          a.x, lane, x, [&](int k) { return __ldcg(p.part_lse + at(a.y, k, r)); },
+      const float2 sum = join_row<D>(
+          a.x, lane, x, [&](int k) { return __ldcg(p.part_sum + at(a.y, k, r)); },
           [&](int k) { return p.part + at(a.y, k, r) * D; });
-      write_o<D>(p, a.z, a.w, b.y + r, x, lse2 * kLn2, lane);
+      write_o<D>(p, a.z, a.w, b.y + r, x, lse_of(sum.x, sum.y), lane);
     }
   }
 
@@ -962,18 +970,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 1) k_cache_attention_join(con
       float x[V];
       if (r < nrows) {
         const int k0 = m * run / each, k1 = m * (run + 1) / each;
-        const float part = join_row<D>(
-            k1 - k0, lane, x, [&](int k) { return __ldcg(p.part_lse + at(e, k0 + k, r)); },
+        const float2 part = join_row<D>(
+            k1 - k0, lane, x, [&](int k) { return __ldcg(p.part_sum + at(e, k0 + k, r)); },
             [&](int k) { return p.part + at(e, k0 + k, r) * D; });
 #pragma unroll
         for (int v = 0; v < V; ++v) s_x[warp][lane * V + v] = x[v];
-        if (lane == 0) s_lse[warp] = part;
+        if (lane == 0) s_sum[warp] = part;
       }
       __syncthreads();
       if (r < nrows && run == 0) {
-        const float lse2 = join_row<D>(each, lane, x, [&](int k) { return s_lse[warp + k]; },
+        const float2 sum = join_row<D>(each, lane, x, [&](int k) { return s_sum[warp + k]; },
                                        [&](int k) { return &s_x[warp + k][0]; });
-        write_o<D>(p, a.z, a.w, b.y + r, x, lse2 * kLn2, lane);
+        write_o<D>(p, a.z, a.w, b.y + r, x, lse_of(sum.x, sum.y), lane);
       }
       __syncthreads();  // the sums have been read
     }
@@ -999,13 +1007,13 @@ hdp_status_t sm_count(int* device, int* sms) {
 
 struct Layout {
   int pieces;
-  size_t part, part_lse, open, head, bytes;
+  size_t part, part_sum, open, head, bytes;
   Layout(int sms, int d) {
     const size_t rows = 8 * kMaxNt;
     pieces = sms * kWarps * (1 + kMorePieces);
     part = 0;
-    part_lse = part + align256(pieces * 2 * rows * d * sizeof(float));
-    open = part_lse + align256(pieces * 2 * rows * sizeof(float));
+    part_sum = part + align256(pieces * 2 * rows * d * sizeof(float));
+    open = part_sum + align256(pieces * 2 * rows * sizeof(float2));
     head = open + align256(pieces * sizeof(Open));
     bytes = head + 256;
   }
@@ -1119,7 +1127,7 @@ extern "C" hdp_status_t hdp_cache_attention(const hdp_cache_t* cache, const int3
   p.scale_log2 = scale * 1.4426950408889634f;
   char* ws = static_cast<char*>(workspace);
   p.part = reinterpret_cast<float*>(ws + lay.part);
-  p.part_lse = reinterpret_cast<float*>(ws + lay.part_lse);
+  p.part_sum = reinterpret_cast<float2*>(ws + lay.part_sum);
   p.open = reinterpret_cast<Open*>(ws + lay.open);
   p.head = reinterpret_cast<int*>(ws + lay.head);
 

@@ -1,0 +1,116 @@
+"""The 8-bit cache's attention where numbers get large, small or far apart: one key with nearly all of the weight, scores
+of any size, K and V scales at both ends of their range.  Against 64 bits on the values that the cache holds."""
+import numpy as np
+import pytest
+import torch
+
+import packed_varlen_attention_aware_gb300 as pkg
+
+pytestmark = pytest.mark.gpu
+FMTS = [pkg.HDP_CACHE_E4M3, pkg.HDP_CACHE_INT8]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+
+
+def _i32(x):
+    return torch.tensor(np.asarray(x, np.int32), device="cuda")
+
+
+def _randn(shape, seed, std=1.0):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)) * std
+
+
+def _cache_of(k, v, fmt, seqs=1):
+    """A cache of the rows k, v [keys][hkv][d], pages in no order; a table in which `seqs` sequences share the pages; and
+    the rows as the cache holds them, in 64 bits."""
+    keys, hkv, d = k.shape
+    pages = (keys + 63) // 64
+    cache = pkg.KVCache.empty(pages, hkv, d, fmt)
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(keys)).int().cuda()[None]
+    lens, cu = _i32([keys]), _i32([0, keys])
+    pkg.cache_append(cache, table, lens, k.bfloat16().cuda(), v.bfloat16().cuda(), cu=cu)
+    held = pkg.cache_read(cache, table, lens, keys, cu=cu)
+    return cache, table.expand(seqs, pages).contiguous(), *(x.double() for x in held)
+
+
+def _exact(q, k, v, scale, pos=None, blocks=None):
+    """(o, lse, a, x) in 64 bits of rows q that see the keys up to their pos (all): a = sum p |v| of each output, x = each
+    row's largest sum |q k| scale."""
+    rows, hq, d = q.shape
+    keys, hkv, _ = k.shape
+    q = q.double().view(rows, hkv, hq // hkv, d)
+    s = torch.einsum("rhgd,nhd->rhgn", q, k) * scale
+    x = torch.einsum("rhgd,nhd->rhgn", q.abs(), k.abs()) * scale
+    at = torch.arange(keys, device="cuda")
+    if pos is not None:
+        s = s.masked_fill(at > torch.as_tensor(pos, device="cuda")[:, None, None, None], -torch.inf)
+    if blocks is not None:
+        chosen = (blocks[..., None] == at // 64).any(2)  # [rows][hkv][keys]
+        s = s.masked_fill(~chosen[:, :, None], -torch.inf)
+    p = s.softmax(-1)
+    o, a = (torch.einsum("rhgn,nhd->rhgd", p, y).reshape(rows, hq, d) for y in (v, v.abs()))
+    x = x.masked_fill(torch.isneginf(s), 0).amax(-1).reshape(rows, hq)
+    return o, s.logsumexp(-1).reshape(rows, hq).t(), a, x
+
+
+def _check(o, lse, exact, same_scores=False):
+    """Bounds, from the roundings alone; nothing is added for small probabilities.
+    Scores: products of fp16 operands are exact; 128 fp32 additions and four multiplications are off by at most 2^-16 of
+    x, and so is log2(e) in them: d_s.  Keys that are equal bit by bit have equal scores, so where all are (same_scores)
+    d_s moves the LSE alone.
+    P: d_s and exp2's 2^-22, and its rounding to fp16, half a step, 2^-11 of it (it is scaled into fp16's normal numbers).
+    So o is off by (2^-11 + 2 d_s + 2^-18) a, and by half a bf16 step, 2^-8, of |o|; twice 2^-11 are allowed.  fp32 ends at
+    2^-126 of the largest p s: not in reach of any case here.
+    LSE: d_s, and 2^-20 for the logarithm and the sum, relative to max(1, |lse|)."""
+    want, lse_want, a, x = exact
+    ds = 2.0 ** -16 * x
+    off = (lse.double() - lse_want).abs() - ds.t() - 2.0 ** -20 * lse_want.abs().clamp(min=1)
+    assert (off <= 0).all(), f"lse over by {off.max()}"
+    ds = 0 if same_scores else ds[..., None]
+    err = (o.double() - want).abs()
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -10 + 2.0 ** -18 + 2 * ds) * a
+    assert (err <= tol).all(), f"o over by {(err - tol).max()}: {o.double()[err > tol][:4].tolist()} for {want[err > tol][:4].tolist()}"
+
+
+# ---------------------------------------------------------------- scores of any size
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("std", [1e7, 1e9, 1e15, 1e33])
+@pytest.mark.parametrize("order,sign", [(1, 1), (1, -1), (-1, 1), (-1, -1)])
+def test_large_scores_and_scales_far_apart(fmt, std, order, sign):
+    """One key takes all: its V, whatever its block's scale and the others'."""
+    d, n, hq = 64, 256, 2
+    k, v = _randn((n, 1, d), 31), _randn((n, 1, d), 32)
+    v *= torch.exp2((torch.arange(n) // 64 * 20.0 - 30) * order)[:, None, None]
+    cache, table, k, v = _cache_of(k, v, fmt)
+    q = (_randn((1, hq, d), 33, std) * sign).bfloat16().cuda()
+    exact = _exact(q, k, v, 0.125)
+    s = torch.einsum("hd,nd->hn", q[0].double(), k[:, 0]) * 0.125
+    first, second = s.topk(2, 1).values.unbind(1)
+    assert (first - second > 800 + 2 * 2.0 ** -16 * exact[3][0]).all()  # e^-800 is 0 in 64 bits; the scores' errors
+    o, lse = pkg.cache_attention(cache, table, _i32([n]), q)
+    _check(o, lse, exact, same_scores=True)  # the weight is 1 for one key, with no error
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("size", [1.0, 1e4, 1e6, 3e7, 1e12, -1e7, -1e12, -3e30, -1e36])
+@pytest.mark.parametrize("seqs,new", [(1, 1), (40, 1), (30, 3)])
+def test_equal_keys_with_scores_of_any_size(fmt, size, seqs, new):
+    """All keys are the same: the output is the mean of V, however the keys are split over warps and joined, and the
+    V scales differ from block to block."""
+    n, hq, hkv, d = 20011, 8, 2, 64
+    k = _randn((1, hkv, d), 41).sign().expand(n, hkv, d)
+    v = (_randn((n, hkv, d), 42) + 1) * torch.exp2(torch.arange(n) // 64 % 7 - 3.0)[:, None, None]
+    cache, table, k, v = _cache_of(k, v, fmt, seqs)
+    q = k[:1].float().repeat_interleave(hq // hkv, 1).expand(seqs * new, hq, d) * (size * torch.linspace(0.5, 1, hq, device="cuda")[:, None] / 8)
+    q = q.bfloat16()
+    cu = None if new == 1 else _i32(np.arange(seqs + 1) * new)
+    o, lse = pkg.cache_attention(cache, table, _i32([n] * seqs), q, cu=cu)
+    pos = np.tile(np.arange(n - new, n), seqs)
+    _check(o, lse, _exact(q, k, v, 0.125, pos=pos), same_scores=True)
