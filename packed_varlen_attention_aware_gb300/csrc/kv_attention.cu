@@ -812,13 +812,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
       const size_t part_at = (static_cast<size_t>(this_piece) * 2 + (begins ? 1 : 0)) * kRows;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float inv[2];
+        float inv[2], unit[2];  // two factors: 2^-126 / l would be a subnormal number of few bits
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
 #pragma unroll
           for (int d = 4; d < 32; d *= 2) l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], d);
           const bool none = l[t][k] == 0.f;
-          inv[k] = none ? 0.f : exp2_approx(gap[t][k]) / l[t][k];
+          inv[k] = none ? 0.f : 1.f / l[t][k];
+          unit[k] = none ? 0.f : exp2_approx(gap[t][k]);
         }
         if (whole) {
           const int r = t * 8 + gr;
@@ -830,7 +831,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               // [8 channels][8 rows] to [8 rows][8 channels]: lane then has row gr, channels 2 tc and 2 tc + 1
-              const __nv_bfloat162 y = __floats2bfloat162_rn(acc[t][i][2 * h] * inv[0], acc[t][i][2 * h + 1] * inv[1]);
+              const __nv_bfloat162 y = __floats2bfloat162_rn(acc[t][i][2 * h] * inv[0] * unit[0],
+                                                             acc[t][i][2 * h + 1] * inv[1] * unit[1]);
               const uint32_t z = transpose8x8(*reinterpret_cast<const uint32_t*>(&y));
               if (r < nrows && live) *reinterpret_cast<uint32_t*>(out + i * 16 + h * 8) = z;
             }
@@ -850,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
             if (r < nrows) {
 #pragma unroll
               for (int i = 0; i < kMt; ++i)
-                p.part[(part_at + r) * D + i * 16 + (k >> 1) * 8 + gr] = acc[t][i][k] * inv[k & 1];
+                p.part[(part_at + r) * D + i * 16 + (k >> 1) * 8 + gr] = acc[t][i][k] * inv[k & 1] * unit[k & 1];
               if (gr == 0 && k < 2) p.part_sum[part_at + r] = make_float2(m[t][k & 1], l[t][k & 1]);
             }
           }

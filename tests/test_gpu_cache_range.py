@@ -114,3 +114,21 @@ def test_equal_keys_with_scores_of_any_size(fmt, size, seqs, new):
     o, lse = pkg.cache_attention(cache, table, _i32([n] * seqs), q, cu=cu)
     pos = np.tile(np.arange(n - new, n), seqs)
     _check(o, lse, _exact(q, k, v, 0.125, pos=pos), same_scores=True)
+
+
+def test_the_smallest_v_in_long_sequences():
+    """V of 2^-121 (a scale of 2^-126) over 1.1M keys of equal weight: the mean, to the last bit but the roundings."""
+    n, seqs, hkv, d = 1100000, 152, 8, 64
+    k = torch.zeros((n, hkv, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.full((n, hkv, d), 1.5 * 2.0 ** -121, dtype=torch.bfloat16, device="cuda")
+    pages = (n + 63) // 64
+    cache = pkg.KVCache.empty(pages, hkv, d, 1)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    pkg.cache_append(cache, table, _i32([n]), k, v, cu=_i32([0, n]))
+    assert (cache.scales[:, :, 1] == 2.0 ** -126).all()
+    o, lse = pkg.cache_attention(cache, table.expand(seqs, pages).contiguous(), _i32([n] * seqs),
+                                 torch.ones((seqs, hkv, d), dtype=torch.bfloat16, device="cuda"))
+    # probabilities are powers of two here and codes equal: sums of 1.1M of them in fp32 are off by 2^-24 an addition at
+    # most, one for the 64 keys of a step, 2^-24 * 17188 < 2^-9; then half a bf16 step
+    assert ((o.double() / (1.5 * 2.0 ** -121) - 1).abs() <= 2.0 ** -8 + 2.0 ** -9).all()
+    assert ((lse.double() - np.log(n)).abs() <= 2.0 ** -9).all()
