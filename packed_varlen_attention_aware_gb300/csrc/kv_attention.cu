@@ -701,11 +701,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             float top[2] = {-__int_as_float(0x7f800000), -__int_as_float(0x7f800000)};
+            // The products are below 2^31: times a scale above one they may pass fp32's end
+            // where a small q brings the score back, so the row's factor goes first then.
+            const bool large = meta.sk > 1.f;
+            const float first[2] = {large ? qs[t][0] : meta.sk, large ? qs[t][1] : meta.sk};
+            const float second[2] = {large ? meta.sk : qs[t][0], large ? meta.sk : qs[t][1]};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                float x = s[t][i][k] * meta.sk * qs[t][k & 1];
+                float x = s[t][i][k] * first[k & 1] * second[k & 1];
                 if (masked && meta.key0 + 16 * i + 8 * (k >> 1) + gr > pos[t][k & 1]) x = -__int_as_float(0x7f800000);
                 s[t][i][k] = x;
                 top[k & 1] = fmaxf(top[k & 1], x);

@@ -116,6 +116,19 @@ def test_equal_keys_with_scores_of_any_size(fmt, size, seqs, new):
     _check(o, lse, _exact(q, k, v, 0.125, pos=pos), same_scores=True)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("ks", [3e36, 3e-36])
+@pytest.mark.parametrize("hq", [2, 12])
+def test_keys_and_queries_at_opposite_ends_of_the_range(fmt, ks, hq):
+    """|K| of 3e36 and q of 3e-37, or the other way round: scores of order one."""
+    n, d = 200, 64
+    k, v = _randn((n, 1, d), 51, ks), _randn((n, 1, d), 52)
+    cache, table, k, v = _cache_of(k, v, fmt)
+    q = _randn((1, hq, d), 53, 1 / ks).bfloat16().cuda()
+    o, lse = pkg.cache_attention(cache, table, _i32([n]), q)
+    _check(o, lse, _exact(q, k, v, 0.125))
+
+
 def test_the_smallest_v_in_long_sequences():
     """V of 2^-121 (a scale of 2^-126) over 1.1M keys of equal weight: the mean, to the last bit but the roundings."""
     n, seqs, hkv, d = 1100000, 152, 8, 64
