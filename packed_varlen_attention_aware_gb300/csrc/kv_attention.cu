@@ -21,9 +21,15 @@
 //   e4m3 by the conversion instruction); the cache's order of bytes is the
 //   fragments' order.  The query row is shifted by a power of two to
 //   [2^14, 2^15), which is exact in fp16 down to 2^-31 of its largest element
-//   (below, the error is at most 2^-39 of it).  P <= 1 is rounded to fp16:
-//   half a step is 2^-11 of a probability (2^-25 absolute below 2^-14), 1/8 of
-//   the bf16 rounding of the output.  All sums are fp32.
+//   (below, the error is at most 2^-39 of it).  P is rounded to fp16 at 2^15 times
+//   its share of the block's largest: half a step is 2^-11 of it, 1/8 of the bf16
+//   rounding of the output, as long as it is one of fp16's normal numbers, down to
+//   2^-29.  A block's O^T is summed alone and added to the output's in fp32 by its
+//   power of two, so a key with nearly all of a row's weight costs the other blocks
+//   nothing.  In its own block, keys 20 nats below it lose bits; that counts only
+//   where its V is zero and theirs is the output.  So where a block's O^T is small,
+//   what fp16 left of P takes further passes over the V codes, each for the next 40
+//   bits, down to fp32's end.  All sums are fp32.
 //   Softmax.  The row sum's reference is a whole number of bits, m.  The output's
 //   takes in the V scales' exponents as well and is kept as its distance `gap` from
 //   m: that stays small (-126 to 122) whatever the scores are, where the sum of the
@@ -35,10 +41,13 @@
 //   in the order of the keys.
 //
 // Measured (one GB300, in a captured graph): one token over 2M cached ones, 8 kv
-// heads of 128, 628 to 636 us (4.3 GB, 6.8 TB/s); 64 sequences of 256 to 29K
-// tokens 147 us (843 MB, 5.7 TB/s: while the runs stream, a block takes a warp
-// 5.2K cycles, 7.2 TB/s; the rest is the start and the ends); 64 x 32 chosen
-// blocks 56 us (270 MB).
+// heads of 128, 635 to 641 us (4.3 GB, 6.7 to 6.8 TB/s); 64 sequences of 256 to
+// 29K tokens 149 us (843 MB, 5.7 TB/s: while the runs stream, a block takes a warp
+// 5.3K cycles; the rest is the start and the ends); 64 x 32 chosen blocks 56 us
+// (270 MB).  Of these, the blocks' own sums take 1 us, 2, 1 (and of 66 us for 16
+// sequences of up to 5 tokens 2), the look at small outputs and P's wait in shared
+// memory 3, 1, 1 (5).  The loop's size in instructions costs as much as what it
+// does: with the further passes unrolled those were 5, 4, 2 (11).
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -61,6 +70,14 @@ constexpr int kRingBytes = NT == 1 && !SPARSE ? 24576 : 16384;
 constexpr int kMeta = 8;           // blocks whose scales and first key are kept
 constexpr float kLow = -3.402823466e38f;  // reference exponent before the first key: below every finite score
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kBias = 15.f;                  // P is at most 2^15, in fp16
+constexpr float kBiasMost = 1048576.f;         // references above it are not biased: far below 2^24, so exactly
+constexpr float kNormal = 6.103515625e-05f;    // 2^-14, fp16's smallest normal number
+constexpr float kNextPass = 1099511627776.f;   // 2^40: what rounding to fp16 leaves below kNormal, 2^-25, to 2^15
+// What rounding to fp16 leaves of a block's P is at most 64 * 2^-25 times its largest
+// code, 127 or 448; 2^12 times that is enough of an output to forget it.
+template <int FMT>
+constexpr float kEnough = FMT == HDP_CACHE_INT8 ? 1.f : 4.f;
 
 struct Meta {
   float sk, sv;
@@ -109,11 +126,26 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
+// The smallest magnitude.
+__device__ __forceinline__ float least_of(float a, float b, float c) {
+  float r;
+  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same without a sum to add to.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -124,6 +156,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 __device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+
+// What rounding x, below fp16's normal numbers, to fp16 leaves of it, for the next pass; 0 for normal ones.
+__device__ __forceinline__ float left_by_fp16(float x) {
+  return fabsf(x) < kNormal ? (x - __half2float(__float2half_rn(x))) * kNextPass : 0.f;
+}
 
 // Four codes to fp16: bytes 0, 1 and bytes 2, 3.
 template <int FMT>
@@ -177,6 +214,7 @@ struct Shared {
   unsigned char ring[kWarps][kRingBytes<NT, SPARSE>];
   SeqPlace seq[kSeqs];
   Meta meta[kWarps][kMeta];
+  float4 p[kWarps][NT][4][32];  // P of a block, each lane its own
   long long pre[kThreads];  // steps before each thread's sequences
   long long warp_sum[kWarps];
 };
@@ -321,9 +359,10 @@ __device__ __forceinline__ float2 join_row(int m, int lane, float (&x)[D / 32], 
   return make_float2(top, sum);
 }
 
-// Natural logarithm of sum 2^m.
+// Natural logarithm of sum 2^m; the bias of most references is taken out first,
+// so that a single key's LSE is its score.
 __device__ __forceinline__ float lse_of(float m, float sum) {
-  return sum == 0.f ? -__int_as_float(0x7f800000) : (m + log2f(sum)) * kLn2;
+  return sum == 0.f ? -__int_as_float(0x7f800000) : ((m + kBias) + log2f(sum * (1.f / 32768.f))) * kLn2;
 }
 
 // How the flat order of `total` steps is cut.  `used` warps of each CTA have a
@@ -377,6 +416,341 @@ struct Cut {
   }
 };
 
+// The arithmetic of one block of 64 keys for a tile of 8 NT query rows; lane (gr, tc)
+// has keys 8 i + gr, i = 0..7, of rows 8 t + 2 tc and 8 t + 2 tc + 1.
+
+constexpr int kTogether = 2;  // 16-row tiles whose chains of products are interleaved
+
+// Raw query rows of a unit, this lane's channels.
+template <int D, int NT>
+__device__ __forceinline__ void fetch_rows(const AttnParams& p, int row0, int head, unsigned rr0, int nrows,
+                                           uint4 (&qx)[NT][D / 32]) {
+  const int lane = threadIdx.x & 31, gr = lane >> 2, tc = lane & 3;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int r = t * 8 + gr;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) qx[t][i] = make_uint4(0, 0, 0, 0);
+    if (r < nrows) {
+      const unsigned token = (rr0 + r) / p.g;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + (static_cast<long long>(row0 + token) * p.hq + head * p.g + (rr0 + r - token * p.g)) * D + tc * 16);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) qx[t][i] = __ldg(src + (i >> 1) * 8 + (i & 1));
+    }
+  }
+}
+
+template <int D, int NT>
+struct Rows {
+  static constexpr int kMt = D / 16;
+  uint32_t q[NT][kMt][2];
+  float scale[NT][2];  // scale * log2(e) * 2^(shift) of rows 2 tc and 2 tc + 1
+  int pos[NT][2];      // their positions
+
+  __device__ __forceinline__ Rows(const AttnParams& p, const uint4 (&qx)[NT][D / 32], int p0, unsigned rr0, int nrows) {
+    const int tc = threadIdx.x & 3;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < kMt / 2; ++i)
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(qx[t][i].x & 0x7fff7fffu, qx[t][i].y & 0x7fff7fffu),
+                                     __vmaxu2(qx[t][i].z & 0x7fff7fffu, qx[t][i].w & 0x7fff7fffu)));
+      top = max(top & 0xffffu, top >> 16);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // the largest element's exponent goes to 14; infinities and NaN stay what they are
+      const int e = min(max(static_cast<int>(top >> 7) - 127, -112), 127) - 14;
+      const float down = pow2i(-e);
+#pragma unroll
+      for (int i = 0; i < kMt / 2; ++i) {
+        const uint32_t w[4] = {qx[t][i].x, qx[t][i].y, qx[t][i].z, qx[t][i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __half2 y = __floats2half2_rn(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
+          q[t][i * 2 + (k >> 1)][k & 1] = h2_bits(y);
+        }
+      }
+      const float s = p.scale_log2 * pow2i(e);
+      scale[t][0] = __shfl_sync(0xffffffffu, s, tc * 8);
+      scale[t][1] = __shfl_sync(0xffffffffu, s, tc * 8 + 4);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const unsigned rc = rr0 + min(t * 8 + 2 * tc + k, nrows - 1);
+        pos[t][k] = max(-1, p0 + static_cast<int>(rc / p.g));
+      }
+    }
+  }
+};
+
+// What a warp keeps of a unit between blocks.
+template <int D, int NT>
+struct Sums {
+  static constexpr int kMt = D / 16;
+  float acc[NT][kMt][4];  // O^T, relative to 2^(m + gap)
+  float m[NT][2], gap[NT][2], l[NT][2];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int i = 0; i < kMt; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[t][i][k] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        m[t][k] = gap[t][k] = kLow;
+        l[t][k] = 0.f;
+      }
+    }
+  }
+};
+
+// S^T = K Q^T; key_at(i, j) is chunk j of this lane's key 8 i + gr.
+template <int D, int FMT, int NT, class K>
+__device__ __forceinline__ void first_product(const Rows<D, NT>& rows, float (&s)[NT][4][4], K key_at) {
+#pragma unroll
+  for (int i = 0; i < 4; i += kTogether) {
+#pragma unroll
+    for (int h = 0; h < kTogether; ++h)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[t][i + h][k] = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      uint4 u[kTogether], w[kTogether];
+#pragma unroll
+      for (int h = 0; h < kTogether; ++h) {
+        u[h] = key_at(2 * (i + h), j);
+        w[h] = key_at(2 * (i + h) + 1, j);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int h = 0; h < kTogether; ++h) {
+          uint32_t a0, a1, a2, a3;
+          decode4<FMT>(word(u[h], k), a0, a2);
+          decode4<FMT>(word(w[h], k), a1, a3);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            mma16816(s[t][i + h], a0, a1, a2, a3, rows.q[t][j * 4 + k][0], rows.q[t][j * 4 + k][1]);
+        }
+      }
+    }
+  }
+}
+
+// Scores to P, at most 2^15, in place; brings the sums to the new references, and f
+// to the power of two (<= 1) of the block in the output.
+template <int D, int NT>
+__device__ __forceinline__ void softmax(const Rows<D, NT>& rows, Sums<D, NT>& sums, float sk, float sv, int key0,
+                                        bool masked, float (&s)[NT][4][4], float (&f)[NT][2]) {
+  const int gr = (threadIdx.x & 31) >> 2;
+  const int ev = static_cast<int>((__float_as_uint(sv) >> 23) & 0xff) - 127;
+  const float lsv = sv == sv ? static_cast<float>(ev) : sv;  // log2 of the V scale
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    float top[2] = {-__int_as_float(0x7f800000), -__int_as_float(0x7f800000)};
+    // The products are below 2^31: times a scale above one they may pass fp32's end
+    // where a small q brings the score back, so the row's factor goes first then.
+    const bool large = sk > 1.f;
+    const float first[2] = {large ? rows.scale[t][0] : sk, large ? rows.scale[t][1] : sk};
+    const float second[2] = {large ? sk : rows.scale[t][0], large ? sk : rows.scale[t][1]};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float x = s[t][i][k] * first[k & 1] * second[k & 1];
+        if (masked && key0 + 16 * i + 8 * (k >> 1) + gr > rows.pos[t][k & 1]) x = -__int_as_float(0x7f800000);
+        s[t][i][k] = x;
+        top[k & 1] = fmaxf(top[k & 1], x);
+      }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int d = 4; d < 32; d *= 2) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], d));
+      const bool none = top[k] == -__int_as_float(0x7f800000);
+      float c = none ? 0.f : ceilf(top[k]);
+      if (fabsf(c) < kBiasMost) c -= kBias;
+      const float m = sums.m[t][k], gap = sums.gap[t][k];
+      const float m1 = none ? m : fmaxf(m, c);
+      const float down = m - m1;
+      const float gap1 = none ? gap : fmaxf(gap + down, (c - m1) + lsv);
+      sums.l[t][k] *= exp2_approx(down);
+      const float up = exp2_approx(down + (gap - gap1));
+      if (up != 1.f) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          sums.acc[t][i][k] *= up;
+          sums.acc[t][i][k + 2] *= up;
+        }
+      }
+      sums.m[t][k] = m1;
+      sums.gap[t][k] = gap1;
+      const float fl = none ? 0.f : exp2_approx(c - m1);
+      f[t][k] = none ? 0.f : exp2_approx((c - m1) + (lsv - gap1));
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[t][i][k] = exp2_approx(s[t][i][k] - c);
+        s[t][i][k + 2] = exp2_approx(s[t][i][k + 2] - c);
+        sum += s[t][i][k] + s[t][i][k + 2];
+      }
+      sums.l[t][k] = fmaf(sum, fl, sums.l[t][k]);
+    }
+  }
+}
+
+// A lane's numbers of P between the softmax and the second product.  They wait in
+// shared memory: the copies of the next blocks are issued in between.
+template <int NT>
+struct Probabilities {
+  float4 (*p)[4][32];
+  __device__ __forceinline__ float4& at(int i) const { return p[i >> 2][i & 3][threadIdx.x & 31]; }
+  __device__ __forceinline__ void put(const float (&s)[NT][4][4]) const {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) at(t * 4 + i) = make_float4(s[t][i][0], s[t][i][1], s[t][i][2], s[t][i][3]);
+  }
+  // To fp16, in the second product's order.
+  __device__ __forceinline__ void get(uint32_t (&pf)[NT][4][2]) const {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 x = at(t * 4 + i);
+        const uint32_t a = h2_bits(__floats2half2_rn(x.x, x.y)), b = h2_bits(__floats2half2_rn(x.z, x.w));
+        pf[t][i][0] = transpose8x8(a);
+        pf[t][i][1] = transpose8x8(b);
+      }
+  }
+  // Does fp16 leave something of them?
+  __device__ __forceinline__ bool more() const {
+    bool any = false;
+#pragma unroll 1
+    for (int i = 0; i < 4 * NT; ++i) {
+      const float4 x = at(i);
+      any |= left_by_fp16(x.x) != 0.f || left_by_fp16(x.y) != 0.f || left_by_fp16(x.z) != 0.f || left_by_fp16(x.w) != 0.f;
+    }
+    return any;
+  }
+  // To what fp16 left of them.
+  __device__ __forceinline__ void next() const {
+#pragma unroll 1
+    for (int i = 0; i < 4 * NT; ++i) {
+      const float4 x = at(i);
+      at(i) = make_float4(left_by_fp16(x.x), left_by_fp16(x.y), left_by_fp16(x.z), left_by_fp16(x.w));
+    }
+  }
+};
+
+// O^T += f Y, Y = V^T P^T; value_at(i) is this lane's chunk of channel 8 i + gr, least
+// the smallest |Y| of this lane's rows.
+template <int D, int FMT, int NT, class V>
+__device__ __forceinline__ void second_product(Sums<D, NT>& sums, const uint32_t (&pf)[NT][4][2], const float (&f)[NT][2],
+                                               bool masked, float (&least)[NT][2], V value_at) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) least[t][0] = least[t][1] = __int_as_float(0x7f800000);
+#pragma unroll
+  for (int i = 0; i < D / 16; i += kTogether) {
+    uint4 u[kTogether], w[kTogether];
+    float y[NT][kTogether][4];
+#pragma unroll
+    for (int h = 0; h < kTogether; ++h) {
+      u[h] = value_at(2 * (i + h));
+      w[h] = value_at(2 * (i + h) + 1);
+      if (masked) {
+        u[h] = without_nan<FMT>(u[h]);
+        w[h] = without_nan<FMT>(w[h]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int h = 0; h < kTogether; ++h) {
+        uint32_t a0, a1, a2, a3;
+        decode4<FMT>(word(u[h], k), a0, a2);
+        decode4<FMT>(word(w[h], k), a1, a3);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if (k == 0) mma16816_first(y[t][h], a0, a1, a2, a3, pf[t][k][0], pf[t][k][1]);
+          else mma16816(y[t][h], a0, a1, a2, a3, pf[t][k][0], pf[t][k][1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < kTogether; ++h)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          sums.acc[t][i + h][k] = fmaf(y[t][h][k], f[t][k & 1], sums.acc[t][i + h][k]);
+          if (k < 2) least[t][k] = least_of(least[t][k], y[t][h][k], y[t][h][k + 2]);
+        }
+  }
+}
+
+// Normalises the sums of a unit, or of a piece's part of it, and writes them.
+template <int D, int NT>
+__device__ __forceinline__ void write_part(const AttnParams& p, const Sums<D, NT>& sums, int head, int row0, int rr0,
+                                           int nrows, bool whole, size_t part_at) {
+  const int lane = threadIdx.x & 31, gr = lane >> 2, tc = lane & 3;
+  constexpr int kMt = D / 16;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    float l[2], inv[2], unit[2];  // two factors: 2^-126 / l would be a subnormal number of few bits
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      l[k] = sums.l[t][k];
+#pragma unroll
+      for (int d = 4; d < 32; d *= 2) l[k] += __shfl_xor_sync(0xffffffffu, l[k], d);
+      const bool none = l[k] == 0.f;
+      inv[k] = none ? 0.f : 1.f / l[k];
+      unit[k] = none ? 0.f : exp2_approx(sums.gap[t][k]);
+    }
+    if (whole) {
+      const int r = t * 8 + gr;
+      const unsigned rr = rr0 + r, token = rr / p.g;
+      __nv_bfloat16* out =
+          p.o + (static_cast<long long>(row0 + token) * p.hq + head * p.g + (rr - token * p.g)) * D + tc * 2;
+#pragma unroll
+      for (int i = 0; i < kMt; ++i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // [8 channels][8 rows] to [8 rows][8 channels]: lane then has row gr, channels 2 tc and 2 tc + 1
+          const __nv_bfloat162 y = __floats2bfloat162_rn(sums.acc[t][i][2 * h] * inv[0] * unit[0],
+                                                         sums.acc[t][i][2 * h + 1] * inv[1] * unit[1]);
+          const uint32_t z = transpose8x8(*reinterpret_cast<const uint32_t*>(&y));
+          if (r < nrows) *reinterpret_cast<uint32_t*>(out + i * 16 + h * 8) = z;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int rc = t * 8 + 2 * tc + k;
+        if (gr == 0 && rc < nrows) {
+          const unsigned tk = static_cast<unsigned>(rr0 + rc) / p.g;
+          p.lse[(static_cast<long long>(head) * p.g + (rr0 + rc - tk * p.g)) * p.c.rows + row0 + tk] =
+              lse_of(sums.m[t][k], l[k]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = t * 8 + 2 * tc + (k & 1);
+        if (r < nrows) {
+#pragma unroll
+          for (int i = 0; i < kMt; ++i)
+            p.part[(part_at + r) * D + i * 16 + (k >> 1) * 8 + gr] = sums.acc[t][i][k] * inv[k & 1] * unit[k & 1];
+          if (gr == 0 && k < 2) p.part_sum[part_at + r] = make_float2(sums.m[t][k & 1], l[k & 1]);
+        }
+      }
+    }
+  }
+}
+
 template <int D, int FMT, int NT, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParams p) {
   constexpr int kHalf = kBlock * D;               // bytes of a block's K or V codes of one head
@@ -384,7 +758,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
   constexpr int kKeyChunks = D / 64;              // 16-byte chunks that a lane has of a key
   constexpr int kMt = D / 16;
   constexpr int kRows = 8 * NT;
-  constexpr int kTogether = 2;  // 16-row tiles whose chains of products are interleaved
   using Cur = Cursor<SPARSE, NT>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   auto& sm = *reinterpret_cast<Shared<NT, SPARSE>*>(smem_raw);
@@ -579,23 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
     int slot = 0, meta_at = 0, at_piece = run * cut.pieces;  // (the copies may be in a later piece already)
     long long at = start;
     uint4 qx[NT][kMt / 2];  // raw query rows of cc's unit, this lane's channels
-    auto fetch_q = [&]() {
-      const unsigned rr0 = cc.rr0();
-      const int nrows = cc.nrows(p.g);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int r = t * 8 + gr;
-#pragma unroll
-        for (int i = 0; i < kMt / 2; ++i) qx[t][i] = make_uint4(0, 0, 0, 0);
-        if (r < nrows) {
-          const unsigned token = (rr0 + r) / p.g;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              p.q + (static_cast<long long>(cc.s.row0 + token) * p.hq + cc.head * p.g + (rr0 + r - token * p.g)) * D + tc * 16);
-#pragma unroll
-          for (int i = 0; i < kMt / 2; ++i) qx[t][i] = __ldg(src + (i >> 1) * 8 + (i & 1));
-        }
-      }
-    };
+    auto fetch_q = [&]() { fetch_rows<D, NT>(p, cc.s.row0, cc.head, cc.rr0(), cc.nrows(p.g), qx); };
     fetch_q();
     while (true) {
       // ---- one unit, or the part of it that the piece has
@@ -605,55 +962,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
       const int nrows = cc.nrows(p.g), rr0 = cc.rr0(), row0 = cc.s.row0, head = cc.head;
       const bool live = !SPARSE || cc.seq >= 0;
 
-      uint32_t qf[NT][kMt][2];
-      float qs[NT][2];   // scale * log2(e) * 2^(shift) of columns 2 tc and 2 tc + 1
-      int pos[NT][2];    // their positions
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < kMt / 2; ++i)
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(qx[t][i].x & 0x7fff7fffu, qx[t][i].y & 0x7fff7fffu),
-                                       __vmaxu2(qx[t][i].z & 0x7fff7fffu, qx[t][i].w & 0x7fff7fffu)));
-        top = max(top & 0xffffu, top >> 16);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the largest element's exponent goes to 14; infinities and NaN stay what they are
-        const int e = min(max(static_cast<int>(top >> 7) - 127, -112), 127) - 14;
-        const float down = pow2i(-e);
-#pragma unroll
-        for (int i = 0; i < kMt / 2; ++i) {
-          const uint32_t w[4] = {qx[t][i].x, qx[t][i].y, qx[t][i].z, qx[t][i].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __half2 y = __floats2half2_rn(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
-            qf[t][i * 2 + (k >> 1)][k & 1] = h2_bits(y);
-          }
-        }
-        const float s = p.scale_log2 * pow2i(e);
-        qs[t][0] = __shfl_sync(0xffffffffu, s, tc * 8);
-        qs[t][1] = __shfl_sync(0xffffffffu, s, tc * 8 + 4);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const unsigned rc = rr0 + min(t * 8 + 2 * tc + k, nrows - 1);
-          pos[t][k] = max(-1, cc.s.p0 + static_cast<int>(rc / p.g));
-        }
-      }
       const int low_pos = cc.first_pos(p.g);
-
-      float acc[NT][kMt][4], m[NT][2], gap[NT][2], l[NT][2];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int i = 0; i < kMt; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[t][i][k] = 0.f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          m[t][k] = gap[t][k] = kLow;
-          l[t][k] = 0.f;
-        }
-      }
+      const Rows<D, NT> rows(p, qx, cc.s.p0, rr0, nrows);
+      Sums<D, NT> sums;
+      sums.clear();
 
       for (int step = 0; step < steps; ++step) {
         copies_wait<kSlots - 1>();
@@ -662,99 +974,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
         meta_at = (meta_at + 1) % kMeta;
         const bool seen = meta.key0 >= 0;
         const bool masked = meta.key0 + kBlock - 1 > low_pos;  // some row does not see the whole block
-        uint32_t pf[NT][4][2];
+        float f[NT][2];
+        const Probabilities<NT> prob = {sm.p[warp]};
         if (seen) {
           const uint4* kx = reinterpret_cast<const uint4*>(sm.ring[warp] + slot * kHalf) + lane;
           float s[NT][4][4];
-#pragma unroll
-          for (int i = 0; i < 4; i += kTogether) {
-#pragma unroll
-            for (int h = 0; h < kTogether; ++h)
-#pragma unroll
-              for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) s[t][i + h][k] = 0.f;
-#pragma unroll
-            for (int j = 0; j < kKeyChunks; ++j) {
-              uint4 u[kTogether], w[kTogether];
-#pragma unroll
-              for (int h = 0; h < kTogether; ++h) {
-                u[h] = kx[((2 * (i + h)) * kKeyChunks + j) * 32];
-                w[h] = kx[((2 * (i + h) + 1) * kKeyChunks + j) * 32];
-              }
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-#pragma unroll
-                for (int h = 0; h < kTogether; ++h) {
-                  uint32_t a0, a1, a2, a3;
-                  decode4<FMT>(word(u[h], k), a0, a2);
-                  decode4<FMT>(word(w[h], k), a1, a3);
-#pragma unroll
-                  for (int t = 0; t < NT; ++t)
-                    mma16816(s[t][i + h], a0, a1, a2, a3, qf[t][j * 4 + k][0], qf[t][j * 4 + k][1]);
-                }
-              }
-            }
-          }
-          const int ev = static_cast<int>((__float_as_uint(meta.sv) >> 23) & 0xff) - 127;
-          const float lsv = meta.sv == meta.sv ? static_cast<float>(ev) : meta.sv;  // log2 of the V scale
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            float top[2] = {-__int_as_float(0x7f800000), -__int_as_float(0x7f800000)};
-            // The products are below 2^31: times a scale above one they may pass fp32's end
-            // where a small q brings the score back, so the row's factor goes first then.
-            const bool large = meta.sk > 1.f;
-            const float first[2] = {large ? qs[t][0] : meta.sk, large ? qs[t][1] : meta.sk};
-            const float second[2] = {large ? meta.sk : qs[t][0], large ? meta.sk : qs[t][1]};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float x = s[t][i][k] * first[k & 1] * second[k & 1];
-                if (masked && meta.key0 + 16 * i + 8 * (k >> 1) + gr > pos[t][k & 1]) x = -__int_as_float(0x7f800000);
-                s[t][i][k] = x;
-                top[k & 1] = fmaxf(top[k & 1], x);
-              }
-            float f[2], ref[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-#pragma unroll
-              for (int d = 4; d < 32; d *= 2) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], d));
-              const bool none = top[k] == -__int_as_float(0x7f800000);
-              const float c = none ? 0.f : ceilf(top[k]);
-              ref[k] = c;
-              const float m1 = none ? m[t][k] : fmaxf(m[t][k], c);
-              const float down = m[t][k] - m1;
-              const float gap1 = none ? gap[t][k] : fmaxf(gap[t][k] + down, (c - m1) + lsv);
-              l[t][k] *= exp2_approx(down);
-              const float up = exp2_approx(down + (gap[t][k] - gap1));
-              if (up != 1.f) {
-#pragma unroll
-                for (int i = 0; i < kMt; ++i) {
-                  acc[t][i][k] *= up;
-                  acc[t][i][k + 2] *= up;
-                }
-              }
-              m[t][k] = m1;
-              gap[t][k] = gap1;
-              const float fl = none ? 0.f : exp2_approx(c - m1);
-              f[k] = none ? 0.f : exp2_approx((c - m1) + (lsv - gap1));
-              float sum = 0.f;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                s[t][i][k] = exp2_approx(s[t][i][k] - c);
-                s[t][i][k + 2] = exp2_approx(s[t][i][k + 2] - c);
-                sum += s[t][i][k] + s[t][i][k + 2];
-              }
-              l[t][k] = fmaf(sum, fl, l[t][k]);
-            }
-            const __half2 ff = __floats2half2_rn(f[0], f[1]);  // a power of two <= 1
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              pf[t][i][0] = transpose8x8(h2_bits(__hmul2(__floats2half2_rn(s[t][i][0], s[t][i][1]), ff)));
-              pf[t][i][1] = transpose8x8(h2_bits(__hmul2(__floats2half2_rn(s[t][i][2], s[t][i][3]), ff)));
-            }
-          }
+          first_product<D, FMT, NT>(rows, s, [&](int i, int j) { return kx[(i * kKeyChunks + j) * 32]; });
+          softmax<D, NT>(rows, sums, meta.sk, meta.sv, meta.key0, masked, s, f);
+          prob.put(s);
         }
         slot = slot + 1 == kSlots ? 0 : slot + 1;
         issue();
@@ -762,28 +989,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
         copies_wait<kSlots - 1>();
         if (seen) {
           const uint4* vx = reinterpret_cast<const uint4*>(sm.ring[warp] + slot * kHalf) + lane;
+          bool sure = false;  // that further passes are needed
+          while (true) {
+            uint32_t pf[NT][4][2];
+            float least[NT][2];
+            prob.get(pf);
+            second_product<D, FMT, NT>(sums, pf, f, masked, least, [&](int i) { return vx[i * 32]; });
+            // Is an output so small that what fp16 leaves of P could count?
 #pragma unroll
-          for (int i = 0; i < kMt; i += kTogether) {
-            uint4 u[kTogether], w[kTogether];
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int h = 0; h < kTogether; ++h) {
-              u[h] = vx[(2 * (i + h)) * 32];
-              w[h] = vx[(2 * (i + h) + 1) * 32];
-              if (masked) {
-                u[h] = without_nan<FMT>(u[h]);
-                w[h] = without_nan<FMT>(w[h]);
-              }
-            }
+              for (int k = 0; k < 2; ++k)
+                sure |= t * 8 + 2 * tc + k < nrows && f[t][k] != 0.f && !(least[t][k] >= kEnough<FMT>);
+            if (!__any_sync(0xffffffffu, sure) || !__any_sync(0xffffffffu, prob.more())) break;
+            sure = true;
+            prob.next();  // four times at most
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-#pragma unroll
-              for (int h = 0; h < kTogether; ++h) {
-                uint32_t a0, a1, a2, a3;
-                decode4<FMT>(word(u[h], k), a0, a2);
-                decode4<FMT>(word(w[h], k), a1, a3);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) mma16816(acc[t][i + h], a0, a1, a2, a3, pf[t][k][0], pf[t][k][1]);
-              }
+            for (int t = 0; t < NT; ++t) {
+              f[t][0] *= 1.f / kNextPass;
+              f[t][1] *= 1.f / kNextPass;
             }
           }
         }
@@ -812,57 +1036,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
       }
       if (more) fetch_q();
 
-      // ---- the unit's part is done: normalise, then out, or into a partial
+      // ---- the unit's part is done: out, or into a partial
       const bool whole = begins && ends;
       const size_t part_at = (static_cast<size_t>(this_piece) * 2 + (begins ? 1 : 0)) * kRows;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float inv[2], unit[2];  // two factors: 2^-126 / l would be a subnormal number of few bits
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-          for (int d = 4; d < 32; d *= 2) l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], d);
-          const bool none = l[t][k] == 0.f;
-          inv[k] = none ? 0.f : 1.f / l[t][k];
-          unit[k] = none ? 0.f : exp2_approx(gap[t][k]);
-        }
-        if (whole) {
-          const int r = t * 8 + gr;
-          const unsigned rr = rr0 + r, token = rr / p.g;
-          __nv_bfloat16* out =
-              p.o + (static_cast<long long>(row0 + token) * p.hq + head * p.g + (rr - token * p.g)) * D + tc * 2;
-#pragma unroll
-          for (int i = 0; i < kMt; ++i) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              // [8 channels][8 rows] to [8 rows][8 channels]: lane then has row gr, channels 2 tc and 2 tc + 1
-              const __nv_bfloat162 y = __floats2bfloat162_rn(acc[t][i][2 * h] * inv[0] * unit[0],
-                                                             acc[t][i][2 * h + 1] * inv[1] * unit[1]);
-              const uint32_t z = transpose8x8(*reinterpret_cast<const uint32_t*>(&y));
-              if (r < nrows && live) *reinterpret_cast<uint32_t*>(out + i * 16 + h * 8) = z;
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int rc = t * 8 + 2 * tc + k;
-            if (gr == 0 && rc < nrows && live) {
-              const unsigned tk = static_cast<unsigned>(rr0 + rc) / p.g;
-              p.lse[(static_cast<long long>(head) * p.g + (rr0 + rc - tk * p.g)) * p.c.rows + row0 + tk] = lse_of(m[t][k], l[t][k]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = t * 8 + 2 * tc + (k & 1);
-            if (r < nrows) {
-#pragma unroll
-              for (int i = 0; i < kMt; ++i)
-                p.part[(part_at + r) * D + i * 16 + (k >> 1) * 8 + gr] = acc[t][i][k] * inv[k & 1] * unit[k & 1];
-              if (gr == 0 && k < 2) p.part_sum[part_at + r] = make_float2(m[t][k & 1], l[t][k & 1]);
-            }
-          }
-        }
-      }
+      if (live) write_part<D, NT>(p, sums, head, row0, rr0, nrows, whole, part_at);
       if (begins && !ends && live && lane == 0) {
         Open o = {};
         o.first = this_piece;

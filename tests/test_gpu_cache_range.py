@@ -78,6 +78,98 @@ def _check(o, lse, exact, same_scores=False):
     assert (err <= tol).all(), f"o over by {(err - tol).max()}: {o.double()[err > tol][:4].tolist()} for {want[err > tol][:4].tolist()}"
 
 
+def _sink(n, hkv, d, weight, seed):
+    """Keys of which the first takes `weight` of a row whose channel 0 is 8, with V = 0; the others' scores are close
+    together and their V has a mean."""
+    k, v = _randn((n, hkv, d), seed), _randn((n, hkv, d), seed + 1) + 0.5
+    k[:, :, 0] = 0
+    k[0] = 0
+    v[0] = 0
+    k[0, :, 0] = float(np.log(n * weight / (1 - weight)) / (8 * d ** -0.5))
+    return k, v
+
+
+def _sink_rows(rows, hq, d, seed):
+    q = _randn((rows, hq, d), seed, 0.5)
+    q[:, :, 0] = 8
+    return q.bfloat16().cuda()
+
+
+# ---------------------------------------------------------------- probabilities of any size
+
+@pytest.mark.parametrize("weight", [0.9, 0.99, 0.999, 0.9999, 1 - 1e-7])
+@pytest.mark.parametrize("fmt,hq,d", [(0, 8, 64), (1, 8, 64), (1, 32, 128)])
+def test_one_key_with_nearly_all_of_the_weight(fmt, hq, d, weight):
+    """160 sequences of 8 heads share 8,192 keys: a warp has most of a (sequence, head), the heavy key among it, and
+    what the other keys leave in the output is 1 - weight of it."""
+    n, seqs, hkv, scale = 8192, 160, 8, d ** -0.5
+    k, v = _sink(n, hkv, d, weight, 3)
+    cache, table, k, v = _cache_of(k, v, fmt, seqs)
+    q = _sink_rows(seqs, hq, d, 5)
+    o, lse = pkg.cache_attention(cache, table, _i32([n] * seqs), q)
+    _check(o, lse, _exact(q, k, v, scale))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_one_key_with_nearly_all_of_the_weight_drafts(fmt):
+    """The same for three tokens of each sequence, 12 rows of a head's group."""
+    n, seqs, new, hq, hkv, d = 4096, 100, 3, 16, 4, 128
+    k, v = _sink(n, hkv, d, 0.9999, 7)
+    cache, table, k, v = _cache_of(k, v, fmt, seqs)
+    q = _sink_rows(seqs * new, hq, d, 8)
+    o, lse = pkg.cache_attention(cache, table, _i32([n] * seqs), q, cu=_i32(np.arange(seqs + 1) * new))
+    _check(o, lse, _exact(q, k, v, d ** -0.5, pos=np.tile(np.arange(n - new, n), seqs)))
+
+
+@pytest.mark.parametrize("fmt,d", [(0, 128), (1, 64)])
+def test_one_key_with_nearly_all_of_the_weight_chosen_blocks(fmt, d):
+    n, seqs, hq, hkv = 4096, 60, 8, 2
+    k, v = _sink(n, hkv, d, 0.9999, 9)
+    cache, table, k, v = _cache_of(k, v, fmt, seqs)
+    q = _sink_rows(seqs, hq, d, 10)
+    blocks = torch.rand((seqs, hkv, 64), generator=torch.Generator().manual_seed(1)).topk(24, 2).indices
+    blocks[:, :, 0] = 0  # the heavy key's
+    blocks = blocks.sort(2).values.int().cuda()
+    o, lse = pkg.cache_attention(cache, table, _i32([n] * seqs), q, blocks=blocks)
+    _check(o, lse, _exact(q, k, v, d ** -0.5, blocks=blocks))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("hq,d", [(1, 64), (4, 128), (12, 64)])
+@pytest.mark.parametrize("heavy", [0, 70, 150])
+def test_probabilities_over_the_range_of_fp32(fmt, hq, d, heavy):
+    """Scores 0 to -85 in steps of one and V of one channel each, so an output is one probability: from 1 to 1e-37, in
+    the heavy key's own block and in others."""
+    n = 192
+    k, v = torch.zeros((n, 1, d)), torch.zeros((n, 1, d))
+    at = torch.arange(n)
+    k[:, 0, 0] = -(20.0 + at % 64)  # whole numbers below 2^7; e4m3 rounds the upper ones
+    k[heavy, 0, 0] = 0
+    v[at, 0, at % 64] = 1
+    v[heavy] = 0
+    cache, table, k, v = _cache_of(k, v, fmt)
+    q = torch.zeros((1, hq, d))
+    q[:, :, 0] = torch.linspace(1, 0.7, hq) * d ** 0.5
+    q = q.bfloat16().cuda()
+    o, lse = pkg.cache_attention(cache, table, _i32([n]), q)
+    exact = _exact(q, k, v, d ** -0.5)
+    assert (exact[0][0, 0, 1:60] > 0).all() and exact[0][0, 0, :60].min() < 1e-30
+    _check(o, lse, exact)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("bits", [18, 24, 30, 60])
+def test_one_channel_of_v_much_larger_in_one_block(fmt, bits):
+    """2^bits in channel 0 of 64 keys: the other channels' outputs come from the other blocks."""
+    n, seqs, hkv, d = 8192, 160, 8, 64
+    k, v = _randn((n, hkv, d), 11), _randn((n, hkv, d), 12) + 0.5
+    v[640:704, :, 0] = 2.0 ** bits
+    cache, table, k, v = _cache_of(k, v, fmt, seqs)
+    q = _randn((seqs, hkv, d), 13).bfloat16().cuda()
+    o, lse = pkg.cache_attention(cache, table, _i32([n] * seqs), q)
+    _check(o, lse, _exact(q, k, v, 0.125))
+
+
 # ---------------------------------------------------------------- scores of any size
 
 @pytest.mark.parametrize("fmt", FMTS)
