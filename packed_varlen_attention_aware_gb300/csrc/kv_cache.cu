@@ -119,6 +119,12 @@ __device__ __forceinline__ int scale_exponent(uint32_t abs_bits) {
   return max(e, -126);
 }
 
+// x * unit (a power of two) to the whole number below and above.  The product is exact
+// but where it is below fp32's range; rounded outwards there too, it keeps its side
+// of zero, so that rounding nests (bounds depend on the rows alone).
+__device__ __forceinline__ float below(float x, float unit) { return floorf(__fmul_rd(x, unit)); }
+__device__ __forceinline__ float above(float x, float unit) { return ceilf(__fmul_ru(x, unit)); }
+
 __device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); }
 __device__ __forceinline__ uint32_t bits(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); }
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
@@ -377,11 +383,12 @@ __device__ __forceinline__ void append_rows(const CacheView& c, const Touched& t
       const float unit = FMT == HDP_CACHE_INT8 ? inv : inv * 0.25f;
       const __nv_bfloat16 lo = __hmin(__hmin(s_bound[0][0][i], s_bound[1][0][i]), __hmin(s_bound[2][0][i], s_bound[3][0][i]));
       const __nv_bfloat16 hi = __hmax(__hmax(s_bound[0][1][i], s_bound[1][1][i]), __hmax(s_bound[2][1][i], s_bound[3][1][i]));
-      float a = floorf(__bfloat162float(lo) * unit), b = ceilf(__bfloat162float(hi) * unit);
+      float a = below(__bfloat162float(lo), unit), b = above(__bfloat162float(hi), unit);
       int8_t* out = c.bounds + ph * (2 * D) + i;
       if (!t.fresh) {
-        a = fminf(a, floorf(static_cast<float>(out[0]) * ratio));
-        b = fmaxf(b, ceilf(static_cast<float>(out[D]) * ratio));
+        // before * inv alone may be below fp32's range
+        a = fminf(a, below(static_cast<float>(out[0]) * before, inv));
+        b = fmaxf(b, above(static_cast<float>(out[D]) * before, inv));
       }
       out[0] = static_cast<int8_t>(fminf(fmaxf(a, -127.f), 127.f));
       out[D] = static_cast<int8_t>(fminf(fmaxf(b, -127.f), 127.f));
@@ -491,11 +498,11 @@ __global__ void __launch_bounds__(kThreads) k_cache_append_one(CacheView c, cons
     int8_t lo[8], hi[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float a = floorf(f[i] * unit_inv), b = ceilf(f[i] * unit_inv);
+      float a = below(f[i], unit_inv), b = above(f[i], unit_inv);
       if (!fresh) {
         const uint32_t ol = (i < 4 ? blo.x : blo.y) >> (8 * (i & 3)), oh = (i < 4 ? bhi.x : bhi.y) >> (8 * (i & 3));
-        a = fminf(a, floorf(static_cast<float>(static_cast<int8_t>(ol & 0xff)) * ratio));
-        b = fmaxf(b, ceilf(static_cast<float>(static_cast<int8_t>(oh & 0xff)) * ratio));
+        a = fminf(a, below(static_cast<float>(static_cast<int8_t>(ol & 0xff)) * before, inv));
+        b = fmaxf(b, above(static_cast<float>(static_cast<int8_t>(oh & 0xff)) * before, inv));
       }
       lo[i] = static_cast<int8_t>(fminf(fmaxf(a, -127.f), 127.f));
       hi[i] = static_cast<int8_t>(fminf(fmaxf(b, -127.f), 127.f));

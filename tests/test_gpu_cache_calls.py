@@ -1,0 +1,59 @@
+"""Calls of the 8-bit cache around the ordinary ones: steps without rows, empty block lists, inputs that die while another
+stream still reads them, two graphs that overlap, bounds of values far below their block's scale."""
+import numpy as np
+import pytest
+import torch
+
+import packed_varlen_attention_aware_gb300 as pkg
+from oracle import kv_cache as kc
+
+pytestmark = pytest.mark.gpu
+FMTS = [pkg.HDP_CACHE_E4M3, pkg.HDP_CACHE_INT8]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+
+
+def _i32(x):
+    return torch.tensor(np.asarray(x, np.int32), device="cuda")
+
+
+def _bf16(shape, seed, std=1.0):
+    return (torch.randn(shape, generator=torch.Generator().manual_seed(seed)) * std).to(torch.bfloat16).cuda()
+
+
+# ---------------------------------------------------------------- bounds
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("single", [False, True])
+def test_bounds_are_rounded_outwards_below_the_smallest_float(fmt, single):
+    """Values whose share of the block's scale is below 2^-149 still widen the bounds, whether they come with the
+    large one, before it or after it: bounds are a function of the rows alone."""
+    d, hkv, big = 64, 2, 1e30
+    row = torch.zeros((3, hkv, d))
+    row[:, 0, 1], row[:, 0, 2], row[:, 1, 3] = -1e-38, 3e-37, -2.0 ** -133
+    row[1, :, 0] = big  # the scale grows by some 2^200
+    row[1, 0, 5], row[2, 0, 6] = 2.0 ** -126, -2.0 ** -126
+    row = row.to(torch.bfloat16)
+    table = _i32([[0]])
+    cache, ref = pkg.KVCache.empty(1, hkv, d, fmt), kc.Cache(1, hkv, d, fmt)
+    f64 = row.double().numpy()
+    if single:
+        for r in range(3):
+            pkg.cache_append(cache, table, _i32([r + 1]), row[r:r + 1].cuda(), row[r:r + 1].cuda())
+            ref.append([[0]], [r + 1], f64[r:r + 1], f64[r:r + 1], [0, 1])
+    else:
+        for a, z in ((0, 1), (1, 3)):
+            pkg.cache_append(cache, table, _i32([z]), row[a:z].cuda(), row[a:z].cuda(), cu=_i32([0, z - a]))
+            ref.append([[0]], [z], f64[a:z], f64[a:z], [0, z - a])
+    got = cache.bounds.cpu().numpy()
+    assert np.array_equal(got, ref.bounds), [(i.tolist(), got[tuple(i)], ref.bounds[tuple(i)]) for i in np.argwhere(got != ref.bounds)]
+    whole = pkg.KVCache.empty(1, hkv, d, fmt)
+    pkg.cache_append(whole, table, _i32([3]), row.cuda(), row.cuda(), cu=_i32([0, 3]))
+    assert torch.equal(whole.bounds, cache.bounds)
+    assert (got[0, 0, 0, 1], got[0, 0, 1, 2], got[0, 1, 0, 3]) == (-1, 1, -1)
