@@ -415,7 +415,9 @@ class KVCache:
 
         if blocks is None:
             return 0, None
-        count = blocks.shape[-1]
+        count = blocks.shape[-1] if blocks.dim() == 3 else -1
+        if count < 1:  # an empty tensor has no address, and a list without one means every block
+            raise ValueError("blocks must be [rows][hkv][count] with count >= 1")
         _tensor(blocks, "blocks", torch.int32, (rows, self.hkv, count), self._dev)
         return count, blocks.data_ptr()
 

@@ -104,3 +104,13 @@ def test_the_binding_wants_cuda_tensors_of_the_right_types():
         pkg.KVCache(k, k, torch.zeros((2, 1, 2)), torch.zeros((2, 1, 2, 64), dtype=torch.int8), 0)
     with pytest.raises(ValueError, match="k must be"):
         pkg.KVCache(k[0], k, None, None, 0)
+
+
+def test_an_empty_list_of_blocks_is_refused():
+    """Width 0 must not be taken for "every block": its tensor has no address."""
+    cache = object.__new__(pkg.KVCache)
+    cache.hkv, cache._dev = 2, 0
+    for shape in ((3, 2, 0), (0, 2, 0), (3, 2), (0,), ()):
+        with pytest.raises(ValueError, match="blocks must be"):
+            cache._blocks_of(torch.empty(shape, dtype=torch.int32), 3)
+    assert cache._blocks_of(None, 3) == (0, None)

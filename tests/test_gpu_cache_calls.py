@@ -27,6 +27,21 @@ def _bf16(shape, seed, std=1.0):
     return (torch.randn(shape, generator=torch.Generator().manual_seed(seed)) * std).to(torch.bfloat16).cuda()
 
 
+def _filled(lens, hkv, d, fmt, seed):
+    """A cache of sequences of these lengths: (cache, table, lens)."""
+    need = [(l + 63) // 64 for l in lens]
+    table = torch.zeros((len(lens), max(need) + 1), dtype=torch.int32)
+    order = torch.randperm(sum(need) + len(lens), generator=torch.Generator().manual_seed(seed)).int()
+    at = 0
+    for i, m in enumerate(need):
+        table[i, :m + 1] = order[at:at + m + 1]
+        at += m + 1
+    cache = pkg.KVCache.empty(len(order), hkv, d, fmt)
+    cu = _i32(np.concatenate([[0], np.cumsum(lens)]))
+    pkg.cache_append(cache, table.cuda(), _i32(lens), _bf16((sum(lens), hkv, d), seed), _bf16((sum(lens), hkv, d), seed + 1), cu=cu)
+    return cache, table.cuda(), _i32(lens)
+
+
 # ---------------------------------------------------------------- bounds
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -57,3 +72,13 @@ def test_bounds_are_rounded_outwards_below_the_smallest_float(fmt, single):
     pkg.cache_append(whole, table, _i32([3]), row.cuda(), row.cuda(), cu=_i32([0, 3]))
     assert torch.equal(whole.bounds, cache.bounds)
     assert (got[0, 0, 0, 1], got[0, 0, 1, 2], got[0, 1, 0, 3]) == (-1, 1, -1)
+
+
+# ---------------------------------------------------------------- steps without rows, empty lists
+
+def test_an_empty_list_of_blocks_is_not_all_blocks():
+    cache, table, lens = _filled([100, 70], 2, 64, 0, 1)
+    q = _bf16((2, 4, 64), 3)
+    with pytest.raises(ValueError, match="blocks"):
+        pkg.cache_attention(cache, table, lens, q, blocks=torch.empty((2, 2, 0), dtype=torch.int32, device="cuda"))
+    pkg.hdp_device_status()
