@@ -1283,7 +1283,8 @@ extern "C" hdp_status_t hdp_cache_attention(const hdp_cache_t* cache, const int3
   if (hq < 1 || hq % cache->hkv != 0)
     return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_attention: need hq >= 1 and hq % hkv == 0");
   if (!(scale > 0.f)) return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_attention: scale must be > 0");
-  if (blocks ? count < 1 : count != 0)
+  // a list for no rows may be an empty tensor, which has no address
+  if (blocks ? count < 1 : count < 0 || (count > 0 && rows > 0))
     return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_attention: count must be >= 1 with blocks and 0 without");
   if (rows == 0) return HDP_OK;
   if (rows * (hq / cache->hkv) > 2147483647LL)

@@ -114,3 +114,11 @@ def test_an_empty_list_of_blocks_is_refused():
         with pytest.raises(ValueError, match="blocks must be"):
             cache._blocks_of(torch.empty(shape, dtype=torch.int32), 3)
     assert cache._blocks_of(None, 3) == (0, None)
+
+
+def test_no_rows_and_a_list_without_an_address(lib):
+    assert _attend(lib, _cache(), rows=0, blocks=None, count=4, q=None, o=None, lse=None, ws=None) == pkg.HDP_OK
+    assert _attend(lib, _cache(), rows=0, blocks=V(256), count=4) == pkg.HDP_OK
+    assert _attend(lib, _cache(), rows=1, blocks=None, count=4) == INVALID
+    assert _attend(lib, _cache(), rows=0, blocks=None, count=-1) == INVALID
+    assert _attend(lib, _cache(), rows=0, blocks=V(256), count=0) == INVALID

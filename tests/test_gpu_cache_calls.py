@@ -82,3 +82,20 @@ def test_an_empty_list_of_blocks_is_not_all_blocks():
     with pytest.raises(ValueError, match="blocks"):
         pkg.cache_attention(cache, table, lens, q, blocks=torch.empty((2, 2, 0), dtype=torch.int32, device="cuda"))
     pkg.hdp_device_status()
+
+
+def test_a_step_without_rows_goes_through_all_calls():
+    cache, table, lens = _filled([100, 70], 2, 64, 1, 2)
+    cu = _i32([0, 0, 0])
+    before = [t.clone() for t in (cache.k, cache.v, cache.scales, cache.bounds)]
+    kv, q = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda"), torch.empty((0, 4, 64), dtype=torch.bfloat16, device="cuda")
+    pkg.cache_append(cache, table, lens, kv, kv, cu=cu)
+    blocks = pkg.cache_select(cache, table, lens, q, 3, cu=cu)
+    assert blocks.shape == (0, 2, 3)
+    for b in (None, blocks):
+        o, lse = pkg.cache_attention(cache, table, lens, q, cu=cu, blocks=b)
+        assert o.shape == (0, 4, 64) and lse.shape == (4, 0)
+    k, v = pkg.cache_read(cache, table, lens, 0, cu=cu)
+    assert k.shape == v.shape == (0, 2, 64)
+    pkg.hdp_device_status()
+    assert all(torch.equal(a, b) for a, b in zip(before, (cache.k, cache.v, cache.scales, cache.bounds)))
