@@ -121,15 +121,29 @@ def _pool(stream, cache):
     return torch.cuda.stream(stream)
 
 
+def _in_use(stream, cache, *inputs):
+    """Inputs of a call on another torch stream: their memory, freed, is not given out before that stream has read it.
+    (Nothing can be noted for a raw handle, which may be destroyed before the tensors are.)"""
+    if stream is not None and not isinstance(stream, int):
+        for t in (cache.k, cache.v, cache.scales, cache.bounds, *inputs):
+            if t is not None:
+                t.record_stream(stream)
+
+
+# The calls below run on `stream`, or on the current one.  As everywhere in torch, a call on another stream than the one
+# that made its inputs has to be ordered behind it (stream.wait_stream).  A torch stream keeps its inputs' memory until
+# it has read them; with a raw handle (int) the caller keeps the inputs alive until the call has run.  What a call on
+# another stream than the current one returns belongs to that stream.
+
 def cache_append(cache: KVCache, page_table, lens, k, v, cu=None, stream=None):
     """Writes k, v [rows][hkv][d] bf16 into the cache: the newest tokens of each sequence, packed, with prefix sums cu
     (None: one row for each sequence).  lens counts them already."""
     hdp_cache_append(cache, page_table, lens, k, v, cu=cu, stream=stream)
+    _in_use(stream, cache, page_table, lens, k, v, cu)
 
 
 def cache_read(cache: KVCache, page_table, lens, rows: int, cu=None, stream=None):
-    """The newest tokens of each sequence as (k, v) [rows][hkv][d] bf16, exactly code * scale.  Outputs that a cache
-    call on another stream than the current one returns belong to that stream."""
+    """The newest tokens of each sequence as (k, v) [rows][hkv][d] bf16, exactly code * scale."""
     import torch
 
     s = cache._with(page_table, lens, cu, rows)
@@ -137,6 +151,7 @@ def cache_read(cache: KVCache, page_table, lens, rows: int, cu=None, stream=None
         k = torch.empty((rows, cache.hkv, cache.d), dtype=torch.bfloat16, device=cache.device)
         v = torch.empty_like(k)
     cache._call("hdp_cache_read", stream, s, None if cu is None else cu.data_ptr(), rows, k.data_ptr(), v.data_ptr())
+    _in_use(stream, cache, page_table, lens, cu)
     return k, v
 
 
@@ -154,6 +169,7 @@ def cache_select(cache: KVCache, page_table, lens, q, count: int, cu=None, keep_
         ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
     cache._call("hdp_cache_select", stream, s, None if cu is None else cu.data_ptr(), rows, q.data_ptr(), hq, count,
                 keep_first, keep_last, ws.data_ptr(), nbytes, blocks.data_ptr())
+    _in_use(stream, cache, page_table, lens, q, cu)
     return blocks
 
 
@@ -177,4 +193,5 @@ def cache_attention(cache: KVCache, page_table, lens, q, cu=None, blocks=None, s
         ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
     cache._call("hdp_cache_attention", stream, s, None if cu is None else cu.data_ptr(), rows, q.data_ptr(), hq, scale,
                 list_ptr, count, ws.data_ptr(), nbytes, o.data_ptr(), lse.data_ptr())
+    _in_use(stream, cache, page_table, lens, q, cu, blocks)
     return o, lse

@@ -99,3 +99,66 @@ def test_a_step_without_rows_goes_through_all_calls():
     assert k.shape == v.shape == (0, 2, 64)
     pkg.hdp_device_status()
     assert all(torch.equal(a, b) for a, b in zip(before, (cache.k, cache.v, cache.scales, cache.bounds)))
+
+
+# ---------------------------------------------------------------- streams and graphs
+
+def test_inputs_that_die_while_another_stream_reads_them():
+    """Temporaries as arguments of a call on another stream: what the caller's stream allocates next must not be given
+    their memory before the call has read them."""
+    cache, table, lens = _filled([1000, 700], 2, 64, 1, 4)
+    q, k, v = _bf16((2, 8, 64), 5), _bf16((2, 2, 64), 6), _bf16((2, 2, 64), 7)
+    cu = _i32([0, 1, 2])
+    state = [t.clone() for t in (cache.k, cache.v, cache.scales, cache.bounds)]
+
+    def calls(stream, t):
+        """All calls, with arguments that only the call holds (t makes them)."""
+        now = lens + 1
+        pkg.cache_append(cache, t(table), t(now), t(k), t(v), cu=t(cu), stream=stream)
+        b = pkg.cache_select(cache, t(table), t(now), t(q), 4, cu=t(cu), stream=stream)
+        return (b, *pkg.cache_attention(cache, t(table), t(now), t(q), cu=t(cu), stream=stream),
+                *pkg.cache_attention(cache, t(table), t(now), t(q), cu=t(cu), blocks=b, stream=stream),
+                *pkg.cache_read(cache, t(table), t(now), 2, cu=t(cu), stream=stream))
+
+    want = calls(None, lambda x: x)
+    side = torch.cuda.Stream()
+    for again in range(2):  # the first time for the memory pools' sake
+        for x, y in zip((cache.k, cache.v, cache.scales, cache.bounds), state):
+            x.copy_(y)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(400_000_000)  # a fifth of a second in front of the calls
+        got = calls(side, torch.clone)
+        junk = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in [512] * 200 + [2048] * 50 + [4096] * 50]
+        torch.cuda.current_stream().synchronize()
+        waiting = not side.query()
+        side.synchronize()
+        del junk
+    assert waiting  # the calls had not run when the temporaries' memory was given out again
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    pkg.hdp_device_status()
+
+
+def test_a_captured_call_on_a_forked_stream():
+    """Inside a capture, attention on another stream than the capture's, with a temporary as its input."""
+    cache, table, lens = _filled([1000, 700], 2, 64, 0, 8)
+    q = _bf16((2, 8, 64), 9)
+    want = pkg.cache_attention(cache, table, lens, -q)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        negative = -q
+        side.wait_stream(torch.cuda.current_stream())
+        outs = pkg.cache_attention(cache, table, lens, negative, stream=side)
+        del negative
+        torch.cuda.current_stream().wait_stream(side)
+        blank = [torch.zeros((2, 8, 64), dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+    for _ in range(3):
+        for t in outs:
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)) and not any(t.any() for t in blank)
+    del graph, outs, blank
+    torch.cuda.synchronize()
+    assert torch.equal(pkg.cache_attention(cache, table, lens, -q)[0], want[0])
