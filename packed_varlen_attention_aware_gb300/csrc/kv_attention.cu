@@ -952,7 +952,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
     int slot = 0, meta_at = 0, at_piece = run * cut.pieces;  // (the copies may be in a later piece already)
     long long at = start;
     uint4 qx[NT][kMt / 2];  // raw query rows of cc's unit, this lane's channels
-    auto fetch_q = [&]() { fetch_rows<D, NT>(p, cc.s.row0, cc.head, cc.rr0(), cc.nrows(p.g), qx); };
+    auto fetch_q = [&]() {  // a row of no sequence is not read
+      fetch_rows<D, NT>(p, cc.s.row0, cc.head, cc.rr0(), !SPARSE || cc.seq >= 0 ? cc.nrows(p.g) : 0, qx);
+    };
     fetch_q();
     while (true) {
       // ---- one unit, or the part of it that the piece has
