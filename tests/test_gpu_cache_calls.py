@@ -162,3 +162,41 @@ def test_a_captured_call_on_a_forked_stream():
     del graph, outs, blank
     torch.cuda.synchronize()
     assert torch.equal(pkg.cache_attention(cache, table, lens, -q)[0], want[0])
+
+
+def test_two_graphs_overlap():
+    """Captured steps of two models on two streams, replayed without waiting for each other, each with the results that
+    it has alone."""
+    models = []
+    for m, (lens, hq, hkv, d, fmt) in enumerate([([40000, 100, 9000], 8, 2, 128, 1), ([30000] * 4, 4, 4, 64, 0)]):
+        cache, table, dl = _filled([l - 1 for l in lens], hkv, d, fmt, 11 + m)
+        dl.add_(1)
+        n = len(lens)
+        q, k, v = _bf16((n, hq, d), 21 + m), _bf16((n, hkv, d), 31 + m), _bf16((n, hkv, d), 41 + m)
+
+        def step(cache=cache, table=table, dl=dl, q=q, k=k, v=v):
+            pkg.cache_append(cache, table, dl, k, v)  # the same rows at the same places: nothing changes after the first
+            b = pkg.cache_select(cache, table, dl, q, 20)
+            return (b, *pkg.cache_attention(cache, table, dl, q), *pkg.cache_attention(cache, table, dl, q, blocks=b),
+                    *pkg.cache_read(cache, table, dl, dl.shape[0]))
+
+        step()
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = step()
+        models.append((graph, torch.cuda.Stream(), outs, want, step))  # step keeps the graph's inputs
+    for _ in range(5):
+        for _, _, outs, _, _ in models:
+            for t in outs:
+                t.fill_(7)
+        torch.cuda.synchronize()
+        for _ in range(6):
+            for graph, stream, _, _, _ in models:
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for _, _, outs, want, _ in models:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    pkg.hdp_device_status()
