@@ -455,14 +455,15 @@ __global__ void __launch_bounds__(kTopThreads) k_cache_top(const SelectParams p)
                 [&](int at, int i) { out[at] = base + i * 32; });
 }
 
-// CTAs of k_cache_select for a (row, kv head): enough for the blocks, and as many
-// as leave no more than one for each SM; 0: not for this size.
+// CTAs of k_cache_select for a (row, kv head), as few as hold its keys; 0: not for
+// this size.  More of them cost more than they save (us a call for 8 and 64 heads
+// of 2,048 blocks: 9.7 and 13.8 with one, 13.8 and 18.2 with two, 14.0 and 40.8
+// with eight).
 int select_ctas(int64_t units, int max_pages, int count) {
   const int least = (max_pages + kSelectBlocks - 1) / kSelectBlocks;
   int ctas = 1;
   while (ctas < least) ctas *= 2;
   if (ctas > kTopCtas || (ctas > 1 && count > kTopMost) || units * ctas > 2147483647LL) return 0;
-  while (ctas < kTopCtas && count <= kTopMost && units * ctas * 2 <= 152 && max_pages > ctas * kTopThreads) ctas *= 2;
   return ctas;
 }
 
@@ -518,9 +519,13 @@ extern "C" hdp_status_t hdp_cache_select(const hdp_cache_t* cache, const int32_t
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t units = rows * cache->hkv;
   const int ctas = select_ctas(units, cache->max_pages, count);
-  // Few long rows: the scores want every SM, the choice has 8 CTAs for each head
-  // at most (32,768 blocks, 8 heads: 41 us from one kernel).
-  const bool scored = !ctas || (units * ctas < 100 && cache->max_pages > 2 * kTopThreads);
+  // Few (row, kv head)s: the scores want every SM and have a kernel of their own.
+  // us a call with it and without, heads x blocks: 8 x 1,024 9.8 and 13.4, 64 x 2,048
+  // 13.8 and 18.2, 64 x 4,096 19.2 and 26.9, 8 x 32,768 23.3 and 30.8.  Where the heads
+  // fill the SMs themselves, one launch does: 128 x 2,048 18.9 and 18.9, 128 x 3,000
+  // 29.6 and 27.5, 128 x 4,096 39.4 and 38.2 (128 x 32,768, by 8 CTAs each: 271 and 314).
+  constexpr int kFewUnits = 100;
+  const bool scored = !ctas || units < kFewUnits;
   if (scored) {
     const int chunks = (cache->max_pages + kScoreBlocks - 1) / kScoreBlocks;
     const unsigned grid = static_cast<unsigned>(units * chunks);

@@ -101,6 +101,36 @@ def test_a_step_without_rows_goes_through_all_calls():
     assert all(torch.equal(a, b) for a, b in zip(before, (cache.k, cache.v, cache.scales, cache.bounds)))
 
 
+# ---------------------------------------------------------------- choice of blocks
+
+@pytest.mark.parametrize("blocks,rows,count,hkv", [(700, 1, 3, 2), (4096, 3, 512, 1), (4097, 40, 64, 2), (9000, 99, 20, 1),
+                                                   (700, 50, 16, 2), (5000, 101, 64, 1), (9000, 52, 33, 2), (20000, 100, 512, 1)])
+def test_select_with_and_without_a_kernel_for_the_scores(blocks, rows, count, hkv):
+    """On both sides of the rule (100 rows times heads), 1 to 8 CTAs a row and head, rows of unequal lengths."""
+    d = 64
+    g = torch.Generator().manual_seed(blocks + rows)
+    bounds = torch.randint(-90, 91, (blocks, hkv, 2, d), generator=g).sort(2).values.to(torch.int8)
+    scales = torch.exp2(torch.randint(-1, 1, (blocks, hkv, 2), generator=g).float())
+    cache = pkg.KVCache(torch.empty((blocks, hkv, 64, d), dtype=torch.uint8, device="cuda"),
+                        torch.empty((blocks, hkv, d, 64), dtype=torch.uint8, device="cuda"), scales.cuda(), bounds.cuda(), 0)
+    table = torch.stack([torch.randperm(blocks, generator=g) for _ in range(rows)]).int()
+    q = torch.randint(-127, 128, (rows, hkv, d), generator=g).to(torch.bfloat16)
+    q[:, :, 0] = 127  # whole numbers that the rounding of q leaves alone
+    lens = torch.randint(1, blocks * 64 + 1, (rows,), generator=g).int()
+    lens[0] = blocks * 64
+    got = pkg.cache_select(cache, table.cuda(), lens.cuda(), q.cuda(), count, keep_first=1, keep_last=min(2, count - 1)).cpu()
+    pkg.hdp_device_status()
+    for r in range(rows):
+        have = (int(lens[r]) - 1) // 64 + 1
+        page = table[r, :have].long()
+        for h in range(hkv):
+            x, b = q[r, h].long(), bounds[page, h].long()
+            score = (b[:, 1] @ x.clamp(min=0) + b[:, 0] @ x.clamp(max=0)).float() * scales[page, h, 0]
+            score[:1] = score[max(0, have - min(2, count - 1)):] = float("inf")
+            want = score.sort(descending=True, stable=True).indices[:count].sort().values
+            assert torch.equal(got[r, h, :len(want)].long(), want) and (got[r, h, len(want):] == -1).all(), (r, h)
+
+
 # ---------------------------------------------------------------- streams and graphs
 
 def test_inputs_that_die_while_another_stream_reads_them():
