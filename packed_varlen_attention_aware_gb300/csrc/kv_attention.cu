@@ -41,13 +41,10 @@
 //   in the order of the keys.
 //
 // Measured (one GB300, in a captured graph): one token over 2M cached ones, 8 kv
-// heads of 128, 635 to 641 us (4.3 GB, 6.7 to 6.8 TB/s); 64 sequences of 256 to
-// 29K tokens 149 us (843 MB, 5.7 TB/s: while the runs stream, a block takes a warp
-// 5.3K cycles; the rest is the start and the ends); 64 x 32 chosen blocks 56 us
-// (270 MB).  Of these, the blocks' own sums take 1 us, 2, 1 (and of 66 us for 16
-// sequences of up to 5 tokens 2), the look at small outputs and P's wait in shared
-// memory 3, 1, 1 (5).  The loop's size in instructions costs as much as what it
-// does: with the further passes unrolled those were 5, 4, 2 (11).
+// heads of 128, 629 to 637 us (4.3 GB, 6.7 to 6.8 TB/s); 64 sequences of 256 to
+// 29K tokens 146.5 us (843 MB, 5.8 TB/s: while the runs stream, a block takes a warp
+// 5.2K cycles; the rest is the start and the ends); 64 x 32 chosen blocks 54 us
+// (270 MB); 16 sequences with up to 5 drafted tokens 62 us.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -308,7 +305,7 @@ __device__ __forceinline__ void write_o(const AttnParams& p, int row0, int head,
 template <int D, class S, class O>
 __device__ __forceinline__ float2 join_row(int m, int lane, float (&x)[D / 32], S sum_at, O o_at) {
   constexpr int V = D / 32;
-  constexpr int kAhead = 16;  // partial rows in flight
+  constexpr int kAhead = 8;  // partial rows in flight (16: a spill, 64 x 32 chosen blocks 54.3 us against 53.7)
   float top = kLow, sum = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) x[i] = 0.f;
@@ -946,8 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
       copies_commit();
     };
 
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) issue();
+    int ahead = kSlots;  // half steps that the copies go in front at first
 
     int slot = 0, meta_at = 0, at_piece = run * cut.pieces;  // (the copies may be in a later piece already)
     long long at = start;
@@ -969,53 +965,60 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
       Sums<D, NT> sums;
       sums.clear();
 
-      for (int step = 0; step < steps; ++step) {
-        copies_wait<kSlots - 1>();
-        __syncwarp();
-        const Meta meta = sm.meta[warp][meta_at];
-        meta_at = (meta_at + 1) % kMeta;
-        const bool seen = meta.key0 >= 0;
-        const bool masked = meta.key0 + kBlock - 1 > low_pos;  // some row does not see the whole block
-        float f[NT][2];
-        const Probabilities<NT> prob = {sm.p[warp]};
-        if (seen) {
-          const uint4* kx = reinterpret_cast<const uint4*>(sm.ring[warp] + slot * kHalf) + lane;
-          float s[NT][4][4];
-          first_product<D, FMT, NT>(rows, s, [&](int i, int j) { return kx[(i * kKeyChunks + j) * 32]; });
-          softmax<D, NT>(rows, sums, meta.sk, meta.sv, meta.key0, masked, s, f);
-          prob.put(s);
-        }
-        slot = slot + 1 == kSlots ? 0 : slot + 1;
-        issue();
-
-        copies_wait<kSlots - 1>();
-        if (seen) {
-          const uint4* vx = reinterpret_cast<const uint4*>(sm.ring[warp] + slot * kHalf) + lane;
-          bool sure = false;  // that further passes are needed
-          while (true) {
-            uint32_t pf[NT][4][2];
-            float least[NT][2];
-            prob.get(pf);
-            second_product<D, FMT, NT>(sums, pf, f, masked, least, [&](int i) { return vx[i * 32]; });
-            // Is an output so small that what fp16 leaves of P could count?
+      // Half a step is a block's scores or its output; then the next half block is asked
+      // for.  That is a page of code with a place of its own, once in the kernel: the
+      // loop is bound by the fetch of its instructions as much as by what they do.  Twice
+      // in the loop and once in front of it, unrolled, 64 sequences took 149.4 us against
+      // 146.5, 16 drafts 66.3 against 61.8, four short documents 11.3 against 9.9.
+      const Probabilities<NT> prob = {sm.p[warp]};
+      float f[NT][2];
+      bool seen = false, masked = false;
+#pragma unroll 1
+      for (int half_step = -ahead; half_step < 2 * steps; ++half_step) {
+        if (half_step >= 0) {
+          copies_wait<kSlots - 1>();
+          if (half_step % 2 == 0) {
+            __syncwarp();
+            const Meta meta = sm.meta[warp][meta_at];
+            meta_at = (meta_at + 1) % kMeta;
+            seen = meta.key0 >= 0;
+            masked = meta.key0 + kBlock - 1 > low_pos;  // some row does not see the whole block
+            if (seen) {
+              const uint4* kx = reinterpret_cast<const uint4*>(sm.ring[warp] + slot * kHalf) + lane;
+              float s[NT][4][4];
+              first_product<D, FMT, NT>(rows, s, [&](int i, int j) { return kx[(i * kKeyChunks + j) * 32]; });
+              softmax<D, NT>(rows, sums, meta.sk, meta.sv, meta.key0, masked, s, f);
+              prob.put(s);
+            }
+          } else if (seen) {
+            const uint4* vx = reinterpret_cast<const uint4*>(sm.ring[warp] + slot * kHalf) + lane;
+            bool sure = false;  // that further passes are needed
+            while (true) {
+              uint32_t pf[NT][4][2];
+              float least[NT][2];
+              prob.get(pf);
+              second_product<D, FMT, NT>(sums, pf, f, masked, least, [&](int i) { return vx[i * 32]; });
+              // Is an output so small that what fp16 leaves of P could count?
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+              for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
-                sure |= t * 8 + 2 * tc + k < nrows && f[t][k] != 0.f && !(least[t][k] >= kEnough<FMT>);
-            if (!__any_sync(0xffffffffu, sure) || !__any_sync(0xffffffffu, prob.more())) break;
-            sure = true;
-            prob.next();  // four times at most
+                for (int k = 0; k < 2; ++k)
+                  sure |= t * 8 + 2 * tc + k < nrows && f[t][k] != 0.f && !(least[t][k] >= kEnough<FMT>);
+              if (!__any_sync(0xffffffffu, sure) || !__any_sync(0xffffffffu, prob.more())) break;
+              sure = true;
+              prob.next();  // four times at most
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              f[t][0] *= 1.f / kNextPass;
-              f[t][1] *= 1.f / kNextPass;
+              for (int t = 0; t < NT; ++t) {
+                f[t][0] *= 1.f / kNextPass;
+                f[t][1] *= 1.f / kNextPass;
+              }
             }
           }
+          slot = slot + 1 == kSlots ? 0 : slot + 1;
         }
-        slot = slot + 1 == kSlots ? 0 : slot + 1;
         issue();
       }
+      ahead = 0;
       at += steps;
       done += steps;
       const int rest = cc.nb - cc.blk - steps;  // steps of the unit behind the piece
