@@ -274,8 +274,8 @@ hdp_status_t hdp_flops_per_shard(hdp_plan_t plan, int32_t d, int32_t hq, int64_t
  * value is code * scale.  A scale is a power of two: the smallest 2^e,
  * e >= -126, with |x| <= M 2^e for every row ever written to the block since
  * its first one (M = 448 for e4m3, 127 for int8).  Division by it, code *
- * scale (in bf16 too) and a change of scale are exact but for one rounding of
- * the code to the nearest (ties to even).  When a row needs a larger scale,
+ * scale (in bf16 too, see hdp_cache_read) and a change of scale are exact but
+ * for one rounding of the code to the nearest (ties to even).  When a row needs a larger scale,
  * the block's codes are rounded to the new one; over any number of such
  * changes an int8 value is off by less than one step and an e4m3 value by at
  * most half a step plus one subnormal step (2^-9 scale).  A row with an
@@ -339,7 +339,9 @@ typedef struct {
 hdp_status_t hdp_cache_append(const hdp_cache_t* cache, const int32_t* cu, int64_t rows, const void* k, const void* v,
                               void* stream);
 
-/* Reads the rows back: k, v [rows][hkv][d] bf16 (exactly code * scale). */
+/* Reads the rows back: k, v [rows][hkv][d] bf16: exactly code * scale, but for
+ * e4m3 codes at scales of 2^-126 and 2^-125, whose smallest products are below
+ * bf16's smallest number and are rounded to it. */
 hdp_status_t hdp_cache_read(const hdp_cache_t* cache, const int32_t* cu, int64_t rows, void* k, void* v, void* stream);
 
 /*
@@ -348,15 +350,21 @@ hdp_status_t hdp_cache_read(const hdp_cache_t* cache, const int32_t* cu, int64_t
  *   S_j = scale * q . k_j over cached tokens j <= p,
  *   lse = ln sum_j exp(S_j),  o = sum_j exp(S_j - lse) v_j,
  * and o = 0, lse = -inf where no token is left.  Inputs are the dequantised
- * codes; sums and the softmax's statistics are fp32.
+ * codes; sums and the softmax's statistics are fp32.  That holds for q, K and V
+ * over all of bf16's range, scores up to fp32's end, and weights down to 2^-126
+ * of a row's largest.  Elements of a query row below 2^-31 of its largest keep
+ * fewer bits (they are rounded to multiples of 2^-38 of it).
  *   q, o [rows][hq][d] bf16, 16-byte aligned; lse [hq][rows] fp32; hq % hkv == 0.
  *   blocks NULL (count 0): every block.  Else device int32 [rows][hkv][count],
  *   count >= 1: for each row and kv head the blocks to attend to, strictly
  *   ascending.  An entry that is negative, beyond the row's position or not
- *   above the entry before it is skipped (hdp_cache_select pads with -1).
+ *   above the entry directly before it is skipped (hdp_cache_select pads with
+ *   -1).  Nothing else is checked: a block that stands twice in a list that does
+ *   not ascend may count twice.
  *   workspace: device, 256-byte aligned, at least
  *   hdp_cache_attention_workspace_bytes (which depends on the device's SM
- *   count, hq, hkv and d only); calls that may overlap need one each.
+ *   count and d only: 122 MB for d = 128 on 152 SMs, 62 MB for d = 64); calls
+ *   that may overlap need one each.
  * Deterministic: the order of all sums depends only on the shapes and lengths.
  * Made for a few rows per sequence (16 rows times heads of a group share one
  * pass over the cache); more rows are correct and read the cache again.
@@ -383,7 +391,7 @@ hdp_status_t hdp_cache_attention(const hdp_cache_t* cache, const int32_t* cu, in
  *   blocks [rows][hkv][count] int32 out: ascending, -1 behind the last;
  *   count >= 1, keep_first >= 0, keep_last >= 0, keep_first + keep_last <= count;
  *   workspace: device, 256-byte aligned, hdp_cache_select_workspace_bytes
- *   (rows * hkv * max_pages scores).
+ *   (rows * hkv * max_pages scores of 4 bytes, also where they are not used).
  */
 hdp_status_t hdp_cache_select_workspace_bytes(const hdp_cache_t* cache, int64_t rows, size_t* bytes);
 hdp_status_t hdp_cache_select(const hdp_cache_t* cache, const int32_t* cu, int64_t rows, const void* q, int32_t hq,

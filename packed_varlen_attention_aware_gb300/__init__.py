@@ -143,7 +143,7 @@ def cache_append(cache: KVCache, page_table, lens, k, v, cu=None, stream=None):
 
 
 def cache_read(cache: KVCache, page_table, lens, rows: int, cu=None, stream=None):
-    """The newest tokens of each sequence as (k, v) [rows][hkv][d] bf16, exactly code * scale."""
+    """The newest tokens of each sequence as (k, v) [rows][hkv][d] bf16: code * scale, exactly down to bf16's smallest number."""
     import torch
 
     s = cache._with(page_table, lens, cu, rows)

@@ -237,3 +237,27 @@ def test_the_smallest_v_in_long_sequences():
     # most, one for the 64 keys of a step, 2^-24 * 17188 < 2^-9; then half a bf16 step
     assert ((o.double() / (1.5 * 2.0 ** -121) - 1).abs() <= 2.0 ** -8 + 2.0 ** -9).all()
     assert ((lse.double() - np.log(n)).abs() <= 2.0 ** -9).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_read_at_the_smallest_scales(fmt, d):
+    """Every code at scales of 2^-126 to 2^-122 and 2^119: the nearest bf16 to code * scale, exact from 2^-124 on."""
+    exponents = [-126, -125, -124, -123, -122, 119]
+    pages = len(exponents)
+    cache = pkg.KVCache.empty(pages, 1, d, fmt)
+    codes = torch.arange(64 * d, device="cuda").view(64, d) % 254
+    codes = (codes - 127).to(torch.int8).view(torch.uint8) if fmt else torch.where(codes < 127, codes, codes + 1).to(torch.uint8)
+    cache.k.copy_(codes.expand(pages, 1, 64, d))
+    at = torch.tensor([16 * (t // 2 % 4) + 4 * (t // 16) + 2 * (t // 8 % 2) + t % 2 for t in range(64)], device="cuda")
+    cache.v[..., at] = codes.t().expand(pages, 1, d, 64)
+    cache.scales.copy_(torch.tensor([2.0 ** e for e in exponents], device="cuda")[:, None, None].expand(pages, 1, 2))
+    n = 64 * pages
+    k, v = pkg.cache_read(cache, torch.arange(pages, dtype=torch.int32, device="cuda")[None], _i32([n]), n, cu=_i32([0, n]))
+    value = codes.view(torch.int8).double() if fmt else codes.view(torch.float8_e4m3fn).double()
+    want = (value[None] * cache.scales[:, 0, :1, None].double()).view(n, 1, d)
+    step = torch.where(want.abs() < 2.0 ** -126, 2.0 ** -133, 0.0)  # of bf16's subnormal numbers
+    exact = torch.tensor([bool(fmt) or e >= -124 for e in exponents], device="cuda").repeat_interleave(64)[:, None, None]
+    for got in (k.double(), v.double()):
+        assert torch.equal(got[exact.expand_as(got)], want[exact.expand_as(got)])
+        assert ((got - want).abs() <= step / 2).all()
