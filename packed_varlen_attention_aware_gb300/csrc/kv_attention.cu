@@ -60,8 +60,10 @@ constexpr int kThreads = kWarps * 32;
 // Bytes of a warp's ring of half blocks.  More in flight streams a long run
 // better; less leaves the memory's queues shorter, and with them every other
 // access (lists, pages, query rows), which short runs wait for.  Measured at
-// 24 KB and 16 KB: one 2M-token sequence 646 and 654 us, 64 x 32 chosen blocks
-// 59 and 55 us, 16 sequences with up to 5 drafted tokens 67 and 62 us.
+// 24 KB and 16 KB: one 2M-token sequence 636 and 647 us, 64 sequences 146.7 and
+// 148.7, 64 x 32 chosen blocks 56.4 and 53.7.  (24 KB do not fit beside two tiles' P;
+// before it had a place there, 16 sequences with up to 5 drafted tokens took 67 and
+// 62 us.)
 template <int NT, bool SPARSE>
 constexpr int kRingBytes = NT == 1 && !SPARSE ? 24576 : 16384;
 constexpr int kMeta = 8;           // blocks whose scales and first key are kept
