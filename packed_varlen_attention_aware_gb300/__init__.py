@@ -123,8 +123,12 @@ def _pool(stream, cache):
 
 def _in_use(stream, cache, *inputs):
     """Inputs of a call on another torch stream: their memory, freed, is not given out before that stream has read it.
-    (Nothing can be noted for a raw handle, which may be destroyed before the tensors are.)"""
-    if stream is not None and not isinstance(stream, int):
+    (Nothing can be noted for a stream that torch does not own, which may be destroyed before the tensors are.)"""
+    if stream is None or isinstance(stream, int):
+        return
+    import torch
+
+    if isinstance(stream, torch.cuda.Stream) and not isinstance(stream, torch.cuda.ExternalStream):
         for t in (cache.k, cache.v, cache.scales, cache.bounds, *inputs):
             if t is not None:
                 t.record_stream(stream)
@@ -132,7 +136,7 @@ def _in_use(stream, cache, *inputs):
 
 # The calls below run on `stream`, or on the current one.  As everywhere in torch, a call on another stream than the one
 # that made its inputs has to be ordered behind it (stream.wait_stream).  A torch stream keeps its inputs' memory until
-# it has read them; with a raw handle (int) the caller keeps the inputs alive until the call has run.  What a call on
+# it has read them; with a raw handle or another's stream the caller keeps the inputs alive until the call has run.  What a call on
 # another stream than the current one returns belongs to that stream.
 
 def cache_append(cache: KVCache, page_table, lens, k, v, cu=None, stream=None):
