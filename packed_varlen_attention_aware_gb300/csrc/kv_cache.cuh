@@ -102,4 +102,44 @@ __device__ __forceinline__ int page_of(const CacheView& c, int i, int b) {
   return p;
 }
 
+// The block of a CTA: which sequence, block and rows `slot` stands for.
+// Sequence i has the slots from cu[i] / 64 + 2 i on; n rows touch at most
+// ceil((n + 62) / 64) + 1 <= cu[i+1] / 64 - cu[i] / 64 + 2 blocks.
+struct Touched {
+  int seq, block;
+  int first, count;  // first token of the block that the call has, and how many
+  long long row;     // row of that token
+  bool fresh;        // the block's first token is among them
+  long long row0, before;  // the slot also stands for `before` rows from row0 on, at negative positions
+};
+
+__device__ __forceinline__ bool touched_block(const CacheView& c, int slot, Touched& t) {
+  const int i = c.cu ? find_last(c.num_seqs, slot,
+                                 [&](int s) { return static_cast<long long>(__ldg(c.cu + s)) / kBlock + 2LL * s; })
+                     : slot;
+  int row0, n;
+  seq_rows(c, i, row0, n);
+  t.before = 0;
+  if (n == 0) return false;
+  const long long len = seq_len(c, i), p0 = first_position(c, i, len);
+  const long long nth = c.cu ? slot - (row0 / kBlock + 2LL * i) : 0;
+  if (nth == 0 && p0 < 0) {
+    t.row0 = row0;
+    t.before = min(static_cast<long long>(n), -p0);
+  }
+  const long long a0 = p0 > 0 ? p0 : 0;
+  const long long b = a0 / kBlock + nth;
+  const long long end = min(len, p0 + n);
+  if (nth < 0 || b * kBlock >= end) return false;
+  const long long a = max(a0, b * kBlock), z = min(end, (b + 1) * kBlock);
+  if (z <= a) return false;
+  t.seq = i;
+  t.block = static_cast<int>(b);
+  t.first = static_cast<int>(a - b * kBlock);
+  t.count = static_cast<int>(z - a);
+  t.row = row0 + (a - p0);
+  t.fresh = t.first == 0;
+  return true;
+}
+
 }  // namespace hdp
