@@ -398,12 +398,139 @@ hdp_status_t hdp_cache_select(const hdp_cache_t* cache, const int32_t* cu, int64
                               int32_t count, int32_t keep_first, int32_t keep_last, void* workspace,
                               size_t workspace_bytes, int32_t* blocks, void* stream);
 
+/* ====================================================================== */
+/* 4-bit key/value cache: half the bytes of the 8-bit one, with finer scales and
+ * the same pages, page tables, lengths, rows and rules ("Common to the calls
+ * below" above holds here too, with workspaces and streams).  A row's codes
+ * depend on that row alone, so rows may be written in any order and pieces, and
+ * written again, and every bit of the cache that they decide is the same.
+ *
+ * Codes are e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 for the low three bits, the fourth
+ * is the sign; two in a byte, the first in its low half.  A value is code *
+ * scale.  A scale is a power of two, held in a byte as its exponent plus 127
+ * (255: NaN): the smallest 2^e, e >= -126, with |x| <= 6 2^e over the 32 channels
+ * of K, or over the d channels of V, that share it.  x / scale is exact and is
+ * rounded to the nearest code (ties to the even one); half a step of it is at most
+ * scale.  (Values beyond 3 * 2^126 are taken as that: the next code is past bf16's
+ * end.)  Channels that share a scale with an infinity or NaN read as NaN.  Byte 0 is
+ * never written; what is read through it is unspecified, but below 2^-124.
+ */
+typedef struct {
+  void* k;               /* [num_pages][hkv][64][d/2], 16-byte aligned: channel
+                            32 g + 8 c + 2 b + e of a token stands in byte
+                            (d/8) c + 4 g + b of its row, half e                */
+  void* v;               /* [num_pages][hkv][d/16][512], 16-byte aligned: channel
+                            16 i + 8 h + r of token 16 s + 8 p + 2 c + e stands in
+                            byte 64 r + 16 c + 8 h + 2 s + p of row i, half e   */
+  uint8_t* scales;       /* [num_pages][hkv][d/32 + 1][64], 16-byte aligned: row g
+                            of channels 32 g .. 32 g + 31 of K, the last row of V,
+                            token 8 j + r at place 8 r + j                      */
+  int32_t num_pages;     /* >= 1                                               */
+  int32_t hkv;           /* >= 1                                               */
+  int32_t d;             /* 64 or 128                                          */
+  int32_t num_seqs;      /* >= 1                                               */
+  const int32_t* page_table; /* [num_seqs][max_pages] page of each block       */
+  const int32_t* lens;   /* [num_seqs] tokens of each sequence, the rows of the
+                            call included                                      */
+  int32_t max_pages;     /* columns of page_table, >= 1                        */
+} hdp_fourbit_cache_t;
+
+/* Writes K and V rows (bf16 [rows][hkv][d], 16-byte aligned) into the cache.
+ * Nothing but their codes and scales is changed.  A page that the call writes must
+ * belong to one sequence only; complete pages may be shared. */
+hdp_status_t hdp_fourbit_append(const hdp_fourbit_cache_t* cache, const int32_t* cu, int64_t rows, const void* k,
+                                const void* v, void* stream);
+
+/* Reads the rows back: k, v [rows][hkv][d] bf16, exactly code * scale. */
+hdp_status_t hdp_fourbit_read(const hdp_fourbit_cache_t* cache, const int32_t* cu, int64_t rows, void* k, void* v,
+                              void* stream);
+
+/* hdp_cache_attention over this cache: the same formulas, arguments and promises,
+ * over all blocks (there are no lists).  workspace: device, 256-byte aligned, at
+ * least hdp_fourbit_attention_workspace_bytes, which depends on the device's SM
+ * count and d only; calls that may overlap need one each. */
+hdp_status_t hdp_fourbit_attention_workspace_bytes(const hdp_fourbit_cache_t* cache, int32_t hq, size_t* bytes);
+hdp_status_t hdp_fourbit_attention(const hdp_fourbit_cache_t* cache, const int32_t* cu, int64_t rows, const void* q,
+                                   int32_t hq, float scale, void* workspace, size_t workspace_bytes, void* o, float* lse,
+                                   void* stream);
+
+/* ====================================================================== */
+/* Block tables and slot maps from the requests' lengths, for either cache.
+ *
+ * hdp_cache_assign brings the pages that the sequences hold in line with their
+ * lengths.  The free pages of a pool are a stack: free_pages [num_pages], of which
+ * the first free_count[0] are free, the last of them on top.  Sequence i holds the
+ * pages of its blocks 0 .. held[i] - 1, page_table [num_seqs][max_pages] says
+ * which, and it needs ceil(lens[i] / 64).
+ *   1. Pages beyond that go back on the stack: the last sequence's first, and of a
+ *      sequence the last block's first.
+ *   2. Then each sequence, in order, takes a page from the top for every block
+ *      that it lacks, in order.  A sequence whose blocks are not all there, and
+ *      every later one that lacks any, takes none and keeps its held[i]; the next
+ *      hdp_device_status then reports OUT_OF_MEMORY.
+ * free_pages, free_count, held and page_table are updated in place; taking pages
+ * and giving them back leaves the stack as it was.  Entries of page_table beyond
+ * held[i] are left as they are.  Lengths, held and free_count outside their ranges
+ * are taken as the nearest bound and reported as INVALID_ARGUMENT.  All pointers
+ * are device pointers; calls on one pool must not overlap.  A page belongs to one
+ * sequence: pages that sequences share are not for this call to give back.
+ * num_seqs at most 2^24.
+ */
+hdp_status_t hdp_cache_assign(int32_t* free_pages, int32_t* free_count, int32_t num_pages, int32_t* page_table,
+                              int32_t* held, const int32_t* lens, int32_t num_seqs, int32_t max_pages, void* stream);
+
+/*
+ * Where the rows of a call lie (rows, cu and lens as in the cache calls):
+ * sequence [rows] int32, position [rows] int32 and slot [rows] int64 = page * 64 +
+ * position % 64; each may be NULL.  Rows of no sequence get -1 in all three, rows
+ * at a negative position and rows on a page outside [0, num_pages) get slot -1
+ * (the latter is reported like a bad page of a cache call).  page_table NULL: no
+ * slots, slot must be NULL, max_pages and num_pages are ignored and lengths are
+ * only bounded below, by 0: with lens the lengths of packed documents and cu their
+ * prefix sums, position is each token's place in its document.
+ */
+hdp_status_t hdp_cache_rows(const int32_t* page_table, const int32_t* lens, const int32_t* cu, int32_t num_seqs,
+                            int32_t max_pages, int32_t num_pages, int64_t rows, int32_t* sequence, int32_t* position,
+                            int64_t* slot, void* stream);
+
+/* ====================================================================== */
+/* Rotary positions.  Pair i (0 .. rot/2 - 1) of a head's channels, (a, b) =
+ * channels (i, i + rot/2), or with HDP_ROTARY_NEIGHBOURS (2 i, 2 i + 1), becomes
+ *   (factor (a cos x - b sin x), factor (b cos x + a sin x)),  x = position * freqs[i],
+ * channels from rot on are copied.  With HDP_ROTARY_BACKWARD x is negated: the
+ * gradient of the rows before the turn from that of the rows behind it.
+ *   q, k: either may be NULL.  Rows [rows][heads][d] of `type`, channels
+ *   contiguous, other strides in elements; out may be in (with the same strides),
+ *   else the two must not overlap.  Any alignment; 16-byte steps where the
+ *   addresses, strides and rot allow them.
+ *   position [rows] int32; a row at a negative one is not read, its output is left
+ *   as it was.  freqs [rot/2] double, radians, finite (device; scaling for long
+ *   contexts is in them and in factor).  2 <= rot <= d <= 256, rot even; factor > 0.
+ * The angle's fraction of a turn is exact to 2^-31 over all positions.  Products
+ * and sums are fp32, rounded once to `type`.
+ */
+#define HDP_TYPE_BF16 0
+#define HDP_TYPE_FP16 1
+#define HDP_TYPE_FP32 2
+#define HDP_ROTARY_NEIGHBOURS 1
+#define HDP_ROTARY_BACKWARD 2
+typedef struct {
+  const void* in;
+  void* out;
+  int64_t in_row_stride, in_head_stride, out_row_stride, out_head_stride;
+  int32_t heads; /* 0 .. 2^20 */
+} hdp_rotary_rows_t;
+hdp_status_t hdp_rotary(const hdp_rotary_rows_t* q, const hdp_rotary_rows_t* k, int64_t rows, int32_t d, int32_t type,
+                        const int32_t* position, const double* freqs, int32_t rot, int32_t flags, float factor,
+                        void* stream);
+
 /*
  * Synchronizes `stream` and reports (then clears) a device-side failure
  * recorded by an earlier kernel of this library on the current device:
  * HDP_ERR_DEVICE_TIMEOUT when a bounded wait expired, INVALID_ARGUMENT when a
- * cache call met a length or page outside its tables, HDP_ERR_CUDA when the
- * stream reports a CUDA error, else HDP_OK.
+ * cache call met a length or page outside its tables, OUT_OF_MEMORY when
+ * hdp_cache_assign ran out of free pages, HDP_ERR_CUDA when the stream reports a
+ * CUDA error, else HDP_OK.
  */
 hdp_status_t hdp_device_status(void* stream);
 

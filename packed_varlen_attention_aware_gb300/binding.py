@@ -30,6 +30,11 @@ HDP_BALANCE_PP = 1
 HDP_CACHE_BLOCK = 64
 HDP_CACHE_E4M3 = 0
 HDP_CACHE_INT8 = 1
+HDP_TYPE_BF16 = 0
+HDP_TYPE_FP16 = 1
+HDP_TYPE_FP32 = 2
+HDP_ROTARY_NEIGHBOURS = 1
+HDP_ROTARY_BACKWARD = 2
 
 # Every symbol include/hdpattn.h declares.
 EXPORTED = (
@@ -41,6 +46,8 @@ EXPORTED = (
     "hdp_balance_schedule", "hdp_attention_bwd_workspace_bytes", "hdp_attention_bwd",
     "hdp_cache_append", "hdp_cache_read", "hdp_cache_attention_workspace_bytes", "hdp_cache_attention",
     "hdp_cache_select_workspace_bytes", "hdp_cache_select",
+    "hdp_fourbit_append", "hdp_fourbit_read", "hdp_fourbit_attention_workspace_bytes", "hdp_fourbit_attention",
+    "hdp_cache_assign", "hdp_cache_rows", "hdp_rotary",
 )
 
 
@@ -57,6 +64,21 @@ class CacheStruct(ctypes.Structure):
                 ("bounds", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("hkv", ctypes.c_int32),
                 ("d", ctypes.c_int32), ("format", ctypes.c_int32), ("page_table", ctypes.c_void_p),
                 ("lens", ctypes.c_void_p), ("num_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class Cache4Struct(ctypes.Structure):
+    """hdp_fourbit_cache_t."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("num_seqs", ctypes.c_int32), ("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("max_pages", ctypes.c_int32)]
+
+
+class RotaryRows(ctypes.Structure):
+    """hdp_rotary_rows_t."""
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("in_row_stride", ctypes.c_int64),
+                ("in_head_stride", ctypes.c_int64), ("out_row_stride", ctypes.c_int64),
+                ("out_head_stride", ctypes.c_int64), ("heads", ctypes.c_int32)]
 
 
 class HdpError(RuntimeError):
@@ -122,6 +144,13 @@ def load(path: str | None = None):
             "hdp_cache_attention": [ctypes.POINTER(CacheStruct), V, I64, V, I32, F32, V, I32, V, SZ, V, V, V],
             "hdp_cache_select_workspace_bytes": [ctypes.POINTER(CacheStruct), I64, ctypes.POINTER(SZ)],
             "hdp_cache_select": [ctypes.POINTER(CacheStruct), V, I64, V, I32, I32, I32, I32, V, SZ, V, V],
+            "hdp_fourbit_append": [ctypes.POINTER(Cache4Struct), V, I64, V, V, V],
+            "hdp_fourbit_read": [ctypes.POINTER(Cache4Struct), V, I64, V, V, V],
+            "hdp_fourbit_attention_workspace_bytes": [ctypes.POINTER(Cache4Struct), I32, ctypes.POINTER(SZ)],
+            "hdp_fourbit_attention": [ctypes.POINTER(Cache4Struct), V, I64, V, I32, F32, V, SZ, V, V, V],
+            "hdp_cache_assign": [V, V, I32, V, V, V, I32, I32, V],
+            "hdp_cache_rows": [V, V, V, I32, I32, I32, I64, V, V, V, V],
+            "hdp_rotary": [ctypes.POINTER(RotaryRows), ctypes.POINTER(RotaryRows), I64, I32, I32, V, V, I32, I32, F32, V],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -334,6 +363,10 @@ def hdp_last_error_message() -> str:
 _CACHE_FORMAT = struct.Struct("PPPPiiiiPPii")
 assert _CACHE_FORMAT.size == ctypes.sizeof(CacheStruct)
 _cache_calls = None
+_CACHE4_FORMAT = struct.Struct("PPPiiiiPPi4x")
+assert _CACHE4_FORMAT.size == ctypes.sizeof(Cache4Struct)
+_ROTARY_FORMAT = struct.Struct("PPqqqqi4x")
+assert _ROTARY_FORMAT.size == ctypes.sizeof(RotaryRows)
 
 
 def _cache_lib():
@@ -341,16 +374,46 @@ def _cache_lib():
     global _cache_calls
     if _cache_calls is None:
         lib, calls = load(), {}
-        for name in ("hdp_cache_append", "hdp_cache_read", "hdp_cache_attention", "hdp_cache_select"):
-            f = lib[name]  # a handle of its own: the attribute keeps its typed struct argument
-            f.argtypes = [ctypes.c_void_p] + getattr(lib, name).argtypes[1:]
+        for name in ("hdp_cache_append", "hdp_cache_read", "hdp_cache_attention", "hdp_cache_select", "hdp_fourbit_append",
+                     "hdp_fourbit_read", "hdp_fourbit_attention", "hdp_cache_assign", "hdp_cache_rows", "hdp_rotary"):
+            f = lib[name]  # a handle of its own: the attribute keeps its typed struct arguments
+            f.argtypes = [ctypes.c_void_p if issubclass(a, ctypes._Pointer) else a for a in getattr(lib, name).argtypes]
             f.restype = ctypes.c_int
             calls[name] = f
         _cache_calls = calls
     return _cache_calls
 
 
-class KVCache:
+class _Cache:
+    """What the caches of 8 and of 4 bits share."""
+
+    def _rows_of(self, q, name):
+        """(rows, hq) of q [rows][hq][d] bf16."""
+        import torch
+
+        rows, hq = q.shape[0], q.shape[1] if q.dim() == 3 else -1
+        _tensor(q, name, torch.bfloat16, (rows, hq, self.d), self._dev)
+        return rows, hq
+
+    def _sequences(self, page_table, lens, cu, rows):
+        """(sequences, columns) of a call."""
+        import torch
+
+        n = lens.shape[0] if lens.dim() == 1 else -1
+        columns = page_table.shape[1] if page_table.dim() == 2 else -1
+        _tensor(lens, "lens", torch.int32, (n,), self._dev)
+        _tensor(page_table, "page_table", torch.int32, (n, columns), self._dev)
+        if cu is not None:
+            _tensor(cu, "cu", torch.int32, (n + 1,), self._dev)
+        elif rows != n:
+            raise ValueError(f"without cu there is one row for each of the {n} sequences, not {rows}")
+        return n, columns
+
+    def _call(self, name, stream, *args):
+        _run(self._dev, name, stream, *args)
+
+
+class KVCache(_Cache):
     """A pool of pages of 64 tokens with 8-bit K and V codes (hdp_cache_t without the sequences).
 
     k [pages][hkv][64][d] and v [pages][hkv][d][64] uint8 codes, scales [pages][hkv][2] float32, bounds
@@ -387,27 +450,13 @@ class KVCache:
 
     def _with(self, page_table, lens, cu, rows):
         """hdp_cache_t of a call over these sequences, as bytes."""
-        import torch
-
-        n = lens.shape[0] if lens.dim() == 1 else -1
-        columns = page_table.shape[1] if page_table.dim() == 2 else -1
-        _tensor(lens, "lens", torch.int32, (n,), self._dev)
-        _tensor(page_table, "page_table", torch.int32, (n, columns), self._dev)
-        if cu is not None:
-            _tensor(cu, "cu", torch.int32, (n + 1,), self._dev)
-        elif rows != n:
-            raise ValueError(f"without cu there is one row for each of the {n} sequences, not {rows}")
+        n, columns = self._sequences(page_table, lens, cu, rows)
         return _CACHE_FORMAT.pack(self.k.data_ptr(), self.v.data_ptr(), self.scales.data_ptr(), self.bounds.data_ptr(),
                                   self.num_pages, self.hkv, self.d, self.format, page_table.data_ptr(),
                                   lens.data_ptr(), n, columns)
 
-    def _rows_of(self, q, name):
-        """(rows, hq) of q [rows][hq][d] bf16."""
-        import torch
-
-        rows, hq = q.shape[0], q.shape[1] if q.dim() == 3 else -1
-        _tensor(q, name, torch.bfloat16, (rows, hq, self.d), self._dev)
-        return rows, hq
+    def _buffers(self):
+        return self.k, self.v, self.scales, self.bounds
 
     def _blocks_of(self, blocks, rows):
         """(count, address) of a block list."""
@@ -421,25 +470,81 @@ class KVCache:
         _tensor(blocks, "blocks", torch.int32, (rows, self.hkv, count), self._dev)
         return count, blocks.data_ptr()
 
-    def _call(self, name, stream, *args):
-        """Runs an entry point with the cache's device current, on `stream` or that device's current one."""
+
+class KVCache4(_Cache):
+    """A pool of pages of 64 tokens with 4-bit K and V codes (hdp_fourbit_cache_t without the sequences).
+
+    k [pages][hkv][64][d/2], v [pages][hkv][d/16][512] and scales [pages][hkv][d/32 + 1][64], all uint8: contiguous CUDA
+    tensors of one device.  It goes where a KVCache goes, but that it has no lists of blocks."""
+
+    _names = {"hdp_cache_append": "hdp_fourbit_append", "hdp_cache_read": "hdp_fourbit_read",
+              "hdp_cache_attention": "hdp_fourbit_attention"}
+
+    def __init__(self, k, v, scales):
         import torch
 
-        f = (_cache_calls or _cache_lib())[name]
-        if torch._C._cuda_getDevice() != self._dev:
-            with torch.cuda.device(self._dev):
-                status = f(*args, self._raw(stream))
-        else:
-            status = f(*args, self._raw(stream))
-        if status:
-            _check(status, name)
+        if k.dim() != 4:
+            raise ValueError("k must be [pages][hkv][64][d/2]")
+        pages, hkv, _, d = k.shape
+        d *= 2
+        dev = k.get_device()
+        _tensor(k, "k", torch.uint8, (pages, hkv, HDP_CACHE_BLOCK, d // 2), dev)
+        _tensor(v, "v", torch.uint8, (pages, hkv, d // 16, 512), dev)
+        _tensor(scales, "scales", torch.uint8, (pages, hkv, d // 32 + 1, HDP_CACHE_BLOCK), dev)
+        self.k, self.v, self.scales = k, v, scales
+        self.num_pages, self.hkv, self.d, self._dev, self.device = pages, hkv, d, dev, k.device
+        self._attention_bytes = _attention_bytes.get((dev, d, 4))
 
-    def _raw(self, stream):
-        if stream is None:
-            import torch
+    @classmethod
+    def empty(cls, num_pages: int, hkv: int, d: int, device="cuda"):
+        """A pool of unwritten pages."""
+        import torch
 
-            return torch._C._cuda_getCurrentRawStream(self._dev)
-        return stream if isinstance(stream, int) else stream.cuda_stream
+        make = lambda *shape: torch.empty((num_pages, hkv) + shape, dtype=torch.uint8, device=torch.device(device))
+        return cls(make(HDP_CACHE_BLOCK, d // 2), make(d // 16, 512), make(d // 32 + 1, HDP_CACHE_BLOCK))
+
+    def _with(self, page_table, lens, cu, rows):
+        """hdp_fourbit_cache_t of a call over these sequences, as bytes."""
+        n, columns = self._sequences(page_table, lens, cu, rows)
+        return _CACHE4_FORMAT.pack(self.k.data_ptr(), self.v.data_ptr(), self.scales.data_ptr(), self.num_pages, self.hkv,
+                                   self.d, n, page_table.data_ptr(), lens.data_ptr(), columns)
+
+    def _buffers(self):
+        return self.k, self.v, self.scales
+
+    def _blocks_of(self, blocks, rows):
+        if blocks is not None:
+            raise TypeError("a KVCache4 has no lists of blocks")
+        return 0, None
+
+    def _call(self, name, stream, *args):
+        if name not in self._names:
+            raise TypeError(f"{name} is not for a KVCache4")
+        if name == "hdp_cache_attention":  # without the list and its count
+            args = args[:6] + args[8:]
+        _run(self._dev, self._names[name], stream, *args)
+
+
+def _run(dev, name, stream, *args):
+    """Runs an entry point with device `dev` current, on `stream` or that device's current one."""
+    import torch
+
+    f = (_cache_calls or _cache_lib())[name]
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            status = f(*args, _raw(dev, stream))
+    else:
+        status = f(*args, _raw(dev, stream))
+    if status:
+        _check(status, name)
+
+
+def _raw(dev, stream):
+    if stream is None:
+        import torch
+
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _tensor(t, name, dtype, shape, device):
@@ -521,6 +626,162 @@ def hdp_cache_select(cache: KVCache, page_table, lens, q, keep_first: int, keep_
     cache._call("hdp_cache_select", stream, cache._with(page_table, lens, cu, rows),
                 None if cu is None else cu.data_ptr(), rows, q.data_ptr(), hq, count, keep_first, keep_last,
                 workspace.data_ptr(), workspace.numel(), list_ptr)
+
+
+# ---------------------------------------------------------------- 4-bit key/value cache
+
+def hdp_fourbit_append(cache: KVCache4, page_table, lens, k, v, cu=None, stream=None):
+    """Writes the rows k, v [rows][hkv][d] bf16, the newest tokens of each sequence, into the cache."""
+    hdp_cache_append(cache, page_table, lens, k, v, cu=cu, stream=stream)
+
+
+def hdp_fourbit_read(cache: KVCache4, page_table, lens, k, v, cu=None, stream=None):
+    """Reads the newest tokens of each sequence into k, v [rows][hkv][d] bf16."""
+    hdp_cache_read(cache, page_table, lens, k, v, cu=cu, stream=stream)
+
+
+def hdp_fourbit_attention_workspace_bytes(cache: KVCache4, hq: int) -> int:
+    import torch
+
+    n = ctypes.c_size_t()
+    s = Cache4Struct(hkv=cache.hkv, d=cache.d)
+    with torch.cuda.device(cache._dev):
+        _check(load().hdp_fourbit_attention_workspace_bytes(s, hq, ctypes.byref(n)),
+               "hdp_fourbit_attention_workspace_bytes")
+    _attention_bytes[cache._dev, cache.d, 4] = n.value
+    return n.value
+
+
+def hdp_fourbit_attention(cache: KVCache4, page_table, lens, q, scale: float, workspace, o, lse, cu=None, stream=None):
+    """Attention of the rows q [rows][hq][d] bf16 over the cache into o (like q) and lse [hq][rows] float32."""
+    hdp_cache_attention(cache, page_table, lens, q, scale, workspace, o, lse, cu=cu, stream=stream)
+
+
+# ---------------------------------------------------------------- block tables and slot maps
+
+class PagePool:
+    """The free pages of a pool: a stack, free int32 [num_pages] with the first count[0] of them free, the last on top.
+    Contiguous CUDA tensors of one device."""
+
+    def __init__(self, free, count):
+        import torch
+
+        self._dev = free.get_device()
+        _tensor(free, "free", torch.int32, (free.numel(),), self._dev)
+        _tensor(count, "count", torch.int32, (1,), self._dev)
+        if free.numel() < 1:
+            raise ValueError("a pool has one page at least")
+        self.free, self.count, self.num_pages, self.device = free, count, free.numel(), free.device
+
+    @classmethod
+    def full(cls, num_pages: int, device="cuda"):
+        """All pages free, page 0 on top."""
+        import torch
+
+        dev = torch.device(device)
+        return cls(torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=dev),
+                   torch.tensor([num_pages], dtype=torch.int32, device=dev))
+
+
+def hdp_cache_assign(pool: PagePool, page_table, held, lens, stream=None):
+    """Brings the pages that the sequences hold (held int32 [sequences]) in line with their lengths, in place."""
+    import torch
+
+    n = lens.shape[0] if lens.dim() == 1 else -1
+    columns = page_table.shape[1] if page_table.dim() == 2 else -1
+    _tensor(lens, "lens", torch.int32, (n,), pool._dev)
+    _tensor(held, "held", torch.int32, (n,), pool._dev)
+    _tensor(page_table, "page_table", torch.int32, (n, columns), pool._dev)
+    _run(pool._dev, "hdp_cache_assign", stream, pool.free.data_ptr(), pool.count.data_ptr(), pool.num_pages,
+         page_table.data_ptr(), held.data_ptr(), lens.data_ptr(), n, columns)
+
+
+def hdp_cache_rows(lens, rows: int, sequence, position, slot, cu=None, page_table=None, num_pages=None, stream=None):
+    """Where the rows of a call lie, into sequence, position int32 [rows] and slot int64 [rows] (each may be None)."""
+    import torch
+
+    dev = lens.get_device()
+    n = lens.shape[0] if lens.dim() == 1 else -1
+    _tensor(lens, "lens", torch.int32, (n,), dev)
+    if cu is not None:
+        _tensor(cu, "cu", torch.int32, (n + 1,), dev)
+    elif rows != n:
+        raise ValueError(f"without cu there is one row for each of the {n} sequences, not {rows}")
+    columns = 0
+    if page_table is not None:
+        columns = page_table.shape[1] if page_table.dim() == 2 else -1
+        _tensor(page_table, "page_table", torch.int32, (n, columns), dev)
+        if num_pages is None:
+            raise ValueError("num_pages, the pages of the pool, goes with a page table")
+    for t, name, dtype in ((sequence, "sequence", torch.int32), (position, "position", torch.int32), (slot, "slot", torch.int64)):
+        if t is not None:
+            _tensor(t, name, dtype, (rows,), dev)
+    _run(dev, "hdp_cache_rows", stream, None if page_table is None else page_table.data_ptr(), lens.data_ptr(),
+         None if cu is None else cu.data_ptr(), n, columns, num_pages or 0, rows,
+         None if sequence is None else sequence.data_ptr(), None if position is None else position.data_ptr(),
+         None if slot is None else slot.data_ptr())
+
+
+# ---------------------------------------------------------------- rotary positions
+
+_rotary_types = None
+
+
+def _rotary_type(dtype):
+    global _rotary_types
+    if _rotary_types is None:
+        import torch
+
+        _rotary_types = {torch.bfloat16: HDP_TYPE_BF16, torch.float16: HDP_TYPE_FP16, torch.float32: HDP_TYPE_FP32}
+    return _rotary_types.get(dtype)
+
+
+def _apart(x):
+    """Do the rows and heads of x [rows][heads][d] not overlap?"""
+    end = x.shape[2]
+    for stride, size in sorted(zip(x.stride()[:2], x.shape[:2])):
+        if size > 1:
+            if stride < end:
+                return False
+            end += stride * (size - 1)
+    return True
+
+
+def _rotary_side(x, out, name, like):
+    """hdp_rotary_rows_t of x [rows][heads][d] turned into out, as bytes."""
+    if x.dim() != 3 or x.dtype is not like.dtype or x.get_device() != like.get_device() or not x.is_cuda:
+        raise TypeError(f"{name} must be a {like.dtype} tensor [rows][heads][d] on a CUDA device")
+    if x.shape[0] != like.shape[0] or x.shape[2] != like.shape[2]:
+        raise ValueError(f"{name} must have the rows and channels of the others")
+    if out.dtype is not x.dtype or out.shape != x.shape or out.get_device() != x.get_device():
+        raise ValueError(f"the output of {name} must be a tensor like it")
+    a, b = x.stride(), out.stride()
+    if x.shape[2] > 1 and (a[2] != 1 or b[2] != 1):
+        raise ValueError(f"the channels of {name} must be contiguous")
+    return _ROTARY_FORMAT.pack(x.data_ptr(), out.data_ptr(), a[0], a[1], b[0], b[1], x.shape[1])
+
+
+def hdp_rotary(q, k, position, freqs, q_out, k_out, neighbours: bool = False, backward: bool = False, factor: float = 1.0,
+               stream=None):
+    """Turns the rows of q and k (one may be None) [rows][heads][d] into q_out and k_out, which may be q and k."""
+    import torch
+
+    like = q if q is not None else k
+    if like is None or like.dim() != 3 or not like.is_cuda:
+        raise TypeError("q and k must be CUDA tensors [rows][heads][d], and one of them be given")
+    kind = _rotary_type(like.dtype)
+    if kind is None:
+        raise TypeError("q and k must be bfloat16, float16 or float32")
+    dev, rows = like.get_device(), like.shape[0]
+    _tensor(position, "position", torch.int32, (rows,), dev)
+    _tensor(freqs, "freqs", torch.float64, (freqs.numel(),), dev)
+    for x, out in ((q, q_out), (k, k_out)):
+        if x is not None and not _apart(out):
+            raise ValueError("rows and heads of an output must not overlap")
+    sq = None if q is None else _rotary_side(q, q_out, "q", like)
+    sk = None if k is None else _rotary_side(k, k_out, "k", like)
+    _run(dev, "hdp_rotary", stream, sq, sk, rows, like.shape[2], kind, position.data_ptr(), freqs.data_ptr(),
+         2 * freqs.numel(), (HDP_ROTARY_NEIGHBOURS if neighbours else 0) | (HDP_ROTARY_BACKWARD if backward else 0), factor)
 
 
 # ---------------------------------------------------------------- cost models (host arithmetic)

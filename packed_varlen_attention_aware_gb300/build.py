@@ -17,8 +17,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhdpattn.so")
 SOURCES = ["api.cu", "plan.cu", "attn_fwd.cu", "attn_bwd.cu", "lse_merge.cu", "kv_cache.cu",
-           "kv_attention.cu", "kv_select.cu", "cost_model.cpp", "balance.cpp"]
-HEADERS = ["internal.h", "kv_attention.cuh", "kv_cache.cuh", "sm103_ptx.cuh"]
+           "kv_attention.cu", "kv_select.cu", "kv_cache4.cu", "kv_attention4.cu", "pages.cu", "rotary.cu",
+           "cost_model.cpp", "balance.cpp"]
+HEADERS = ["internal.h", "kv_cache.cuh", "kv_cache4.cuh", "kv_attention.cuh", "sm103_ptx.cuh"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -90,6 +90,7 @@ hdp_status_t hdp_device_status(void* stream) {
     if (code == hdp::kErrCacheTable)
       return hdp::fail(HDP_ERR_INVALID_ARGUMENT,
                        "a cache call met a length outside its page table or a page outside the pool");
+    if (code == hdp::kErrCachePool) return hdp::fail(HDP_ERR_OUT_OF_MEMORY, "hdp_cache_assign ran out of free pages");
     char buf[128];
     std::snprintf(buf, sizeof buf, "a kernel's bounded wait expired (code %u)", code);
     return hdp::fail(HDP_ERR_DEVICE_TIMEOUT, buf);

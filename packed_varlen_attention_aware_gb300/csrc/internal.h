@@ -35,6 +35,8 @@ unsigned int* device_error_word();
 // Code of a cache length or page outside its bounds (the codes of expired
 // waits are 0x1xx and 0x2xx).
 constexpr unsigned int kErrCacheTable = 0x301;
+// Code of a pool of pages that ran out.
+constexpr unsigned int kErrCachePool = 0x302;
 
 // Count one kernel enqueued by this library (reported by hdp_kernel_launch_count).
 void note_launch();
