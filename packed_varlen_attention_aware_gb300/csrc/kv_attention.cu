@@ -50,6 +50,9 @@
 namespace hdp {
 namespace {
 
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kWarpsOf[kMaxNt] = {kWarps, kWarps};
 // Bytes of a warp's ring of half blocks.  More in flight streams a long run
 // better; less leaves the memory's queues shorter, and with them every other
 // access (lists, pages, query rows), which short runs wait for.  Measured at
@@ -93,6 +96,17 @@ template <int FMT>
 __device__ __forceinline__ uint4 without_nan(uint4 x) {
   return make_uint4(without_nan<FMT>(x.x), without_nan<FMT>(x.y), without_nan<FMT>(x.z), without_nan<FMT>(x.w));
 }
+
+template <int NT, bool SPARSE>
+struct Shared {
+  unsigned char ring[kWarps][kRingBytes<NT, SPARSE>];
+  SeqPlace seq[kSeqs];
+  Meta meta[kWarps][kMeta];
+  float4 p[kWarps][NT][4][32];  // P of a block, each lane its own
+  long long pre[kThreads];  // steps before each thread's sequences
+  long long warp_sum[kWarps];
+};
+
 // Raw query rows of a unit, this lane's channels.
 template <int D, int NT>
 __device__ __forceinline__ void fetch_rows(const AttnParams& p, int row0, int head, unsigned rr0, int nrows,
@@ -255,58 +269,335 @@ __device__ __forceinline__ void second_product(Sums<D, NT>& sums, const uint32_t
   }
 }
 
+template <int D, int FMT, int NT, bool SPARSE>
+__global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParams p) {
+  constexpr int kHalf = kBlock * D;               // bytes of a block's K or V codes of one head
+  constexpr int kSlots = kRingBytes<NT, SPARSE> / kHalf;  // half blocks in flight
+  constexpr int kKeyChunks = D / 64;              // 16-byte chunks that a lane has of a key
+  constexpr int kMt = D / 16;
+  constexpr int kRows = 8 * NT;
+  using Cur = Cursor<SPARSE, NT>;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  auto& sm = *reinterpret_cast<Shared<NT, SPARSE>*>(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gr = lane >> 2, tc = lane & 3;  // fragment row group and column pair
+
+  // ---- the flat order: total steps, and where this warp starts
+  long long total;
+  const int per_thread = (p.c.num_seqs + kThreads - 1) / kThreads;
+  const int per_row = SPARSE ? p.c.hkv * Cur::tiles_of(1, p.g) : 0;
+  if constexpr (SPARSE) {
+    total = static_cast<long long>(p.c.rows) * per_row * p.count;
+  } else {
+    long long mine = 0;
+    for (int i = 0; i < per_thread; ++i) {
+      const int s = threadIdx.x * per_thread + i;
+      if (s < p.c.num_seqs) {
+        const SeqPlace at = seq_place(p.c, s);
+        if (s < kSeqs) sm.seq[s] = at;
+        mine += Cur::cost(p, at);
+      }
+    }
+    long long run = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) {
+      const long long up = __shfl_up_sync(0xffffffffu, run, s);
+      if (lane >= s) run += up;
+    }
+    if (lane == 31) sm.warp_sum[warp] = run;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sm.warp_sum[w];
+      total += sm.warp_sum[w];
+    }
+    sm.pre[threadIdx.x] = before + run - mine;
+  }
+  __syncthreads();
+  const Cut cut(total, gridDim.x, kWarps, p.dynamic);
+  const int used = cut.used(gridDim.x);
+  if (!p.dynamic && blockIdx.x == 0 && threadIdx.x == 0) p.head[2] = cut.workers;
+  if (warp >= used) return;
+  const int run = blockIdx.x * used + warp;
+  if (!p.dynamic && lane == 0) p.open[run].parts = 0;
+
+  // Puts a cursor on a step of the flat order.
+  auto locate = [&](Cur& cur, long long x) {
+    if constexpr (SPARSE) {
+      const long long row_cost = static_cast<long long>(per_row) * p.count;
+      const int row = static_cast<int>(x / row_cost);
+      const long long off = x - row * row_cost;
+      const int head = static_cast<int>(off / (static_cast<long long>(p.count) * (per_row / p.c.hkv)));
+      const int at = min(static_cast<int>(off % p.count) + lane, p.count - 1);  // of the list that comes next
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(p.blocks + (static_cast<long long>(row) * p.c.hkv + head) * p.count + at));
+      cur.enter(p, sm.seq, row);
+      cur.skip(off);
+    } else {
+      const int slice = find_last(kThreads, x, [&](int s) { return sm.pre[s]; });
+      long long at = sm.pre[slice];
+      int i = slice * per_thread;
+      for (long long c; x - at >= (c = Cur::cost(p, Cur::place(p, sm.seq, i))) && i + 1 < p.c.num_seqs; ++i) at += c;
+      cur.enter(p, sm.seq, i);
+      cur.skip(x - at);
+    }
+  };
+
+  long long start, stop;
+  cut.range(run, 0, start, stop);
+  if (start < total) {
+    Cur cc, lc;  // of the arithmetic; of the copies, which run ahead
+    locate(lc, start);
+    cc = lc;
+    int piece = run * cut.pieces;  // of the copies
+    long long to_load = stop - start;
+    int loaded = 0, done = 0;      // blocks
+    int ticket = 0;                // lane 0: the next piece to take
+    bool asked = false, more_pieces = p.dynamic;
+    auto ask = [&]() {
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
+      if (lane == 0) ticket = atomicAdd(p.head + 1, 1);
+      asked = true;
+    };
+    int half = 0;                 // 0: K of lc's block next, 1: V
+    int load_slot = 0, load_meta = 0;
+    int ids = -1, ids_at = -1;    // 32 blocks' pages (dense) or blocks and pages (sparse) of lc's unit, one a lane
+    int ids_page = -1;
+    int next_page = 0, next_of = -1;  // dense: a page of sequence next_of's first blocks, asked for early
+    const unsigned char* cur_v = nullptr;  // V of the block whose K went last
+    const uint32_t ring = smem_addr(sm.ring[warp]) + lane * 16;
+
+    auto issue = [&]() {
+      while (to_load == 0 && more_pieces) {
+        if (!asked) ask();
+        asked = false;
+        const int j = __shfl_sync(0xffffffffu, ticket, 0);
+        const int k = 1 + j / cut.workers, w = j - (k - 1) * cut.workers;
+        more_pieces = k < cut.pieces;
+        if (!more_pieces) break;
+        long long a, z;
+        cut.range(w, k, a, z);
+        if (a >= z) continue;
+        locate(lc, a);
+        to_load = z - a;
+        piece = w * cut.pieces + k;
+        ids_at = -1;
+      }
+      if (to_load > 0) {
+        if (half == 0) {
+          ++loaded;
+          if (ids_at != (lc.blk & ~31)) {  // a new list, or the next 32 blocks
+            const int last = lc.last_pos(p.g);
+            ids_at = lc.blk & ~31;
+            const int b = ids_at + lane;
+            ids = ids_page = -1;
+            if constexpr (SPARSE) {
+              if (b < lc.nb && lc.seq >= 0) {
+                const int32_t* list = p.blocks + (static_cast<long long>(lc.s.row0) * p.c.hkv + lc.head) * p.count;
+                const int x = __ldg(list + b), before = b ? __ldg(list + b - 1) : -1;
+                if (x > before && x >= 0 && x <= last / kBlock && last >= 0) {
+                  ids = x;
+                  ids_page = page_of(p.c, lc.seq, x);
+                }
+              }
+            } else {
+              const bool early = next_of == lc.seq && ids_at == 0;
+              if (b < lc.nb && b <= last / kBlock && last >= 0) {
+                ids = b;
+                ids_page = early ? next_page : __ldg(p.c.table + static_cast<long long>(lc.seq) * p.c.max_pages + b);
+                if (ids_page < 0 || ids_page >= p.c.num_pages) {
+                  report_table(p.c);
+                  ids_page = -1;
+                }
+              }
+              next_of = -1;
+            }
+          }
+          if (!SPARSE && next_of < 0 && lc.last_unit(p)) {
+            next_of = lc.next_seq(p, sm.seq);
+            if (next_of < p.c.num_seqs && lane < p.c.max_pages)
+              next_page = __ldg(p.c.table + static_cast<long long>(next_of) * p.c.max_pages + lane);
+          }
+          const int b = __shfl_sync(0xffffffffu, ids, lc.blk & 31);
+          const int page = __shfl_sync(0xffffffffu, ids_page, lc.blk & 31);
+          const bool seen = b >= 0 && page >= 0;
+          Meta* meta = &sm.meta[warp][load_meta];
+          if (lane == 0) meta->piece = piece;
+          if (seen) {
+            const size_t ph = static_cast<size_t>(page) * p.c.hkv + lc.head;
+            if (lane == 0) {
+              copy8(smem_addr(meta), p.c.scales + 2 * ph);
+              meta->key0 = b * kBlock;
+            }
+            const unsigned char* kb = p.c.k + ph * kHalf + gr * D + tc * 16;
+            const uint32_t dst = ring + load_slot * kHalf;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int j = 0; j < kKeyChunks; ++j) copy16(dst + (i * kKeyChunks + j) * 512, kb + i * 8 * D + j * 64);
+            cur_v = p.c.v + ph * kHalf + lane * 16;
+          } else {
+            if (lane == 0) meta->key0 = -1;
+            cur_v = nullptr;
+          }
+        } else {
+          if (cur_v) {
+            const uint32_t dst = ring + load_slot * kHalf;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) copy16(dst + i * 512, cur_v + i * 512);
+          }
+          load_meta = (load_meta + 1) % kMeta;
+          --to_load;
+          if (to_load == 1 && more_pieces) ask();  // not earlier: a slow warp must not sit on a piece
+          if (++lc.blk == lc.nb && to_load > 0) {
+            // heads of a sequence share its pages: a list of up to 32 serves them all (its
+            // visible blocks are those of the sequence's last rows)
+            const bool same = !SPARSE && lc.nb <= 32 && lc.tiles == 1 && !lc.last_unit(p);
+            lc.next_unit(p, sm.seq);
+            if (!same) ids_at = -1;
+          }
+        }
+        half ^= 1;
+        load_slot = load_slot + 1 == kSlots ? 0 : load_slot + 1;
+      }
+      copies_commit();
+    };
+
+    int ahead = kSlots;  // half steps that the copies go in front at first
+
+    int slot = 0, meta_at = 0, at_piece = run * cut.pieces;  // (the copies may be in a later piece already)
+    long long at = start;
+    uint4 qx[NT][kMt / 2];  // raw query rows of cc's unit, this lane's channels
+    auto fetch_q = [&]() {  // a row of no sequence is not read
+      fetch_rows<D, NT>(p, cc.s.row0, cc.head, cc.rr0(), !SPARSE || cc.seq >= 0 ? cc.nrows(p.g) : 0, qx);
+    };
+    fetch_q();
+    while (true) {
+      // ---- one unit, or the part of it that the piece has
+      const bool begins = cc.blk == 0;
+      const int steps = static_cast<int>(min(static_cast<long long>(cc.nb - cc.blk), stop - at));
+      const bool ends = cc.blk + steps == cc.nb;
+      const int nrows = cc.nrows(p.g), rr0 = cc.rr0(), row0 = cc.s.row0, head = cc.head;
+      const bool live = !SPARSE || cc.seq >= 0;
+
+      const int low_pos = cc.first_pos(p.g);
+      const Rows<D, NT> rows(p, qx, cc.s.p0, rr0, nrows);
+      Sums<D, NT> sums;
+      sums.clear();
+
+      // Half a step is a block's scores or its output; then the next half block is asked
+      // for.  That is a page of code with a place of its own, once in the kernel: the
+      // loop is bound by the fetch of its instructions as much as by what they do.  Twice
+      // in the loop and once in front of it, unrolled, 64 sequences took 149.4 us against
+      // 146.5, 16 drafts 66.3 against 61.8, four short documents 11.3 against 9.9.
+      const Probabilities<NT> prob = {sm.p[warp]};
+      float f[NT][2];
+      bool seen = false, masked = false;
+#pragma unroll 1
+      for (int half_step = -ahead; half_step < 2 * steps; ++half_step) {
+        if (half_step >= 0) {
+          copies_wait<kSlots - 1>();
+          if (half_step % 2 == 0) {
+            __syncwarp();
+            const Meta meta = sm.meta[warp][meta_at];
+            meta_at = (meta_at + 1) % kMeta;
+            seen = meta.key0 >= 0;
+            masked = meta.key0 + kBlock - 1 > low_pos;  // some row does not see the whole block
+            if (seen) {
+              const uint4* kx = reinterpret_cast<const uint4*>(sm.ring[warp] + slot * kHalf) + lane;
+              float s[NT][4][4];
+              first_product<D, FMT, NT>(rows, s, [&](int i, int j) { return kx[(i * kKeyChunks + j) * 32]; });
+              softmax<D, NT>(rows, sums, meta.sk, meta.sv, meta.key0, masked, s, f);
+              prob.put(s);
+            }
+          } else if (seen) {
+            const uint4* vx = reinterpret_cast<const uint4*>(sm.ring[warp] + slot * kHalf) + lane;
+            bool sure = false;  // that further passes are needed
+            while (true) {
+              uint32_t pf[NT][4][2];
+              float least[NT][2];
+              prob.get(pf);
+              second_product<D, FMT, NT>(sums, pf, f, masked, least, [&](int i) { return vx[i * 32]; });
+              // Is an output so small that what fp16 leaves of P could count?
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                  sure |= t * 8 + 2 * tc + k < nrows && f[t][k] != 0.f && !(least[t][k] >= kEnough<FMT>);
+              if (!__any_sync(0xffffffffu, sure) || !__any_sync(0xffffffffu, prob.more())) break;
+              sure = true;
+              prob.next();  // four times at most
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                f[t][0] *= 1.f / kNextPass;
+                f[t][1] *= 1.f / kNextPass;
+              }
+            }
+          }
+          slot = slot + 1 == kSlots ? 0 : slot + 1;
+        }
+        issue();
+      }
+      ahead = 0;
+      at += steps;
+      done += steps;
+      const int rest = cc.nb - cc.blk - steps;  // steps of the unit behind the piece
+      const int this_piece = at_piece;
+      const long long this_at = at;
+
+      // ---- the next unit's query rows are asked for before this one is written
+      bool more = true;
+      if (at < stop) {
+        cc.next_unit(p, sm.seq);
+      } else {
+        __syncwarp();
+        more = done != loaded;
+        if (more) {  // the piece that the copies went on to
+          at_piece = sm.meta[warp][meta_at].piece;
+          const int w = at_piece / cut.pieces;
+          cut.range(w, at_piece - w * cut.pieces, at, stop);
+          locate(cc, at);
+        }
+      }
+      if (more) fetch_q();
+
+      // ---- the unit's part is done: out, or into a partial
+      const bool whole = begins && ends;
+      const size_t part_at = (static_cast<size_t>(this_piece) * 2 + (begins ? 1 : 0)) * kRows;
+      if (live) write_part<D, NT>(p, sums, head, row0, rr0, nrows, whole, part_at);
+      if (begins && !ends && live && lane == 0) {
+        Open o = {};
+        o.first = this_piece;
+        o.parts = cut.piece_of(this_at + rest - 1) - this_piece + 1;
+        o.row0 = row0;
+        o.head = head;
+        o.nrows = nrows;
+        o.rr0 = rr0;
+        p.open[p.dynamic ? atomicAdd(p.head, 1) : this_piece] = o;
+      }
+      if (!more) break;
+    }
+    copies_wait<0>();
+  }
+  // Even a call without work ends after the kernels in front of it: what comes
+  // next in the stream (another thread's kernel, perhaps) waits for this one only.
+  if (p.dynamic) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <int D, int FMT, int NT, bool SPARSE>
+hdp_status_t launch8(const AttnParams& p, int device, int ctas, cudaStream_t st) {
+  static std::atomic<bool> ready[kDevices];
+  constexpr int smem = sizeof(Shared<NT, SPARSE>);
+  static_assert(smem <= 232448, "shared memory of a CTA");
+  return launch<D, NT>(k_cache_attention<D, FMT, NT, SPARSE>, kWarps, smem, ready, p, device, ctas, st);
+}
+
 template <int D, int FMT>
-struct Codes8 {
-  static constexpr int kD = D;
-  static constexpr int kSlot = kBlock * D;       // bytes of a block's K or V codes of one head
-  static constexpr int kKeyChunks = D / 64;      // 16-byte chunks that a lane has of a key
-  template <int NT, bool SPARSE>
-  static constexpr int kSlots = kRingBytes<NT, SPARSE> / kSlot;
-  static constexpr float kEnough = hdp::kEnough<FMT>;
-
-  template <int NT>
-  __device__ __forceinline__ static void fetch_rows(const AttnParams& p, int row0, int head, unsigned rr0, int nrows,
-                                                    uint4 (&qx)[NT][D / 32]) {
-    hdp::fetch_rows<D, NT>(p, row0, head, rr0, nrows, qx);
-  }
-  __device__ __forceinline__ static void copy_k(const AttnParams& p, size_t ph, uint32_t dst, Meta* meta) {
-    const int lane = threadIdx.x & 31, gr = lane >> 2, tc = lane & 3;
-    if (lane == 0) copy8(smem_addr(meta), p.c.scales + 2 * ph);
-    const unsigned char* kb = p.c.k + ph * kSlot + gr * D + tc * 16;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < kKeyChunks; ++j) copy16(dst + (i * kKeyChunks + j) * 512, kb + i * 8 * D + j * 64);
-  }
-  __device__ __forceinline__ static const unsigned char* v_of(const AttnParams& p, size_t ph) {
-    return p.c.v + ph * kSlot + (threadIdx.x & 31) * 16;
-  }
-  __device__ __forceinline__ static void copy_v(const unsigned char* v, uint32_t dst) {
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) copy16(dst + i * 512, v + i * 512);
-  }
-  template <int NT>
-  __device__ __forceinline__ static void scores(const Rows<D, NT>& rows, Sums<D, NT>& sums, const unsigned char* slot,
-                                                const Meta& meta, bool masked, const Probabilities<NT>& prob,
-                                                float (&f)[NT][2]) {
-    const uint4* kx = reinterpret_cast<const uint4*>(slot) + (threadIdx.x & 31);
-    float s[NT][4][4];
-    first_product<D, FMT, NT>(rows, s, [&](int i, int j) { return kx[(i * kKeyChunks + j) * 32]; });
-    softmax<D, NT>(rows, sums, meta.sk, meta.sv, meta.key0, masked, s, f);
-    prob.put(s);
-  }
-  template <int NT>
-  __device__ __forceinline__ static void output(Sums<D, NT>& sums, const uint32_t (&pf)[NT][4][2], const float (&f)[NT][2],
-                                                const unsigned char* slot, bool masked, float (&least)[NT][2]) {
-    const uint4* vx = reinterpret_cast<const uint4*>(slot) + (threadIdx.x & 31);
-    second_product<D, FMT, NT>(sums, pf, f, masked, least, [&](int i) { return vx[i * 32]; });
-  }
-};
-
-template <class F>
 hdp_status_t launch_for(const AttnParams& p, int nt, int device, int ctas, cudaStream_t st) {
-  if (p.blocks) return nt == 1 ? launch<F, 1, true>(p, device, ctas, st) : launch<F, 2, true>(p, device, ctas, st);
-  return nt == 1 ? launch<F, 1, false>(p, device, ctas, st) : launch<F, 2, false>(p, device, ctas, st);
+  if (p.blocks) return nt == 1 ? launch8<D, FMT, 1, true>(p, device, ctas, st) : launch8<D, FMT, 2, true>(p, device, ctas, st);
+  return nt == 1 ? launch8<D, FMT, 1, false>(p, device, ctas, st) : launch8<D, FMT, 2, false>(p, device, ctas, st);
 }
 
 }  // namespace
@@ -316,7 +607,7 @@ using namespace hdp;
 
 extern "C" hdp_status_t hdp_cache_attention_workspace_bytes(const hdp_cache_t* cache, int32_t hq, size_t* bytes) {
   if (!cache || !bytes) return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_attention_workspace_bytes: NULL argument");
-  return workspace_bytes_of("hdp_cache_attention_workspace_bytes", cache->hkv, cache->d, hq, bytes);
+  return workspace_bytes_of("hdp_cache_attention_workspace_bytes", kWarpsOf, cache->hkv, cache->d, hq, bytes);
 }
 
 extern "C" hdp_status_t hdp_cache_attention(const hdp_cache_t* cache, const int32_t* cu, int64_t rows, const void* q,
@@ -327,12 +618,12 @@ extern "C" hdp_status_t hdp_cache_attention(const hdp_cache_t* cache, const int3
   const hdp_status_t r = cache_view("hdp_cache_attention", cache, cu, rows, &p.c);
   if (r != HDP_OK) return r;
   const bool i8 = cache->format == HDP_CACHE_INT8, wide = cache->d == 128;
-  return attend("hdp_cache_attention", p, cache->d, rows, q, hq, scale, blocks, count, workspace, workspace_bytes, o, lse,
+  return attend("hdp_cache_attention", kWarpsOf, p, cache->d, rows, q, hq, scale, blocks, count, workspace, workspace_bytes, o, lse,
                 stream, [=](const AttnParams& a, int nt, int device, int ctas, cudaStream_t st) {
                   if (wide)
-                    return i8 ? launch_for<Codes8<128, HDP_CACHE_INT8>>(a, nt, device, ctas, st)
-                              : launch_for<Codes8<128, HDP_CACHE_E4M3>>(a, nt, device, ctas, st);
-                  return i8 ? launch_for<Codes8<64, HDP_CACHE_INT8>>(a, nt, device, ctas, st)
-                            : launch_for<Codes8<64, HDP_CACHE_E4M3>>(a, nt, device, ctas, st);
+                    return i8 ? launch_for<128, HDP_CACHE_INT8>(a, nt, device, ctas, st)
+                              : launch_for<128, HDP_CACHE_E4M3>(a, nt, device, ctas, st);
+                  return i8 ? launch_for<64, HDP_CACHE_INT8>(a, nt, device, ctas, st)
+                            : launch_for<64, HDP_CACHE_E4M3>(a, nt, device, ctas, st);
                 });
 }

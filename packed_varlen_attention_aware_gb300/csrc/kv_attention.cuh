@@ -1,17 +1,10 @@
 // Attention of the newest tokens of each sequence over a paged cache: what the
-// formats share.  How the work is cut, how the copies run ahead, the softmax's
-// references and the joining are explained in kv_attention.cu.
-//
-// A format F says what a block of 64 keys is and does its arithmetic:
-//   F::kD, F::kSlot             channels of a head, bytes of a half block in the ring
-//   F::kSlots<NT, SPARSE>       half blocks in the ring of a warp
-//   F::copy_k, F::copy_v        ask for a half block
-//   F::scores                   scores of a block to P, sums brought to new references
-//   F::output                   adds V^T P^T; how small its smallest number is
-//   F::kEnough                  an output above it can forget what fp16 left of P
+// kernels for 8 and for 4 bits share.  How the work is cut, the softmax's references
+// and the joining are explained in kv_attention.cu.
 #pragma once
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <atomic>
 #include <string>
 
@@ -20,8 +13,6 @@
 namespace hdp {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kMeta = 8;           // blocks whose scales and first key are kept
 constexpr float kLow = -3.402823466e38f;  // reference exponent before the first key: below every finite score
 constexpr float kLn2 = 0.6931471805599453f;
@@ -130,16 +121,6 @@ __device__ __forceinline__ SeqPlace seq_place(const CacheView& c, int i) {
 }
 
 __device__ __forceinline__ uint32_t word(const uint4& x, int k) { return k == 0 ? x.x : k == 1 ? x.y : k == 2 ? x.z : x.w; }
-
-template <class F, int NT, bool SPARSE>
-struct Shared {
-  unsigned char ring[kWarps][F::template kSlots<NT, SPARSE> * F::kSlot];
-  SeqPlace seq[kSeqs];
-  Meta meta[kWarps][kMeta];
-  float4 p[kWarps][NT][4][32];  // P of a block, each lane its own
-  long long pre[kThreads];  // steps before each thread's sequences
-  long long warp_sum[kWarps];
-};
 
 // A place in the flat order.  A unit is (sequence or row, kv head, tile of
 // query rows); a step is one block of it.
@@ -298,9 +279,9 @@ constexpr int kLeast = 4;
 struct Cut {
   long long total, per, tail;
   int workers, pieces;  // warps with a run, pieces of a run
-  __device__ __forceinline__ Cut(long long steps, int ctas, bool dynamic) : total(steps) {
+  __device__ __forceinline__ Cut(long long steps, int ctas, int warps, bool dynamic) : total(steps) {
     const long long each = (total + ctas - 1) / ctas;
-    const int used = static_cast<int>(min(static_cast<long long>(kWarps), max(1LL, each)));
+    const int used = static_cast<int>(min(static_cast<long long>(warps), max(1LL, each)));
     workers = ctas * used;
     per = max(1LL, (total + workers - 1) / workers);
     tail = dynamic && per >= 5 * kLeast ? per / 5 : 0;
@@ -511,305 +492,6 @@ __device__ __forceinline__ void write_part(const AttnParams& p, const Sums<D, NT
   }
 }
 
-template <class F, int NT, bool SPARSE>
-__global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParams p) {
-  constexpr int D = F::kD;
-  constexpr int kSlots = F::template kSlots<NT, SPARSE>;  // half blocks in flight
-  constexpr int kMt = D / 16;
-  constexpr int kRows = 8 * NT;
-  using Cur = Cursor<SPARSE, NT>;
-  extern __shared__ __align__(128) unsigned char smem_raw[];
-  auto& sm = *reinterpret_cast<Shared<F, NT, SPARSE>*>(smem_raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tc = lane & 3;  // fragment column pair
-
-  // ---- the flat order: total steps, and where this warp starts
-  long long total;
-  const int per_thread = (p.c.num_seqs + kThreads - 1) / kThreads;
-  const int per_row = SPARSE ? p.c.hkv * Cur::tiles_of(1, p.g) : 0;
-  if constexpr (SPARSE) {
-    total = static_cast<long long>(p.c.rows) * per_row * p.count;
-  } else {
-    long long mine = 0;
-    for (int i = 0; i < per_thread; ++i) {
-      const int s = threadIdx.x * per_thread + i;
-      if (s < p.c.num_seqs) {
-        const SeqPlace at = seq_place(p.c, s);
-        if (s < kSeqs) sm.seq[s] = at;
-        mine += Cur::cost(p, at);
-      }
-    }
-    long long run = mine;
-#pragma unroll
-    for (int s = 1; s < 32; s *= 2) {
-      const long long up = __shfl_up_sync(0xffffffffu, run, s);
-      if (lane >= s) run += up;
-    }
-    if (lane == 31) sm.warp_sum[warp] = run;
-    __syncthreads();
-    long long before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += sm.warp_sum[w];
-      total += sm.warp_sum[w];
-    }
-    sm.pre[threadIdx.x] = before + run - mine;
-  }
-  __syncthreads();
-  const Cut cut(total, gridDim.x, p.dynamic);
-  const int used = cut.used(gridDim.x);
-  if (!p.dynamic && blockIdx.x == 0 && threadIdx.x == 0) p.head[2] = cut.workers;
-  if (warp >= used) return;
-  const int run = blockIdx.x * used + warp;
-  if (!p.dynamic && lane == 0) p.open[run].parts = 0;
-
-  // Puts a cursor on a step of the flat order.
-  auto locate = [&](Cur& cur, long long x) {
-    if constexpr (SPARSE) {
-      const long long row_cost = static_cast<long long>(per_row) * p.count;
-      const int row = static_cast<int>(x / row_cost);
-      const long long off = x - row * row_cost;
-      const int head = static_cast<int>(off / (static_cast<long long>(p.count) * (per_row / p.c.hkv)));
-      const int at = min(static_cast<int>(off % p.count) + lane, p.count - 1);  // of the list that comes next
-      asm volatile("prefetch.global.L1 [%0];" ::"l"(p.blocks + (static_cast<long long>(row) * p.c.hkv + head) * p.count + at));
-      cur.enter(p, sm.seq, row);
-      cur.skip(off);
-    } else {
-      const int slice = find_last(kThreads, x, [&](int s) { return sm.pre[s]; });
-      long long at = sm.pre[slice];
-      int i = slice * per_thread;
-      for (long long c; x - at >= (c = Cur::cost(p, Cur::place(p, sm.seq, i))) && i + 1 < p.c.num_seqs; ++i) at += c;
-      cur.enter(p, sm.seq, i);
-      cur.skip(x - at);
-    }
-  };
-
-  long long start, stop;
-  cut.range(run, 0, start, stop);
-  if (start < total) {
-    Cur cc, lc;  // of the arithmetic; of the copies, which run ahead
-    locate(lc, start);
-    cc = lc;
-    int piece = run * cut.pieces;  // of the copies
-    long long to_load = stop - start;
-    int loaded = 0, done = 0;      // blocks
-    int ticket = 0;                // lane 0: the next piece to take
-    bool asked = false, more_pieces = p.dynamic;
-    auto ask = [&]() {
-      asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
-      if (lane == 0) ticket = atomicAdd(p.head + 1, 1);
-      asked = true;
-    };
-    int half = 0;                 // 0: K of lc's block next, 1: V
-    int load_slot = 0, load_meta = 0;
-    int ids = -1, ids_at = -1;    // 32 blocks' pages (dense) or blocks and pages (sparse) of lc's unit, one a lane
-    int ids_page = -1;
-    int next_page = 0, next_of = -1;  // dense: a page of sequence next_of's first blocks, asked for early
-    const unsigned char* cur_v = nullptr;  // V of the block whose K went last
-    const uint32_t ring = smem_addr(sm.ring[warp]) + lane * 16;
-
-    auto issue = [&]() {
-      while (to_load == 0 && more_pieces) {
-        if (!asked) ask();
-        asked = false;
-        const int j = __shfl_sync(0xffffffffu, ticket, 0);
-        const int k = 1 + j / cut.workers, w = j - (k - 1) * cut.workers;
-        more_pieces = k < cut.pieces;
-        if (!more_pieces) break;
-        long long a, z;
-        cut.range(w, k, a, z);
-        if (a >= z) continue;
-        locate(lc, a);
-        to_load = z - a;
-        piece = w * cut.pieces + k;
-        ids_at = -1;
-      }
-      if (to_load > 0) {
-        if (half == 0) {
-          ++loaded;
-          if (ids_at != (lc.blk & ~31)) {  // a new list, or the next 32 blocks
-            const int last = lc.last_pos(p.g);
-            ids_at = lc.blk & ~31;
-            const int b = ids_at + lane;
-            ids = ids_page = -1;
-            if constexpr (SPARSE) {
-              if (b < lc.nb && lc.seq >= 0) {
-                const int32_t* list = p.blocks + (static_cast<long long>(lc.s.row0) * p.c.hkv + lc.head) * p.count;
-                const int x = __ldg(list + b), before = b ? __ldg(list + b - 1) : -1;
-                if (x > before && x >= 0 && x <= last / kBlock && last >= 0) {
-                  ids = x;
-                  ids_page = page_of(p.c, lc.seq, x);
-                }
-              }
-            } else {
-              const bool early = next_of == lc.seq && ids_at == 0;
-              if (b < lc.nb && b <= last / kBlock && last >= 0) {
-                ids = b;
-                ids_page = early ? next_page : __ldg(p.c.table + static_cast<long long>(lc.seq) * p.c.max_pages + b);
-                if (ids_page < 0 || ids_page >= p.c.num_pages) {
-                  report_table(p.c);
-                  ids_page = -1;
-                }
-              }
-              next_of = -1;
-            }
-          }
-          if (!SPARSE && next_of < 0 && lc.last_unit(p)) {
-            next_of = lc.next_seq(p, sm.seq);
-            if (next_of < p.c.num_seqs && lane < p.c.max_pages)
-              next_page = __ldg(p.c.table + static_cast<long long>(next_of) * p.c.max_pages + lane);
-          }
-          const int b = __shfl_sync(0xffffffffu, ids, lc.blk & 31);
-          const int page = __shfl_sync(0xffffffffu, ids_page, lc.blk & 31);
-          const bool seen = b >= 0 && page >= 0;
-          Meta* meta = &sm.meta[warp][load_meta];
-          if (lane == 0) meta->piece = piece;
-          if (seen) {
-            const size_t ph = static_cast<size_t>(page) * p.c.hkv + lc.head;
-            if (lane == 0) meta->key0 = b * kBlock;
-            F::copy_k(p, ph, ring + load_slot * F::kSlot, meta);
-            cur_v = F::v_of(p, ph);
-          } else {
-            if (lane == 0) meta->key0 = -1;
-            cur_v = nullptr;
-          }
-        } else {
-          if (cur_v) F::copy_v(cur_v, ring + load_slot * F::kSlot);
-          load_meta = (load_meta + 1) % kMeta;
-          --to_load;
-          if (to_load == 1 && more_pieces) ask();  // not earlier: a slow warp must not sit on a piece
-          if (++lc.blk == lc.nb && to_load > 0) {
-            // heads of a sequence share its pages: a list of up to 32 serves them all (its
-            // visible blocks are those of the sequence's last rows)
-            const bool same = !SPARSE && lc.nb <= 32 && lc.tiles == 1 && !lc.last_unit(p);
-            lc.next_unit(p, sm.seq);
-            if (!same) ids_at = -1;
-          }
-        }
-        half ^= 1;
-        load_slot = load_slot + 1 == kSlots ? 0 : load_slot + 1;
-      }
-      copies_commit();
-    };
-
-    int ahead = kSlots;  // half steps that the copies go in front at first
-
-    int slot = 0, meta_at = 0, at_piece = run * cut.pieces;  // (the copies may be in a later piece already)
-    long long at = start;
-    uint4 qx[NT][kMt / 2];  // raw query rows of cc's unit, this lane's channels
-    auto fetch_q = [&]() {  // a row of no sequence is not read
-      F::template fetch_rows<NT>(p, cc.s.row0, cc.head, cc.rr0(), !SPARSE || cc.seq >= 0 ? cc.nrows(p.g) : 0, qx);
-    };
-    fetch_q();
-    while (true) {
-      // ---- one unit, or the part of it that the piece has
-      const bool begins = cc.blk == 0;
-      const int steps = static_cast<int>(min(static_cast<long long>(cc.nb - cc.blk), stop - at));
-      const bool ends = cc.blk + steps == cc.nb;
-      const int nrows = cc.nrows(p.g), rr0 = cc.rr0(), row0 = cc.s.row0, head = cc.head;
-      const bool live = !SPARSE || cc.seq >= 0;
-
-      const int low_pos = cc.first_pos(p.g);
-      const Rows<D, NT> rows(p, qx, cc.s.p0, rr0, nrows);
-      Sums<D, NT> sums;
-      sums.clear();
-
-      // Half a step is a block's scores or its output; then the next half block is asked
-      // for.  That is a page of code with a place of its own, once in the kernel: the
-      // loop is bound by the fetch of its instructions as much as by what they do.  Twice
-      // in the loop and once in front of it, unrolled, 64 sequences took 149.4 us against
-      // 146.5, 16 drafts 66.3 against 61.8, four short documents 11.3 against 9.9.
-      const Probabilities<NT> prob = {sm.p[warp]};
-      float f[NT][2];
-      bool seen = false, masked = false;
-#pragma unroll 1
-      for (int half_step = -ahead; half_step < 2 * steps; ++half_step) {
-        if (half_step >= 0) {
-          copies_wait<kSlots - 1>();
-          if (half_step % 2 == 0) {
-            __syncwarp();
-            const Meta meta = sm.meta[warp][meta_at];
-            meta_at = (meta_at + 1) % kMeta;
-            seen = meta.key0 >= 0;
-            masked = meta.key0 + kBlock - 1 > low_pos;  // some row does not see the whole block
-            if (seen) {
-              F::template scores<NT>(rows, sums, sm.ring[warp] + slot * F::kSlot, meta, masked, prob, f);
-            }
-          } else if (seen) {
-            bool sure = false;  // that further passes are needed
-            while (true) {
-              uint32_t pf[NT][4][2];
-              float least[NT][2];
-              prob.get(pf);
-              F::template output<NT>(sums, pf, f, sm.ring[warp] + slot * F::kSlot, masked, least);
-              // Is an output so small that what fp16 leaves of P could count?
-#pragma unroll
-              for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                  sure |= t * 8 + 2 * tc + k < nrows && f[t][k] != 0.f && !(least[t][k] >= F::kEnough);
-              if (!__any_sync(0xffffffffu, sure) || !__any_sync(0xffffffffu, prob.more())) break;
-              sure = true;
-              prob.next();  // four times at most
-#pragma unroll
-              for (int t = 0; t < NT; ++t) {
-                f[t][0] *= 1.f / kNextPass;
-                f[t][1] *= 1.f / kNextPass;
-              }
-            }
-          }
-          slot = slot + 1 == kSlots ? 0 : slot + 1;
-        }
-        issue();
-      }
-      ahead = 0;
-      at += steps;
-      done += steps;
-      const int rest = cc.nb - cc.blk - steps;  // steps of the unit behind the piece
-      const int this_piece = at_piece;
-      const long long this_at = at;
-
-      // ---- the next unit's query rows are asked for before this one is written
-      bool more = true;
-      if (at < stop) {
-        cc.next_unit(p, sm.seq);
-      } else {
-        __syncwarp();
-        more = done != loaded;
-        if (more) {  // the piece that the copies went on to
-          at_piece = sm.meta[warp][meta_at].piece;
-          const int w = at_piece / cut.pieces;
-          cut.range(w, at_piece - w * cut.pieces, at, stop);
-          locate(cc, at);
-        }
-      }
-      if (more) fetch_q();
-
-      // ---- the unit's part is done: out, or into a partial
-      const bool whole = begins && ends;
-      const size_t part_at = (static_cast<size_t>(this_piece) * 2 + (begins ? 1 : 0)) * kRows;
-      if (live) write_part<D, NT>(p, sums, head, row0, rr0, nrows, whole, part_at);
-      if (begins && !ends && live && lane == 0) {
-        Open o = {};
-        o.first = this_piece;
-        o.parts = cut.piece_of(this_at + rest - 1) - this_piece + 1;
-        o.row0 = row0;
-        o.head = head;
-        o.nrows = nrows;
-        o.rr0 = rr0;
-        p.open[p.dynamic ? atomicAdd(p.head, 1) : this_piece] = o;
-      }
-      if (!more) break;
-    }
-    copies_wait<0>();
-  }
-  // Even a call without work ends after the kernels in front of it: what comes
-  // next in the stream (another thread's kernel, perhaps) waits for this one only.
-  if (p.dynamic) asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // Zeroes the counters while the attention's CTAs are starting.
 __global__ void k_cache_attention_start(const AttnParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -822,15 +504,15 @@ __global__ void k_cache_attention_start(const AttnParams p) {
 // units are dealt to all CTAs, whose warps then share a row's parts (that call:
 // 646 us with each unit's CTA joining its rows itself, 636 us so).
 constexpr int kJoinWarps = 16;
+// Two units share at most one piece, so n units of more than kAlone (48) parts take
+// more than n (kAlone - 1) pieces; of the others a CTA has one for each gridDim.x
+// pieces.  The host keeps both below this.
+constexpr int kMostShared = 256;
 template <int D, int NT>
 __global__ void __launch_bounds__(kJoinWarps * 32, 1) k_cache_attention_join(const AttnParams p, int pieces) {
   constexpr int kRows = 8 * NT;
   constexpr int kAlone = 48;  // most parts of a row that a warp joins alone
   constexpr int kFew = 256;   // most parts of rows that a CTA joins at once
-  // Two units share at most one piece, so n units of more than kAlone parts take
-  // more than n (kAlone - 1) pieces; of the others a CTA has one for each
-  // gridDim.x pieces.  The host keeps both below this.
-  constexpr int kMostShared = 192;
   constexpr int V = D / 32;
   __shared__ __align__(16) float s_x[kJoinWarps][D];
   __shared__ float2 s_sum[kJoinWarps];
@@ -940,14 +622,14 @@ hdp_status_t sm_count(int* device, int* sms) {
 }
 
 struct Layout {
-  int pieces;
   size_t part, part_sum, open, head, bytes;
-  Layout(int sms, int d) {
-    const size_t rows = 8 * kMaxNt;
-    pieces = sms * kWarps * (1 + kMorePieces);
+  // warps: of a CTA, for one tile of query rows and for two
+  Layout(int sms, int d, const int (&warps)[kMaxNt]) {
+    const size_t pieces = static_cast<size_t>(sms) * std::max(warps[0], warps[1]) * (1 + kMorePieces);
+    const size_t rows = static_cast<size_t>(sms) * std::max(8 * warps[0], 16 * warps[1]) * (1 + kMorePieces) * 2;
     part = 0;
-    part_sum = part + align256(pieces * 2 * rows * d * sizeof(float));
-    open = part_sum + align256(pieces * 2 * rows * sizeof(float2));
+    part_sum = part + align256(rows * d * sizeof(float));
+    open = part_sum + align256(rows * sizeof(float2));
     head = open + align256(pieces * sizeof(Open));
     bytes = head + 256;
   }
@@ -972,36 +654,35 @@ hdp_status_t launch_early(void (*kernel)(T...), dim3 grid, int threads, int smem
   return HDP_OK;
 }
 
-template <class F, int NT, bool SPARSE>
-hdp_status_t launch(const AttnParams& p, int device, int ctas, cudaStream_t st) {
-  auto* kernel = k_cache_attention<F, NT, SPARSE>;
-  constexpr int smem = sizeof(Shared<F, NT, SPARSE>);
-  static_assert(smem <= 232448, "shared memory of a CTA");
-  static std::atomic<bool> ready[kDevices];
+// Launches `kernel` (`warps` a CTA, `smem` bytes) and the join behind it; `ready`: the
+// devices on which the kernel may have that much.
+template <int D, int NT>
+hdp_status_t launch(void (*kernel)(AttnParams), int warps, int smem, std::atomic<bool> (&ready)[kDevices], const AttnParams& p,
+                    int device, int ctas, cudaStream_t st) {
   if (device >= kDevices || !ready[device].load(std::memory_order_relaxed)) {
     HDP_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     if (device < kDevices) ready[device].store(true, std::memory_order_relaxed);
   }
-  const int pieces = ctas * kWarps * (p.dynamic ? 1 + kMorePieces : 1);
-  if (pieces > 47 * 192)  // k_cache_attention_join's lists; a device of over 188 SMs
-    return fail(HDP_ERR_UNSUPPORTED, "hdp_cache_attention: too many SMs");
+  const int pieces = ctas * warps * (p.dynamic ? 1 + kMorePieces : 1);
+  if (pieces > 47 * kMostShared)  // a device of over 256 (12 warps: 170) SMs
+    return fail(HDP_ERR_UNSUPPORTED, "attention over the cache: too many SMs");
   if (p.dynamic) {
     k_cache_attention_start<<<1, 32, 0, st>>>(p);
     note_launch();
     HDP_CUDA_TRY(cudaGetLastError());
-    const hdp_status_t r = launch_early(kernel, dim3(ctas), kThreads, smem, st, p);
+    const hdp_status_t r = launch_early(kernel, dim3(ctas), warps * 32, smem, st, p);
     if (r != HDP_OK) return r;
   } else {
-    kernel<<<ctas, kThreads, smem, st>>>(p);
+    kernel<<<ctas, warps * 32, smem, st>>>(p);
     note_launch();
     HDP_CUDA_TRY(cudaGetLastError());
   }
-  return launch_early(k_cache_attention_join<F::kD, NT>, dim3(ctas), kJoinWarps * 32, 0, st, p, pieces);
+  return launch_early(k_cache_attention_join<D, NT>, dim3(ctas), kJoinWarps * 32, 0, st, p, pieces);
 }
 
 // Checks and launches a call whose view is in p.c (`name`: the entry point).
 template <class Launch>
-hdp_status_t attend(const char* entry, AttnParams& p, int d, int64_t rows, const void* q, int32_t hq, float scale,
+hdp_status_t attend(const char* entry, const int (&warps)[kMaxNt], AttnParams& p, int d, int64_t rows, const void* q, int32_t hq, float scale,
                     const int32_t* blocks, int32_t count, void* workspace, size_t workspace_bytes, void* o, float* lse,
                     void* stream, Launch launch_with) {
   const std::string name(entry);
@@ -1019,7 +700,7 @@ hdp_status_t attend(const char* entry, AttnParams& p, int d, int64_t rows, const
   int device = 0, sms = 0;
   const hdp_status_t r = sm_count(&device, &sms);
   if (r != HDP_OK) return r;
-  const Layout lay(sms, d);
+  const Layout lay(sms, d, warps);
   if (!workspace || workspace_bytes < lay.bytes)
     return fail(HDP_ERR_INVALID_ARGUMENT, name + ": workspace too small (need " + std::to_string(lay.bytes) + " bytes)");
   if (reinterpret_cast<uintptr_t>(workspace) & 255)
@@ -1050,19 +731,20 @@ hdp_status_t attend(const char* entry, AttnParams& p, int d, int64_t rows, const
   const int ctas = steps < sms ? static_cast<int>(steps) + 1 : sms;
   // Handing out the ends of runs costs one more small launch: from 16 steps a
   // warp on, where the runs' ends are more than a step.
-  p.dynamic = steps >= 16.0 * kWarps * sms;
+  p.dynamic = steps >= 16.0 * warps[nt - 1] * sms;
   return launch_with(p, nt, device, ctas, static_cast<cudaStream_t>(stream));
 }
 
 // Bytes of the workspace.
-inline hdp_status_t workspace_bytes_of(const char* entry, int32_t hkv, int32_t d, int32_t hq, size_t* bytes) {
+inline hdp_status_t workspace_bytes_of(const char* entry, const int (&warps)[kMaxNt], int32_t hkv, int32_t d, int32_t hq,
+                                       size_t* bytes) {
   const std::string name(entry);
   if (hkv < 1 || hq < 1 || hq % hkv != 0) return fail(HDP_ERR_INVALID_ARGUMENT, name + ": need hq >= 1 and hq % hkv == 0");
   if (d != 64 && d != 128) return fail(HDP_ERR_UNSUPPORTED, name + ": d must be 64 or 128");
   int device = 0, sms = 0;
   const hdp_status_t r = sm_count(&device, &sms);
   if (r != HDP_OK) return r;
-  *bytes = Layout(sms, d).bytes;
+  *bytes = Layout(sms, d, warps).bytes;
   return HDP_OK;
 }
 
