@@ -52,7 +52,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kWarpsOf[kMaxNt] = {kWarps, kWarps};
+constexpr PartCount kCount = {kWarps * (1 + kMorePieces), kWarps * (1 + kMorePieces) * 2};
 // Bytes of a warp's ring of half blocks.  More in flight streams a long run
 // better; less leaves the memory's queues shorter, and with them every other
 // access (lists, pages, query rows), which short runs wait for.  Measured at
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
       // ---- the unit's part is done: out, or into a partial
       const bool whole = begins && ends;
       const size_t part_at = (static_cast<size_t>(this_piece) * 2 + (begins ? 1 : 0)) * kRows;
-      if (live) write_part<D, NT>(p, sums, head, row0, rr0, nrows, whole, part_at);
+      if (live) write_part<D, NT>(p, sums, head, row0, rr0, nrows, whole, p.part + part_at * D, p.part_sum + part_at);
       if (begins && !ends && live && lane == 0) {
         Open o = {};
         o.first = this_piece;
@@ -591,7 +591,8 @@ hdp_status_t launch8(const AttnParams& p, int device, int ctas, cudaStream_t st)
   static std::atomic<bool> ready[kDevices];
   constexpr int smem = sizeof(Shared<NT, SPARSE>);
   static_assert(smem <= 232448, "shared memory of a CTA");
-  return launch<D, NT>(k_cache_attention<D, FMT, NT, SPARSE>, kWarps, smem, ready, p, device, ctas, st);
+  const int pieces = ctas * kWarps * (p.dynamic ? 1 + kMorePieces : 1);
+  return launch<D, NT>(k_cache_attention<D, FMT, NT, SPARSE>, kWarps, smem, pieces, ready, p, device, ctas, st);
 }
 
 template <int D, int FMT>
@@ -607,7 +608,7 @@ using namespace hdp;
 
 extern "C" hdp_status_t hdp_cache_attention_workspace_bytes(const hdp_cache_t* cache, int32_t hq, size_t* bytes) {
   if (!cache || !bytes) return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_cache_attention_workspace_bytes: NULL argument");
-  return workspace_bytes_of("hdp_cache_attention_workspace_bytes", kWarpsOf, cache->hkv, cache->d, hq, bytes);
+  return workspace_bytes_of("hdp_cache_attention_workspace_bytes", kCount, cache->hkv, cache->d, hq, bytes);
 }
 
 extern "C" hdp_status_t hdp_cache_attention(const hdp_cache_t* cache, const int32_t* cu, int64_t rows, const void* q,
@@ -618,7 +619,7 @@ extern "C" hdp_status_t hdp_cache_attention(const hdp_cache_t* cache, const int3
   const hdp_status_t r = cache_view("hdp_cache_attention", cache, cu, rows, &p.c);
   if (r != HDP_OK) return r;
   const bool i8 = cache->format == HDP_CACHE_INT8, wide = cache->d == 128;
-  return attend("hdp_cache_attention", kWarpsOf, p, cache->d, rows, q, hq, scale, blocks, count, workspace, workspace_bytes, o, lse,
+  return attend("hdp_cache_attention", kCount, kWarps, p, cache->d, rows, q, hq, scale, blocks, count, workspace, workspace_bytes, o, lse,
                 stream, [=](const AttnParams& a, int nt, int device, int ctas, cudaStream_t st) {
                   if (wide)
                     return i8 ? launch_for<128, HDP_CACHE_INT8>(a, nt, device, ctas, st)

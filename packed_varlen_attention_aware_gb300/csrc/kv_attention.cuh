@@ -434,10 +434,11 @@ struct Probabilities {
   }
 };
 
-// Normalises the sums of a unit, or of a piece's part of it, and writes them.
+// Normalises the sums of a unit, or of a piece's part of it, and writes them (a part to
+// part and part_sum, row by row).
 template <int D, int NT>
 __device__ __forceinline__ void write_part(const AttnParams& p, const Sums<D, NT>& sums, int head, int row0, int rr0,
-                                           int nrows, bool whole, size_t part_at) {
+                                           int nrows, bool whole, float* part, float2* part_sum) {
   const int lane = threadIdx.x & 31, gr = lane >> 2, tc = lane & 3;
   constexpr int kMt = D / 16;
 #pragma unroll
@@ -484,8 +485,8 @@ __device__ __forceinline__ void write_part(const AttnParams& p, const Sums<D, NT
         if (r < nrows) {
 #pragma unroll
           for (int i = 0; i < kMt; ++i)
-            p.part[(part_at + r) * D + i * 16 + (k >> 1) * 8 + gr] = sums.acc[t][i][k] * inv[k & 1] * unit[k & 1];
-          if (gr == 0 && k < 2) p.part_sum[part_at + r] = make_float2(sums.m[t][k & 1], l[k & 1]);
+            part[r * D + i * 16 + (k >> 1) * 8 + gr] = sums.acc[t][i][k] * inv[k & 1] * unit[k & 1];
+          if (gr == 0 && k < 2) part_sum[r] = make_float2(sums.m[t][k & 1], l[k & 1]);
         }
       }
     }
@@ -605,6 +606,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 1) k_cache_attention_join(con
 }
 
 constexpr int kMaxNt = 2;
+// For each SM: entries of open, and parts of 16 rows.
+struct PartCount {
+  int open, parts;
+};
 constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 constexpr int kDevices = 64;
@@ -623,10 +628,8 @@ hdp_status_t sm_count(int* device, int* sms) {
 
 struct Layout {
   size_t part, part_sum, open, head, bytes;
-  // warps: of a CTA, for one tile of query rows and for two
-  Layout(int sms, int d, const int (&warps)[kMaxNt]) {
-    const size_t pieces = static_cast<size_t>(sms) * std::max(warps[0], warps[1]) * (1 + kMorePieces);
-    const size_t rows = static_cast<size_t>(sms) * std::max(8 * warps[0], 16 * warps[1]) * (1 + kMorePieces) * 2;
+  Layout(const PartCount& n, int sms, int d) {
+    const size_t pieces = static_cast<size_t>(sms) * n.open, rows = static_cast<size_t>(sms) * n.parts * 8 * kMaxNt;
     part = 0;
     part_sum = part + align256(rows * d * sizeof(float));
     open = part_sum + align256(rows * sizeof(float2));
@@ -654,16 +657,15 @@ hdp_status_t launch_early(void (*kernel)(T...), dim3 grid, int threads, int smem
   return HDP_OK;
 }
 
-// Launches `kernel` (`warps` a CTA, `smem` bytes) and the join behind it; `ready`: the
-// devices on which the kernel may have that much.
+// Launches `kernel` (`warps` a CTA, `smem` bytes) and the join of its pieces behind it;
+// `ready`: the devices on which the kernel may have that much.
 template <int D, int NT>
-hdp_status_t launch(void (*kernel)(AttnParams), int warps, int smem, std::atomic<bool> (&ready)[kDevices], const AttnParams& p,
-                    int device, int ctas, cudaStream_t st) {
+hdp_status_t launch(void (*kernel)(AttnParams), int warps, int smem, int pieces, std::atomic<bool> (&ready)[kDevices],
+                    const AttnParams& p, int device, int ctas, cudaStream_t st) {
   if (device >= kDevices || !ready[device].load(std::memory_order_relaxed)) {
     HDP_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     if (device < kDevices) ready[device].store(true, std::memory_order_relaxed);
   }
-  const int pieces = ctas * warps * (p.dynamic ? 1 + kMorePieces : 1);
   if (pieces > 47 * kMostShared)  // a device of over 256 (12 warps: 170) SMs
     return fail(HDP_ERR_UNSUPPORTED, "attention over the cache: too many SMs");
   if (p.dynamic) {
@@ -680,9 +682,10 @@ hdp_status_t launch(void (*kernel)(AttnParams), int warps, int smem, std::atomic
   return launch_early(k_cache_attention_join<D, NT>, dim3(ctas), kJoinWarps * 32, 0, st, p, pieces);
 }
 
-// Checks and launches a call whose view is in p.c (`name`: the entry point).
+// Checks and launches a call whose view is in p.c; hand_out: warps of a CTA that can hand
+// out the ends of their runs, or 0.
 template <class Launch>
-hdp_status_t attend(const char* entry, const int (&warps)[kMaxNt], AttnParams& p, int d, int64_t rows, const void* q, int32_t hq, float scale,
+hdp_status_t attend(const char* entry, const PartCount& count_of, int hand_out, AttnParams& p, int d, int64_t rows, const void* q, int32_t hq, float scale,
                     const int32_t* blocks, int32_t count, void* workspace, size_t workspace_bytes, void* o, float* lse,
                     void* stream, Launch launch_with) {
   const std::string name(entry);
@@ -700,7 +703,7 @@ hdp_status_t attend(const char* entry, const int (&warps)[kMaxNt], AttnParams& p
   int device = 0, sms = 0;
   const hdp_status_t r = sm_count(&device, &sms);
   if (r != HDP_OK) return r;
-  const Layout lay(sms, d, warps);
+  const Layout lay(count_of, sms, d);
   if (!workspace || workspace_bytes < lay.bytes)
     return fail(HDP_ERR_INVALID_ARGUMENT, name + ": workspace too small (need " + std::to_string(lay.bytes) + " bytes)");
   if (reinterpret_cast<uintptr_t>(workspace) & 255)
@@ -731,12 +734,12 @@ hdp_status_t attend(const char* entry, const int (&warps)[kMaxNt], AttnParams& p
   const int ctas = steps < sms ? static_cast<int>(steps) + 1 : sms;
   // Handing out the ends of runs costs one more small launch: from 16 steps a
   // warp on, where the runs' ends are more than a step.
-  p.dynamic = steps >= 16.0 * warps[nt - 1] * sms;
+  p.dynamic = hand_out > 0 && steps >= 16.0 * hand_out * sms;
   return launch_with(p, nt, device, ctas, static_cast<cudaStream_t>(stream));
 }
 
 // Bytes of the workspace.
-inline hdp_status_t workspace_bytes_of(const char* entry, const int (&warps)[kMaxNt], int32_t hkv, int32_t d, int32_t hq,
+inline hdp_status_t workspace_bytes_of(const char* entry, const PartCount& count_of, int32_t hkv, int32_t d, int32_t hq,
                                        size_t* bytes) {
   const std::string name(entry);
   if (hkv < 1 || hq < 1 || hq % hkv != 0) return fail(HDP_ERR_INVALID_ARGUMENT, name + ": need hq >= 1 and hq % hkv == 0");
@@ -744,7 +747,7 @@ inline hdp_status_t workspace_bytes_of(const char* entry, const int (&warps)[kMa
   int device = 0, sms = 0;
   const hdp_status_t r = sm_count(&device, &sms);
   if (r != HDP_OK) return r;
-  *bytes = Layout(sms, d, warps).bytes;
+  *bytes = Layout(count_of, sms, d).bytes;
   return HDP_OK;
 }
 

@@ -55,9 +55,8 @@ __device__ __forceinline__ float scale_at(const uint2& x, int j) {
 __device__ __forceinline__ float exponent_bits(const uint2& x, int j) {
   return __uint_as_float(__byte_perm(scale_word(x, j), 0x4b000000u, 0x7650 + (j & 3)));
 }
-// Of bytes: the top bit of those that are 192 (2^65) or more, of those that are 255.
+// The top bit of bytes that are 192 (2^65) or more.
 __device__ __forceinline__ uint32_t large_bytes(uint32_t w) { return w & (w << 1); }
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & w & 0x80808080u; }
 
 // Bytes of a block whose scales go up to 2^126, times 2^-32; bit j of the result: some
 // scale of key j is NaN.
@@ -83,8 +82,9 @@ __device__ __forceinline__ uint32_t lower_scales(uint2 (&ks)[G]) {
   return lost;
 }
 
-// Warps of a CTA for one tile of query rows and for two.
-constexpr int kWarpsOf[kMaxNt] = {8, 8};
+constexpr int kWarps = 8;
+// A part for each warp, and two for each CTA in front of them.
+constexpr PartCount kCount = {1, kWarps + 2};
 
 constexpr float kHeadroom = 4.f;    // bits of a fresh reference above what needs it
 constexpr float kCommon = 8.f;      // most bits that an output's reference is raised to be its neighbours', or above a V scale
@@ -95,18 +95,29 @@ constexpr float kEnough4 = 0.0625f;
 template <int D>
 constexpr int kBlock4 = 2 * kCodes4<D> + kScales4<D>;
 
+// What a warp's run leaves of units that it shares with its neighbours: [0] of one begun
+// before it, [1] of one begun in it that goes on behind it.
+struct RunEnds {
+  bool has[2];
+  bool ends;           // [0] is the unit's last
+  const float* o[2];   // the part's rows
+  int row0[2], head[2], nrows[2], rr0[2];
+  long long last;      // [1]: the unit's last step
+};
+
 template <int D, int NT>
 struct Shared4 {
-  static constexpr int kWarps = kWarpsOf[NT - 1];
   // P of a block on its way round takes the place of the codes of K, if it fits.
   static constexpr bool kOwnP = NT * 2048 > kCodes4<D>;
   static constexpr int kSlots = D == 128 ? 3 : kOwnP ? 5 : 6;
   unsigned char ring[kWarps][kSlots][kBlock4<D>];
   float4 p[kOwnP ? kWarps : 1][NT][4][32];
   SeqPlace seq[kSeqs];
-  int piece[kWarps][kSlots];
-  long long pre[kWarps * 32];  // steps before each thread's sequences
-  long long warp_sum[kWarps];
+  longlong2 pre[kWarps * 32];  // steps, and blocks, before each thread's sequences
+  longlong2 warp_sum[kWarps];
+  long long last_blocks;  // of the last thread's sequences
+  RunEnds ends[kWarps];
+  float2 part_sum[kWarps][2][8 * NT];
 };
 
 // Query rows of a unit: of each group of channels this lane's 8.
@@ -202,15 +213,35 @@ struct Common {
   int gap;  // + 127, as a scale's byte; below 0: no block yet
 };
 
+// What stands behind it in a rare branch is not computed in front of the branch.
+__device__ __forceinline__ void stay_here() { asm volatile("" ::: "memory"); }
+
+// A place in a row of scales (of a lane's two, at 2 lane) to its token.
+__device__ __forceinline__ int place_token(int place) { return 8 * (place & 7) + (place >> 3); }
+
 // Scores of a block to P under the references that the sums have.  True, and the row sums
-// have their share, if every P is a normal number of fp16.
+// have their share, if every P is a normal number of fp16.  Of a block that is not seen
+// whole (`masked`) the scores that a row does not see are -infinity already, and the tokens
+// from `limit` on, which no row sees, may hold anything.
 template <int D, int NT>
 __device__ __forceinline__ bool as_is(const Rows<D, NT>& rows, Sums<D, NT>& sums, const Common& common,
-                                      const unsigned char* scales, int lane, const float (&s)[NT][4][4],
-                                      uint32_t (&pf)[NT][4][2]) {
-  const uint2 vs = reinterpret_cast<const uint2*>(scales + (D / 32) * kBlock)[lane >> 2];
+                                      const unsigned char* scales, int lane, bool masked, int limit,
+                                      const float (&s)[NT][4][4], uint32_t (&pf)[NT][4][2]) {
+  uint2 vs = reinterpret_cast<const uint2*>(scales + (D / 32) * kBlock)[lane >> 2];
   // V scales of the block, two a lane: 2^-14 to 1 of the output's reference, as normal numbers of fp16
-  const uint32_t two = reinterpret_cast<const uint16_t*>(scales + (D / 32) * kBlock)[lane];
+  uint32_t two = reinterpret_cast<const uint16_t*>(scales + (D / 32) * kBlock)[lane];
+  if (masked) {
+    stay_here();
+    const uint32_t any = static_cast<uint32_t>(common.gap) & 0xffu;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (8 * j + (lane >> 2) >= limit) {
+        uint32_t& w = j < 4 ? vs.x : vs.y;
+        w = (w & ~(0xffu << (8 * (j & 3)))) | any << (8 * (j & 3));
+      }
+    if (place_token(2 * lane) >= limit) two = (two & 0xff00u) | any;
+    if (place_token(2 * lane + 1) >= limit) two = (two & 0x00ffu) | any << 8;
+  }
   bool ok = static_cast<uint32_t>(common.gap) - (two & 0xffu) <= 14u && static_cast<uint32_t>(common.gap) - (two >> 8) <= 14u;
   const uint32_t back = (15u - static_cast<uint32_t>(common.gap)) * 0x04000400u;
   float l[NT][2];
@@ -234,6 +265,16 @@ __device__ __forceinline__ bool as_is(const Rows<D, NT>& rows, Sums<D, NT>& sums
       least = __hmin2(least, x);
       pf[t][j >> 1][j & 1] = h2_bits(x);
     }
+    if (masked) {  // a score of -infinity may have its 0
+      stay_here();
+      least = __half2half2(__ushort_as_half(0x7c00));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t low = s[t][j >> 1][2 * (j & 1)] == -__int_as_float(0x7f800000) ? 0x7c00u : 0u;
+        const uint32_t up = s[t][j >> 1][1 + 2 * (j & 1)] == -__int_as_float(0x7f800000) ? 0x7c000000u : 0u;
+        least = __hmin2(least, as_h2(pf[t][j >> 1][j & 1] | low | up));
+      }
+    }
     // (a NaN is in the sum, and in neither of the extremes)
     ok = ok && high <= kBias && __hbge2(least, __half2half2(__ushort_as_half(0x0400))) && l[t][0] == l[t][0] && l[t][1] == l[t][1];
   }
@@ -252,9 +293,9 @@ __device__ __forceinline__ bool as_is(const Rows<D, NT>& rows, Sums<D, NT>& sums
 // its V scales, where they are not that high already.
 template <int D, int NT>
 __device__ __forceinline__ void refer(const Rows<D, NT>& rows, Sums<D, NT>& sums, Common& common, const unsigned char* scales,
-                                      int lane, const float (&s)[NT][4][4]) {
+                                      int lane, int limit, const float (&s)[NT][4][4]) {
   const uint32_t two = reinterpret_cast<const uint16_t*>(scales + (D / 32) * kBlock)[lane];
-  int above = static_cast<int>(max(two & 0xffu, two >> 8));
+  int above = static_cast<int>(max(place_token(2 * lane) < limit ? two & 0xffu : 0u, place_token(2 * lane + 1) < limit ? two >> 8 : 0u));
   above = __reduce_max_sync(0xffffffffu, above);
   if (above > common.gap) common.gap = above + 1;
   const float gap = static_cast<float>(common.gap - 127);
@@ -281,129 +322,7 @@ __device__ __forceinline__ void refer(const Rows<D, NT>& rows, Sums<D, NT>& sums
     }
 }
 
-// Scores of any kind to P from the block's own largest, at most 2^15, in place; brings the
-// sums to new references, and f to the power of two (<= 1) of the block in the output.
-template <int D, int NT>
-__device__ __forceinline__ void softmax(const Rows<D, NT>& rows, Sums<D, NT>& sums, Common& common, const unsigned char* scales,
-                                        int key0, bool masked, bool careful, uint32_t lost, float (&s)[NT][4][4],
-                                        float (&f)[NT][2]) {
-  const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fc00000);
-  const int gr = (threadIdx.x & 31) >> 2;
-  const uint2 vs = reinterpret_cast<const uint2*>(scales + (D / 32) * kBlock)[gr];
-  bool fresh = false;
-  float most_gap = -inf;
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    float top[2] = {-inf, -inf};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float r = rows.scale[t][k & 1], back = 4294967296.f;  // 2^32
-        float x = s[t][i][k];
-        if (careful) x = x * (r < 1.f ? r : back) * (r < 1.f ? back : r);
-        else x *= r;
-        if (lost >> (2 * i + (k >> 1)) & 1) x = nan;
-        if (masked && key0 + 16 * i + 8 * (k >> 1) + gr > rows.pos[t][k & 1]) x = -inf;
-        s[t][i][k] = x;
-        top[k & 1] = fmaxf(top[k & 1], x);
-      }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int d = 4; d < 32; d *= 2) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], d));
-      const bool none = top[k] == -inf;
-      float ref = none ? 0.f : ceilf(top[k]);
-      const bool biased = fabsf(ref) < kBiasMost;
-      if (biased) ref -= kBias;
-      // the row sum's share, and the exponents of P with the V scales
-      float sum = 0.f, most = -inf;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float& x = s[t][j >> 1][k + 2 * (j & 1)];
-        const float y = x - ref;
-        sum += exp2_approx(y);
-        x = y + (exponent_bits(vs, j) - 8388735.f);
-        most = fmaxf(most, x);
-      }
-#pragma unroll
-      for (int d = 4; d < 32; d *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-      const float e = most == -inf ? 0.f : ceilf(most) - kBias;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[t][i][k] = exp2_approx(s[t][i][k] - e);
-        s[t][i][k + 2] = exp2_approx(s[t][i][k + 2] - e);
-      }
-      const float m = sums.m[t][k], gap = sums.gap[t][k];
-      const float m1 = none || ref <= m ? m : ref + (biased ? kHeadroom : 0.f);
-      const float down = m - m1, up = none ? -inf : ref - m1;
-      const float gap1 = none ? gap : fmaxf(gap + down, up + e);
-      fresh |= gap1 > gap + down;
-      most_gap = fmaxf(most_gap, gap1);
-      sums.l[t][k] = fmaf(sum, exp2_approx(up), sums.l[t][k] * exp2_approx(down));
-      f[t][k] = exp2_approx(up + (e - gap1));  // 0 where no key is seen
-      const float turn = exp2_approx(down + (gap - gap1));
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        sums.acc[t][i][k] *= turn;
-        sums.acc[t][i][k + 2] *= turn;
-      }
-      sums.m[t][k] = m1;
-      sums.gap[t][k] = gap1;
-    }
-  }
-  // One distance for all rows, as long as it is not far above what a row needs.
-#pragma unroll
-  for (int d = 1; d < 4; d *= 2) most_gap = fmaxf(most_gap, __shfl_xor_sync(0xffffffffu, most_gap, d));
-  // It is above the scales of V too, which quick blocks need, if they are not far above it.
-  int scale = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    bool seen = !masked;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) seen = seen || key0 + 8 * j + gr <= max(rows.pos[t][0], rows.pos[t][1]);
-    if (seen) scale = max(scale, static_cast<int>(scale_word(vs, j) >> (8 * (j & 3)) & 0xffu));
-  }
-  const float above = static_cast<float>(__reduce_max_sync(0xffffffffu, scale) - 126);
-  const float least_gap = most_gap;
-  if (__any_sync(0xffffffffu, fresh)) most_gap += kHeadroom;
-  if (above <= least_gap + kCommon) most_gap = fmaxf(most_gap, above);
-  bool same = true;
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const bool near = most_gap - sums.gap[t][k] <= kCommon;
-      const float turn = near ? exp2_approx(sums.gap[t][k] - most_gap) : 1.f;
-      same = same && near;
-      f[t][k] *= turn;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        sums.acc[t][i][k] *= turn;
-        sums.acc[t][i][k + 2] *= turn;
-      }
-      if (near) sums.gap[t][k] = most_gap;
-    }
-  common.any = __all_sync(0xffffffffu, same);
-  common.gap = static_cast<int>(fminf(fmaxf(most_gap, -1126.f), 999.f)) + 127;
-  // A NaN scale of a V row that a query row sees makes its output NaN.
-  if (__any_sync(0xffffffffu, (nan_bytes(vs.x) | nan_bytes(vs.y)) != 0)) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        int bad = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          bad |= (scale_word(vs, j) >> (8 * (j & 3)) & 0xffu) == 255u && key0 + 8 * j + gr <= rows.pos[t][k];
-#pragma unroll
-        for (int d = 4; d < 32; d *= 2) bad |= __shfl_xor_sync(0xffffffffu, bad, d);
-        if (bad) f[t][k] = nan;
-      }
-  }
-}
-
-// What the block that is not quick needs and changes.
+// What a block that is not quick needs and changes.
 template <int D, int NT>
 struct Slow {
   Rows<D, NT> rows;
@@ -412,22 +331,26 @@ struct Slow {
   float s[NT][4][4];
 };
 
-// A block with scores of any kind.  Not inlined: the loop over quick blocks would lose its
-// registers to it (12 warps an SM, 2M tokens: 855 us with it inlined).
+// A block with scores of any kind: P from the block's own largest, at most 2^15, the sums
+// brought to new references.  Not inlined: the loop over quick blocks would lose its
+// registers to it (12 warps an SM, 2M tokens: 855 us with it inlined); and written as loops:
+// few calls come here, and fetch their instructions from far.
 template <int D, int NT>
 __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, int key0, bool masked, int nrows) {
   using Sh = Shared4<D, NT>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   auto& sm = *reinterpret_cast<Sh*>(smem_raw);
-  const int lane = threadIdx.x & 31, tc = lane & 3;  // fragment column pair
+  const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fc00000);
+  const int lane = threadIdx.x & 31, gr = lane >> 2, tc = lane & 3;
   unsigned char* block = sm.ring[warp][slot];
   const unsigned char* scales = block + kCodes4<D>;
   const uint4* vx = reinterpret_cast<const uint4*>(scales + kScales4<D>) + lane;
+  const uint2 vs = reinterpret_cast<const uint2*>(scales + (D / 32) * kBlock)[gr];
   uint2 ks[D / 32];
   uint32_t large = 0, lost = 0;
 #pragma unroll
   for (int g = 0; g < D / 32; ++g) {
-    ks[g] = reinterpret_cast<const uint2*>(scales + g * kBlock)[lane >> 2];
+    ks[g] = reinterpret_cast<const uint2*>(scales + g * kBlock)[gr];
     large |= large_bytes(ks[g].x) | large_bytes(ks[g].y);
   }
   const bool careful = __any_sync(0xffffffffu, (large & 0x80808080u) != 0);
@@ -435,8 +358,97 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
     lost = lower_scales<D / 32>(ks);
     first_product<D, NT>(slow.rows, block, lane, ks, slow.s);
   }
-  float f[NT][2];
-  softmax<D, NT>(slow.rows, slow.sums, slow.common, scales, key0, masked, careful, lost, slow.s, f);
+  int scale = 0;  // the largest V scale that a row sees
+  float f[NT][2];  // the power of two (<= 1) of the block in the output
+  float most_gap = -inf;
+  bool fresh = false;
+#pragma unroll 1
+  for (int tk = 0; tk < 2 * NT; ++tk) {
+    const int t = tk >> 1, k = tk & 1;
+    const float r = slow.rows.scale[t][k], back = 4294967296.f;  // 2^32
+    const int pos = slow.rows.pos[t][k];
+    float x[8], top = -inf;
+    int bad = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] = slow.s[t][j >> 1][k + 2 * (j & 1)];
+      if (careful) x[j] = x[j] * (r < 1.f ? r : back) * (r < 1.f ? back : r);
+      else x[j] *= r;
+      if (lost >> j & 1) x[j] = nan;
+      const bool seen = !masked || key0 + 8 * j + gr <= pos;
+      if (!seen) x[j] = -inf;
+      top = fmaxf(top, x[j]);
+      const int byte = static_cast<int>(scale_word(vs, j) >> (8 * (j & 3)) & 0xffu);
+      if (seen) scale = max(scale, byte);
+      bad |= seen && byte == 255;
+    }
+#pragma unroll
+    for (int d = 4; d < 32; d *= 2) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      bad |= __shfl_xor_sync(0xffffffffu, bad, d);
+    }
+    const bool none = top == -inf;
+    float ref = none ? 0.f : ceilf(top);
+    const bool biased = fabsf(ref) < kBiasMost;
+    if (biased) ref -= kBias;
+    // the row sum's share, and the exponents of P with the V scales
+    float sum = 0.f, most = -inf;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float y = x[j] - ref;
+      sum += exp2_approx(y);
+      x[j] = y + (exponent_bits(vs, j) - 8388735.f);
+      most = fmaxf(most, x[j]);
+    }
+#pragma unroll
+    for (int d = 4; d < 32; d *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+    const float e = most == -inf ? 0.f : ceilf(most) - kBias;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) slow.s[t][j >> 1][k + 2 * (j & 1)] = exp2_approx(x[j] - e);
+    const float m = slow.sums.m[t][k], gap = slow.sums.gap[t][k];
+    const float m1 = none || ref <= m ? m : ref + (biased ? kHeadroom : 0.f);
+    const float down = m - m1, up = none ? -inf : ref - m1;
+    const float gap1 = none ? gap : fmaxf(gap + down, up + e);
+    fresh |= gap1 > gap + down;
+    most_gap = fmaxf(most_gap, gap1);
+    slow.sums.l[t][k] = fmaf(sum, exp2_approx(up), slow.sums.l[t][k] * exp2_approx(down));
+    // 0 where no key is seen; NaN where the scale of a seen V row is
+    f[t][k] = bad ? nan : exp2_approx(up + (e - gap1));
+    const float turn = exp2_approx(down + (gap - gap1));
+#pragma unroll 1
+    for (int i = 0; i < D / 16; ++i) {
+      slow.sums.acc[t][i][k] *= turn;
+      slow.sums.acc[t][i][k + 2] *= turn;
+    }
+    slow.sums.m[t][k] = m1;
+    slow.sums.gap[t][k] = gap1;
+  }
+  // One distance for all rows, as long as it is not far above what a row needs.  It is
+  // above the scales of V too, which quick blocks need, if they are not far above it.
+#pragma unroll
+  for (int d = 1; d < 4; d *= 2) most_gap = fmaxf(most_gap, __shfl_xor_sync(0xffffffffu, most_gap, d));
+  const float above = static_cast<float>(__reduce_max_sync(0xffffffffu, scale) - 126);
+  const float least_gap = most_gap;
+  if (__any_sync(0xffffffffu, fresh)) most_gap += kHeadroom;
+  if (above <= least_gap + kCommon) most_gap = fmaxf(most_gap, above);
+  bool same = true;
+#pragma unroll 1
+  for (int tk = 0; tk < 2 * NT; ++tk) {
+    const int t = tk >> 1, k = tk & 1;
+    const bool near = most_gap - slow.sums.gap[t][k] <= kCommon;
+    const float turn = near ? exp2_approx(slow.sums.gap[t][k] - most_gap) : 1.f;
+    same = same && near;
+    f[t][k] *= turn;
+#pragma unroll 1
+    for (int i = 0; i < D / 16; ++i) {
+      slow.sums.acc[t][i][k] *= turn;
+      slow.sums.acc[t][i][k + 2] *= turn;
+    }
+    if (near) slow.sums.gap[t][k] = most_gap;
+  }
+  slow.common.any = __all_sync(0xffffffffu, same);
+  slow.common.gap = static_cast<int>(fminf(fmaxf(most_gap, -1126.f), 999.f)) + 127;
+
   copies_wait<2 * Sh::kSlots - 2>();
   __syncwarp();  // V is there, and the codes of K have been read
   const Probabilities<NT> prob = {Sh::kOwnP ? sm.p[Sh::kOwnP ? warp : 0] : reinterpret_cast<float4(*)[4][32]>(block)};
@@ -446,7 +458,7 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
   while (true) {
     uint32_t pf[NT][4][2];
     prob.get(pf);
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < D / 16; i += kTogether) {
       float y[NT][kTogether][4];
       second_product<true, NT>(vx, i, pf, y);
@@ -472,11 +484,23 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
   }
 }
 
+// A unit takes a warp its blocks and about three blocks' time more: its query rows, its
+// first references, its output.  The flat order has that many steps in front of it (64
+// sequences of 256 to 29K tokens: 110.6 us with none, 97.1 with two, 93.5 with three).
+constexpr int kUnitSteps = 3;
+
+// Steps of all units of a sequence.
+template <int NT>
+__device__ __forceinline__ long long steps_of(const AttnParams& p, const SeqPlace& s) {
+  using Cur = Cursor<false, NT>;
+  return s.n ? static_cast<long long>(Cur::blocks_of(s) + kUnitSteps) * Cur::tiles_of(s.n, p.g) * p.c.hkv : 0;
+}
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarpsOf[NT - 1] * 32, 1) k_cache4_attention(const AttnParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 1) k_cache4_attention(const AttnParams p) {
   using Sh = Shared4<D, NT>;
   using Cur = Cursor<false, NT>;
-  constexpr int kWarps = Sh::kWarps, kThreads = kWarps * 32, kSlots = Sh::kSlots;
+  constexpr int kThreads = kWarps * 32, kSlots = Sh::kSlots;
   constexpr int kRows = 8 * NT;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   auto& sm = *reinterpret_cast<Sh*>(smem_raw);
@@ -486,64 +510,78 @@ __global__ void __launch_bounds__(kWarpsOf[NT - 1] * 32, 1) k_cache4_attention(c
 
   // ---- the flat order: total steps, and where this warp starts
   const int per_thread = (p.c.num_seqs + kThreads - 1) / kThreads;
-  long long mine = 0;
+  longlong2 mine = make_longlong2(0, 0);
   for (int i = 0; i < per_thread; ++i) {
     const int s = threadIdx.x * per_thread + i;
     if (s < p.c.num_seqs) {
       const SeqPlace at = seq_place(p.c, s);
       if (s < kSeqs) sm.seq[s] = at;
-      mine += Cur::cost(p, at);
+      mine.x += steps_of<NT>(p, at);
+      mine.y += Cur::cost(p, at);
     }
   }
-  long long upto = mine;
+  longlong2 upto = mine;
 #pragma unroll
   for (int s = 1; s < 32; s *= 2) {
-    const long long x = __shfl_up_sync(0xffffffffu, upto, s);
-    if (lane >= s) upto += x;
+    const long long x = __shfl_up_sync(0xffffffffu, upto.x, s), y = __shfl_up_sync(0xffffffffu, upto.y, s);
+    if (lane >= s) {
+      upto.x += x;
+      upto.y += y;
+    }
   }
   if (lane == 31) sm.warp_sum[warp] = upto;
   __syncthreads();
-  long long before = 0, total = 0;
+  longlong2 before = make_longlong2(0, 0);
+  long long total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sm.warp_sum[w];
-    total += sm.warp_sum[w];
+    if (w < warp) {
+      before.x += sm.warp_sum[w].x;
+      before.y += sm.warp_sum[w].y;
+    }
+    total += sm.warp_sum[w].x;
   }
-  sm.pre[threadIdx.x] = before + upto - mine;
+  if (threadIdx.x == kThreads - 1) sm.last_blocks = mine.y;
+  sm.pre[threadIdx.x] = make_longlong2(before.x + upto.x - mine.x, before.y + upto.y - mine.y);
   __syncthreads();
-  const Cut cut(total, gridDim.x, kWarps, p.dynamic);
+  const Cut cut(total, gridDim.x, kWarps, false);  // a run is one piece
   const int used = cut.used(gridDim.x);
-  if (!p.dynamic && blockIdx.x == 0 && threadIdx.x == 0) p.head[2] = cut.workers;
-  if (warp >= used) return;
   const int run = blockIdx.x * used + warp;
-  if (!p.dynamic && lane == 0) p.open[run].parts = 0;
+  if (threadIdx.x == 0) {
+    if (blockIdx.x == 0) p.head[2] = gridDim.x;
+    p.open[blockIdx.x].parts = 0;
+  }
+  if (lane < 2) sm.ends[warp].has[lane] = false;
+  __syncwarp();
 
-  // Puts a cursor on a step of the flat order.
-  auto locate = [&](Cur& cur, long long x) {
-    const int slice = find_last(kThreads, x, [&](int s) { return sm.pre[s]; });
-    long long at = sm.pre[slice];
+  // Puts a cursor on a step of the flat order, and says how many blocks lie before it.
+  auto locate = [&](Cur& cur, long long x) -> long long {
+    const int slice = find_last(kThreads, x, [&](int s) { return sm.pre[s].x; });
+    longlong2 at = sm.pre[slice];
     int i = slice * per_thread;
-    for (long long c; x - at >= (c = Cur::cost(p, Cur::place(p, sm.seq, i))) && i + 1 < p.c.num_seqs; ++i) at += c;
+    SeqPlace s = Cur::place(p, sm.seq, i);
+    for (long long c; x - at.x >= (c = steps_of<NT>(p, s)) && i + 1 < p.c.num_seqs; s = Cur::place(p, sm.seq, ++i)) {
+      at.x += c;
+      at.y += Cur::cost(p, s);
+    }
     cur.enter(p, sm.seq, i);
-    cur.skip(x - at);
+    const long long off = x - at.x, unit = off / (cur.nb + kUnitSteps);
+    const long long block = max(0LL, off - unit * (cur.nb + kUnitSteps) - kUnitSteps);
+    cur.skip(unit * cur.nb + block);
+    return at.y + unit * cur.nb + block;
   };
 
   long long start, stop;
   cut.range(run, 0, start, stop);
-  if (start < total) {
-    Cur cc, lc;  // of the arithmetic; of the copies, which run ahead
-    locate(lc, start);
+  long long todo = 0;  // blocks of the run
+  Cur cc, lc;          // of the arithmetic; of the copies, which run ahead
+  if (warp < used && start < total) {
+    const long long end = stop < total ? locate(lc, stop) : sm.pre[kThreads - 1].y + sm.last_blocks;
+    todo = end - locate(lc, start);
     cc = lc;
-    int piece = run * cut.pieces;  // of the copies
-    long long to_load = stop - start;
-    int loaded = 0, done = 0;      // blocks
-    int ticket = 0;                // lane 0: the next piece to take
-    bool asked = false, more_pieces = p.dynamic;
-    auto ask = [&]() {
-      asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
-      if (lane == 0) ticket = atomicAdd(p.head + 1, 1);
-      asked = true;
-    };
+  }
+  if (todo > 0) {
+    long long to_load = todo;
     int load_slot = 0;
     int left = 0;                  // blocks that can be asked for without a look at anything else
     uint32_t unseen = 0;           // a bit for each slot whose block is on no page of the pool
@@ -554,26 +592,10 @@ __global__ void __launch_bounds__(kWarpsOf[NT - 1] * 32, 1) k_cache4_attention(c
     const unsigned char* values = nullptr;  // V of the block whose K went last
     const long long page_codes = static_cast<long long>(p.c.hkv) * kCodes4<D>, page_scales = static_cast<long long>(p.c.hkv) * kScales4<D>;
 
-    // The end of a unit, of a list of pages or of a piece: what comes next.  left stays 0
-    // where nothing does, and before a block that is on no page of the pool.
+    // The end of a unit or of a list of pages: what comes next.  left stays 0 where nothing
+    // does, and before a block that is on no page of the pool.
     auto refill = [&]() {
-      while (to_load == 0) {
-        if (!more_pieces) return;
-        if (!asked) ask();
-        asked = false;
-        const int j = __shfl_sync(0xffffffffu, ticket, 0);
-        const int k = 1 + j / cut.workers, w = j - (k - 1) * cut.workers;
-        more_pieces = k < cut.pieces;
-        if (!more_pieces) return;
-        long long a, z;
-        cut.range(w, k, a, z);
-        if (a >= z) continue;
-        locate(lc, a);
-        to_load = z - a;
-        piece = w * cut.pieces + k;
-        if (lane == 0) sm.piece[warp][load_slot] = piece;
-        pages_at = -1;
-      }
+      if (to_load == 0) return;
       if (lc.blk == lc.nb) {
         // heads of a sequence share its pages: a list of up to 32 serves them all
         const bool same = lc.nb <= 32 && lc.tiles == 1 && !lc.last_unit(p);
@@ -583,7 +605,6 @@ __global__ void __launch_bounds__(kWarpsOf[NT - 1] * 32, 1) k_cache4_attention(c
       k_at = p.c.k + static_cast<long long>(lc.head) * kCodes4<D> + lane * 16;
       v_at = p.c.v + static_cast<long long>(lc.head) * kCodes4<D> + lane * 16;
       s_at = p.scale_bytes + static_cast<long long>(lc.head) * kScales4<D> + lane * 16;
-      if (to_load == 1 && more_pieces && !asked) ask();  // not earlier: a slow warp must not sit on a piece
       if (pages_at != (lc.blk & ~31)) {  // a new unit, or the next 32 blocks
         const int last = lc.last_pos(p.g);
         const bool early = next_of == lc.seq && (lc.blk & ~31) == 0;
@@ -606,7 +627,7 @@ __global__ void __launch_bounds__(kWarpsOf[NT - 1] * 32, 1) k_cache4_attention(c
       }
       const uint32_t bad = __ballot_sync(0xffffffffu, pages < 0) >> (lc.blk & 31);
       const int good = min(bad ? __ffs(bad) - 1 : 32, min(lc.nb - lc.blk, 32 - (lc.blk & 31)));
-      left = static_cast<int>(min(static_cast<long long>(good), to_load > 1 && more_pieces ? to_load - 1 : to_load));
+      left = static_cast<int>(min(static_cast<long long>(good), to_load));
       to_load -= left;
     };
     // Asks for K of the next block, if there is one, and then for its V.
@@ -619,7 +640,6 @@ __global__ void __launch_bounds__(kWarpsOf[NT - 1] * 32, 1) k_cache4_attention(c
           unseen |= 1u << load_slot;
           --to_load;
           ++lc.blk;
-          ++loaded;
           load_slot = load_slot + 1 == kSlots ? 0 : load_slot + 1;
         }
       }
@@ -633,7 +653,6 @@ __global__ void __launch_bounds__(kWarpsOf[NT - 1] * 32, 1) k_cache4_attention(c
         if (lane < kScales4<D> / 16) copy16(dst + kCodes4<D>, s_at + page * page_scales);
         --left;
         ++lc.blk;
-        ++loaded;
       }
       copies_commit();
     };
@@ -653,18 +672,18 @@ __global__ void __launch_bounds__(kWarpsOf[NT - 1] * 32, 1) k_cache4_attention(c
       issue_v();
     }
 
-    int slot = 0, at_piece = run * cut.pieces;  // (the copies may be in a later piece already)
-    long long at = start;
+    int slot = 0;
     uint4 qx[NT][D / 32];  // raw query rows of cc's unit, this lane's channels
     auto fetch_q = [&]() { fetch_rows<D, NT>(p, cc.s.row0, cc.head, cc.rr0(), cc.nrows(p.g), qx); };
     fetch_q();
     while (true) {
       // ---- one unit, or the part of it that the piece has
       const bool begins = cc.blk == 0;
-      const int steps = static_cast<int>(min(static_cast<long long>(cc.nb - cc.blk), stop - at));
+      const int steps = static_cast<int>(min(static_cast<long long>(cc.nb - cc.blk), todo));
       const bool ends = cc.blk + steps == cc.nb;
       const int nrows = cc.nrows(p.g), rr0 = cc.rr0(), row0 = cc.s.row0, head = cc.head;
       const int clear = (cc.first_pos(p.g) + 1) / kBlock - cc.blk;  // blocks that every row sees whole
+      const int last_pos = cc.last_pos(p.g);
       const Rows<D, NT> rows(p, qx, cc.s.p0, rr0, nrows);
       Sums<D, NT> sums;
       sums.clear();
@@ -683,11 +702,23 @@ __global__ void __launch_bounds__(kWarpsOf[NT - 1] * 32, 1) k_cache4_attention(c
           for (int g = 0; g < D / 32; ++g) ks[g] = reinterpret_cast<const uint2*>(scales + g * kBlock)[lane >> 2];
           float s[NT][4][4];
           first_product<D, NT>(rows, block, lane, ks, s);
-          if (step < clear && common.any) {
-            quick = as_is<D, NT>(rows, sums, common, scales, lane, s, pf);
+          const bool masked = step >= clear;
+          const int key0 = (cc.blk + step) * kBlock, limit = last_pos + 1 - key0;
+          if (masked) {
+            stay_here();
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (key0 + 16 * i + 8 * (k >> 1) + (lane >> 2) > rows.pos[t][k & 1]) s[t][i][k] = -__int_as_float(0x7f800000);
+          }
+          if (common.any) {
+            quick = as_is<D, NT>(rows, sums, common, scales, lane, masked, limit, s, pf);
             if (!quick) {
-              refer<D, NT>(rows, sums, common, scales, lane, s);
-              quick = as_is<D, NT>(rows, sums, common, scales, lane, s, pf);
+              refer<D, NT>(rows, sums, common, scales, lane, limit, s);
+              quick = as_is<D, NT>(rows, sums, common, scales, lane, masked, limit, s, pf);
             }
           }
           if (!quick) {
@@ -698,7 +729,7 @@ __global__ void __launch_bounds__(kWarpsOf[NT - 1] * 32, 1) k_cache4_attention(c
               for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) slow.s[t][i][k] = s[t][i][k];
-            any_block<D, NT>(slow, warp, slot, (cc.blk + step) * kBlock, step >= clear, nrows);
+            any_block<D, NT>(slow, warp, slot, key0, masked, nrows);
             sums = slow.sums;
             common = slow.common;
           }
@@ -730,47 +761,79 @@ __global__ void __launch_bounds__(kWarpsOf[NT - 1] * 32, 1) k_cache4_attention(c
         issue_v();
         slot = slot + 1 == kSlots ? 0 : slot + 1;
       }
-      at += steps;
-      done += steps;
-      const int rest = cc.nb - cc.blk - steps;  // steps of the unit behind the piece
-      const int this_piece = at_piece;
-      const long long this_at = at;
-
+      todo -= steps;
+      const int rest = cc.nb - cc.blk - steps;  // steps of the unit behind the run
       // ---- the next unit's query rows are asked for before this one is written
-      bool more = true;
-      if (at < stop) {
-        cc.next_unit(p, sm.seq);
-      } else {
-        __syncwarp();
-        more = done != loaded;
-        if (more) {  // the piece that the copies went on to
-          at_piece = sm.piece[warp][slot];
-          const int w = at_piece / cut.pieces;
-          cut.range(w, at_piece - w * cut.pieces, at, stop);
-          locate(cc, at);
-        }
-      }
+      const bool more = todo > 0;
+      if (more) cc.next_unit(p, sm.seq);
       if (more) fetch_q();
 
       // ---- the unit's part is done: out, or into a partial
-      const size_t part_at = (static_cast<size_t>(this_piece) * 2 + (begins ? 1 : 0)) * kRows;
-      write_part<D, NT>(p, sums, head, row0, rr0, nrows, begins && ends, part_at);
-      if (begins && !ends && lane == 0) {
-        Open o = {};
-        o.first = this_piece;
-        o.parts = cut.piece_of(this_at + rest - 1) - this_piece + 1;
-        o.row0 = row0;
-        o.head = head;
-        o.nrows = nrows;
-        o.rr0 = rr0;
-        p.open[p.dynamic ? atomicAdd(p.head, 1) : this_piece] = o;
+      // (at the end of the run the ring is free for it)
+      float* part = p.part + (static_cast<size_t>(gridDim.x) * 2 + run) * kRows * D;
+      if (!more) {
+        copies_wait<0>();
+        __syncwarp();
+        part = reinterpret_cast<float*>(sm.ring[warp][0]);
+      }
+      write_part<D, NT>(p, sums, head, row0, rr0, nrows, begins && ends, part, sm.part_sum[warp][begins]);
+      if (!(begins && ends) && lane == 0) {
+        RunEnds& e = sm.ends[warp];
+        e.has[begins] = true;
+        if (!begins) e.ends = ends;
+        e.o[begins] = part;
+        e.row0[begins] = row0;
+        e.head[begins] = head;
+        e.nrows[begins] = nrows;
+        e.rr0[begins] = rr0;
+        e.last = stop + rest - 1;
       }
       if (!more) break;
     }
-    copies_wait<0>();
   }
-  // Even a call without work ends after the kernels in front of it (see the 8-bit kernel).
-  if (p.dynamic) asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---- units that the warps of this CTA share are joined, row by row
+  __syncthreads();
+  int nth = 0;
+#pragma unroll 1
+  for (int first = -1; first < used; ++first) {
+    const int kind = first >= 0;  // begun in this CTA, by run `first`, or before it
+    const int w0 = max(first, 0);
+    if (!sm.ends[w0].has[kind]) continue;
+    int m = 1;
+    bool whole = !kind && sm.ends[w0].ends;
+    while (!whole && w0 + m < used && sm.ends[w0 + m].has[0]) {
+      whole = sm.ends[w0 + m].ends;
+      ++m;
+    }
+    const RunEnds& e = sm.ends[w0];
+    const int nrows = e.nrows[kind];
+    for (int r = 0; r < nrows; ++r) {
+      if (nth++ % kWarps != warp) continue;
+      float x[D / 32];
+      const float2 sum = join_row<D>(
+          m, lane, x, [&](int k) { return sm.part_sum[w0 + k][k == 0 ? kind : 0][r]; },
+          [&](int k) { return sm.ends[w0 + k].o[k == 0 ? kind : 0] + r * D; });
+      if (kind && whole) {
+        write_o<D>(p, e.row0[1], e.head[1], e.rr0[1] + r, x, lse_of(sum.x, sum.y), lane);
+      } else {
+        const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + kind) * kRows + r;
+#pragma unroll
+        for (int v = 0; v < D / 32; ++v) p.part[at * D + lane * (D / 32) + v] = x[v];
+        if (lane == 0) p.part_sum[at] = sum;
+      }
+    }
+    if (kind && !whole && threadIdx.x == 0) {
+      Open o = {};
+      o.first = blockIdx.x;
+      o.parts = cut.piece_of(e.last) / used - blockIdx.x + 1;
+      o.row0 = e.row0[1];
+      o.head = e.head[1];
+      o.nrows = nrows;
+      o.rr0 = e.rr0[1];
+      p.open[blockIdx.x] = o;
+    }
+  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
@@ -779,7 +842,7 @@ hdp_status_t launch4(const AttnParams& p, int device, int ctas, cudaStream_t st)
   static std::atomic<bool> ready[kDevices];
   constexpr int smem = sizeof(Shared4<D, NT>);
   static_assert(smem <= 232448, "shared memory of a CTA");
-  return launch<D, NT>(k_cache4_attention<D, NT>, kWarpsOf[NT - 1], smem, ready, p, device, ctas, st);
+  return launch<D, NT>(k_cache4_attention<D, NT>, kWarps, smem, ctas, ready, p, device, ctas, st);
 }
 
 template <int D>
@@ -794,7 +857,7 @@ using namespace hdp;
 
 extern "C" hdp_status_t hdp_fourbit_attention_workspace_bytes(const hdp_fourbit_cache_t* cache, int32_t hq, size_t* bytes) {
   if (!cache || !bytes) return fail(HDP_ERR_INVALID_ARGUMENT, "hdp_fourbit_attention_workspace_bytes: NULL argument");
-  return workspace_bytes_of("hdp_fourbit_attention_workspace_bytes", kWarpsOf, cache->hkv, cache->d, hq, bytes);
+  return workspace_bytes_of("hdp_fourbit_attention_workspace_bytes", kCount, cache->hkv, cache->d, hq, bytes);
 }
 
 extern "C" hdp_status_t hdp_fourbit_attention(const hdp_fourbit_cache_t* cache, const int32_t* cu, int64_t rows,
@@ -807,7 +870,7 @@ extern "C" hdp_status_t hdp_fourbit_attention(const hdp_fourbit_cache_t* cache, 
   p.c = c;
   p.scale_bytes = c.scale_bytes;
   const bool wide = cache->d == 128;
-  return attend("hdp_fourbit_attention", kWarpsOf, p, cache->d, rows, q, hq, scale, nullptr, 0, workspace, workspace_bytes, o, lse,
+  return attend("hdp_fourbit_attention", kCount, 0, p, cache->d, rows, q, hq, scale, nullptr, 0, workspace, workspace_bytes, o, lse,
                 stream, [=](const AttnParams& a, int nt, int device, int ctas, cudaStream_t st) {
                   return wide ? launch_for<128>(a, nt, device, ctas, st)
                               : launch_for<64>(a, nt, device, ctas, st);
