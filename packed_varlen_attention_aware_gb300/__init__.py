@@ -13,6 +13,8 @@ import contextlib
 import math
 
 from .binding import (  # noqa: F401
+    _cache_rows,
+    _rotary,
     EXPORTED,
     HDP_BALANCE_DP,
     HDP_BALANCE_PP,
@@ -232,9 +234,10 @@ def cache_rows(lens, rows: int, cu=None, page_table=None, num_pages: int | None 
     import torch
 
     with _pool(stream, lens):
-        seq, pos = (torch.empty(rows, dtype=torch.int32, device=lens.device) for _ in range(2))
-        slot = None if page_table is None else torch.empty(rows, dtype=torch.int64, device=lens.device)
-    hdp_cache_rows(lens, rows, seq, pos, slot, cu=cu, page_table=page_table, num_pages=num_pages, stream=stream)
+        seq = lens.new_empty(rows, dtype=torch.int32)
+        pos = lens.new_empty(rows, dtype=torch.int32)
+        slot = None if page_table is None else lens.new_empty(rows, dtype=torch.int64)
+    _cache_rows(lens, rows, seq, pos, slot, cu, page_table, num_pages, stream)
     _in_use(stream, None, lens, cu, page_table)
     return seq, pos, slot
 
@@ -270,17 +273,11 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = No
 
 
 def _turned(q, k, position, freqs, neighbours, backward, factor, inplace, stream):
-    import torch
-
-    like = q if q is not None else k
-    if inplace:
-        oq, ok = q, k
-    else:
-        with _pool(stream, like):
-            oq, ok = (None if x is None else torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
-    hdp_rotary(q, k, position, freqs, oq, ok, neighbours=neighbours, backward=backward, factor=factor, stream=stream)
+    out = (q, k) if inplace else (None, None)
+    with _pool(stream, q if q is not None else k):
+        out = _rotary(q, k, position, freqs, *out, neighbours, backward, factor, stream)
     _in_use(stream, None, q, k, position, freqs)
-    return oq, ok
+    return out
 
 
 def rotary(q, k, position, freqs, neighbours: bool = False, factor: float = 1.0, inplace: bool = False, stream=None):

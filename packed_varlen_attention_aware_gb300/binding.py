@@ -701,6 +701,17 @@ def hdp_cache_rows(lens, rows: int, sequence, position, slot, cu=None, page_tabl
     import torch
 
     dev = lens.get_device()
+    for t, name, dtype in ((sequence, "sequence", torch.int32), (position, "position", torch.int32), (slot, "slot", torch.int64)):
+        if t is not None:
+            _tensor(t, name, dtype, (rows,), dev)
+    _cache_rows(lens, rows, sequence, position, slot, cu, page_table, num_pages, stream)
+
+
+def _cache_rows(lens, rows, sequence, position, slot, cu, page_table, num_pages, stream):
+    """The same for outputs that are known to be right."""
+    import torch
+
+    dev = lens.get_device()
     n = lens.shape[0] if lens.dim() == 1 else -1
     _tensor(lens, "lens", torch.int32, (n,), dev)
     if cu is not None:
@@ -713,9 +724,6 @@ def hdp_cache_rows(lens, rows: int, sequence, position, slot, cu=None, page_tabl
         _tensor(page_table, "page_table", torch.int32, (n, columns), dev)
         if num_pages is None:
             raise ValueError("num_pages, the pages of the pool, goes with a page table")
-    for t, name, dtype in ((sequence, "sequence", torch.int32), (position, "position", torch.int32), (slot, "slot", torch.int64)):
-        if t is not None:
-            _tensor(t, name, dtype, (rows,), dev)
     _run(dev, "hdp_cache_rows", stream, None if page_table is None else page_table.data_ptr(), lens.data_ptr(),
          None if cu is None else cu.data_ptr(), n, columns, num_pages or 0, rows,
          None if sequence is None else sequence.data_ptr(), None if position is None else position.data_ptr(),
@@ -727,13 +735,12 @@ def hdp_cache_rows(lens, rows: int, sequence, position, slot, cu=None, page_tabl
 _rotary_types = None
 
 
-def _rotary_type(dtype):
+def _rotary_kinds():
     global _rotary_types
-    if _rotary_types is None:
-        import torch
+    import torch
 
-        _rotary_types = {torch.bfloat16: HDP_TYPE_BF16, torch.float16: HDP_TYPE_FP16, torch.float32: HDP_TYPE_FP32}
-    return _rotary_types.get(dtype)
+    _rotary_types = {torch.bfloat16: HDP_TYPE_BF16, torch.float16: HDP_TYPE_FP16, torch.float32: HDP_TYPE_FP32}
+    return _rotary_types
 
 
 def _apart(x):
@@ -747,41 +754,59 @@ def _apart(x):
     return True
 
 
-def _rotary_side(x, out, name, like):
-    """hdp_rotary_rows_t of x [rows][heads][d] turned into out, as bytes."""
-    if x.dim() != 3 or x.dtype is not like.dtype or x.get_device() != like.get_device() or not x.is_cuda:
-        raise TypeError(f"{name} must be a {like.dtype} tensor [rows][heads][d] on a CUDA device")
-    if x.shape[0] != like.shape[0] or x.shape[2] != like.shape[2]:
+def _rotary_side(x, out, name, dtype, dev, rows, d):
+    """hdp_rotary_rows_t of x [rows][heads][d] turned into out (None: a new tensor), as bytes, and out."""
+    if x.dtype is not dtype or x.get_device() != dev or x.dim() != 3:
+        raise TypeError(f"{name} must be a {dtype} tensor [rows][heads][d] on CUDA device {dev}")
+    shape, a = x.shape, x.stride()
+    heads = shape[1]
+    if shape[0] != rows or shape[2] != d:
         raise ValueError(f"{name} must have the rows and channels of the others")
-    if out.dtype is not x.dtype or out.shape != x.shape or out.get_device() != x.get_device():
-        raise ValueError(f"the output of {name} must be a tensor like it")
-    a, b = x.stride(), out.stride()
-    if x.shape[2] > 1 and (a[2] != 1 or b[2] != 1):
+    if a[2] != 1 and d > 1:
         raise ValueError(f"the channels of {name} must be contiguous")
-    return _ROTARY_FORMAT.pack(x.data_ptr(), out.data_ptr(), a[0], a[1], b[0], b[1], x.shape[1])
+    if out is None:
+        out = x.new_empty(shape)
+        return _ROTARY_FORMAT.pack(x.data_ptr(), out.data_ptr(), a[0], a[1], heads * d, d, heads), out
+    if out.dtype is not dtype or out.shape != shape or out.get_device() != dev:
+        raise ValueError(f"the output of {name} must be a tensor like it")
+    b = out.stride()
+    if (b[2] != 1 and d > 1) or not _apart(out):
+        raise ValueError(f"the output of {name} must have contiguous channels, and rows and heads that do not overlap")
+    return _ROTARY_FORMAT.pack(x.data_ptr(), out.data_ptr(), a[0], a[1], b[0], b[1], heads), out
+
+
+def _rotary(q, k, position, freqs, q_out, k_out, neighbours, backward, factor, stream):
+    """Turns the rows of q and k into q_out and k_out, or where these are None into new tensors; returns them."""
+    import torch
+
+    like = q if q is not None else k
+    if like is None or not like.is_cuda or like.dim() != 3:
+        raise TypeError("q and k must be CUDA tensors [rows][heads][d], and one of them be given")
+    dtype = like.dtype
+    kind = (_rotary_types or _rotary_kinds()).get(dtype)
+    if kind is None:
+        raise TypeError("q and k must be bfloat16, float16 or float32")
+    dev = like.get_device()
+    rows, _, d = like.shape
+    half = freqs.shape[0] if freqs.dim() == 1 else -1
+    _tensor(position, "position", torch.int32, (rows,), dev)
+    _tensor(freqs, "freqs", torch.float64, (half,), dev)
+    sq = sk = None
+    if q is not None:
+        sq, q_out = _rotary_side(q, q_out, "q", dtype, dev, rows, d)
+    if k is not None:
+        sk, k_out = _rotary_side(k, k_out, "k", dtype, dev, rows, d)
+    _run(dev, "hdp_rotary", stream, sq, sk, rows, d, kind, position.data_ptr(), freqs.data_ptr(), 2 * half,
+         (HDP_ROTARY_NEIGHBOURS if neighbours else 0) | (HDP_ROTARY_BACKWARD if backward else 0), factor)
+    return q_out, k_out
 
 
 def hdp_rotary(q, k, position, freqs, q_out, k_out, neighbours: bool = False, backward: bool = False, factor: float = 1.0,
                stream=None):
     """Turns the rows of q and k (one may be None) [rows][heads][d] into q_out and k_out, which may be q and k."""
-    import torch
-
-    like = q if q is not None else k
-    if like is None or like.dim() != 3 or not like.is_cuda:
-        raise TypeError("q and k must be CUDA tensors [rows][heads][d], and one of them be given")
-    kind = _rotary_type(like.dtype)
-    if kind is None:
-        raise TypeError("q and k must be bfloat16, float16 or float32")
-    dev, rows = like.get_device(), like.shape[0]
-    _tensor(position, "position", torch.int32, (rows,), dev)
-    _tensor(freqs, "freqs", torch.float64, (freqs.numel(),), dev)
-    for x, out in ((q, q_out), (k, k_out)):
-        if x is not None and not _apart(out):
-            raise ValueError("rows and heads of an output must not overlap")
-    sq = None if q is None else _rotary_side(q, q_out, "q", like)
-    sk = None if k is None else _rotary_side(k, k_out, "k", like)
-    _run(dev, "hdp_rotary", stream, sq, sk, rows, like.shape[2], kind, position.data_ptr(), freqs.data_ptr(),
-         2 * freqs.numel(), (HDP_ROTARY_NEIGHBOURS if neighbours else 0) | (HDP_ROTARY_BACKWARD if backward else 0), factor)
+    if (q is not None and q_out is None) or (k is not None and k_out is None):
+        raise TypeError("q and k need outputs")
+    _rotary(q, k, position, freqs, q_out, k_out, neighbours, backward, factor, stream)
 
 
 # ---------------------------------------------------------------- cost models (host arithmetic)

@@ -265,12 +265,15 @@ __global__ void __launch_bounds__(kThreads) k_cache4_append_one(const Cache4View
   }
 }
 
+// Everything that a block has is asked for before anything of it is used: 16 words of codes
+// and a word of scales a thread.
 template <int D>
 __global__ void __launch_bounds__(kThreads) k_cache4_read(const Cache4View c, uint4* __restrict__ k, uint4* __restrict__ v) {
   constexpr int kLanes = D / 8;
   constexpr int kRows = kThreads / kLanes;
   constexpr int kPasses = kBlock / kRows;
   __shared__ uint32_t s_word[kBlock][kLanes + 1];
+  __shared__ uint32_t s_scale[kScales4<D> / 4];
   Touched t;
   const bool any = touched_block(c, blockIdx.x, t);
   const int head = blockIdx.y;
@@ -281,28 +284,36 @@ __global__ void __launch_bounds__(kThreads) k_cache4_read(const Cache4View c, ui
   if (!any) return;
   const int page = page_of(c, t.seq, t.block);
   const size_t ph = static_cast<size_t>(max(page, 0)) * c.hkv + head;
-  const uint8_t* scales = c.scale_bytes + ph * kScales4<D>;
-  if (page >= 0 && threadIdx.x < VPart<D>::kParts) {
+  const int l = threadIdx.x % kLanes, mine = threadIdx.x / kLanes;
+  uint32_t word[kPasses];
+  if (page >= 0) {
     const VPart<D> part;
     uint32_t w[8];
+    if (threadIdx.x < VPart<D>::kParts) {
 #pragma unroll
-    for (int r = 0; r < 8; ++r) w[r] = __ldg(reinterpret_cast<const uint32_t*>(c.v + ph * kCodes4<D> + part.byte(r)));
-    transpose8(w);
+      for (int r = 0; r < 8; ++r) w[r] = __ldg(reinterpret_cast<const uint32_t*>(c.v + ph * kCodes4<D> + part.byte(r)));
+    }
+    const uint8_t* kc = c.k + ph * kCodes4<D> + D / 8 * (l & 3) + 4 * (l >> 2);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_word[part.token(i)][part.word()] = w[i];
+    for (int p = 0; p < kPasses; ++p) word[p] = __ldg(reinterpret_cast<const uint32_t*>(kc + (p * kRows + mine) * (D / 2)));
+    if (threadIdx.x < kScales4<D> / 4)
+      s_scale[threadIdx.x] = __ldg(reinterpret_cast<const uint32_t*>(c.scale_bytes + ph * kScales4<D>) + threadIdx.x);
+    if (threadIdx.x < VPart<D>::kParts) {
+      transpose8(w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s_word[part.token(i)][part.word()] = w[i];
+    }
   }
   __syncthreads();
-  const int l = threadIdx.x % kLanes, mine = threadIdx.x / kLanes;
-  const uint8_t* kc = c.k + ph * kCodes4<D> + D / 8 * (l & 3) + 4 * (l >> 2);
+  const uint8_t* scales = reinterpret_cast<const uint8_t*>(s_scale);
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int token = p * kRows + mine, r = token - t.first;
     if (r < 0 || r >= t.count) continue;
     uint4 x = make_uint4(0, 0, 0, 0), y = x;
     if (page >= 0) {
-      x = values_of(__ldg(reinterpret_cast<const uint32_t*>(kc + token * (D / 2))),
-                    scale_value(__ldg(scales + (l >> 2) * kBlock + scale_place(token))));
-      y = values_of(s_word[token][l], scale_value(__ldg(scales + (D / 32) * kBlock + scale_place(token))));
+      x = values_of(word[p], scale_value(scales[(l >> 2) * kBlock + scale_place(token)]));
+      y = values_of(s_word[token][l], scale_value(scales[(D / 32) * kBlock + scale_place(token)]));
     }
     const size_t at = ((static_cast<size_t>(t.row) + r) * c.hkv + head) * kLanes + l;
     k[at] = x;

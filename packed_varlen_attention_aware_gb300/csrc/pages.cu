@@ -13,11 +13,14 @@
 // The work is a few bytes for each sequence and page moved; latency bounds it: a
 // launch, the lengths, the scan, one or two rounds of dependent loads.  One CTA
 // does it while the table is small; else a cluster of 8 shares the moves, each
-// CTA scanning all sequences for itself (a scan of 4,096 takes less than handing
-// its results on would).  256 sequences, 4 pages moved: see hdp_cache_rows below.
+// CTA scanning all sequences for itself (a scan of 2,048 takes less than handing
+// its results on would).  Measured (one GB300, in a captured graph, by one CTA and
+// by the cluster): 256 sequences, 4 pages taken 6.5 and 6.5 us; 64 sequences take
+// 8,556 pages 13.5 and 8.0; one takes 32,768 16.7 and 6.9.
 //
 // hdp_cache_rows.  16 bytes written for each row: a warp has 128 consecutive
 // rows, finds the first one's sequence together, and each lane walks on from it.
+// 256 rows 3.3 us, 2M rows 9.4 (33.6 MB).
 #include <cooperative_groups.h>
 
 #include <string>
@@ -29,7 +32,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 1024;              // 32 warps: scan() has a lane for each
 constexpr int kEach = 2;                    // sequences of a thread
 constexpr int kChunk = kThreads * kEach;    // sequences scanned at once
 constexpr int kCtas = 8;                    // of a cluster
@@ -64,6 +67,7 @@ __device__ __forceinline__ Need need_of(const Assign& p, int i) {
 
 // Exclusive sums of x over the CTA's threads, in their order, and the total.
 __device__ __forceinline__ long long scan(long long x, long long& total, long long* warp_sums) {
+  static_assert(kThreads == 1024, "a lane for each warp");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long run = x;
 #pragma unroll

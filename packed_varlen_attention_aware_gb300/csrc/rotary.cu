@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const Rotary p) {
   const int g = threadIdx.x / group, j = threadIdx.x - g * group;
   if (g >= groups) return;
   const int all = p.heads[0] + p.heads[1], units = n * all;
-#pragma unroll 2
+#pragma unroll 4
   for (int u = g; u < units; u += groups) {
     const int t = u / all;
     int h = u - t * all;
