@@ -14,7 +14,13 @@
 //   Sharing.  A token's cosines and sines serve all its heads: a CTA works them out
 //   for a tile of tokens, one pair a thread, and its threads then go over the
 //   tile's (token, head) units, 16 bytes of each half of a pair at a time.
-//   Rows whose layout does not allow 16 bytes go by one pair of elements a thread.
+//   Where only rot does not allow 16 bytes of each half, a lane has 16 bytes of a head and
+//   looks for their partners in it or in shared memory; other rows go by two elements or
+//   one at a time.
+//
+// Measured: 40,121 rows of 40 heads of 128 bf16, 125 us, 0.97 of the copy rate; 131,072 of
+// 40 heads with 64 of 128 channels turned, the gradient, 417 us, 0.95; 131,072 of 10
+// heads, as many turned, 126 us, 0.78: there a token's angles count.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -28,7 +34,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMostD = 256;
-constexpr int kMostTile = 8;  // tokens of a CTA
+constexpr int kMostTile = 16;  // tokens of a CTA
 
 struct RotaryTensor {
   const char* in;
@@ -76,37 +82,55 @@ __device__ __forceinline__ void put(T* p, const Vec<T, V>& x) {
   *reinterpret_cast<Vec<T, V>*>(p) = x;
 }
 
-template <class T, int V, bool NEIGHBOURS>
-__global__ void __launch_bounds__(kThreads) k_rotary(const Rotary p) {
-  __shared__ __align__(16) float s_cos[kMostTile * kMostD / 2];
-  __shared__ __align__(16) float s_sin[kMostTile * kMostD / 2];
-  __shared__ int s_pos[kMostTile];
-  const int half = p.rot / 2;
-  const long long row0 = static_cast<long long>(blockIdx.x) * p.tile;
-  const int n = static_cast<int>(min(static_cast<long long>(p.tile), p.rows - row0));
+// Cosines, sines and positions of a tile.
+extern __shared__ __align__(16) float s_angles[];
 
-  for (int x = threadIdx.x; x < n * half; x += kThreads) {
-    const int t = x / half, i = x - t * half;
-    const int at = __ldg(p.pos + row0 + t);
+int shared_bytes(const Rotary& p) { return p.tile * (p.rot + 1) * 4; }
+
+// Positions of the tile's tokens, and cosines and sines of their pairs.
+__device__ __forceinline__ void angles(const Rotary& p, long long row0, int n, float* s_cos, float* s_sin, int* s_pos) {
+  const int half = p.rot / 2, tokens = kThreads / half;  // at a time
+  const int t0 = threadIdx.x / half, i = threadIdx.x - t0 * half;
+  if (t0 < tokens && t0 < n) {
+    int at = __ldg(p.pos + row0 + t0);
     double turn = __ldg(p.freqs + i) * 0.15915494309189535;  // 1 / 2 pi
     turn -= floor(turn);
     const unsigned long long step = static_cast<unsigned long long>(turn * 18446744073709551616.0);
-    const unsigned long long fraction = step * static_cast<unsigned long long>(static_cast<long long>(at));
-    float s, c;
-    sincospif(__ll2float_rn(static_cast<long long>(fraction)) * 1.0842021724855044e-19f, &s, &c);  // 2^-63
-    s_cos[x] = c * p.factor;
-    s_sin[x] = s * p.factor * p.sign;
-    if (i == 0) s_pos[t] = at;
+    for (int t = t0, now; t < n; t += tokens) {
+      now = at;
+      if (t + tokens < n) at = __ldg(p.pos + row0 + t + tokens);
+      const unsigned long long fraction = step * static_cast<unsigned long long>(static_cast<long long>(now));
+      float s, c;
+      sincospif(__ll2float_rn(static_cast<long long>(fraction)) * 1.0842021724855044e-19f, &s, &c);  // 2^-63
+      s_cos[t * half + i] = c * p.factor;
+      s_sin[t * half + i] = s * p.factor * p.sign;
+      if (i == 0) s_pos[t] = now;
+    }
   }
   __syncthreads();
+}
+
+// A thread has V pairs of a unit, W elements at a time: W = V, but for one pair of
+// neighbours, whose two elements may be one access (W = 2).
+template <class T, int V, int W, bool NEIGHBOURS>
+__global__ void __launch_bounds__(kThreads) k_rotary(const Rotary p) {
+  const int half = p.rot / 2;
+  float* s_cos = s_angles;
+  float* s_sin = s_angles + p.tile * half;
+  int* s_pos = reinterpret_cast<int*>(s_angles + 2 * p.tile * half);
+  const long long row0 = static_cast<long long>(blockIdx.x) * p.tile;
+  const int n = static_cast<int>(min(static_cast<long long>(p.tile), p.rows - row0));
+  angles(p, row0, n, s_cos, s_sin, s_pos);
 
   // A unit is one head of one token: `pairs` threads with V pairs each, then those that copy.
-  const int pairs = half / V, group = pairs + (p.copy ? (p.d - p.rot + 2 * V - 1) / (2 * V) : 0);
+  const int pairs = half / V, group = pairs + (p.copy ? (p.d - p.rot + 2 * W - 1) / (2 * W) : 0);
   const int groups = kThreads / group;
   const int g = threadIdx.x / group, j = threadIdx.x - g * group;
   if (g >= groups) return;
   const int all = p.heads[0] + p.heads[1], units = n * all;
-#pragma unroll 4
+  // Other warps hide a unit's latency better than its neighbours do: unrolled by four, 131,072
+  // rows of 40 heads with half of their channels turned took 471 us, not 417.
+#pragma unroll 1
   for (int u = g; u < units; u += groups) {
     const int t = u / all;
     int h = u - t * all;
@@ -116,7 +140,13 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const Rotary p) {
     const RotaryTensor& x = p.x[second];
     const T* in = reinterpret_cast<const T*>(x.in) + (row0 + t) * x.in_row + h * x.in_head;
     T* out = reinterpret_cast<T*>(x.out) + (row0 + t) * x.out_row + h * x.out_head;
-    if (j < pairs) {
+    if (j < pairs && W == 2 * V) {
+      Vec<T, W> a = get<T, W>(in + 2 * j);
+      const float c = s_cos[t * half + j], s = s_sin[t * half + j], y0 = to_float(a.v[0]), y1 = to_float(a.v[W - 1]);
+      a.v[0] = from_float<T>(turned(y0, c, -y1, s));
+      a.v[W - 1] = from_float<T>(turned(y1, c, y0, s));
+      put(out + 2 * j, a);
+    } else if (j < pairs) {
       const int a0 = NEIGHBOURS ? 2 * V * j : V * j, b0 = NEIGHBOURS ? a0 + V : half + V * j;
       Vec<T, V> a = get<T, V>(in + a0), b = get<T, V>(in + b0);
       const float* cos = s_cos + t * half + V * j;
@@ -141,25 +171,103 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const Rotary p) {
       put(out + a0, a);
       put(out + b0, b);
     } else {
-      const int c0 = p.rot + (j - pairs) * 2 * V;
-      put(out + c0, get<T, V>(in + c0));
-      if (c0 + V < p.d) put(out + c0 + V, get<T, V>(in + c0 + V));
+      const int c0 = p.rot + (j - pairs) * 2 * W;
+      put(out + c0, get<T, W>(in + c0));
+      if (c0 + W < p.d) put(out + c0 + W, get<T, W>(in + c0 + W));
     }
   }
 }
 
-template <class T, int V>
-void launch(const Rotary& p, bool neighbours, cudaStream_t st) {
-  const unsigned ctas = static_cast<unsigned>((p.rows + p.tile - 1) / p.tile);
-  if (neighbours) k_rotary<T, V, true><<<ctas, kThreads, 0, st>>>(p);
-  else k_rotary<T, V, false><<<ctas, kThreads, 0, st>>>(p);
+// Rows that allow 16 bytes but for rot: a unit is whole 16-byte pieces of a head, a lane
+// each.  Neighbours are in one piece; halves are found in shared memory, where the warp
+// puts its pieces.  Channels behind rot keep their bits.
+template <class T, bool NEIGHBOURS>
+__global__ void __launch_bounds__(kThreads) k_rotary_pieces(const Rotary p) {
+  constexpr int V = 16 / sizeof(T);
+  __shared__ __align__(16) T s_x[NEIGHBOURS ? 1 : kThreads * V];
+  const int half = p.rot / 2;
+  float* s_cos = s_angles;
+  float* s_sin = s_angles + p.tile * half;
+  int* s_pos = reinterpret_cast<int*>(s_angles + 2 * p.tile * half);
+  const long long row0 = static_cast<long long>(blockIdx.x) * p.tile;
+  const int n = static_cast<int>(min(static_cast<long long>(p.tile), p.rows - row0));
+  angles(p, row0, n, s_cos, s_sin, s_pos);
+
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int pieces = p.d / V, each = 32 / pieces;  // of a unit; units of a warp
+  const int mine = lane / pieces, j = lane - mine * pieces;
+  const int all = p.heads[0] + p.heads[1], units = n * all;
+  T* x0 = s_x + (NEIGHBOURS ? 0 : (warp * 32 + mine * pieces) * V);  // the unit's channels
+  for (int u0 = warp * each; u0 < units; u0 += kThreads / 32 * each) {
+    const int u = u0 + mine;
+    const bool on = mine < each && u < units && s_pos[u / all] >= 0 && (p.copy || j * V < p.rot);
+    const int t = u / all;
+    int h = u - t * all;
+    const bool second = h >= p.heads[0];
+    if (second) h -= p.heads[0];
+    const RotaryTensor& x = p.x[second];
+    Vec<T, V> y;
+    if (on) y = get<T, V>(reinterpret_cast<const T*>(x.in) + (row0 + t) * x.in_row + h * x.in_head + j * V);
+    if constexpr (!NEIGHBOURS) {
+      __syncwarp();
+      if (on) put(x0 + j * V, y);
+      __syncwarp();
+    }
+    if (!on) continue;
+    const float* cos = s_cos + t * half;
+    const float* sin = s_sin + t * half;
+    if constexpr (NEIGHBOURS) {
+#pragma unroll
+      for (int k = 0; k < V; k += 2) {
+        const int i = (j * V + k) / 2;
+        if (i >= half) continue;
+        const float c = cos[i], s = sin[i], y0 = to_float(y.v[k]), y1 = to_float(y.v[k + 1]);
+        y.v[k] = from_float<T>(turned(y0, c, -y1, s));
+        y.v[k + 1] = from_float<T>(turned(y1, c, y0, s));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int ch = j * V + k;
+        if (ch >= p.rot) continue;
+        const bool up = ch >= half;
+        const int i = up ? ch - half : ch;
+        const float other = to_float(x0[up ? i : ch + half]);
+        y.v[k] = from_float<T>(turned(to_float(y.v[k]), cos[i], up ? other : -other, sin[i]));
+      }
+    }
+    put(reinterpret_cast<T*>(x.out) + (row0 + t) * x.out_row + h * x.out_head + j * V, y);
+  }
 }
 
+template <class T, int V, int W, bool NEIGHBOURS>
+void launch(const Rotary& p, cudaStream_t st) {
+  k_rotary<T, V, W, NEIGHBOURS><<<static_cast<unsigned>((p.rows + p.tile - 1) / p.tile), kThreads, shared_bytes(p), st>>>(p);
+}
+
+// `bits`: of addresses and strides, `lengths`: of rot / 2 and what is copied, in bytes: an
+// access of a size needs both to be multiples of it, pieces need the former only.  Measured
+// on 4,687 rows of 72 heads of 64 bf16 (12.7 us at the copy rate): 30 channels turned, by
+// pieces 25 us (neighbours) and 37 (halves), by two elements 39 (neighbours), one at a time
+// 47 and 51; 36 channels, halves, by two elements 29 us, by pieces 38.
 template <class T>
-void launch_for(const Rotary& p, int bytes, bool neighbours, cudaStream_t st) {
+void launch_for(const Rotary& p, uintptr_t bits, uintptr_t lengths, bool neighbours, cudaStream_t st) {
   constexpr int wide = 16 / sizeof(T);
-  if (bytes >= 16) launch<T, wide>(p, neighbours, st);
-  else launch<T, 1>(p, neighbours, st);
+  const int two = 2 * sizeof(T);
+  const unsigned ctas = static_cast<unsigned>((p.rows + p.tile - 1) / p.tile);
+  const bool pieces = !(bits & 15) && p.d % wide == 0 && p.d / wide <= 32;
+  if (!((bits | lengths) & 15)) {
+    if (neighbours) launch<T, wide, wide, true>(p, st);
+    else launch<T, wide, wide, false>(p, st);
+  } else if (neighbours) {
+    if (pieces) k_rotary_pieces<T, true><<<ctas, kThreads, shared_bytes(p), st>>>(p);
+    else if (bits % two == 0 && (!p.copy || (p.d - p.rot) % 2 == 0)) launch<T, 1, 2, true>(p, st);
+    else launch<T, 1, 1, true>(p, st);
+  } else {
+    if ((bits | lengths) % two == 0) launch<T, 2, 2, false>(p, st);
+    else if (pieces) k_rotary_pieces<T, false><<<ctas, kThreads, shared_bytes(p), st>>>(p);
+    else launch<T, 1, 1, false>(p, st);
+  }
 }
 
 }  // namespace
@@ -183,7 +291,7 @@ extern "C" hdp_status_t hdp_rotary(const hdp_rotary_rows_t* q, const hdp_rotary_
   const int size = type == HDP_TYPE_FP32 ? 4 : 2;
   const bool neighbours = flags & HDP_ROTARY_NEIGHBOURS;
   Rotary p = {};
-  uintptr_t bits = 0;  // of everything that 16-byte accesses need to be a multiple of 16
+  uintptr_t bits = 0;  // of addresses and strides in bytes
   const hdp_rotary_rows_t* both[2] = {q, k};
   for (int i = 0; i < 2; ++i) {
     const hdp_rotary_rows_t* x = both[i];
@@ -205,8 +313,8 @@ extern "C" hdp_status_t hdp_rotary(const hdp_rotary_rows_t* q, const hdp_rotary_
   if (!position || !freqs) return fail(HDP_ERR_INVALID_ARGUMENT, name + "position or freqs is NULL");
   if (reinterpret_cast<uintptr_t>(freqs) & 7) return fail(HDP_ERR_INVALID_ARGUMENT, name + "freqs must be 8-byte aligned");
   p.copy = p.copy && rot < d;
-  bits |= static_cast<uintptr_t>(rot / 2) * size;
-  if (p.copy) bits |= static_cast<uintptr_t>(d - rot) * size;
+  uintptr_t lengths = static_cast<uintptr_t>(rot / 2) * size;
+  if (p.copy) lengths |= static_cast<uintptr_t>(d - rot) * size;
   p.pos = position;
   p.freqs = freqs;
   p.rows = static_cast<int>(rows);
@@ -214,12 +322,16 @@ extern "C" hdp_status_t hdp_rotary(const hdp_rotary_rows_t* q, const hdp_rotary_
   p.rot = rot;
   p.factor = factor;
   p.sign = flags & HDP_ROTARY_BACKWARD ? -1.f : 1.f;
-  p.tile = rows <= 4 * 152 ? 1 : 4;
-  const int bytes = bits & 15 ? size : 16;
+  // Tokens of a CTA: as many as make 1,280 accesses of 16 bytes of each half, and as leave
+  // four CTAs for each SM.  Measured with 1, 2, 4, 8, 16: 40,121 rows of 40 heads of 128,
+  // 160, 135, 125, 127, 130 us; 50,000 of 20, 137, 106, 88, 81, 85; 131,072 of 10, half of their channels turned,
+  // 317, 200, 166, 138, 126; 608 of 40, 4.6, 4.6, 5.1, 7.4, 12.
+  const int64_t accesses = static_cast<int64_t>(p.heads[0] + p.heads[1]) * (((p.copy ? d : rot) * size + 31) / 32);
+  for (p.tile = 1; p.tile < kMostTile && p.tile * accesses < 1280 && rows > 4 * 152 * p.tile;) p.tile *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (type == HDP_TYPE_BF16) launch_for<__nv_bfloat16>(p, bytes, neighbours, st);
-  else if (type == HDP_TYPE_FP16) launch_for<__half>(p, bytes, neighbours, st);
-  else launch_for<float>(p, bytes, neighbours, st);
+  if (type == HDP_TYPE_BF16) launch_for<__nv_bfloat16>(p, bits, lengths, neighbours, st);
+  else if (type == HDP_TYPE_FP16) launch_for<__half>(p, bits, lengths, neighbours, st);
+  else launch_for<float>(p, bits, lengths, neighbours, st);
   note_launch();
   HDP_CUDA_TRY(cudaGetLastError());
   return HDP_OK;

@@ -221,6 +221,32 @@ def test_rows_at_any_alignment_turn_alike(dtype):
         assert none is None and torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("neighbours", [False, True])
+@pytest.mark.parametrize("d,rot,pitch,offset", [(64, 48, 66, 0), (64, 46, 66, 2), (64, 36, 64, 0), (128, 6, 136, 0), (128, 126, 128, 0), (7, 6, 8, 0), (250, 250, 250, 0)])
+def test_every_way_through_a_head_turns_alike(dtype, neighbours, d, rot, pitch, offset):
+    """By 16 bytes, pieces, two elements and one, in place and not; infinities behind rot stay, and what lies between
+    rows is left alone."""
+    rng = np.random.default_rng(rot)
+    whole = torch.tensor(rng.normal(size=21 * 5 * pitch + offset)).to(dtype).cuda()
+    x = whole[offset:].view(21, 5, pitch)[:, :, :d]
+    if rot < d:
+        x[:, :, rot::3] = float("inf")
+    before = whole.clone()
+    f = torch.tensor(np.exp(-rng.uniform(0, 9, rot // 2)), device="cuda")
+    pos = rng.integers(0, 9999, 21)
+    a, b = pkg.rotary(x[:, :4], x[:, 4:], _i32(pos), f, neighbours=neighbours, factor=0.75)
+    assert torch.equal(whole, before)
+    for got, src in ((a, x[:, :4]), (b, x[:, 4:])):
+        _turn_check(got[..., :rot], src[..., :rot], pos, f.cpu().numpy(), neighbours, False, 0.75)
+        assert torch.equal(got[..., rot:], src[..., rot:])
+    pkg.rotary(x[:, :4], x[:, 4:], _i32(pos), f, neighbours=neighbours, factor=0.75, inplace=True)
+    assert torch.equal(x, torch.cat((a, b), 1))
+    between = torch.ones_like(whole, dtype=torch.bool)
+    between[offset:].view(21, 5, pitch)[:, :, :d] = False
+    assert torch.equal(whole[between], before[between])
+
+
 def test_rows_at_negative_positions_and_other_rows_between_are_left_alone():
     rng = np.random.default_rng(6)
     x = torch.tensor(rng.normal(size=(9, 6, 64))).to(torch.bfloat16).cuda()
