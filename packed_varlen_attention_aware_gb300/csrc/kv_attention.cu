@@ -620,7 +620,7 @@ extern "C" hdp_status_t hdp_cache_attention(const hdp_cache_t* cache, const int3
   if (r != HDP_OK) return r;
   const bool i8 = cache->format == HDP_CACHE_INT8, wide = cache->d == 128;
   return attend("hdp_cache_attention", kCount, kWarps, p, cache->d, rows, q, hq, scale, blocks, count, workspace, workspace_bytes, o, lse,
-                stream, [=](const AttnParams& a, int nt, int device, int ctas, cudaStream_t st) {
+                stream, [=](const AttnParams& a, int nt, int device, int, int ctas, cudaStream_t st) {
                   if (wide)
                     return i8 ? launch_for<128, HDP_CACHE_INT8>(a, nt, device, ctas, st)
                               : launch_for<128, HDP_CACHE_E4M3>(a, nt, device, ctas, st);

@@ -46,6 +46,7 @@ struct AttnParams {
   Open* open;        // [pieces]: one for each piece, or, with a counter, as they come
   int* head;         // [0] entries of open (dynamic), [1] next ticket, [2] entries of open (static)
   const uint8_t* scale_bytes;  // of a 4-bit cache
+  bool alone;                  // a CTA of its kernel has a whole unit
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -657,7 +658,7 @@ hdp_status_t launch_early(void (*kernel)(T...), dim3 grid, int threads, int smem
   return HDP_OK;
 }
 
-// Launches `kernel` (`warps` a CTA, `smem` bytes) and the join of its pieces behind it;
+// Launches `kernel` (`warps` a CTA, `smem` bytes) and the join of its pieces, if any, behind it;
 // `ready`: the devices on which the kernel may have that much.
 template <int D, int NT>
 hdp_status_t launch(void (*kernel)(AttnParams), int warps, int smem, int pieces, std::atomic<bool> (&ready)[kDevices],
@@ -679,6 +680,7 @@ hdp_status_t launch(void (*kernel)(AttnParams), int warps, int smem, int pieces,
     note_launch();
     HDP_CUDA_TRY(cudaGetLastError());
   }
+  if (pieces == 0) return HDP_OK;
   return launch_early(k_cache_attention_join<D, NT>, dim3(ctas), kJoinWarps * 32, 0, st, p, pieces);
 }
 
@@ -735,7 +737,7 @@ hdp_status_t attend(const char* entry, const PartCount& count_of, int hand_out, 
   // Handing out the ends of runs costs one more small launch: from 16 steps a
   // warp on, where the runs' ends are more than a step.
   p.dynamic = hand_out > 0 && steps >= 16.0 * hand_out * sms;
-  return launch_with(p, nt, device, ctas, static_cast<cudaStream_t>(stream));
+  return launch_with(p, nt, device, sms, ctas, static_cast<cudaStream_t>(stream));
 }
 
 // Bytes of the workspace.

@@ -513,81 +513,95 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_cache4_attention(const AttnP
   asm volatile("mov.u32 %0, %%tid.x;" : "=r"(thread));
   const int warp = thread >> 5, lane = thread & 31;
 
-  // ---- the flat order: total steps, and where this warp starts
-  const int per_thread = (p.c.num_seqs + kThreads - 1) / kThreads;
-  longlong2 mine = make_longlong2(0, 0);
-  for (int i = 0; i < per_thread; ++i) {
-    const int s = threadIdx.x * per_thread + i;
-    if (s < p.c.num_seqs) {
-      const SeqPlace at = seq_place(p.c, s);
-      if (s < kSeqs) sm.seq[s] = at;
-      mine.x += steps_of<NT>(p, at);
-      mine.y += Cur::cost(p, at);
-    }
-  }
-  longlong2 upto = mine;
-#pragma unroll
-  for (int s = 1; s < 32; s *= 2) {
-    const long long x = __shfl_up_sync(0xffffffffu, upto.x, s), y = __shfl_up_sync(0xffffffffu, upto.y, s);
-    if (lane >= s) {
-      upto.x += x;
-      upto.y += y;
-    }
-  }
-  if (lane == 31) sm.warp_sum[warp] = upto;
-  __syncthreads();
-  longlong2 before = make_longlong2(0, 0);
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) {
-      before.x += sm.warp_sum[w].x;
-      before.y += sm.warp_sum[w].y;
-    }
-    total += sm.warp_sum[w].x;
-  }
-  if (threadIdx.x == kThreads - 1) sm.last_blocks = mine.y;
-  sm.pre[threadIdx.x] = make_longlong2(before.x + upto.x - mine.x, before.y + upto.y - mine.y);
-  __syncthreads();
-  const Cut cut(total, gridDim.x, kWarps, false);  // a run is one piece
-  const int used = cut.used(gridDim.x);
-  const int run = blockIdx.x * used + warp;
-  if (threadIdx.x == 0) {
-    if (blockIdx.x == 0) p.head[2] = gridDim.x;
-    p.open[blockIdx.x].parts = 0;
-  }
+  // ---- the blocks of this warp: `todo` from cc's on, of the `used` runs of the CTA
+  long long todo = 0, stop = 0, total = 0;
+  int used;
+  Cur cc, lc;  // of the arithmetic; of the copies, which run ahead
   if (lane < 2) sm.ends[warp].has[lane] = false;
   __syncwarp();
-
-  // Puts a cursor on a step of the flat order, and says how many blocks lie before it.
-  auto locate = [&](Cur& cur, long long x) -> long long {
-    const int slice = find_last(kThreads, x, [&](int s) { return sm.pre[s].x; });
-    longlong2 at = sm.pre[slice];
-    int i = slice * per_thread;
-    SeqPlace s = Cur::place(p, sm.seq, i);
-    for (long long c; x - at.x >= (c = steps_of<NT>(p, s)) && i + 1 < p.c.num_seqs; s = Cur::place(p, sm.seq, ++i)) {
-      at.x += c;
-      at.y += Cur::cost(p, s);
+  if (p.alone) {  // one unit for the CTA
+    cc.tiles = Cur::tiles_of(1, p.g);
+    const int row = static_cast<int>(blockIdx.x) / (p.c.hkv * cc.tiles);
+    cc.seq = row;
+    cc.s = seq_place(p.c, row);
+    cc.nb = Cur::blocks_of(cc.s);
+    cc.head = (static_cast<int>(blockIdx.x) - row * p.c.hkv * cc.tiles) / cc.tiles;
+    cc.tile = static_cast<int>(blockIdx.x) % cc.tiles;
+    used = min(cc.nb, kWarps);
+    if (warp < used) {
+      cc.blk = cc.nb * warp / used;
+      todo = cc.nb * (warp + 1) / used - cc.blk;
     }
-    cur.enter(p, sm.seq, i);
-    const int each = cur.nb + kUnitSteps;
-    const long long off = x - at.x, unit = quotient(off, each);
-    cur.blk = max(0, static_cast<int>(off - unit * each) - kUnitSteps);
-    cur.head = static_cast<int>(quotient(unit, cur.tiles));
-    cur.tile = static_cast<int>(unit - static_cast<long long>(cur.head) * cur.tiles);
-    return at.y + unit * cur.nb + cur.blk;
-  };
+  } else {  // an equal run of the flat order for each warp
+    const int per_thread = (p.c.num_seqs + kThreads - 1) / kThreads;
+    longlong2 mine = make_longlong2(0, 0);
+    for (int i = 0; i < per_thread; ++i) {
+      const int s = threadIdx.x * per_thread + i;
+      if (s < p.c.num_seqs) {
+        const SeqPlace at = seq_place(p.c, s);
+        if (s < kSeqs) sm.seq[s] = at;
+        mine.x += steps_of<NT>(p, at);
+        mine.y += Cur::cost(p, at);
+      }
+    }
+    longlong2 upto = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto.x, s), y = __shfl_up_sync(0xffffffffu, upto.y, s);
+      if (lane >= s) {
+        upto.x += x;
+        upto.y += y;
+      }
+    }
+    if (lane == 31) sm.warp_sum[warp] = upto;
+    __syncthreads();
+    longlong2 before = make_longlong2(0, 0);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) {
+        before.x += sm.warp_sum[w].x;
+        before.y += sm.warp_sum[w].y;
+      }
+      total += sm.warp_sum[w].x;
+    }
+    if (threadIdx.x == kThreads - 1) sm.last_blocks = mine.y;
+    sm.pre[threadIdx.x] = make_longlong2(before.x + upto.x - mine.x, before.y + upto.y - mine.y);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      if (blockIdx.x == 0) p.head[2] = gridDim.x;
+      p.open[blockIdx.x].parts = 0;
+    }
+    // Puts a cursor on a step of the flat order, and says how many blocks lie before it.
+    auto locate = [&](Cur& cur, long long x) -> long long {
+      const int slice = find_last(kThreads, x, [&](int s) { return sm.pre[s].x; });
+      longlong2 at = sm.pre[slice];
+      int i = slice * per_thread;
+      SeqPlace s = Cur::place(p, sm.seq, i);
+      for (long long c; x - at.x >= (c = steps_of<NT>(p, s)) && i + 1 < p.c.num_seqs; s = Cur::place(p, sm.seq, ++i)) {
+        at.x += c;
+        at.y += Cur::cost(p, s);
+      }
+      cur.enter(p, sm.seq, i);
+      const int each = cur.nb + kUnitSteps;
+      const long long off = x - at.x, unit = quotient(off, each);
+      cur.blk = max(0, static_cast<int>(off - unit * each) - kUnitSteps);
+      cur.head = static_cast<int>(quotient(unit, cur.tiles));
+      cur.tile = static_cast<int>(unit - static_cast<long long>(cur.head) * cur.tiles);
+      return at.y + unit * cur.nb + cur.blk;
+    };
 
-  long long start, stop;
-  cut.range(run, 0, start, stop);
-  long long todo = 0;  // blocks of the run
-  Cur cc, lc;          // of the arithmetic; of the copies, which run ahead
-  if (warp < used && start < total) {
-    const long long end = stop < total ? locate(lc, stop) : sm.pre[kThreads - 1].y + sm.last_blocks;
-    todo = end - locate(lc, start);
-    cc = lc;
+    const Cut cut(total, gridDim.x, kWarps, false);  // a run is one piece
+    used = cut.used(gridDim.x);
+    long long start;
+    cut.range(blockIdx.x * used + warp, 0, start, stop);
+    if (warp < used && start < total) {
+      const long long end = stop < total ? locate(cc, stop) : sm.pre[kThreads - 1].y + sm.last_blocks;
+      todo = end - locate(cc, start);
+    }
   }
+  const int run = blockIdx.x * used + warp;
   if (todo > 0) {
+    lc = cc;
     long long to_load = todo;
     int load_slot = 0;
     int left = 0;                  // blocks that can be asked for without a look at anything else
@@ -627,7 +641,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_cache4_attention(const AttnP
         }
         next_of = -1;
       }
-      if (next_of < 0 && lc.last_unit(p)) {
+      if (next_of < 0 && !p.alone && lc.last_unit(p)) {
         next_of = lc.next_seq(p, sm.seq);
         if (next_of < p.c.num_seqs && lane < p.c.max_pages)
           next_page = __ldg(p.c.table + static_cast<long long>(next_of) * p.c.max_pages + lane);
@@ -833,7 +847,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_cache4_attention(const AttnP
     if (kind && !whole && threadIdx.x == 0) {
       Open o = {};
       o.first = blockIdx.x;
-      o.parts = cut.piece_of(e.last) / used - blockIdx.x + 1;
+      o.parts = Cut(total, gridDim.x, kWarps, false).piece_of(e.last) / used - blockIdx.x + 1;
       o.row0 = e.row0[1];
       o.head = e.head[1];
       o.nrows = nrows;
@@ -845,16 +859,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_cache4_attention(const AttnP
 }
 
 template <int D, int NT>
-hdp_status_t launch4(const AttnParams& p, int device, int ctas, cudaStream_t st) {
+hdp_status_t launch4(AttnParams p, int device, int sms, int ctas, cudaStream_t st) {
   static std::atomic<bool> ready[kDevices];
   constexpr int smem = sizeof(Shared4<D, NT>);
   static_assert(smem <= 232448, "shared memory of a CTA");
-  return launch<D, NT>(k_cache4_attention<D, NT>, kWarps, smem, ctas, ready, p, device, ctas, st);
+  // One token for each sequence, no more units than SMs and at most four blocks for each
+  // warp of a unit: a CTA takes a unit, and nothing is left to join.  Measured (in a captured
+  // graph, so and by runs): four documents of 64 to 512 tokens, 4 heads of 64, 6.7 and 11.3
+  // us; 16 of 2,000 tokens, 8 heads of 128, 13.4 and 18.7; one of 2,048, 13.0 and 13.2; one
+  // of 2,000 and 15 of 60, 13.1 and 12.7.
+  const int64_t units = static_cast<int64_t>(p.c.num_seqs) * p.c.hkv * ((p.g + 8 * NT - 1) / (8 * NT));
+  p.alone = !p.c.cu && units <= sms && p.c.max_pages <= 4 * kWarps;
+  if (p.alone) ctas = static_cast<int>(units);
+  return launch<D, NT>(k_cache4_attention<D, NT>, kWarps, smem, p.alone ? 0 : ctas, ready, p, device, ctas, st);
 }
 
 template <int D>
-hdp_status_t launch_for(const AttnParams& p, int nt, int device, int ctas, cudaStream_t st) {
-  return nt == 1 ? launch4<D, 1>(p, device, ctas, st) : launch4<D, 2>(p, device, ctas, st);
+hdp_status_t launch_for(const AttnParams& p, int nt, int device, int sms, int ctas, cudaStream_t st) {
+  return nt == 1 ? launch4<D, 1>(p, device, sms, ctas, st) : launch4<D, 2>(p, device, sms, ctas, st);
 }
 
 }  // namespace
@@ -878,8 +900,8 @@ extern "C" hdp_status_t hdp_fourbit_attention(const hdp_fourbit_cache_t* cache, 
   p.scale_bytes = c.scale_bytes;
   const bool wide = cache->d == 128;
   return attend("hdp_fourbit_attention", kCount, 0, p, cache->d, rows, q, hq, scale, nullptr, 0, workspace, workspace_bytes, o, lse,
-                stream, [=](const AttnParams& a, int nt, int device, int ctas, cudaStream_t st) {
-                  return wide ? launch_for<128>(a, nt, device, ctas, st)
-                              : launch_for<64>(a, nt, device, ctas, st);
+                stream, [=](const AttnParams& a, int nt, int device, int sms, int ctas, cudaStream_t st) {
+                  return wide ? launch_for<128>(a, nt, device, sms, ctas, st)
+                              : launch_for<64>(a, nt, device, sms, ctas, st);
                 });
 }
