@@ -283,8 +283,10 @@ def _turned(q, k, position, freqs, neighbours, backward, factor, inplace, stream
 def rotary(q, k, position, freqs, neighbours: bool = False, factor: float = 1.0, inplace: bool = False, stream=None):
     """Rotary positions of q [rows][hq][d] and k [rows][hkv][d] (either may be None; views of a fused projection are fine):
     pairs of the first 2 * len(freqs) channels of each head, channels i and i + len(freqs), or with neighbours 2 i and
-    2 i + 1, are turned by position * freqs[i] and scaled by factor.  position int32 [rows] (cache_rows gives them; rows
-    at a negative one are left as they are), freqs float64 (rotary_frequencies).  Returns the turned (q, k)."""
+    2 i + 1, are turned by position * freqs[i] and scaled by factor.  position int32 [rows] (cache_rows gives them), freqs
+    float64 (rotary_frequencies).  Rows at a negative position are not written: in place they keep their values, in the new
+    tensors that are returned otherwise those rows are not initialised.  In place, q and k must not share memory.  Returns
+    the turned (q, k)."""
     return _turned(q, k, position, freqs, neighbours, False, factor, inplace, stream)
 
 

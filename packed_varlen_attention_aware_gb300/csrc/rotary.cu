@@ -310,6 +310,8 @@ extern "C" hdp_status_t hdp_rotary(const hdp_rotary_rows_t* q, const hdp_rotary_
     p.copy = p.copy || x->in != x->out;
   }
   if (rows == 0 || p.heads[0] + p.heads[1] == 0) return HDP_OK;
+  if (p.heads[0] && p.heads[1] && (p.x[0].out == p.x[1].out || p.x[0].out == p.x[1].in || p.x[1].out == p.x[0].in))
+    return fail(HDP_ERR_INVALID_ARGUMENT, name + "what is written for q and k must not be rows of the other");
   if (!position || !freqs) return fail(HDP_ERR_INVALID_ARGUMENT, name + "position or freqs is NULL");
   if (reinterpret_cast<uintptr_t>(freqs) & 7) return fail(HDP_ERR_INVALID_ARGUMENT, name + "freqs must be 8-byte aligned");
   p.copy = p.copy && rot < d;

@@ -221,6 +221,23 @@ def test_rows_at_any_alignment_turn_alike(dtype):
         assert none is None and torch.equal(a, b)
 
 
+def test_rows_that_are_both_q_and_k():
+    """Turned out of place they may be both; where one is written over the other's rows the call is refused."""
+    x = torch.randn(9, 2, 64, device="cuda")
+    f, pos = torch.ones(32, device="cuda", dtype=torch.float64), _i32(np.arange(9))
+    a, b = pkg.rotary(x, x, pos, f)
+    assert torch.equal(a, b)
+    before, y = x.clone(), torch.empty_like(x)
+    for out in ((x, x), (x, y), (y, x), (y, y)):
+        with pytest.raises(pkg.HdpError, match="rows of the other"):
+            pkg.hdp_rotary(x, x, pos, f, *out)
+    with pytest.raises(pkg.HdpError, match="rows of the other"):
+        pkg.rotary(x, x, pos, f, inplace=True)
+    assert torch.equal(x, before)
+    pkg.rotary(x, x[:, :0], pos, f, inplace=True)  # no heads: nothing is shared
+    assert torch.equal(x, a)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("neighbours", [False, True])
 @pytest.mark.parametrize("d,rot,pitch,offset", [(64, 48, 66, 0), (64, 46, 66, 2), (64, 36, 64, 0), (128, 6, 136, 0), (128, 126, 128, 0), (7, 6, 8, 0), (250, 250, 250, 0)])

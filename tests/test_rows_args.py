@@ -106,7 +106,8 @@ def test_rotary_refusals(lib):
     call = lambda **x: lib.hdp_rotary(*{**ok, **x}.values(), None)
     for bad in (dict(q=None), dict(rows=-1), dict(rows=1 << 31), dict(d=1), dict(rot=0), dict(rot=63), dict(rot=66), dict(type=3), dict(type=-1),
                 dict(flags=4), dict(factor=0.0), dict(factor=-1.0), dict(factor=math.inf), dict(factor=math.nan), dict(pos=None), dict(freqs=None),
-                dict(freqs=V(260)), dict(q=_rows(heads=-1)), dict(q=_rows(heads=(1 << 20) + 1)), dict(q=_rows(in_=None)), dict(q=_rows(out=None)),
+                dict(freqs=V(260)), dict(k=_rows()), dict(k=_rows(in_=1024)), dict(k=_rows(out=256)), dict(k=_rows(in_=512, out=1024)),
+                dict(q=_rows(heads=-1)), dict(q=_rows(heads=(1 << 20) + 1)), dict(q=_rows(in_=None)), dict(q=_rows(out=None)),
                 dict(q=_rows(in_=257)), dict(q=_rows(out=513)), dict(type=2, q=_rows(in_=258)), dict(q=_rows(out=256, out_row_stride=512)),
                 dict(k=_rows(out=256, out_head_stride=128))):
         assert call(**bad) == INVALID, bad
