@@ -446,9 +446,12 @@ hdp_status_t hdp_fourbit_read(const hdp_fourbit_cache_t* cache, const int32_t* c
                               void* stream);
 
 /* hdp_cache_attention over this cache: the same formulas, arguments and promises,
- * over all blocks (there are no lists).  workspace: device, 256-byte aligned, at
- * least hdp_fourbit_attention_workspace_bytes, which depends on the device's SM
- * count and d only; calls that may overlap need one each. */
+ * over all blocks (there are no lists).  Where a row's score passes fp32's end before
+ * it is multiplied by `scale`, K scales below 2^-94 may count as 0 in the 64 keys of its
+ * block.  workspace: device, 256-byte aligned, at least
+ * hdp_fourbit_attention_workspace_bytes, which depends on the device's SM count and d
+ * only (152 SMs: 12.7 MB for d = 128, 6.4 MB for d = 64); calls that may overlap need
+ * one each. */
 hdp_status_t hdp_fourbit_attention_workspace_bytes(const hdp_fourbit_cache_t* cache, int32_t hq, size_t* bytes);
 hdp_status_t hdp_fourbit_attention(const hdp_fourbit_cache_t* cache, const int32_t* cu, int64_t rows, const void* q,
                                    int32_t hq, float scale, void* workspace, size_t workspace_bytes, void* o, float* lse,
@@ -501,8 +504,10 @@ hdp_status_t hdp_cache_rows(const int32_t* page_table, const int32_t* lens, cons
  * gradient of the rows before the turn from that of the rows behind it.
  *   q, k: either may be NULL.  Rows [rows][heads][d] of `type`, channels
  *   contiguous, other strides in elements; out may be in (with the same strides),
- *   else the two must not overlap.  Any alignment; 16-byte steps where the
- *   addresses, strides and rot allow them.
+ *   else the two must not overlap, and neither out may overlap the other's rows.
+ *   Any alignment; 16-byte steps where the
+ *   addresses, strides and rot allow them (slower, but the same results, where rot or
+ *   they do not).
  *   position [rows] int32; a row at a negative one is not read, its output is left
  *   as it was.  freqs [rot/2] double, radians, finite (device; scaling for long
  *   contexts is in them and in factor).  2 <= rot <= d <= 256, rot even; factor > 0.

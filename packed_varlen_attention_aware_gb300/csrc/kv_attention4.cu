@@ -16,9 +16,8 @@
 //   Scales of K.  A group's sum is multiplied by its scale in fp32 and added to the
 //   score's: no rounding of a code to a scaled one.  Where that passes fp32's end and a
 //   scale is 2^65 or more, the block is computed again with all scales 2^-32 times as
-//   large and the score back up behind the row's factor, so that only scores beyond
-//   fp32's end pass it; what the smallest scales lose by that is below such a score's
-//   last bit.
+//   large (those below 2^-94 count as 0) and the score back up behind the row's factor,
+//   so that only scores beyond fp32's end pass it.
 //   Scales of V go into P, as powers of two relative to the output's reference.
 //   References.  Where every P of a block, under the references that the sums have, is a
 //   normal number of fp16 (2^-14 to 2^15), it stays under them: nothing is rescaled, no
@@ -353,8 +352,16 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
     ks[g] = reinterpret_cast<const uint2*>(scales + g * kBlock)[gr];
     large |= large_bytes(ks[g].x) | large_bytes(ks[g].y);
   }
-  const bool careful = __any_sync(0xffffffffu, (large & 0x80808080u) != 0);
-  if (careful) {  // scales from 2^65 on
+  bool past = false;  // fp32's end
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        past |= (!masked || key0 + 8 * j + gr <= slow.rows.pos[t][k]) && !(fabsf(slow.s[t][j >> 1][k + 2 * (j & 1)]) < inf);
+  const bool careful = __any_sync(0xffffffffu, (large & 0x80808080u) != 0) && __any_sync(0xffffffffu, past);
+  if (careful) {  // by scales from 2^65 on
     lost = lower_scales<D / 32>(ks);
     first_product<D, NT>(slow.rows, block, lane, ks, slow.s);
   }

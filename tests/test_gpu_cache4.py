@@ -273,6 +273,23 @@ def test_keys_of_any_size_with_queries_that_bring_them_back(shift):
     _check(o, lse, ref.attention(table, lens, _f64(q), [0, 1, 2, 3], d ** -0.5))
 
 
+@pytest.mark.parametrize("rows", [1, 3])
+def test_tiny_scales_beside_huge_ones(rows):
+    """Channels with K scales of 2^-98 decide the scores; others have 2^70 and meet zeros of q."""
+    rng = np.random.default_rng(29 + rows)
+    lens, d = [64, 200, 66], 64
+    table, (cache, ref) = _random_cache(lens, 1, d, rng)
+    ref.scales[:, :, 0] = 29
+    ref.scales[:, :, 1] = rng.choice([1, 197], ref.scales[:, :, 1].shape)
+    cache.scales.copy_(torch.tensor(ref.scales))
+    q = rng.normal(size=(3 * rows, 4, d)) * 2.0 ** 97
+    q[:, :, 32:] = 0
+    q = _bf16(q)
+    cu = np.arange(4) * rows
+    o, lse = pkg.cache_attention(cache, _i32(table), _i32(lens), q.cuda(), cu=_i32(cu))
+    _check(o, lse, ref.attention(table, lens, _f64(q), cu, d ** -0.5))
+
+
 def test_small_weights_count_where_the_heavy_ones_values_are_zero():
     """Within a block one key has all of a row's weight but 10^-9 .. 10^-30, and zero codes of V in half of the channels."""
     rng = np.random.default_rng(11)
