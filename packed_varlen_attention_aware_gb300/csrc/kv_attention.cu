@@ -592,7 +592,7 @@ hdp_status_t launch8(const AttnParams& p, int device, int ctas, cudaStream_t st)
   constexpr int smem = sizeof(Shared<NT, SPARSE>);
   static_assert(smem <= 232448, "shared memory of a CTA");
   const int pieces = ctas * kWarps * (p.dynamic ? 1 + kMorePieces : 1);
-  return launch<D, NT>(k_cache_attention<D, FMT, NT, SPARSE>, kWarps, smem, pieces, ready, p, device, ctas, st);
+  return launch(k_cache_attention<D, FMT, NT, SPARSE>, k_cache_attention_join<D, NT>, kWarps, smem, pieces, ready, p, device, ctas, st);
 }
 
 template <int D, int FMT>

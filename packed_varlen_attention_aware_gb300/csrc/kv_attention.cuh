@@ -658,10 +658,9 @@ hdp_status_t launch_early(void (*kernel)(T...), dim3 grid, int threads, int smem
   return HDP_OK;
 }
 
-// Launches `kernel` (`warps` a CTA, `smem` bytes) and the join of its pieces, if any, behind it;
+// Launches `kernel` (`warps` a CTA, `smem` bytes) and `join` of its pieces, if any, behind it;
 // `ready`: the devices on which the kernel may have that much.
-template <int D, int NT>
-hdp_status_t launch(void (*kernel)(AttnParams), int warps, int smem, int pieces, std::atomic<bool> (&ready)[kDevices],
+hdp_status_t launch(void (*kernel)(AttnParams), void (*join)(AttnParams, int), int warps, int smem, int pieces, std::atomic<bool> (&ready)[kDevices],
                     const AttnParams& p, int device, int ctas, cudaStream_t st) {
   if (device >= kDevices || !ready[device].load(std::memory_order_relaxed)) {
     HDP_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
@@ -681,7 +680,7 @@ hdp_status_t launch(void (*kernel)(AttnParams), int warps, int smem, int pieces,
     HDP_CUDA_TRY(cudaGetLastError());
   }
   if (pieces == 0) return HDP_OK;
-  return launch_early(k_cache_attention_join<D, NT>, dim3(ctas), kJoinWarps * 32, 0, st, p, pieces);
+  return launch_early(join, dim3(ctas), kJoinWarps * 32, 0, st, p, pieces);
 }
 
 // Checks and launches a call whose view is in p.c; hand_out: warps of a CTA that can hand

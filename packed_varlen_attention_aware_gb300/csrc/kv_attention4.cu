@@ -605,10 +605,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_cache4_attention(const AttnP
     if (threadIdx.x == kThreads - 1) sm.last_blocks = mine.y;
     sm.pre[threadIdx.x] = make_longlong2(before.x + upto.x - mine.x, before.y + upto.y - mine.y);
     __syncthreads();
-    if (threadIdx.x == 0) {
-      if (blockIdx.x == 0) p.head[2] = gridDim.x;
-      p.open[blockIdx.x].parts = 0;
-    }
+    if (threadIdx.x == 0) p.open[blockIdx.x].parts = 0;
     // Puts a cursor on a step of the flat order, and says how many blocks lie before it.
     auto locate = [&](Cur& cur, long long x) -> long long {
       const int slice = find_last(kThreads, x, [&](int s) { return sm.pre[s].x; });
@@ -901,6 +898,45 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_cache4_attention(const AttnP
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Joins the unit that a CTA began and did not end, if there is one, with its parts in the
+// CTAs behind it: up to eight warps share a row's parts.  No lists of units are made, which
+// the join of handed-out pieces needs (16 drafts of 4 tokens 37.9 us, 38.9 by that).
+template <int D, int NT>
+__global__ void __launch_bounds__(kJoinWarps * 32, 1) k_cache4_join(const AttnParams p, int) {
+  constexpr int kRows = 8 * NT;
+  static_assert(kRows <= kJoinWarps, "a warp for each row");
+  __shared__ __align__(16) float s_x[kJoinWarps][D];
+  __shared__ float2 s_sum[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4* open = reinterpret_cast<const int4*>(p.open + blockIdx.x);
+  const int4 a = __ldcg(open), b = __ldcg(open + 1);
+  const int m = a.x, nrows = b.x;
+  if (m == 0) return;
+  const int each = min(kWarps, kJoinWarps >> (nrows > 1 ? 32 - __clz(nrows - 1) : 0));  // warps of a row
+  const int r = warp / each, run = warp - r * each;
+  auto at = [&](int k) { return (static_cast<size_t>(a.y + k) * 2 + (k == 0)) * kRows + r; };
+  float x[D / 32];
+  float2 sum;
+  if (r < nrows) {
+    const int k0 = m * run / each, k1 = m * (run + 1) / each;
+    sum = join_row<D>(k1 - k0, lane, x, [&](int k) { return __ldcg(p.part_sum + at(k0 + k)); },
+                      [&](int k) { return p.part + at(k0 + k) * D; });
+  }
+  if (each > 1) {
+#pragma unroll
+    for (int v = 0; v < D / 32; ++v) s_x[warp][lane * (D / 32) + v] = x[v];
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    if (run > 0 || r >= nrows) return;
+    const int mine = min(lane & (kWarps - 1), each - 1);
+    float2 l = s_sum[warp + mine];
+    if ((lane & (kWarps - 1)) >= each) l = make_float2(kLow, 0.f);
+    sum = join_few<D>(each, lane, x, l, s_x[warp + mine]);
+  }
+  if (r < nrows) write_o<D>(p, a.z, a.w, b.y + r, x, lse_of(sum.x, sum.y), lane);
+}
+
 template <int D, int NT>
 hdp_status_t launch4(AttnParams p, int device, int sms, int ctas, cudaStream_t st) {
   static std::atomic<bool> ready[kDevices];
@@ -914,7 +950,7 @@ hdp_status_t launch4(AttnParams p, int device, int sms, int ctas, cudaStream_t s
   const int64_t units = static_cast<int64_t>(p.c.num_seqs) * p.c.hkv * ((p.g + 8 * NT - 1) / (8 * NT));
   p.alone = !p.c.cu && units <= sms && p.c.max_pages <= 4 * kWarps;
   if (p.alone) ctas = static_cast<int>(units);
-  return launch<D, NT>(k_cache4_attention<D, NT>, kWarps, smem, p.alone ? 0 : ctas, ready, p, device, ctas, st);
+  return launch(k_cache4_attention<D, NT>, k_cache4_join<D, NT>, kWarps, smem, p.alone ? 0 : ctas, ready, p, device, ctas, st);
 }
 
 template <int D>
