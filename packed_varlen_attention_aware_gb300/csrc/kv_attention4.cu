@@ -86,6 +86,7 @@ constexpr int kWarps = 8;
 constexpr PartCount kCount = {1, kWarps + 2};
 
 constexpr float kHeadroom = 4.f;    // bits of a fresh reference above what needs it
+constexpr int kMostGap = 254;       // of Common::gap, so that a NaN's byte, 255, is above it: no block with one is quick
 constexpr float kCommon = 8.f;      // most bits that an output's reference is raised to be its neighbours', or above a V scale
 // What fp16 leaves of a block's P is at most 64 * 2^-25 times its largest code, 6; 2^12 times that.
 constexpr float kEnough4 = 0.0625f;
@@ -296,7 +297,9 @@ __device__ __forceinline__ void refer(const Rows<D, NT>& rows, Sums<D, NT>& sums
   const uint32_t two = reinterpret_cast<const uint16_t*>(scales + (D / 32) * kBlock)[lane];
   int above = static_cast<int>(max(place_token(2 * lane) < limit ? two & 0xffu : 0u, place_token(2 * lane + 1) < limit ? two >> 8 : 0u));
   above = __reduce_max_sync(0xffffffffu, above);
-  if (above > common.gap) common.gap = above + 1;
+  const int byte = above > common.gap ? above + 1 : common.gap;
+  if (byte > kMostGap) return;
+  common.gap = byte;
   const float gap = static_cast<float>(common.gap - 127);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -453,8 +456,8 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
     }
     if (near) slow.sums.gap[t][k] = most_gap;
   }
-  slow.common.any = __all_sync(0xffffffffu, same);
   slow.common.gap = static_cast<int>(fminf(fmaxf(most_gap, -1126.f), 999.f)) + 127;
+  slow.common.any = __all_sync(0xffffffffu, same) && slow.common.gap <= kMostGap;
 
   copies_wait<2 * Sh::kSlots - 2>();
   __syncwarp();  // V is there, and the codes of K have been read

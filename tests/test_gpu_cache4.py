@@ -273,6 +273,25 @@ def test_keys_of_any_size_with_queries_that_bring_them_back(shift):
     _check(o, lse, ref.attention(table, lens, _f64(q), [0, 1, 2, 3], d ** -0.5))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("before", [0, 64])
+def test_nan_scales_among_the_largest(d, before):
+    """V scales of 2^116 and more, one token's NaN: the output is NaN wherever that token is seen."""
+    rng = np.random.default_rng(d + before)
+    lens = [before + 64, before + 64]
+    table, (cache, ref) = _random_cache(lens, 1, d, rng)
+    ref.scales[:, :, -1] = rng.integers(243, 248, ref.scales[:, :, -1].shape)
+    page = table[1, before // 64]
+    ref.scales[page, 0, -1, k4.scale_place(20)] = 255
+    for ch in range(d):
+        i, byte, e = k4.v_place(20, ch)
+        ref.v[page, 0, i, byte] &= 0x0F if e else 0xF0
+    cache.v.copy_(torch.tensor(ref.v)), cache.scales.copy_(torch.tensor(ref.scales))
+    q = _bf16(rng.normal(size=(2, 4, d)) * 0.05)
+    o, lse = pkg.cache_attention(cache, _i32(table), _i32(lens), q.cuda())
+    assert torch.isnan(o[1]).all() and torch.isfinite(o[0]).all() and torch.isfinite(lse).all()
+
+
 @pytest.mark.parametrize("rows", [1, 3])
 def test_tiny_scales_beside_huge_ones(rows):
     """Channels with K scales of 2^-98 decide the scores; others have 2^70 and meet zeros of q."""
