@@ -352,8 +352,10 @@ hdp_status_t hdp_cache_read(const hdp_cache_t* cache, const int32_t* cu, int64_t
  * and o = 0, lse = -inf where no token is left.  Inputs are the dequantised
  * codes; sums and the softmax's statistics are fp32.  That holds for q, K and V
  * over all of bf16's range, scores up to fp32's end, and weights down to 2^-126
- * of a row's largest.  Elements of a query row below 2^-31 of its largest keep
- * fewer bits (they are rounded to multiples of 2^-38 of it).
+ * of a row's largest, where weight times V scale is at least 2^-100 of the row's
+ * largest such product.  (What is smaller shows in channels in which the keys above
+ * it have zeros.)  Elements of a query row below 2^-31 of its largest keep fewer
+ * bits (they are rounded to multiples of 2^-38 of it).
  *   q, o [rows][hq][d] bf16, 16-byte aligned; lse [hq][rows] fp32; hq % hkv == 0.
  *   blocks NULL (count 0): every block.  Else device int32 [rows][hkv][count],
  *   count >= 1: for each row and kv head the blocks to attend to, strictly
@@ -448,7 +450,7 @@ hdp_status_t hdp_fourbit_read(const hdp_fourbit_cache_t* cache, const int32_t* c
 /* hdp_cache_attention over this cache: the same formulas, arguments and promises,
  * over all blocks (there are no lists).  Where a row's score passes fp32's end before
  * it is multiplied by `scale`, K scales below 2^-94 may count as 0 in the 64 keys of its
- * block.  workspace: device, 256-byte aligned, at least
+ * block; and weights count down to 2^-100 of a row's largest.  workspace: device, 256-byte aligned, at least
  * hdp_fourbit_attention_workspace_bytes, which depends on the device's SM count and d
  * only (152 SMs: 12.7 MB for d = 128, 6.4 MB for d = 64); calls that may overlap need
  * one each. */

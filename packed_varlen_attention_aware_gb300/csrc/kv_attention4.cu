@@ -87,6 +87,7 @@ constexpr PartCount kCount = {1, kWarps + 2};
 
 constexpr float kHeadroom = 4.f;    // bits of a fresh reference above what needs it
 constexpr int kMostGap = 254;       // of Common::gap, so that a NaN's byte, 255, is above it: no block with one is quick
+constexpr float kFactorBias = 24.f;  // of a block's factor in the output, for the same reason: a product is at most 2^24
 constexpr float kCommon = 8.f;      // most bits that an output's reference is raised to be its neighbours', or above a V scale
 // What fp16 leaves of a block's P is at most 64 * 2^-25 times its largest code, 6; 2^12 times that.
 constexpr float kEnough4 = 0.0625f;
@@ -213,6 +214,11 @@ struct Common {
   int gap;  // + 127, as a scale's byte; below 0: no block yet
 };
 
+// A whole power of two as two factors, so that a sum is only lost where the result is: 2^-126 ends one.
+__device__ __forceinline__ float2 exp2_far(float z) {
+  return make_float2(exp2_approx(fmaxf(z, -100.f)), exp2_approx(fminf(z + 100.f, 0.f)));
+}
+
 // What stands behind it in a rare branch is not computed in front of the branch.
 __device__ __forceinline__ void stay_here() { asm volatile("" ::: "memory"); }
 
@@ -290,17 +296,22 @@ __device__ __forceinline__ bool as_is(const Rows<D, NT>& rows, Sums<D, NT>& sums
 }
 
 // Brings the sums to references that are kHeadroom above the block's scores and a bit above
-// its V scales, where they are not that high already.
+// its V scales, where they are not that high already.  Nothing is changed where that does not
+// make the block quick (its V scales are too far apart), or where V scales of keys that weigh
+// little would take a reference over kCommon bits above what needs it: the sums' range, down
+// to 2^-126 of the largest product, would go to what is not there.
 template <int D, int NT>
 __device__ __forceinline__ void refer(const Rows<D, NT>& rows, Sums<D, NT>& sums, Common& common, const unsigned char* scales,
                                       int lane, int limit, const float (&s)[NT][4][4]) {
   const uint32_t two = reinterpret_cast<const uint16_t*>(scales + (D / 32) * kBlock)[lane];
-  int above = static_cast<int>(max(place_token(2 * lane) < limit ? two & 0xffu : 0u, place_token(2 * lane + 1) < limit ? two >> 8 : 0u));
-  above = __reduce_max_sync(0xffffffffu, above);
+  const bool seen = place_token(2 * lane) < limit, other = place_token(2 * lane + 1) < limit;
+  const int above = __reduce_max_sync(0xffffffffu, static_cast<int>(max(seen ? two & 0xffu : 0u, other ? two >> 8 : 0u)));
+  const int below = __reduce_min_sync(0xffffffffu, static_cast<int>(min(seen ? two & 0xffu : 255u, other ? two >> 8 : 255u)));
   const int byte = above > common.gap ? above + 1 : common.gap;
-  if (byte > kMostGap) return;
-  common.gap = byte;
-  const float gap = static_cast<float>(common.gap - 127);
+  if (byte > kMostGap || byte - below > 14) return;
+  const float gap = static_cast<float>(byte - 127);
+  float m1[NT][2];
+  bool far = false;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -311,15 +322,24 @@ __device__ __forceinline__ void refer(const Rows<D, NT>& rows, Sums<D, NT>& sums
 #pragma unroll
       for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
       const float c = ceilf(top) - kBias, m = sums.m[t][k];
-      const float m1 = c > m && fabsf(c) < kBiasMost ? c + kHeadroom : m;  // (larger ones are not for here)
-      const float turn = exp2_approx((m - m1) + (sums.gap[t][k] - gap));
+      m1[t][k] = c > m && fabsf(c) < kBiasMost ? c + kHeadroom : m;  // (larger ones are not for here)
+      far |= (m1[t][k] - m) + (gap - sums.gap[t][k]) > kCommon && (m1[t][k] - c) + (byte - above) > kCommon;
+    }
+  if (__any_sync(0xffffffffu, far)) return;
+  common.gap = byte;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float m = sums.m[t][k];
+      const float2 turn = exp2_far((m - m1[t][k]) + (sums.gap[t][k] - gap));
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        sums.acc[t][i][k] *= turn;
-        sums.acc[t][i][k + 2] *= turn;
+        sums.acc[t][i][k] = sums.acc[t][i][k] * turn.x * turn.y;
+        sums.acc[t][i][k + 2] = sums.acc[t][i][k + 2] * turn.x * turn.y;
       }
-      sums.l[t][k] *= exp2_approx(m - m1);
-      sums.m[t][k] = m1;
+      sums.l[t][k] *= exp2_approx(m - m1[t][k]);
+      sums.m[t][k] = m1[t][k];
       sums.gap[t][k] = gap;
     }
 }
@@ -369,7 +389,7 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
     first_product<D, NT>(slow.rows, block, lane, ks, slow.s);
   }
   int scale = 0;  // the largest V scale that a row sees
-  float f[NT][2];  // the power of two (<= 1) of the block in the output
+  float f[NT][2];  // the power of two (<= 1) of the block in the output, times 2^kFactorBias
   float most_gap = -inf;
   bool fresh = false;
 #pragma unroll 1
@@ -423,12 +443,12 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
     most_gap = fmaxf(most_gap, gap1);
     slow.sums.l[t][k] = fmaf(sum, exp2_approx(up), slow.sums.l[t][k] * exp2_approx(down));
     // 0 where no key is seen; NaN where the scale of a seen V row is
-    f[t][k] = bad ? nan : exp2_approx(up + (e - gap1));
-    const float turn = exp2_approx(down + (gap - gap1));
+    f[t][k] = bad ? nan : exp2_approx(up + (e - gap1) + kFactorBias);
+    const float2 turn = exp2_far(down + (gap - gap1));
 #pragma unroll 1
     for (int i = 0; i < D / 16; ++i) {
-      slow.sums.acc[t][i][k] *= turn;
-      slow.sums.acc[t][i][k + 2] *= turn;
+      slow.sums.acc[t][i][k] = slow.sums.acc[t][i][k] * turn.x * turn.y;
+      slow.sums.acc[t][i][k + 2] = slow.sums.acc[t][i][k + 2] * turn.x * turn.y;
     }
     slow.sums.m[t][k] = m1;
     slow.sums.gap[t][k] = gap1;
@@ -464,6 +484,7 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
   const Probabilities<NT> prob = {Sh::kOwnP ? sm.p[Sh::kOwnP ? warp : 0] : reinterpret_cast<float4(*)[4][32]>(block)};
   prob.put(slow.s);
   bool sure = false;  // that further passes are needed
+  float pass = 1.f / (1 << static_cast<int>(kFactorBias));  // what this one's P count
 #pragma unroll 1
   while (true) {
     uint32_t pf[NT][4][2];
@@ -478,19 +499,15 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            slow.sums.acc[t][i + h][k] = fmaf(y[t][h][k], f[t][k & 1], slow.sums.acc[t][i + h][k]);
+            slow.sums.acc[t][i + h][k] = fmaf(y[t][h][k] * pass, f[t][k & 1], slow.sums.acc[t][i + h][k]);
             // is an output so small that what fp16 leaves of P could count?
             sure |= t * 8 + 2 * tc + (k & 1) < nrows && f[t][k & 1] != 0.f && !(fabsf(y[t][h][k]) >= kEnough4);
           }
     }
     if (!__any_sync(0xffffffffu, sure) || !__any_sync(0xffffffffu, prob.more())) break;
     sure = true;
-    prob.next();  // four times at most
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      f[t][0] *= 1.f / kNextPass;
-      f[t][1] *= 1.f / kNextPass;
-    }
+    prob.next();  // three times at most: P are 0 or above 2^-126
+    pass *= 1.f / kNextPass;
   }
 }
 

@@ -273,6 +273,44 @@ def test_keys_of_any_size_with_queries_that_bring_them_back(shift):
     _check(o, lse, ref.attention(table, lens, _f64(q), [0, 1, 2, 3], d ** -0.5))
 
 
+def _one_channel(ref, page, token, ch, code):
+    """K's code of a channel, where it was 0."""
+    at, e = k4.k_place(ch, ref.d)
+    ref.k[page, 0, token, at] |= code << 4 * e
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [1, 4])
+@pytest.mark.parametrize("seen", [64, 40])
+def test_large_scales_of_values_that_weigh_nothing_cost_no_range(d, rows, seen):
+    """Key 0 has the row's weight and a V scale of 2^-53; keys 2, 5, 8 .. have V scales of 2^60 and weights of 2^-235 or
+    less; key 1 has a weight of 2^-74 and alone a value in channel 0.  In one block, and behind a block of ordinary keys."""
+    rng = np.random.default_rng(d + rows)
+    lens = [seen, 64 + seen]
+    table = np.array([[2, -7], [0, 1]], np.int32)
+    k, v, s = _garbage(3, 1, d, rng)
+    ref = k4.Cache(k, v, s)
+    ref.k[:] = 0
+    ref.scales[:] = 127
+    for page in (2, 1, 0):
+        ref.v[page, 0] |= 0x22  # no zeros among the other codes: |code| >= 1
+        for t in range(64):
+            _one_channel(ref, page, t, 0, 0xF if page == 0 or t % 3 == 2 else 4 if t == 0 else 2 if t > 1 else 0)  # -6, 2, 1; 0
+            vs = 74 if t == 0 else 95 if t == 1 else 187 if t % 3 == 2 else 74
+            ref.scales[page, 0, -1, k4.scale_place(t)] = 60 if page == 0 else vs
+            i, byte, e = k4.v_place(t, 0)
+            ref.v[page, 0, i, byte] = ref.v[page, 0, i, byte] & (0x0F if e else 0xF0) | (3 if t == 1 and page else 0) << 4 * e
+    cache = pkg.KVCache4(*(torch.tensor(a, device="cuda") for a in (ref.k, ref.v, ref.scales)))
+    q = np.zeros((2 * rows, 2, d))
+    q[:, :, 0] = 26.0  # scores of 52, 26, 0 and -156: weights 1, 2^-37.5, 2^-75, 2^-300
+    q = _bf16(q)
+    cu = np.arange(3) * rows
+    o, lse = pkg.cache_attention(cache, _i32(table), _i32(lens), q.cuda(), cu=_i32(cu), scale=1.0)
+    want = ref.attention(table, lens, _f64(q), cu, 1.0)
+    assert (want[0][:, :, 0] > 0).all()
+    _check(o, lse, want)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("before", [0, 64])
 def test_nan_scales_among_the_largest(d, before):
