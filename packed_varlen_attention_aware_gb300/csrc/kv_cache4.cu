@@ -14,6 +14,11 @@
 //
 // With one token for each sequence a warp has one (sequence, kv head), half of it
 // the K row and half the V row, as in the 8-bit cache.
+//
+// HBM bounds both ways (645 bytes a token and kv head of 128), the ALUs come next.
+// Measured, 8 kv heads of 128: 83,000 tokens written 73 us, 5.9 TB/s; 131,072
+// written 108.5 us and read 108, 6.2 TB/s, 0.92 of the copy rate; 256 sequences, one
+// token each, written 3.6 us and read 5.0, latency.
 #include <cuda_bf16.h>
 
 #include <string>
