@@ -964,9 +964,9 @@ hdp_status_t launch4(AttnParams p, int device, int sms, int ctas, cudaStream_t s
   static_assert(smem <= 232448, "shared memory of a CTA");
   // One token for each sequence, no more units than SMs and at most four blocks for each
   // warp of a unit: a CTA takes a unit, and nothing is left to join.  Measured (in a captured
-  // graph, so and by runs): four documents of 64 to 512 tokens, 4 heads of 64, 6.7 and 11.3
-  // us; 16 of 2,000 tokens, 8 heads of 128, 13.4 and 18.7; one of 2,048, 13.0 and 13.2; one
-  // of 2,000 and 15 of 60, 13.1 and 12.7.
+  // graph, so and by runs): four documents of 64 to 512 tokens, 4 heads of 64, 6.6 and 11.2
+  // us; 16 of 2,000 tokens, 8 heads of 128, 13.0 and 17.9; one of 2,048, 12.5 and 12.7; one
+  // of 2,000 and 15 of 60, 12.6 and 12.3.
   const int64_t units = static_cast<int64_t>(p.c.num_seqs) * p.c.hkv * ((p.g + 8 * NT - 1) / (8 * NT));
   p.alone = !p.c.cu && units <= sms && p.c.max_pages <= 4 * kWarps;
   if (p.alone) ctas = static_cast<int>(units);
