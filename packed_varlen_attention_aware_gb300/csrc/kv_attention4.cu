@@ -26,7 +26,13 @@
 //   of a run unless a block's scores are spread over more than 17 nats.  Else P is taken
 //   from the block's own largest, the sums come to new references, and what fp16 leaves of
 //   P takes further passes where an output is small enough for it to count, as in the
-//   8-bit kernel.
+//   8-bit kernel.  That takes a block many times as long, so it is not done for each block
+//   of a peaked row: what fp16 leaves of a small P counts only in a channel where the keys
+//   that weigh more are zero, and a block on that path also forms the sum of P |v| for each
+//   row and channel.  The smallest of them is a budget: so many blocks with small P stay
+//   quick that all they lose is 2^-12 of that sum, half a step of an fp16 P at most.  (64 sequences whose scores deviate by
+//   1.7, 2.5 and 3.4 nats: 161, 321 and 461 us; 299, 792 and 802 without a budget, and all
+//   sums rescaled for each block; by 0.85, as the cases do, 92.)
 #include "kv_attention.cuh"
 #include "kv_cache4.cuh"
 
@@ -86,6 +92,9 @@ constexpr int kWarps = 8;
 constexpr PartCount kCount = {1, kWarps + 2};
 
 constexpr float kHeadroom = 4.f;    // bits of a fresh reference above what needs it
+// What fp16 leaves of a block's P below its normal numbers (2^-25 each, twice rounded) is at
+// most 64 * 2^-24 times the largest code; 2^12 times that.
+constexpr float kSmallLoss = 0.09375f;
 constexpr int kMostGap = 254;       // of Common::gap, so that a NaN's byte, 255, is above it: no block with one is quick
 constexpr float kFactorBias = 24.f;  // of a block's factor in the output, for the same reason: a product is at most 2^24
 constexpr float kCommon = 8.f;      // most bits that an output's reference is raised to be its neighbours', or above a V scale
@@ -184,8 +193,9 @@ __device__ __forceinline__ void first_product(const Rows<D, NT>& rows, const uns
   }
 }
 
-// Y += V^T P^T for the channels 16 i .. 16 i + 16 kTogether - 1; FIRST: there is no sum to add to.
-template <bool FIRST, int NT>
+// Y += V^T P^T for the channels 16 i .. 16 i + 16 kTogether - 1; FIRST: there is no sum to add
+// to; SIZE: of |V|.
+template <bool FIRST, int NT, bool SIZE = false>
 __device__ __forceinline__ void second_product(const uint4* vx, int i, const uint32_t (&pf)[NT][4][2],
                                                float (&y)[NT][kTogether][4]) {
   uint4 u[kTogether];
@@ -198,6 +208,13 @@ __device__ __forceinline__ void second_product(const uint4* vx, int i, const uin
       uint32_t a[4], b[4];  // channels 16 i + gr and 8 more: tokens of steps k and k + 1
       decode8(word(u[h], k >> 1), a);
       decode8(word(u[h], 2 + (k >> 1)), b);
+      if constexpr (SIZE) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          a[x] &= 0x7fff7fffu;
+          b[x] &= 0x7fff7fffu;
+        }
+      }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         if (FIRST && k == 0) mma16816_first(y[t][h], a[0], b[0], a[1], b[1], pf[t][k][0], pf[t][k][1]);
@@ -212,6 +229,7 @@ __device__ __forceinline__ void second_product(const uint4* vx, int i, const uin
 struct Common {
   bool any;
   int gap;  // + 127, as a scale's byte; below 0: no block yet
+  float budget;  // blocks that may lose what fp16 leaves of small P
 };
 
 // A whole power of two as two factors, so that a sum is only lost where the result is: 2^-126 ends one.
@@ -226,11 +244,12 @@ __device__ __forceinline__ void stay_here() { asm volatile("" ::: "memory"); }
 __device__ __forceinline__ int place_token(int place) { return 8 * (place & 7) + (place >> 3); }
 
 // Scores of a block to P under the references that the sums have.  True, and the row sums
-// have their share, if every P is a normal number of fp16.  Of a block that is not seen
+// have their share, if every P is a normal number of fp16, or the budget allows for small
+// ones.  Of a block that is not seen
 // whole (`masked`) the scores that a row does not see are -infinity already, and the tokens
 // from `limit` on, which no row sees, may hold anything.
 template <int D, int NT>
-__device__ __forceinline__ bool as_is(const Rows<D, NT>& rows, Sums<D, NT>& sums, const Common& common,
+__device__ __forceinline__ bool as_is(const Rows<D, NT>& rows, Sums<D, NT>& sums, Common& common,
                                       const unsigned char* scales, int lane, bool masked, int limit,
                                       const float (&s)[NT][4][4], uint32_t (&pf)[NT][4][2]) {
   uint2 vs = reinterpret_cast<const uint2*>(scales + (D / 32) * kBlock)[lane >> 2];
@@ -251,6 +270,7 @@ __device__ __forceinline__ bool as_is(const Rows<D, NT>& rows, Sums<D, NT>& sums
   bool ok = static_cast<uint32_t>(common.gap) - (two & 0xffu) <= 14u && static_cast<uint32_t>(common.gap) - (two >> 8) <= 14u;
   const uint32_t back = (15u - static_cast<uint32_t>(common.gap)) * 0x04000400u;
   float l[NT][2];
+  bool normal = true;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     float high = -__int_as_float(0x7f800000);
@@ -282,9 +302,12 @@ __device__ __forceinline__ bool as_is(const Rows<D, NT>& rows, Sums<D, NT>& sums
       }
     }
     // (a NaN is in the sum, and in neither of the extremes)
-    ok = ok && high <= kBias && __hbge2(least, __half2half2(__ushort_as_half(0x0400))) && l[t][0] == l[t][0] && l[t][1] == l[t][1];
+    ok = ok && high <= kBias && l[t][0] == l[t][0] && l[t][1] == l[t][1];
+    normal = normal && __hbge2(least, __half2half2(__ushort_as_half(0x0400)));
   }
-  if (!__all_sync(0xffffffffu, ok)) return false;
+  if (!__all_sync(0xffffffffu, ok && (normal || common.budget >= 1.f))) return false;
+  // (a lane has 8 of a row's 64 P)
+  common.budget -= fminf(0.125f * __popc(__ballot_sync(0xffffffffu, !normal)), 1.f);
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -293,6 +316,12 @@ __device__ __forceinline__ bool as_is(const Rows<D, NT>& rows, Sums<D, NT>& sums
     for (int j = 0; j < 8; ++j) pf[t][j >> 1][j & 1] = transpose8x8(pf[t][j >> 1][j & 1]);
   }
   return true;
+}
+
+__device__ __forceinline__ float lowest(float x) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) x = fminf(x, __shfl_xor_sync(0xffffffffu, x, d));
+  return x;
 }
 
 // Brings the sums to references that are kHeadroom above the block's scores and a bit above
@@ -327,12 +356,14 @@ __device__ __forceinline__ void refer(const Rows<D, NT>& rows, Sums<D, NT>& sums
     }
   if (__any_sync(0xffffffffu, far)) return;
   common.gap = byte;
+  float down = 0.f;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const float m = sums.m[t][k];
-      const float2 turn = exp2_far((m - m1[t][k]) + (sums.gap[t][k] - gap));
+      const float m = sums.m[t][k], by = (m - m1[t][k]) + (sums.gap[t][k] - gap);
+      const float2 turn = exp2_far(by);
+      down = fminf(down, by);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         sums.acc[t][i][k] = sums.acc[t][i][k] * turn.x * turn.y;
@@ -342,6 +373,7 @@ __device__ __forceinline__ void refer(const Rows<D, NT>& rows, Sums<D, NT>& sums
       sums.m[t][k] = m1[t][k];
       sums.gap[t][k] = gap;
     }
+  common.budget *= exp2_approx(lowest(down));
 }
 
 // What a block that is not quick needs and changes.
@@ -390,7 +422,7 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
   }
   int scale = 0;  // the largest V scale that a row sees
   float f[NT][2];  // the power of two (<= 1) of the block in the output, times 2^kFactorBias
-  float most_gap = -inf;
+  float most_gap = -inf, shrunk = 0.f;  // the largest step of a row's sums to new references
   bool fresh = false;
 #pragma unroll 1
   for (int tk = 0; tk < 2 * NT; ++tk) {
@@ -445,10 +477,13 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
     // 0 where no key is seen; NaN where the scale of a seen V row is
     f[t][k] = bad ? nan : exp2_approx(up + (e - gap1) + kFactorBias);
     const float2 turn = exp2_far(down + (gap - gap1));
+    shrunk = fminf(shrunk, down + (gap - gap1));
+    if (down + (gap - gap1) != 0.f) {  // (the sums are in local memory here: a fourth of a block's time)
 #pragma unroll 1
-    for (int i = 0; i < D / 16; ++i) {
-      slow.sums.acc[t][i][k] = slow.sums.acc[t][i][k] * turn.x * turn.y;
-      slow.sums.acc[t][i][k + 2] = slow.sums.acc[t][i][k + 2] * turn.x * turn.y;
+      for (int i = 0; i < D / 16; ++i) {
+        slow.sums.acc[t][i][k] = slow.sums.acc[t][i][k] * turn.x * turn.y;
+        slow.sums.acc[t][i][k + 2] = slow.sums.acc[t][i][k + 2] * turn.x * turn.y;
+      }
     }
     slow.sums.m[t][k] = m1;
     slow.sums.gap[t][k] = gap1;
@@ -462,17 +497,21 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
   if (__any_sync(0xffffffffu, fresh)) most_gap += kHeadroom;
   if (above <= least_gap + kCommon) most_gap = fmaxf(most_gap, above);
   bool same = true;
+  float common_by = 0.f;
 #pragma unroll 1
   for (int tk = 0; tk < 2 * NT; ++tk) {
     const int t = tk >> 1, k = tk & 1;
     const bool near = most_gap - slow.sums.gap[t][k] <= kCommon;
     const float turn = near ? exp2_approx(slow.sums.gap[t][k] - most_gap) : 1.f;
+    if (near) common_by = fminf(common_by, slow.sums.gap[t][k] - most_gap);
     same = same && near;
     f[t][k] *= turn;
+    if (turn != 1.f) {
 #pragma unroll 1
-    for (int i = 0; i < D / 16; ++i) {
-      slow.sums.acc[t][i][k] *= turn;
-      slow.sums.acc[t][i][k + 2] *= turn;
+      for (int i = 0; i < D / 16; ++i) {
+        slow.sums.acc[t][i][k] *= turn;
+        slow.sums.acc[t][i][k + 2] *= turn;
+      }
     }
     if (near) slow.sums.gap[t][k] = most_gap;
   }
@@ -484,6 +523,8 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
   const Probabilities<NT> prob = {Sh::kOwnP ? sm.p[Sh::kOwnP ? warp : 0] : reinterpret_cast<float4(*)[4][32]>(block)};
   prob.put(slow.s);
   bool sure = false;  // that further passes are needed
+  bool first = true;  // pass: the same in all lanes, as the products need
+  float least = inf;  // sum of P |v| over rows and channels
   float pass = 1.f / (1 << static_cast<int>(kFactorBias));  // what this one's P count
 #pragma unroll 1
   while (true) {
@@ -492,6 +533,16 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
 #pragma unroll 1
     for (int i = 0; i < D / 16; i += kTogether) {
       float y[NT][kTogether][4];
+      if (first) {
+        second_product<true, NT, true>(vx, i, pf, y);
+#pragma unroll
+        for (int h = 0; h < kTogether; ++h)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (t * 8 + 2 * tc + (k & 1) < nrows) least = fminf(least, y[t][h][k] * pass * f[t][k & 1]);
+      }
       second_product<true, NT>(vx, i, pf, y);
 #pragma unroll
       for (int h = 0; h < kTogether; ++h)
@@ -508,7 +559,9 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
     sure = true;
     prob.next();  // three times at most: P are 0 or above 2^-126
     pass *= 1.f / kNextPass;
+    first = false;
   }
+  slow.common.budget = slow.common.budget * exp2_approx(lowest(shrunk + common_by)) + lowest(least) * (1.f / kSmallLoss);
 }
 
 // A unit takes a warp its blocks and about three blocks' time more: its query rows, its
@@ -763,7 +816,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_cache4_attention(const AttnP
       const Rows<D, NT> rows(p, qx, cc.s.p0, rr0, nrows);
       Sums<D, NT> sums;
       sums.clear();
-      Common common = {true, -999};
+      Common common = {true, -999, 0.f};
 #pragma unroll 1
       for (int step = 0; step < steps; ++step) {
         unsigned char* block = sm.ring[warp][slot];

@@ -50,6 +50,23 @@ def test_scores_spread_from_nothing_to_far(d, rows, size):
     _check(o, lse, ref.attention(table, lens, _f64(q), _cu(new), d ** -0.5))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [2.0, 4.0, 8.0])
+@pytest.mark.parametrize("zeros", [0.0, 0.7, 0.97])
+def test_peaked_rows_over_many_blocks_with_zeros_in_v(d, size, zeros):
+    """Runs of several blocks whose scores deviate by nats, so that small weights meet channels in which the heavy keys are
+    zero: what they add counts all the same."""
+    rng = np.random.default_rng(int(size) + d + int(100 * zeros))
+    lens = [4000] * 20
+    table, (cache, ref) = _random_cache(lens, 4, d, rng, spread=3, low=124)
+    for half in (0x0F, 0xF0):
+        ref.v[rng.random(ref.v.shape) < zeros] &= half
+    cache.v.copy_(torch.tensor(ref.v))
+    q = _bf16(rng.normal(size=(20, 8, d)) * 0.5 * size)
+    o, lse = pkg.cache_attention(cache, _i32(table), _i32(lens), q.cuda())
+    _check(o, lse, ref.attention(table, lens, _f64(q), np.arange(21), d ** -0.5))
+
+
 @pytest.mark.parametrize("rising", [False, True])
 def test_scores_that_rise_and_fall_from_block_to_block(rising):
     """Each block's scores lie some bits beyond the last one's: references are made anew again and again, or are far above."""
