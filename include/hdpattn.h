@@ -449,9 +449,9 @@ hdp_status_t hdp_fourbit_read(const hdp_fourbit_cache_t* cache, const int32_t* c
 
 /* hdp_cache_attention over this cache: the same formulas, arguments and promises,
  * over all blocks (there are no lists), but that weights count down to 2^-100 of a
- * row's largest, and that where a row's score passes fp32's end before it is
- * multiplied by `scale`, K scales below 2^-94 may count as 0 in the 64 keys of its
- * block.  workspace: device, 256-byte aligned, at least
+ * row's largest and to within 2^-12 of a channel's sum of weight times |v|, and that
+ * where a row's score passes fp32's end before it is multiplied by `scale`, K scales
+ * below 2^-94 may count as 0 in the 64 keys of its block.  workspace: device, 256-byte aligned, at least
  * hdp_fourbit_attention_workspace_bytes, which depends on the device's SM count and
  * d only (152 SMs: 12.7 MB for d = 128, 6.4 MB for d = 64); calls that may overlap
  * need one each. */
