@@ -1,14 +1,19 @@
 // Attention of the newest tokens of each sequence over the 4-bit cache.
 //
-// How the work is cut, handed out and joined, and what carries the softmax over scores
-// and V scales of any size, is the 8-bit cache's (kv_attention.cu).  Here are a block's
-// products.  A key and kv head is d + d / 32 + 1 bytes, half of the 8-bit cache's, so the
-// same memory rate leaves half the time for each, and instructions bound the loop, not
-// bytes: on this GPU an m16n8k16 product takes a scheduler 8.3 cycles, and conversions and
-// multiply-adds between products add a cycle each rather than hide behind them (measured
-// in isolation), so the 64 products and 256 conversions of a block are 800 cycles of the
-// 1,450 that HBM takes for it.
+// The flat order of (sequence, head, tile, block), and what carries the softmax over scores
+// and V scales of any size, are the 8-bit cache's (kv_attention.cu).  A key and kv head is
+// d + d / 32 + 1 bytes, half of the 8-bit cache's, so the same memory rate leaves half the
+// time for each: on this GPU an m16n8k16 product takes a scheduler 8.3 cycles, and
+// conversions and multiply-adds between products add a cycle each rather than hide behind
+// them (measured in isolation), so the 64 products and 256 conversions of a block are 800
+// cycles of the 1,450 that HBM takes for it.
 //
+//   Work.  Each of 8 warps an SM has an equal run of the order and a ring of blocks in
+//   shared memory of its own, K and V of a block asked for apart; no barrier stands in the
+//   loop.  Parts of a unit are joined within the CTA, then between CTAs by a small kernel.
+//   Measured (32 / 8 heads of 128, in a captured graph): 2,097,152 tokens 336 us, 6.6 TB/s,
+//   0.98 of the copy rate; 64 sequences of 411,000 tokens 92 us, 0.81: 4 to 8 us until data
+//   flows, SMs that end 9 us apart, 4 us for the join.
 //   Codes.  e2m1 is exact in fp16, and the conversion instruction takes a byte: one
 //   for two codes, where the 8-bit kinds need four and seven cycles for as many.  The
 //   cache's order of bytes is the fragments': K's words have one group of 32 channels
@@ -30,9 +35,9 @@
 //   of a peaked row: what fp16 leaves of a small P counts only in a channel where the keys
 //   that weigh more are zero, and a block on that path also forms the sum of P |v| for each
 //   row and channel.  The smallest of them is a budget: so many blocks with small P stay
-//   quick that all they lose is 2^-12 of that sum, half a step of an fp16 P at most.  (64 sequences whose scores deviate by
-//   1.7, 2.5 and 3.4 nats: 161, 321 and 461 us; 299, 792 and 802 without a budget, and all
-//   sums rescaled for each block; by 0.85, as the cases do, 92.)
+//   quick that all they lose is 2^-12 of that sum (a P's rounding is up to 2^-11 of it).
+//   64 sequences whose scores deviate by 1.7, 2.5 and 3.4 nats: 161, 321 and 461 us; 299,
+//   792 and 802 without a budget and with all sums rescaled for each block; by 0.85, 92.
 #include "kv_attention.cuh"
 #include "kv_cache4.cuh"
 
