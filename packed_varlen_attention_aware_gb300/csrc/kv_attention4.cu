@@ -11,7 +11,7 @@
 //   Work.  Each of 8 warps an SM has an equal run of the order and a ring of blocks in
 //   shared memory of its own, K and V of a block asked for apart; no barrier stands in the
 //   loop.  Parts of a unit are joined within the CTA, then between CTAs by a small kernel.
-//   Measured (32 / 8 heads of 128, in a captured graph): 2,097,152 tokens 336 us, 6.6 TB/s,
+//   Measured (32 / 8 heads of 128, in a captured graph): 2,097,152 tokens 338 us, 6.6 TB/s,
 //   0.98 of the copy rate; 64 sequences of 411,000 tokens 92 us, 0.81: 4 to 8 us until data
 //   flows, SMs that end 9 us apart, 4 us for the join.
 //   Codes.  e2m1 is exact in fp16, and the conversion instruction takes a byte: one
@@ -36,8 +36,13 @@
 //   that weigh more are zero, and a block on that path also forms the sum of P |v| for each
 //   row and channel.  The smallest of them is a budget: so many blocks with small P stay
 //   quick that all they lose is 2^-12 of that sum (a P's rounding is up to 2^-11 of it).
-//   64 sequences whose scores deviate by 1.7, 2.5 and 3.4 nats: 161, 321 and 461 us; 299,
+//   64 sequences whose scores deviate by 1.7, 2.5 and 3.4 nats: 165, 326 and 482 us; 299,
 //   792 and 802 without a budget and with all sums rescaled for each block; by 0.85, 92.
+//   Scores past fp32's end.  A sum of products may pass it before the row's factor brings it
+//   back, and a NaN scale makes it infinite: such a block goes to the general path.  As
+//   -infinity it would pass for a masked one.  Only blocks that are not all normal are
+//   searched for it: in them its P is 0.  (Part of the times above: 161, 321 and 461 us, and
+//   2M tokens 336 instead of 338, without the search.)
 #include "kv_attention.cuh"
 #include "kv_cache4.cuh"
 
@@ -250,9 +255,10 @@ __device__ __forceinline__ int place_token(int place) { return 8 * (place & 7) +
 
 // Scores of a block to P under the references that the sums have.  True, and the row sums
 // have their share, if every P is a normal number of fp16, or the budget allows for small
-// ones.  Of a block that is not seen
-// whole (`masked`) the scores that a row does not see are -infinity already, and the tokens
-// from `limit` on, which no row sees, may hold anything.
+// ones, and no seen score has passed fp32's end.  (Infinity and NaN are noticed as such; the
+// P of -infinity is 0, which is not normal, as a masked key's may be.)  Of a block that is
+// not seen whole (`masked`) the scores that a row does not see are -infinity already, no
+// others are, and the tokens from `limit` on, which no row sees, may hold anything.
 template <int D, int NT>
 __device__ __forceinline__ bool as_is(const Rows<D, NT>& rows, Sums<D, NT>& sums, Common& common,
                                       const unsigned char* scales, int lane, bool masked, int limit,
@@ -310,9 +316,21 @@ __device__ __forceinline__ bool as_is(const Rows<D, NT>& rows, Sums<D, NT>& sums
     ok = ok && high <= kBias && l[t][0] == l[t][0] && l[t][1] == l[t][1];
     normal = normal && __hbge2(least, __half2half2(__ushort_as_half(0x0400)));
   }
-  if (!__all_sync(0xffffffffu, ok && (normal || common.budget >= 1.f))) return false;
-  // (a lane has 8 of a row's 64 P)
-  common.budget -= fminf(0.125f * __popc(__ballot_sync(0xffffffffu, !normal)), 1.f);
+  if (!__all_sync(0xffffffffu, ok && normal)) {
+    if (!(common.budget >= 1.f)) return false;
+    stay_here();
+    if (!masked) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ok = ok && s[t][i][k] != -__int_as_float(0x7f800000);
+    }
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    // (a lane has 8 of a row's 64 P)
+    common.budget -= fminf(0.125f * __popc(__ballot_sync(0xffffffffu, !normal)), 1.f);
+  }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -845,8 +863,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_cache4_attention(const AttnP
 #pragma unroll
               for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  if (key0 + 16 * i + 8 * (k >> 1) + (lane >> 2) > rows.pos[t][k & 1]) s[t][i][k] = -__int_as_float(0x7f800000);
+                for (int k = 0; k < 4; ++k) {
+                  // a seen score that is -infinity has passed fp32's end: NaN, lest it pass for masked
+                  float& x = s[t][i][k];
+                  if (x == -__int_as_float(0x7f800000)) x = __int_as_float(0x7fc00000);
+                  if (key0 + 16 * i + 8 * (k >> 1) + (lane >> 2) > rows.pos[t][k & 1]) x = -__int_as_float(0x7f800000);
+                }
           }
           if (common.any) {
             quick = as_is<D, NT>(rows, sums, common, scales, lane, masked, limit, s, pf);
