@@ -349,7 +349,8 @@ hdp_status_t hdp_cache_read(const hdp_cache_t* cache, const int32_t* cu, int64_t
  * and query head h (kv head h / (hq / hkv)),
  *   S_j = scale * q . k_j over cached tokens j <= p,
  *   lse = ln sum_j exp(S_j),  o = sum_j exp(S_j - lse) v_j,
- * and o = 0, lse = -inf where no token is left.  Inputs are the dequantised
+ * and o = 0, lse = -inf where no token is left; o and lse are NaN for a query row
+ * with an infinity or NaN that has a token left.  Inputs are the dequantised
  * codes; sums and the softmax's statistics are fp32.  That holds for q, K and V
  * over all of bf16's range, scores up to fp32's end, and weights down to 2^-126
  * of a row's largest, where weight times V scale is at least 2^-100 of the row's

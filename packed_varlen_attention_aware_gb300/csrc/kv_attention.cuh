@@ -344,7 +344,7 @@ struct Rows {
       top = max(top & 0xffffu, top >> 16);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // the largest element's exponent goes to 14; infinities and NaN stay what they are
+      // the largest element's exponent goes to 14
       const int e = min(max(static_cast<int>(top >> 7) - 127, -112), 127) - 14;
       const float down = pow2i(-e);
 #pragma unroll
@@ -356,7 +356,9 @@ struct Rows {
           q[t][i * 2 + (k >> 1)][k & 1] = h2_bits(y);
         }
       }
-      const float s = p.scale_log2 * pow2i(e);
+      // A row with an infinity or NaN is NaN whatever the keys are: products that are all
+      // -infinity would read as a row that sees no key.
+      const float s = top >= 0x7f80u ? __int_as_float(0x7fc00000) : p.scale_log2 * pow2i(e);
       scale[t][0] = __shfl_sync(0xffffffffu, s, tc * 8);
       scale[t][1] = __shfl_sync(0xffffffffu, s, tc * 8 + 4);
 #pragma unroll
