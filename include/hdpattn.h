@@ -515,8 +515,10 @@ hdp_status_t hdp_cache_rows(const int32_t* page_table, const int32_t* lens, cons
  *   position [rows] int32; a row at a negative one is not read, its output is left
  *   as it was.  freqs [rot/2] double, radians, finite (device; scaling for long
  *   contexts is in them and in factor).  2 <= rot <= d <= 256, rot even; factor > 0.
- * The angle's fraction of a turn is exact to 2^-31 over all positions.  Products
- * and sums are fp32, rounded once to `type`.
+ * The angle's fraction of a turn is right to 2^-31 over all positions and
+ * frequencies below 2^53 in magnitude (beyond them nothing is promised) and, as a
+ * fraction of half a turn, rounded to fp32.  Products and sums are fp32, rounded once
+ * to `type`.
  */
 #define HDP_TYPE_BF16 0
 #define HDP_TYPE_FP16 1

@@ -7,9 +7,11 @@
 //
 //   Angles.  p theta in fp32 is off by 0.1 radians at two million positions.  The
 //   angle is kept in turns instead, as a 64-bit fraction: theta / 2 pi mod 1 times
-//   2^64 is a whole number, p times it mod 2^64 is exact, and what is left is the
-//   angle's fraction of a turn to 2^-33 for any 31-bit p (theta / 2 pi is rounded at
-//   2^-53 of itself).  As a signed number it is within half a turn, which sincospi
+//   2^64 is a whole number, cut off from the exact product of theta's 53 bits and 128
+//   bits of 1 / 2 pi; p times it mod 2^64 is exact, and what is left is the angle's
+//   fraction of a turn to 2^-33 for any 31-bit p and |theta| < 2^53.  (A double holds
+//   theta / 2 pi to 2^-53 of itself only: times 2^31 that is 2^-18 of a turn at 100
+//   radians a position.)  As a signed number it is within half a turn, which sincospi
 //   takes in fp32.
 //   Sharing.  A token's cosines and sines serve all its heads: a CTA works them out
 //   for a tile of tokens, one pair a thread, and its threads then go over the
@@ -18,9 +20,9 @@
 //   looks for their partners in it or in shared memory; other rows go by two elements or
 //   one at a time.
 //
-// Measured: 40,121 rows of 40 heads of 128 bf16, 125 us, 0.97 of the copy rate; 131,072 of
-// 40 heads with 64 of 128 channels turned, the gradient, 417 us, 0.95; 131,072 of 10
-// heads, as many turned, 126 us, 0.78: there a token's angles count.
+// Measured: 40,121 rows of 40 heads of 128 bf16, 124 us, 0.97 of the copy rate; 131,072 of
+// 40 heads with 64 of 128 channels turned, the gradient, 418 us, 0.95; 131,072 of 10
+// heads, as many turned, 117 us, 0.85: there a token's angles count.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -87,15 +89,33 @@ extern __shared__ __align__(16) float s_angles[];
 
 int shared_bytes(const Rotary& p) { return p.tile * (p.rot + 1) * 4; }
 
+// theta / 2 pi mod 1 in units of 2^-64, cut off: theta = m 2^e, and m / 2 pi, with the digits
+// of 1 / 2 pi as whole numbers (Payne and Hanek, 1983), has 64 bits in front of the point and
+// 128 behind it.
+__device__ __forceinline__ unsigned long long turns(double theta) {
+  using u64 = unsigned long long;
+  constexpr u64 kHigh = 0x28be60db9391054aull, kLow = 0x7f09d5f47d4d3770ull;  // 2^128 / 2 pi
+  const u64 bits = static_cast<u64>(__double_as_longlong(theta));
+  const int e = static_cast<int>(bits >> 52 & 0x7ff) - 1075;
+  const u64 m = (bits & 0xfffffffffffffull) | 1ull << 52;
+  const u64 p0 = kLow * m, p1 = __umul64hi(kLow, m) + kHigh * m;
+  const u64 p2 = __umul64hi(kHigh, m) + (p1 < kHigh * m);
+  const int shift = 64 - e;  // (of a subnormal theta's too: nothing is left)
+  u64 x = 0;
+  if (shift >= 128) x = shift < 192 ? p2 >> (shift - 128) : 0;
+  else if (shift > 64) x = p1 >> (shift - 64) | p2 << (128 - shift);
+  else if (shift == 64) x = p1;
+  else if (shift > 0) x = p0 >> shift | p1 << (64 - shift);
+  return theta < 0 ? 0 - x : x;
+}
+
 // Positions of the tile's tokens, and cosines and sines of their pairs.
 __device__ __forceinline__ void angles(const Rotary& p, long long row0, int n, float* s_cos, float* s_sin, int* s_pos) {
   const int half = p.rot / 2, tokens = kThreads / half;  // at a time
   const int t0 = threadIdx.x / half, i = threadIdx.x - t0 * half;
   if (t0 < tokens && t0 < n) {
     int at = __ldg(p.pos + row0 + t0);
-    double turn = __ldg(p.freqs + i) * 0.15915494309189535;  // 1 / 2 pi
-    turn -= floor(turn);
-    const unsigned long long step = static_cast<unsigned long long>(turn * 18446744073709551616.0);
+    const unsigned long long step = turns(__ldg(p.freqs + i));
     for (int t = t0, now; t < n; t += tokens) {
       now = at;
       if (t + tokens < n) at = __ldg(p.pos + row0 + t + tokens);
