@@ -508,10 +508,10 @@ hdp_status_t hdp_cache_rows(const int32_t* page_table, const int32_t* lens, cons
  * gradient of the rows before the turn from that of the rows behind it.
  *   q, k: either may be NULL.  Rows [rows][heads][d] of `type`, channels
  *   contiguous, other strides in elements; out may be in (with the same strides),
- *   else the two must not overlap, and neither out may overlap the other's rows.
- *   Any alignment; 16-byte steps where the
- *   addresses, strides and rot allow them (slower, but the same results, where rot or
- *   they do not).
+ *   else the two must not overlap, and neither out may overlap the other's rows or
+ *   itself: such calls are refused (so are rows with different strides that lie
+ *   between each other).  Any alignment; 16-byte steps where the addresses, strides
+ *   and rot allow them (slower, but the same results, where rot or they do not).
  *   position [rows] int32; a row at a negative one is not read, its output is left
  *   as it was.  freqs [rot/2] double, radians, finite (device; scaling for long
  *   contexts is in them and in factor).  2 <= rot <= d <= 256, rot even; factor > 0.

@@ -26,8 +26,10 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include <type_traits>
+#include <algorithm>
+#include <cstdlib>
 #include <string>
+#include <type_traits>
 
 #include "internal.h"
 
@@ -290,6 +292,70 @@ void launch_for(const Rotary& p, uintptr_t bits, uintptr_t lengths, bool neighbo
   }
 }
 
+// Rows of a tensor as the host sees them, in elements.
+struct Places {
+  long long at, row, head;
+  int heads;
+};
+
+// Is |x + n step| < d for an n in [-most, most]?
+bool comes_near(long long x, long long step, long long most, int d) {
+  if (step < 0) step = -step;
+  long long n = 0;  // the largest with x + n step <= 0
+  if (step > 0) n = x > 0 ? -((x + step - 1) / step) : -x / step;
+  for (int i = 0; i < 2; ++i) {
+    const long long y = x + std::min(std::max(n + i, -most), most) * step;
+    if (-d < y && y < d) return true;
+  }
+  return false;
+}
+
+// First and last element; false if they are not places in memory.
+bool ends_of(const Places& x, long long rows, int d, long long& first, long long& last) {
+  __int128 lo = x.at, hi = lo + d - 1;
+  for (const __int128 far : {static_cast<__int128>(x.row) * (rows - 1), static_cast<__int128>(x.head) * (x.heads - 1)})
+    (far < 0 ? lo : hi) += far;
+  constexpr long long kMost = 1LL << 61;
+  if (lo < -kMost || hi > kMost) return false;
+  first = static_cast<long long>(lo);
+  last = static_cast<long long>(hi);
+  return true;
+}
+
+// May a and b have an element in common?  A "no" is sure, and so is a "yes" but for rows
+// with different strides, or more heads than are worth comparing, within the same memory.
+bool may_meet(Places a, Places b, long long rows, int d) {
+  long long a0, a1, b0, b1;
+  if (!ends_of(a, rows, d, a0, a1) || !ends_of(b, rows, d, b0, b1)) return true;
+  if (a1 < b0 || b1 < a0) return false;
+  if (rows > 1 && a.row != b.row) return true;
+  if (a.heads == 1) a.head = b.head;
+  if (b.heads == 1) b.head = a.head;
+  const long long x = a.at - b.at;
+  if (a.head == b.head) {
+    for (int m = 1 - b.heads; m < a.heads; ++m)
+      if (comes_near(x + m * a.head, a.row, rows - 1, d)) return true;
+    return false;
+  }
+  if (static_cast<long long>(a.heads) * b.heads > 1 << 16) return true;
+  for (int h = 0; h < a.heads; ++h)
+    for (int g = 0; g < b.heads; ++g)
+      if (comes_near(x + h * a.head - g * b.head, a.row, rows - 1, d)) return true;
+  return false;
+}
+
+// Do two heads of two rows of x have an element in common?
+bool meets_itself(const Places& x, long long rows, int d) {
+  long long first, last;
+  if (!ends_of(x, rows, d, first, last)) return true;
+  const long long row = std::abs(x.row), head = std::abs(x.head);
+  if (rows > 1 && row < d) return true;
+  if (x.heads == 1 || (head >= d && (rows == 1 || row >= head * (x.heads - 1) + d))) return false;
+  for (int m = 1; m < x.heads; ++m)
+    if (comes_near(m * x.head, x.row, rows - 1, d)) return true;
+  return false;
+}
+
 }  // namespace
 }  // namespace hdp
 
@@ -330,7 +396,20 @@ extern "C" hdp_status_t hdp_rotary(const hdp_rotary_rows_t* q, const hdp_rotary_
     p.copy = p.copy || x->in != x->out;
   }
   if (rows == 0 || p.heads[0] + p.heads[1] == 0) return HDP_OK;
-  if (p.heads[0] && p.heads[1] && (p.x[0].out == p.x[1].out || p.x[0].out == p.x[1].in || p.x[1].out == p.x[0].in))
+  Places in[2], out[2];
+  for (int i = 0; i < 2; ++i) {
+    if (!p.heads[i]) continue;
+    const RotaryTensor& x = p.x[i];
+    in[i] = {static_cast<long long>(reinterpret_cast<intptr_t>(x.in) / size), x.in_row, x.in_head, p.heads[i]};
+    out[i] = {static_cast<long long>(reinterpret_cast<intptr_t>(x.out) / size), x.out_row, x.out_head, p.heads[i]};
+    if (meets_itself(out[i], rows, d))
+      return fail(HDP_ERR_INVALID_ARGUMENT, name + "rows and heads of an output must not overlap");
+    if (x.in != x.out && may_meet(in[i], out[i], rows, d))
+      return fail(HDP_ERR_INVALID_ARGUMENT, name + "an output must be its input or not overlap it");
+  }
+  if (p.heads[0] && p.heads[1] &&
+      (may_meet(out[0], out[1], rows, d) || (p.x[1].in != p.x[1].out && may_meet(out[0], in[1], rows, d)) ||
+       (p.x[0].in != p.x[0].out && may_meet(out[1], in[0], rows, d))))
     return fail(HDP_ERR_INVALID_ARGUMENT, name + "what is written for q and k must not be rows of the other");
   if (!position || !freqs) return fail(HDP_ERR_INVALID_ARGUMENT, name + "position or freqs is NULL");
   if (reinterpret_cast<uintptr_t>(freqs) & 7) return fail(HDP_ERR_INVALID_ARGUMENT, name + "freqs must be 8-byte aligned");
