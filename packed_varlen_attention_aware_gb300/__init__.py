@@ -276,6 +276,11 @@ def _turned(q, k, position, freqs, neighbours, backward, factor, inplace, stream
     out = (q, k) if inplace else (None, None)
     with _pool(stream, q if q is not None else k):
         out = _rotary(q, k, position, freqs, *out, neighbours, backward, factor, stream)
+    if inplace:
+        import torch
+
+        # a backward pass that has kept q or k from before refuses to use what is there now
+        torch.autograd.graph.increment_version([x for x in (q, k) if x is not None])
     _in_use(stream, None, q, k, position, freqs)
     return out
 
@@ -285,8 +290,9 @@ def rotary(q, k, position, freqs, neighbours: bool = False, factor: float = 1.0,
     pairs of the first 2 * len(freqs) channels of each head, channels i and i + len(freqs), or with neighbours 2 i and
     2 i + 1, are turned by position * freqs[i] and scaled by factor.  position int32 [rows] (cache_rows gives them), freqs
     float64 (rotary_frequencies).  Rows at a negative position are not written: in place they keep their values, in the new
-    tensors that are returned otherwise those rows are not initialised.  In place, q and k must not share memory.  Returns
-    the turned (q, k)."""
+    tensors that are returned otherwise those rows are not initialised.  In place, q and k must not share memory.  As
+    everywhere in this package, gradients are not recorded: what is returned has no history, whatever q and k require, and
+    rotary_backward is called for the gradients.  Returns the turned (q, k)."""
     return _turned(q, k, position, freqs, neighbours, False, factor, inplace, stream)
 
 
