@@ -351,8 +351,10 @@ hdp_status_t hdp_cache_read(const hdp_cache_t* cache, const int32_t* cu, int64_t
  *   lse = ln sum_j exp(S_j),  o = sum_j exp(S_j - lse) v_j,
  * and o = 0, lse = -inf where no token is left; o and lse are NaN for a query row
  * with an infinity or NaN that has a token left.  Inputs are the dequantised
- * codes; sums and the softmax's statistics are fp32.  That holds for q, K and V
- * over all of bf16's range, scores up to fp32's end, and weights down to 2^-126
+ * codes; sums and the softmax's statistics are fp32, and a weight is rounded to 11
+ * bits where it multiplies V (it is off by 2^-11 of itself at most, and o by 2^-11
+ * of the sum of weight times |v|).  That holds for q, K and V
+ * over all of bf16's range, scores up to 2^127 in magnitude, and weights down to 2^-126
  * of a row's largest, where weight times V scale is at least 2^-100 of the row's
  * largest such product.  (What is smaller shows in channels in which the keys above
  * it have zeros.)  Elements of a query row below 2^-31 of its largest keep fewer
@@ -450,9 +452,12 @@ hdp_status_t hdp_fourbit_read(const hdp_fourbit_cache_t* cache, const int32_t* c
 
 /* hdp_cache_attention over this cache: the same formulas, arguments and promises,
  * over all blocks (there are no lists), but that weights count down to 2^-100 of a
- * row's largest and to within 2^-12 of a channel's sum of weight times |v|, and that
- * where a row's score passes fp32's end before it is multiplied by `scale`, K scales
- * below 2^-94 may count as 0 in the 64 keys of its block.  workspace: device, 256-byte aligned, at least
+ * row's largest; that small ones may together lose 2^-11 of a channel's sum of weight
+ * times |v| besides what each loses to rounding; and that where a row's score passes
+ * fp32's end before it is multiplied by `scale`, K scales below 2^-94 may count as 0 in
+ * the 64 keys of its block.  A call takes longer where the scores of a head deviate by
+ * more than a nat: 1.8 times as long at 1.7 nats, 5 times at 3.4.
+ * workspace: device, 256-byte aligned, at least
  * hdp_fourbit_attention_workspace_bytes, which depends on the device's SM count and
  * d only (152 SMs: 12.7 MB for d = 128, 6.4 MB for d = 64); calls that may overlap
  * need one each. */
@@ -474,7 +479,8 @@ hdp_status_t hdp_fourbit_attention(const hdp_fourbit_cache_t* cache, const int32
  *   2. Then each sequence, in order, takes a page from the top for every block
  *      that it lacks, in order.  A sequence whose blocks are not all there, and
  *      every later one that lacks any, takes none and keeps its held[i]; the next
- *      hdp_device_status then reports OUT_OF_MEMORY.
+ *      hdp_device_status then reports OUT_OF_MEMORY, unless something else has to be
+ *      reported: one call reports one failure.
  * free_pages, free_count, held and page_table are updated in place; taking pages
  * and giving them back leaves the stack as it was.  Entries of page_table beyond
  * held[i] are left as they are.  Lengths, held and free_count outside their ranges

@@ -140,3 +140,29 @@ def test_nan_scales_in_a_few_tokens(sign, rows):
     o, lse = pkg.cache_attention(cache, _i32(table), _i32(lens), q.cuda(), cu=None if rows == 1 else _i32([0, 2, 4]))
     assert torch.isnan(o[rows:]).all() and torch.isnan(lse[:, rows:]).all()
     assert torch.isfinite(o[:rows]).all() and torch.isfinite(lse[:, :rows]).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("runs", [False, True])
+def test_scores_of_the_largest_magnitude(d, runs):
+    """Scores of 1.75 * 2^126, 0 and their negatives: the largest has all of the weight, whichever sign it has."""
+    rng = np.random.default_rng(d)
+    n, tokens = 3, 100
+    table, pages = _table([tokens] * n, rng)
+    cache, ref = _pair(_garbage(pages, 1, d, rng))
+    k, v = np.zeros((n * tokens, 1, d)), _bf16(rng.normal(size=(n * tokens, 1, d)))
+    k[:, 0, 0] = -2.0 ** 100  # sequence 2: all the same
+    k[70, 0, 0], k[tokens + 9, 0, 0] = 2.0 ** 100, 0  # sequence 0: one far above; 1: one between
+    k = _bf16(k)
+    lens, cu = _i32([tokens] * n), _i32(_cu([tokens] * n))
+    pkg.cache_append(cache, _i32(table), lens, k.cuda(), v.cuda(), cu=cu)
+    held = _f64(pkg.cache_read(cache, _i32(table), lens, n * tokens, cu=cu)[1])
+    q = np.zeros((n, 2, d))
+    q[:, :, 0] = 1.75 * 2.0 ** 26
+    o, lse = pkg.cache_attention(cache, _i32(table), lens, _bf16(q).cuda(), cu=_i32(range(n + 1)) if runs else None, scale=1.0)
+    for i, row in ((0, held[70, 0]), (1, held[tokens + 9, 0])):
+        assert np.abs(_f64(o)[i] - row).max() <= 2.0 ** -8 * np.abs(row).max()
+    mean, size = held[2 * tokens:, 0].mean(0), np.abs(held[2 * tokens:, 0]).mean(0)
+    assert (np.abs(_f64(o)[2] - mean) <= 2.0 ** -8 * np.abs(mean) + (2.0 ** -11 + 2.0 ** -18) * size).all()
+    top = 1.75 * 2.0 ** 126
+    assert np.abs(_f64(lse) / top - [1, 0, -1]).max() <= 2.0 ** -20
