@@ -52,6 +52,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+constexpr int kMeta = 8;  // blocks whose scales and first key are kept
 constexpr PartCount kCount = {kWarps * (1 + kMorePieces), kWarps * (1 + kMorePieces) * 2};
 // Bytes of a warp's ring of half blocks.  More in flight streams a long run
 // better; less leaves the memory's queues shorter, and with them every other
@@ -66,6 +67,23 @@ constexpr int kRingBytes = NT == 1 && !SPARSE ? 24576 : 16384;
 // code, 127 or 448; 2^12 times that is enough of an output to forget it.
 template <int FMT>
 constexpr float kEnough = FMT == HDP_CACHE_INT8 ? 1.f : 4.f;
+
+struct Meta {
+  float sk, sv;
+  int key0;   // first key of the block; -1: nothing of it is seen
+  int piece;  // the piece that the block belongs to
+};
+
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// The smallest magnitude.
+__device__ __forceinline__ float least_of(float a, float b, float c) {
+  float r;
+  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 // Four codes to fp16: bytes 0, 1 and bytes 2, 3.
 template <int FMT>
@@ -586,13 +604,138 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attention(const AttnParam
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Zeroes the counters while the attention's CTAs are starting.
+__global__ void k_cache_attention_start(const AttnParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x < 2) p.head[threadIdx.x] = 0;
+}
+
+// Joins the parts of units that several pieces share.  A CTA has every n-th
+// open unit (n CTAs), and its warps take rows of up to kAlone parts in turn.  A
+// 2M-token sequence leaves 600 parts for each of its few heads: the rows of such
+// units are dealt to all CTAs, whose warps then share a row's parts (that call:
+// 646 us with each unit's CTA joining its rows itself, 636 us so).
+template <int D, int NT>
+__global__ void __launch_bounds__(kJoinWarps * 32, 1) k_cache_attention_join(const AttnParams p, int pieces) {
+  constexpr int kRows = 8 * NT;
+  constexpr int kAlone = 48;  // most parts of a row that a warp joins alone
+  constexpr int kFew = 256;   // most parts of rows that a CTA joins at once
+  // Two units share at most one piece, so n units of more than kAlone parts take
+  // more than n (kAlone - 1) pieces; of the others a CTA has one for each
+  // gridDim.x pieces.  The host keeps both below this.
+  constexpr int kMostShared = 192;
+  constexpr int V = D / 32;
+  __shared__ __align__(16) float s_x[kJoinWarps][D];
+  __shared__ float2 s_sum[kJoinWarps];
+  __shared__ int4 s_shared[kMostShared][2], s_own[kMostShared][2];  // shared units, and this CTA's others
+  __shared__ int s_n, s_own_n;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) s_n = s_own_n = 0;
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int made = min(pieces, __ldcg(p.head + (p.dynamic ? 0 : 2)));
+  auto at = [&](int e, int k, int r) { return (static_cast<size_t>(e + k) * 2 + (k == 0 ? 1 : 0)) * kRows + r; };
+
+  // This CTA's open units, and all shared ones where the units are listed as they
+  // came; where each piece has an entry (1,216 of them, which 152 CTAs reading all
+  // would take 4 us for), a CTA keeps to its own.
+  const int stride = p.dynamic ? 1 : gridDim.x, origin = p.dynamic ? 0 : blockIdx.x;
+  constexpr int kScan = 2;
+  for (int base = 0; base == 0 || origin + base * stride < made; base += kScan * kJoinWarps * 32) {
+    int4 a[kScan], b[kScan];  // the first loads do not wait for the units' number
+#pragma unroll
+    for (int u = 0; u < kScan; ++u) {
+      const int i = origin + (base + u * kJoinWarps * 32 + static_cast<int>(threadIdx.x)) * stride;
+      a[u] = b[u] = make_int4(0, 0, 0, 0);
+      if (i < pieces) {
+        a[u] = __ldcg(reinterpret_cast<const int4*>(p.open + i));
+        b[u] = __ldcg(reinterpret_cast<const int4*>(p.open + i) + 1);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kScan; ++u) {
+      const int i = origin + (base + u * kJoinWarps * 32 + static_cast<int>(threadIdx.x)) * stride;
+      if (i >= made || a[u].x == 0) continue;
+      const bool shared = a[u].x > kAlone;
+      if (!shared && i % gridDim.x != blockIdx.x) continue;
+      const int n = atomicAdd(shared ? &s_n : &s_own_n, 1);
+      if (n >= kMostShared) continue;  // cannot be (see there)
+      int4* to = shared ? s_shared[n] : s_own[n];
+      to[0] = a[u];
+      to[1] = b[u];
+    }
+  }
+  __syncthreads();
+
+  const int own = min(s_own_n, kMostShared);
+  int nth = 0;
+  for (int q = 0; q < own; ++q) {
+    const int4 a = s_own[q][0], b = s_own[q][1];
+    for (int r = 0; r < b.x; ++r) {
+      if (nth++ % kJoinWarps != warp) continue;
+      float x[V];
+      const float2 sum = join_row<D>(
+          a.x, lane, x, [&](int k) { return __ldcg(p.part_sum + at(a.y, k, r)); },
+          [&](int k) { return p.part + at(a.y, k, r) * D; });
+      write_o<D>(p, a.z, a.w, b.y + r, x, lse_of(sum.x, sum.y), lane);
+    }
+  }
+
+  const int n = min(s_n, kMostShared);
+  for (int q = 0; q < n; ++q) {
+    const int4 a = s_shared[q][0], b = s_shared[q][1];
+    const int m = a.x, e = a.y, nrows = b.x;
+    int rank = 0;  // of its first piece: the same in every CTA, whose lists differ in order
+    for (int z = lane; z < n; z += 32) rank += s_shared[z][0].y < e;
+    rank = __reduce_add_sync(0xffffffffu, rank);
+    // rows that a CTA joins at once, and warps for each
+    const int rows = m > kFew ? 1 : min(kJoinWarps, 1 << (32 - __clz(nrows - 1)) % 32), each = kJoinWarps / rows;
+    const int nr = warp / each, run = warp - nr * each;
+    for (int r0 = 0; r0 < nrows; r0 += rows) {
+      if (p.dynamic && (rank * nrows + r0) % static_cast<int>(gridDim.x) != static_cast<int>(blockIdx.x)) continue;
+      const int r = r0 + nr;
+      float x[V];
+      if (r < nrows) {
+        const int k0 = m * run / each, k1 = m * (run + 1) / each;
+        const float2 part = join_row<D>(
+            k1 - k0, lane, x, [&](int k) { return __ldcg(p.part_sum + at(e, k0 + k, r)); },
+            [&](int k) { return p.part + at(e, k0 + k, r) * D; });
+#pragma unroll
+        for (int v = 0; v < V; ++v) s_x[warp][lane * V + v] = x[v];
+        if (lane == 0) s_sum[warp] = part;
+      }
+      __syncthreads();
+      if (r < nrows && run == 0) {
+        const float2 sum = join_row<D>(each, lane, x, [&](int k) { return s_sum[warp + k]; },
+                                       [&](int k) { return &s_x[warp + k][0]; });
+        write_o<D>(p, a.z, a.w, b.y + r, x, lse_of(sum.x, sum.y), lane);
+      }
+      __syncthreads();  // the sums have been read
+    }
+  }
+}
+
 template <int D, int FMT, int NT, bool SPARSE>
 hdp_status_t launch8(const AttnParams& p, int device, int ctas, cudaStream_t st) {
   static std::atomic<bool> ready[kDevices];
   constexpr int smem = sizeof(Shared<NT, SPARSE>);
   static_assert(smem <= 232448, "shared memory of a CTA");
+  const auto kernel = k_cache_attention<D, FMT, NT, SPARSE>;
   const int pieces = ctas * kWarps * (p.dynamic ? 1 + kMorePieces : 1);
-  return launch(k_cache_attention<D, FMT, NT, SPARSE>, k_cache_attention_join<D, NT>, kWarps, smem, pieces, ready, p, device, ctas, st);
+  if (pieces > 47 * 192)  // k_cache_attention_join's lists; a device of over 188 SMs
+    return fail(HDP_ERR_UNSUPPORTED, "hdp_cache_attention: too many SMs");
+  hdp_status_t r = allow(kernel, smem, ready, device);
+  if (r != HDP_OK) return r;
+  if (p.dynamic) {
+    k_cache_attention_start<<<1, 32, 0, st>>>(p);
+    note_launch();
+    HDP_CUDA_TRY(cudaGetLastError());
+    r = launch_early(kernel, dim3(ctas), kThreads, smem, st, p);
+  } else {
+    r = launch_attention(kernel, ctas, kThreads, smem, p, st);
+  }
+  if (r != HDP_OK) return r;
+  return launch_early(k_cache_attention_join<D, NT>, dim3(ctas), kJoinWarps * 32, 0, st, p, pieces);
 }
 
 template <int D, int FMT>

@@ -1,6 +1,7 @@
 // Attention of the newest tokens of each sequence over a paged cache: what the
 // kernels for 8 and for 4 bits share.  How the work is cut, the softmax's references
-// and the joining are explained in kv_attention.cu.
+// and the joining are explained in kv_attention.cu.  Lists of blocks (SPARSE) and pieces
+// that are handed out at run time (`dynamic`) are the 8-bit kernel's alone.
 #pragma once
 #include <cuda_fp16.h>
 
@@ -13,19 +14,12 @@
 namespace hdp {
 namespace {
 
-constexpr int kMeta = 8;           // blocks whose scales and first key are kept
 constexpr float kLow = -3.402823466e38f;  // reference exponent before the first key: below every finite score
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kBias = 15.f;                  // P is at most 2^15, in fp16
 constexpr float kBiasMost = 1048576.f;         // references above it are not biased: far below 2^24, so exactly
 constexpr float kNormal = 6.103515625e-05f;    // 2^-14, fp16's smallest normal number
 constexpr float kNextPass = 1099511627776.f;   // 2^40: what rounding to fp16 leaves below kNormal, 2^-25, to 2^15
-struct Meta {
-  float sk, sv;
-  int key0;   // first key of the block; -1: nothing of it is seen
-  int piece;  // the piece that the block belongs to
-};
-
 // A unit that several pieces share, for the kernel that joins them.
 struct __align__(16) Open {
   int parts, first, row0, head;  // parts: pieces first, first + 1, ...; 0: no unit
@@ -54,9 +48,6 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cas
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {
@@ -66,13 +57,6 @@ __device__ __forceinline__ void copies_wait() {
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// The smallest magnitude.
-__device__ __forceinline__ float least_of(float a, float b, float c) {
-  float r;
-  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -496,117 +480,7 @@ __device__ __forceinline__ void write_part(const AttnParams& p, const Sums<D, NT
   }
 }
 
-// Zeroes the counters while the attention's CTAs are starting.
-__global__ void k_cache_attention_start(const AttnParams p) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (threadIdx.x < 2) p.head[threadIdx.x] = 0;
-}
-
-// Joins the parts of units that several pieces share.  A CTA has every n-th
-// open unit (n CTAs), and its warps take rows of up to kAlone parts in turn.  A
-// 2M-token sequence leaves 600 parts for each of its few heads: the rows of such
-// units are dealt to all CTAs, whose warps then share a row's parts (that call:
-// 646 us with each unit's CTA joining its rows itself, 636 us so).
-constexpr int kJoinWarps = 16;
-// Two units share at most one piece, so n units of more than kAlone (48) parts take
-// more than n (kAlone - 1) pieces; of the others a CTA has one for each gridDim.x
-// pieces.  The host keeps both below this.
-constexpr int kMostShared = 256;
-template <int D, int NT>
-__global__ void __launch_bounds__(kJoinWarps * 32, 1) k_cache_attention_join(const AttnParams p, int pieces) {
-  constexpr int kRows = 8 * NT;
-  constexpr int kAlone = 48;  // most parts of a row that a warp joins alone
-  constexpr int kFew = 256;   // most parts of rows that a CTA joins at once
-  constexpr int V = D / 32;
-  __shared__ __align__(16) float s_x[kJoinWarps][D];
-  __shared__ float2 s_sum[kJoinWarps];
-  __shared__ int4 s_shared[kMostShared][2], s_own[kMostShared][2];  // shared units, and this CTA's others
-  __shared__ int s_n, s_own_n;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) s_n = s_own_n = 0;
-  __syncthreads();
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int made = min(pieces, __ldcg(p.head + (p.dynamic ? 0 : 2)));
-  auto at = [&](int e, int k, int r) { return (static_cast<size_t>(e + k) * 2 + (k == 0 ? 1 : 0)) * kRows + r; };
-
-  // This CTA's open units, and all shared ones where the units are listed as they
-  // came; where each piece has an entry (1,216 of them, which 152 CTAs reading all
-  // would take 4 us for), a CTA keeps to its own.
-  const int stride = p.dynamic ? 1 : gridDim.x, origin = p.dynamic ? 0 : blockIdx.x;
-  constexpr int kScan = 2;
-  for (int base = 0; base == 0 || origin + base * stride < made; base += kScan * kJoinWarps * 32) {
-    int4 a[kScan], b[kScan];  // the first loads do not wait for the units' number
-#pragma unroll
-    for (int u = 0; u < kScan; ++u) {
-      const int i = origin + (base + u * kJoinWarps * 32 + static_cast<int>(threadIdx.x)) * stride;
-      a[u] = b[u] = make_int4(0, 0, 0, 0);
-      if (i < pieces) {
-        a[u] = __ldcg(reinterpret_cast<const int4*>(p.open + i));
-        b[u] = __ldcg(reinterpret_cast<const int4*>(p.open + i) + 1);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kScan; ++u) {
-      const int i = origin + (base + u * kJoinWarps * 32 + static_cast<int>(threadIdx.x)) * stride;
-      if (i >= made || a[u].x == 0) continue;
-      const bool shared = a[u].x > kAlone;
-      if (!shared && i % gridDim.x != blockIdx.x) continue;
-      const int n = atomicAdd(shared ? &s_n : &s_own_n, 1);
-      if (n >= kMostShared) continue;  // cannot be (see there)
-      int4* to = shared ? s_shared[n] : s_own[n];
-      to[0] = a[u];
-      to[1] = b[u];
-    }
-  }
-  __syncthreads();
-
-  const int own = min(s_own_n, kMostShared);
-  int nth = 0;
-  for (int q = 0; q < own; ++q) {
-    const int4 a = s_own[q][0], b = s_own[q][1];
-    for (int r = 0; r < b.x; ++r) {
-      if (nth++ % kJoinWarps != warp) continue;
-      float x[V];
-      const float2 sum = join_row<D>(
-          a.x, lane, x, [&](int k) { return __ldcg(p.part_sum + at(a.y, k, r)); },
-          [&](int k) { return p.part + at(a.y, k, r) * D; });
-      write_o<D>(p, a.z, a.w, b.y + r, x, lse_of(sum.x, sum.y), lane);
-    }
-  }
-
-  const int n = min(s_n, kMostShared);
-  for (int q = 0; q < n; ++q) {
-    const int4 a = s_shared[q][0], b = s_shared[q][1];
-    const int m = a.x, e = a.y, nrows = b.x;
-    int rank = 0;  // of its first piece: the same in every CTA, whose lists differ in order
-    for (int z = lane; z < n; z += 32) rank += s_shared[z][0].y < e;
-    rank = __reduce_add_sync(0xffffffffu, rank);
-    // rows that a CTA joins at once, and warps for each
-    const int rows = m > kFew ? 1 : min(kJoinWarps, 1 << (32 - __clz(nrows - 1)) % 32), each = kJoinWarps / rows;
-    const int nr = warp / each, run = warp - nr * each;
-    for (int r0 = 0; r0 < nrows; r0 += rows) {
-      if (p.dynamic && (rank * nrows + r0) % static_cast<int>(gridDim.x) != static_cast<int>(blockIdx.x)) continue;
-      const int r = r0 + nr;
-      float x[V];
-      if (r < nrows) {
-        const int k0 = m * run / each, k1 = m * (run + 1) / each;
-        const float2 part = join_row<D>(
-            k1 - k0, lane, x, [&](int k) { return __ldcg(p.part_sum + at(e, k0 + k, r)); },
-            [&](int k) { return p.part + at(e, k0 + k, r) * D; });
-#pragma unroll
-        for (int v = 0; v < V; ++v) s_x[warp][lane * V + v] = x[v];
-        if (lane == 0) s_sum[warp] = part;
-      }
-      __syncthreads();
-      if (r < nrows && run == 0) {
-        const float2 sum = join_row<D>(each, lane, x, [&](int k) { return s_sum[warp + k]; },
-                                       [&](int k) { return &s_x[warp + k][0]; });
-        write_o<D>(p, a.z, a.w, b.y + r, x, lse_of(sum.x, sum.y), lane);
-      }
-      __syncthreads();  // the sums have been read
-    }
-  }
-}
+constexpr int kJoinWarps = 16;  // of a CTA that joins parts
 
 constexpr int kMaxNt = 2;
 // For each SM: entries of open, and parts of 16 rows.
@@ -660,29 +534,20 @@ hdp_status_t launch_early(void (*kernel)(T...), dim3 grid, int threads, int smem
   return HDP_OK;
 }
 
-// Launches `kernel` (`warps` a CTA, `smem` bytes) and `join` of its pieces, if any, behind it;
-// `ready`: the devices on which the kernel may have that much.
-hdp_status_t launch(void (*kernel)(AttnParams), void (*join)(AttnParams, int), int warps, int smem, int pieces, std::atomic<bool> (&ready)[kDevices],
-                    const AttnParams& p, int device, int ctas, cudaStream_t st) {
+// `kernel` may have `smem` bytes of shared memory; `ready`: the devices on which it has been told so.
+hdp_status_t allow(void (*kernel)(AttnParams), int smem, std::atomic<bool> (&ready)[kDevices], int device) {
   if (device >= kDevices || !ready[device].load(std::memory_order_relaxed)) {
     HDP_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     if (device < kDevices) ready[device].store(true, std::memory_order_relaxed);
   }
-  if (pieces > 47 * kMostShared)  // a device of over 256 (12 warps: 170) SMs
-    return fail(HDP_ERR_UNSUPPORTED, "attention over the cache: too many SMs");
-  if (p.dynamic) {
-    k_cache_attention_start<<<1, 32, 0, st>>>(p);
-    note_launch();
-    HDP_CUDA_TRY(cudaGetLastError());
-    const hdp_status_t r = launch_early(kernel, dim3(ctas), warps * 32, smem, st, p);
-    if (r != HDP_OK) return r;
-  } else {
-    kernel<<<ctas, warps * 32, smem, st>>>(p);
-    note_launch();
-    HDP_CUDA_TRY(cudaGetLastError());
-  }
-  if (pieces == 0) return HDP_OK;
-  return launch_early(join, dim3(ctas), kJoinWarps * 32, 0, st, p, pieces);
+  return HDP_OK;
+}
+
+hdp_status_t launch_attention(void (*kernel)(AttnParams), int ctas, int threads, int smem, const AttnParams& p, cudaStream_t st) {
+  kernel<<<ctas, threads, smem, st>>>(p);
+  note_launch();
+  HDP_CUDA_TRY(cudaGetLastError());
+  return HDP_OK;
 }
 
 // Checks and launches a call whose view is in p.c; hand_out: warps of a CTA that can hand

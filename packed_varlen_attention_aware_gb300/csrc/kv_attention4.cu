@@ -1002,7 +1002,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_cache4_attention(const AttnP
 // CTAs behind it: up to eight warps share a row's parts.  No lists of units are made, which
 // the join of handed-out pieces needs (16 drafts of 4 tokens 37.9 us, 38.9 by that).
 template <int D, int NT>
-__global__ void __launch_bounds__(kJoinWarps * 32, 1) k_cache4_join(const AttnParams p, int) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 1) k_cache4_join(const AttnParams p) {
   constexpr int kRows = 8 * NT;
   static_assert(kRows <= kJoinWarps, "a warp for each row");
   __shared__ __align__(16) float s_x[kJoinWarps][D];
@@ -1050,7 +1050,10 @@ hdp_status_t launch4(AttnParams p, int device, int sms, int ctas, cudaStream_t s
   const int64_t units = static_cast<int64_t>(p.c.num_seqs) * p.c.hkv * ((p.g + 8 * NT - 1) / (8 * NT));
   p.alone = !p.c.cu && units <= sms && p.c.max_pages <= 4 * kWarps;
   if (p.alone) ctas = static_cast<int>(units);
-  return launch(k_cache4_attention<D, NT>, k_cache4_join<D, NT>, kWarps, smem, p.alone ? 0 : ctas, ready, p, device, ctas, st);
+  hdp_status_t r = allow(k_cache4_attention<D, NT>, smem, ready, device);
+  if (r == HDP_OK) r = launch_attention(k_cache4_attention<D, NT>, ctas, kWarps * 32, smem, p, st);
+  if (r != HDP_OK || p.alone) return r;
+  return launch_early(k_cache4_join<D, NT>, dim3(ctas), kJoinWarps * 32, 0, st, p);
 }
 
 template <int D>
