@@ -11,8 +11,8 @@
 //   Work.  Each of 8 warps an SM has an equal run of the order and a ring of blocks in
 //   shared memory of its own, K and V of a block asked for apart; no barrier stands in the
 //   loop.  Parts of a unit are joined within the CTA, then between CTAs by a small kernel.
-//   Measured (32 / 8 heads of 128, in a captured graph): 2,097,152 tokens 338 us, 6.6 TB/s,
-//   0.98 of the copy rate; 64 sequences of 411,000 tokens 92 us, 0.81: 4 to 8 us until data
+//   Measured (32 / 8 heads of 128, in a captured graph): 2,097,152 tokens 341 us, 6.5 TB/s,
+//   0.96 of the copy rate; 64 sequences of 411,000 tokens 93 us, 0.80: 4 to 8 us until data
 //   flows, SMs that end 9 us apart, 4 us for the join.
 //   Codes.  e2m1 is exact in fp16, and the conversion instruction takes a byte: one
 //   for two codes, where the 8-bit kinds need four and seven cycles for as many.  The
@@ -26,7 +26,11 @@
 //   Scales of V go into P, as powers of two relative to the output's reference.
 //   References.  Where every P of a block, under the references that the sums have, is a
 //   normal number of fp16 (2^-14 to 2^15), it stays under them: nothing is rescaled, no
-//   product can lose a small P, and the second product adds to the output in place.
+//   product can lose a small P, and the second product's sums are added to the output's.
+//   (Added in fp32, to nearest: the matrix instruction cuts its sums off.  With the output
+//   as its accumulator an instruction less an element is needed, and 2M tokens take 338 us,
+//   64 sequences 92.0 and 16 drafts of 4 tokens 38.5, but all that is cut off has one sign:
+//   2^-12 of the output where a warp has 131,072 tokens, 2^-6 at 2M.)
 //   Fresh references are 4 bits above what needs them, so that is all but the first blocks
 //   of a run unless a block's scores are spread over more than 17 nats.  Else P is taken
 //   from the block's own largest, the sums come to new references, and what fp16 leaves of
@@ -36,13 +40,12 @@
 //   that weigh more are zero, and a block on that path also forms the sum of P |v| for each
 //   row and channel.  The smallest of them is a budget: so many blocks with small P stay
 //   quick that all they lose is 2^-12 of that sum (a P's rounding is up to 2^-11 of it).
-//   64 sequences whose scores deviate by 1.7, 2.5 and 3.4 nats: 165, 326 and 482 us; 299,
-//   792 and 802 without a budget and with all sums rescaled for each block; by 0.85, 92.
+//   64 sequences whose scores deviate by 1.7, 2.5 and 3.4 nats: 164, 330 and 480 us; 299,
+//   792 and 802 without a budget and with all sums rescaled for each block; by 0.85, 93.
 //   Scores past fp32's end.  A sum of products may pass it before the row's factor brings it
 //   back, and a NaN scale makes it infinite: such a block goes to the general path.  As
 //   -infinity it would pass for a masked one.  Only blocks that are not all normal are
-//   searched for it: in them its P is 0.  (Part of the times above: 161, 321 and 461 us, and
-//   2M tokens 336 instead of 338, without the search.)
+//   searched for it: in them its P is 0.
 #include "kv_attention.cuh"
 #include "kv_cache4.cuh"
 
@@ -203,9 +206,8 @@ __device__ __forceinline__ void first_product(const Rows<D, NT>& rows, const uns
   }
 }
 
-// Y += V^T P^T for the channels 16 i .. 16 i + 16 kTogether - 1; FIRST: there is no sum to add
-// to; SIZE: of |V|.
-template <bool FIRST, int NT, bool SIZE = false>
+// Y = V^T P^T for the channels 16 i .. 16 i + 16 kTogether - 1; SIZE: of |V|.
+template <int NT, bool SIZE = false>
 __device__ __forceinline__ void second_product(const uint4* vx, int i, const uint32_t (&pf)[NT][4][2],
                                                float (&y)[NT][kTogether][4]) {
   uint4 u[kTogether];
@@ -227,7 +229,7 @@ __device__ __forceinline__ void second_product(const uint4* vx, int i, const uin
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        if (FIRST && k == 0) mma16816_first(y[t][h], a[0], b[0], a[1], b[1], pf[t][k][0], pf[t][k][1]);
+        if (k == 0) mma16816_first(y[t][h], a[0], b[0], a[1], b[1], pf[t][k][0], pf[t][k][1]);
         else mma16816(y[t][h], a[0], b[0], a[1], b[1], pf[t][k][0], pf[t][k][1]);
         mma16816(y[t][h], a[2], b[2], a[3], b[3], pf[t][k + 1][0], pf[t][k + 1][1]);
       }
@@ -557,7 +559,7 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
     for (int i = 0; i < D / 16; i += kTogether) {
       float y[NT][kTogether][4];
       if (first) {
-        second_product<true, NT, true>(vx, i, pf, y);
+        second_product<NT, true>(vx, i, pf, y);
 #pragma unroll
         for (int h = 0; h < kTogether; ++h)
 #pragma unroll
@@ -566,7 +568,7 @@ __device__ __noinline__ void any_block(Slow<D, NT>& slow, int warp, int slot, in
             for (int k = 0; k < 4; ++k)
               if (t * 8 + 2 * tc + (k & 1) < nrows) least = fminf(least, y[t][h][k] * pass * f[t][k & 1]);
       }
-      second_product<true, NT>(vx, i, pf, y);
+      second_product<NT>(vx, i, pf, y);
 #pragma unroll
       for (int h = 0; h < kTogether; ++h)
 #pragma unroll
@@ -899,19 +901,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_cache4_attention(const AttnP
 #pragma unroll
           for (int i = 0; i < D / 16; i += kTogether) {
             float y[NT][kTogether][4];
+            second_product<NT>(vx, i, pf, y);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
               for (int h = 0; h < kTogether; ++h)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[t][h][k] = sums.acc[t][i + h][k];
-            second_product<false, NT>(vx, i, pf, y);
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-              for (int h = 0; h < kTogether; ++h)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sums.acc[t][i + h][k] = y[t][h][k];
+                for (int k = 0; k < 4; ++k) sums.acc[t][i + h][k] += y[t][h][k];
           }
         }
         issue_v();
