@@ -168,6 +168,8 @@ hdp_status_t hdp_attention_workspace_bytes(hdp_plan_t plan, int32_t hq, int32_t 
  *   only weaken the pacing (every hold is bounded) and never changes the
  *   results.
  *   q, k, v, o must be 16-byte aligned.
+ *   Sums of products are cut off, not rounded, in fp32: outputs of rows that see n
+ *   keys of like weight are too small by about n 2^-27.5 of themselves (0.6 % at 1M).
  * Device-side wait timeouts are reported by hdp_device_status.
  */
 hdp_status_t hdp_attention_fwd(hdp_plan_t plan, const void* q, const void* k, const void* v, int32_t hq,
@@ -456,7 +458,7 @@ hdp_status_t hdp_fourbit_read(const hdp_fourbit_cache_t* cache, const int32_t* c
  * times |v| besides what each loses to rounding; and that where a row's score passes
  * fp32's end before it is multiplied by `scale`, K scales below 2^-94 may count as 0 in
  * the 64 keys of its block.  A call takes longer where the scores of a head deviate by
- * more than a nat: 1.8 times as long at 1.7 nats, 5 times at 3.4.
+ * more than a nat or so: up to 1.8 times as long at 1.7 nats, 5 times at 3.4.
  * workspace: device, 256-byte aligned, at least
  * hdp_fourbit_attention_workspace_bytes, which depends on the device's SM count and
  * d only (152 SMs: 12.7 MB for d = 128, 6.4 MB for d = 64); calls that may overlap

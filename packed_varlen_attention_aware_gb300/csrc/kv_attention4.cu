@@ -12,7 +12,7 @@
 //   shared memory of its own, K and V of a block asked for apart; no barrier stands in the
 //   loop.  Parts of a unit are joined within the CTA, then between CTAs by a small kernel.
 //   Measured (32 / 8 heads of 128, in a captured graph): 2,097,152 tokens 341 us, 6.5 TB/s,
-//   0.96 of the copy rate; 64 sequences of 411,000 tokens 93 us, 0.80: 4 to 8 us until data
+//   0.97 of the copy rate; 64 sequences of 411,000 tokens 93 us, 0.80: 4 to 8 us until data
 //   flows, SMs that end 9 us apart, 4 us for the join.
 //   Codes.  e2m1 is exact in fp16, and the conversion instruction takes a byte: one
 //   for two codes, where the 8-bit kinds need four and seven cycles for as many.  The
@@ -40,8 +40,9 @@
 //   that weigh more are zero, and a block on that path also forms the sum of P |v| for each
 //   row and channel.  The smallest of them is a budget: so many blocks with small P stay
 //   quick that all they lose is 2^-12 of that sum (a P's rounding is up to 2^-11 of it).
-//   64 sequences whose scores deviate by 1.7, 2.5 and 3.4 nats: 164, 330 and 480 us; 299,
-//   792 and 802 without a budget and with all sums rescaled for each block; by 0.85, 93.
+//   64 sequences of random codes whose scores deviate by 1.7, 2.5 and 3.4 nats: 165, 322 and
+//   478 us; 299, 792 and 802 without a budget and with all sums rescaled for each block; by
+//   0.85, 93.  Of normally distributed V, with fewer zeros: 96, 130 and 282.
 //   Scores past fp32's end.  A sum of products may pass it before the row's factor brings it
 //   back, and a NaN scale makes it infinite: such a block goes to the general path.  As
 //   -infinity it would pass for a masked one.  Only blocks that are not all normal are
