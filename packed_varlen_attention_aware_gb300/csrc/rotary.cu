@@ -400,8 +400,11 @@ extern "C" hdp_status_t hdp_rotary(const hdp_rotary_rows_t* q, const hdp_rotary_
   for (int i = 0; i < 2; ++i) {
     if (!p.heads[i]) continue;
     const RotaryTensor& x = p.x[i];
-    in[i] = {static_cast<long long>(reinterpret_cast<intptr_t>(x.in) / size), x.in_row, x.in_head, p.heads[i]};
-    out[i] = {static_cast<long long>(reinterpret_cast<intptr_t>(x.out) / size), x.out_row, x.out_head, p.heads[i]};
+    const auto places = [&](const char* at, long long row, long long head) -> Places {  // (a stride to nowhere says nothing)
+      return {static_cast<long long>(reinterpret_cast<intptr_t>(at) / size), rows > 1 ? row : 0, p.heads[i] > 1 ? head : 0, p.heads[i]};
+    };
+    in[i] = places(x.in, x.in_row, x.in_head);
+    out[i] = places(x.out, x.out_row, x.out_head);
     if (meets_itself(out[i], rows, d))
       return fail(HDP_ERR_INVALID_ARGUMENT, name + "rows and heads of an output must not overlap");
     if (x.in != x.out && may_meet(in[i], out[i], rows, d))

@@ -78,6 +78,9 @@ def test_outputs_over_themselves(lib):
 def test_strides_that_leave_memory(lib):
     assert ITSELF in _refusal(lib, ((0, 64, 64, 1), (64, 1 << 60, 64, 1)), None, 2 ** 31 - 1, 64)
     assert OWN in _refusal(lib, ((0, 1 << 60, 64, 1), (1 << 16, 64, 64, 1)), None, 2 ** 20, 64)
+    least, most = -2 ** 63, 2 ** 63 - 1  # strides that are never taken
+    assert FREE in _refusal(lib, ((0, most, 64, 2),) * 2, ((128, least, most, 1),) * 2, 1, 64)
+    assert OTHERS in _refusal(lib, ((0, least, least, 1),) * 2, ((63, most, most, 1),) * 2, 1, 64)
 
 
 def _elements(x, rows, d):
